@@ -30,6 +30,7 @@
 //   * every wait is bounded; a timeout aborts all roles, drains in-flight
 //     copies and MMAs, frees TMEM and records QMOE_ERR_TIMEOUT.
 #include "qmoe_prefill.cuh"
+#include "qmoe_tc.cuh"
 
 namespace qmoe {
 
@@ -255,36 +256,8 @@ cudaError_t launch_finalize_acc(float* acc, void* out, size_t n, int dtype, cuda
 }
 
 // ----------------------------------------------------------------------------
-// tcgen05 / TMA helpers
+// tcgen05 helpers of this kernel
 // ----------------------------------------------------------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// The MMA-issuing code runs on a whole converged warp and the tcgen05
-// instructions are predicated on one lane chosen by elect.sync: the operands
-// are then warp-uniform values.  Issued from a single divergent lane, the same
-// loop reached about half the MMA rate (measured: 119 vs 65 cycles per
-// 128x128x16 MMA).
-__device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
 // Four K=16 MMAs of one 64-deep k-step from one asm block: A columns a0 + 8j,
 // B descriptor start advanced 32 bytes per MMA; the first accumulates into D
 // only when `acc` is set, the rest always do.  One elected lane issues.
@@ -305,48 +278,8 @@ __device__ __forceinline__ void umma_ts_x4_elect(uint32_t d, uint32_t a0, uint64
       : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void red_add_f32(float* p, float v) {
   asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
-}
-
-#define TC_LD32(taddr, v)                                                                               \
-  asm volatile(                                                                                         \
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"  \
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"                        \
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), \
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),        \
-        "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),      \
-        "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),      \
-        "=r"(v[29]), "=r"(v[30]), "=r"(v[31])                                                           \
-      : "r"(taddr)                                                                                      \
-      : "memory")
-
-#define TC_ST32(taddr, v)                                                                                \
-  asm volatile(                                                                                          \
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15," \
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),              \
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), \
-      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),    \
-      "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),    \
-      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])                 \
-      : "memory")
-
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFF) >> 4);          // start address
-  d |= (uint64_t)1 << 16;                           // leading byte offset (unused for SW128 K-major)
-  d |= (uint64_t)(1024 >> 4) << 32;                 // stride byte offset
-  d |= (uint64_t)1 << 46;                           // descriptor version
-  d |= (uint64_t)2 << 61;                           // 128-byte swizzle
-  return d;
 }
 
 // Instruction descriptor, kind::f16: D f32, A/B f16 or bf16, both K-major.
@@ -358,27 +291,6 @@ __device__ __forceinline__ uint32_t idesc_f16(bool bf16, int M, int N) {
   d |= (uint32_t)(N >> 3) << 17;
   d |= (uint32_t)(M >> 4) << 24;
   return d;
-}
-
-// One poll of a phase whose answer is the same for the whole warp: every lane
-// polls, lane 0's answer is broadcast.  (Each lane acting on its own answer
-// can split the warp when the phase completes during the poll; the split
-// halves would then reach different warp-synchronous instructions.)
-__device__ __forceinline__ bool warp_test_wait(uint64_t* bar, uint32_t parity) {
-  const int done = mbar_test_wait(bar, parity) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, done, 0) != 0;
-}
-
-// Bounded wait that also gives up when another role has aborted.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const WaitCfg& w,
-                                              volatile int* abort_flag) {
-  for (long long i = 0; i < w.limit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63) == 63 && *abort_flag) return false;
-  }
-  atomicExch(w.status, DEV_TIMEOUT);
-  *abort_flag = 1;
-  return false;
 }
 
 // Bounded wait for a global count (acquire), giving up when another role aborted.
@@ -399,21 +311,6 @@ __device__ __forceinline__ bool count_wait_or_abort(const int* p, int target, co
 // Units (of 2 warps x rows) an item's overlapped gather is cut into: enough
 // that the first wave's items (the first 152 tiles) are spread over every CTA.
 constexpr int kGatherUnits = 32;
-
-// The same with non-blocking polls: for the MMA-issuing thread, whose loop
-// paces the whole pipeline (a parked poll costs ~250 cycles even when the
-// phase has already completed).
-__device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, const WaitCfg& w,
-                                              volatile int* abort_flag) {
-  const long long limit = w.limit * 64;
-  for (long long i = 0; i < limit; ++i) {
-    if (mbar_test_wait(bar, parity)) return true;
-    if ((i & 255) == 255 && *abort_flag) return false;
-  }
-  atomicExch(w.status, DEV_TIMEOUT);
-  *abort_flag = 1;
-  return false;
-}
 
 // ----------------------------------------------------------------------------
 // The grouped GEMM kernel
@@ -594,21 +491,6 @@ __device__ __forceinline__ TileSrc tile_src(const GemmArgs& a, int tile) {
   r.b_bytes = (uint32_t)min(Ring<DEC, BITS>::bsub, ((it.rows + 7) / 8) * 1024);
   r.rot = Ring<DEC, BITS>::ksub > 1 ? 0 : (int)(((long long)nt * L.ksteps) / L.ntiles);
   return r;
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx_elect(uint64_t* bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)), "r"(bytes)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_g2s_elect(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
 }
 
 // Warp roles (8 + 4 * groups warps):
