@@ -383,6 +383,168 @@ const char* qmoe_status_string(qmoe_status status);
  * [qmoe.rs `impl Drop for QMoEKernel`: frees every scratch slot] */
 void qmoe_destroy(qmoe_layer* layer);
 
+/* ========================================================================
+ * Operators around the expert layer
+ *
+ * What a block built from the layer's parts needs beside qmoe_forward: the
+ * routes sorted by expert and the rows taken there and back (with their
+ * gradients), microscaled 4-bit floating point rows and their product, and
+ * the norms on either side of the block.  (No counterpart in the pages but
+ * the grouping and the combine, whose definitions are those of qmoe_forward:
+ * [qmoe.rs launch_grouping, qmoe_combine_impl].)
+ *
+ * Conventions beyond the ones at the top: these calls take no layer, keep
+ * nothing between calls and allocate nothing, so any number may run on any
+ * streams at once and all may be captured into a CUDA graph.  Matrices are
+ * row-major with a row stride ld in elements (at least the row length; the
+ * last axis is contiguous); 16-byte aligned rows run fastest, any alignment
+ * is right.  Outputs without an ld are contiguous and may not overlap inputs.
+ * Zero tokens or rows are OK and launch nothing (sums over rows are written
+ * as zeros).  A failed call's message: qmoe_op_last_error, of the calling
+ * thread.
+ * ======================================================================== */
+
+/* Message of the last failed call below on this thread ("" if none). */
+const char* qmoe_op_last_error(void);
+
+/* Read and clear the device status of these operators: QMOE_OK, or
+ * QMOE_ERR_TIMEOUT if a bounded wait of a qmoe_mx4_matmul of this context ran
+ * out since the last poll (its output is then meaningless).  Synchronises the
+ * device. */
+qmoe_status qmoe_op_poll_status(void);
+
+/* The iteration limit of their bounded waits (0 = the default), and the test
+ * hook that arms the first copy of every later qmoe_mx4_matmul without
+ * issuing it (see qmoe_debug_inject_stall).  Both hold for the process. */
+qmoe_status qmoe_op_set_wait_limit(int64_t iterations);
+qmoe_status qmoe_op_debug_inject_stall(int enable);
+
+/*
+ * Routes sorted by expert.  Route r = t * top_k + j goes to expert ids[t, j];
+ * an id outside [0, experts) drops it (no row).
+ *   ids_dev     int32 (id_bytes 4) or int64 (8) [num_tokens, top_k], rows ld_ids apart
+ *   perm_dev    int32 [num_tokens * top_k]  routes by expert, ascending route
+ *               inside (stable); -1 from offsets[experts] on
+ *   pos_dev     int32 [num_tokens * top_k]  row of each route, -1 if dropped
+ *   offsets_dev int32 [experts + 1]         first row of each expert; the last
+ *               is the number of rows in use
+ * experts <= 1024 (UNSUPPORTED beyond).
+ */
+qmoe_status qmoe_expert_sort(const void* ids_dev, int id_bytes, int64_t ld_ids, int64_t num_tokens, int top_k, int experts,
+                             int32_t* perm_dev, int32_t* pos_dev, int32_t* offsets_dev, void* stream);
+
+/* Token rows into expert order: xs[pos[t, j]] = x[t]; the rows from
+ * offsets[experts] on are zeros.  xs is [num_tokens * top_k, hidden]. */
+qmoe_status qmoe_dispatch(const void* x_dev, int64_t ld_x, const int32_t* pos_dev, const int32_t* offsets_dev,
+                          int64_t num_tokens, int top_k, int experts, int64_t hidden, int dtype, void* xs_dev, void* stream);
+
+/* Its gradient: dx[t] = sum_j dxs[pos[t, j]], slots in order, fp32, one
+ * rounding.  Rows no route owns are not read. */
+qmoe_status qmoe_dispatch_grad(const void* dxs_dev, int64_t ld_dxs, const int32_t* pos_dev, int64_t num_tokens, int top_k,
+                               int64_t hidden, int dtype, void* dx_dev, void* stream);
+
+/* Expert rows back to token order: out[t] = sum_j weights[t, j] * y[pos[t, j]],
+ * slots in order, fp32, one rounding; dropped slots add nothing (a token with
+ * none left gets zeros).  weights float32 [num_tokens, top_k], NULL = ones. */
+qmoe_status qmoe_combine(const void* y_dev, int64_t ld_y, const float* weights_dev, const int32_t* pos_dev,
+                         int64_t num_tokens, int top_k, int64_t hidden, int dtype, void* out_dev, void* stream);
+
+/* Its gradients: dy[pos[t, j]] = weights[t, j] * dout[t] (zeros from
+ * offsets[experts] on) and dweights[t, j] = <dout[t], y[pos[t, j]]> (float32;
+ * 0 for a dropped slot).  dy_dev or dweights_dev may be NULL. */
+qmoe_status qmoe_combine_grad(const void* dout_dev, int64_t ld_dout, const void* y_dev, int64_t ld_y,
+                              const float* weights_dev, const int32_t* pos_dev, const int32_t* offsets_dev,
+                              int64_t num_tokens, int top_k, int experts, int64_t hidden, int dtype, void* dy_dev,
+                              float* dweights_dev, void* stream);
+
+/*
+ * Microscaled 4-bit rows (the MXFP4 format of the OCP Microscaling
+ * specification): blocks of 32 values along a row share a power-of-two scale
+ * 2^(s - 127), s = its byte (255: NaN); elements are E2M1 (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives).
+ *   codes  uint8 [rows, 16 * nb], nb = ceil(cols / 32): element d in byte d / 2
+ *          of its row, even d in the low half; zeros past cols
+ *   scales uint8 [rows / panel_rows][ceil(nb / 4)][panel_rows][4]: in each
+ *          panel the four scales of 128 values of consecutive rows side by
+ *          side; zeros past nb.  A stack of E matrices [E, N, K] has
+ *          panel_rows = N, a single matrix panel_rows = rows.
+ *
+ * qmoe_mx4_quantize: s = clamp(floor(log2(largest magnitude)) - 2 + 127, 0,
+ * 254); elements rounded to the nearest, ties to the even code, saturated at
+ * 6; a block with a NaN or an infinity gets s = 255.
+ *   x_dev       dtype [rows, cols]; with a gated activation [rows, 2 * cols]
+ *               (gate | up), quantised after act(gate) * up in fp32
+ *   activation  QMOE_ACT_NONE, QMOE_ACT_SWIGLU or QMOE_ACT_GEGLU_TANH
+ *   pos_dev     NULL, or int32 [rows, top_k] of qmoe_expert_sort: row t is
+ *               then written to the rows pos[t, j] of a [rows * top_k, cols]
+ *               output, whose rows from offsets[experts] on are zeros.
+ *               offsets_dev, top_k and experts belong to pos_dev.
+ * codes_dev must be 16-byte, scales_dev 4-byte aligned.
+ */
+enum { QMOE_ACT_NONE = -1 };
+qmoe_status qmoe_mx4_quantize(const void* x_dev, int64_t ld_x, int64_t rows, int64_t cols, int dtype, int activation,
+                              const int32_t* pos_dev, const int32_t* offsets_dev, int top_k, int experts,
+                              int64_t panel_rows, uint8_t* codes_dev, uint8_t* scales_dev, void* stream);
+
+/* The values of microscaled rows, rounded once to dtype (exact in float32 and,
+ * but for the very smallest, in bfloat16). */
+qmoe_status qmoe_mx4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_t rows, int64_t cols,
+                                int64_t panel_rows, int dtype, void* out_dev, int64_t ld_out, void* stream);
+
+/*
+ * Product of microscaled rows with microscaled weights:
+ *   out[i, c] = sum_d a[i, d] * w[e, c, d],  offsets[e] <= i < offsets[e + 1]
+ * (fp32 accumulation, one rounding to out_dtype); rows from offsets[experts]
+ * on are zeros.  offsets_dev NULL: one expert, all rows.
+ *   a  [rows, k], one panel of rows;  w  [experts, n, k], panel_rows = n
+ *   out_dev  out_dtype [rows, n], row stride ld_out
+ * Both codes must be 16-byte aligned; experts <= 1024.
+ */
+qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
+                            const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,
+                            int experts, int64_t n, int64_t k, int out_dtype, void* out_dev, int64_t ld_out, void* stream);
+
+/*
+ * The norms on either side of a block, with the gate of its output and the
+ * residual scale, in one pass (all arithmetic in fp32, one rounding):
+ *   r = residual_scale * x + gate * n,  n = o * rstd_post * w_post,
+ *   rstd_post = 1 / sqrt(mean(o^2) + eps) of each row
+ *   h = r * rstd_pre * w_pre,  rstd_pre = 1 / sqrt(mean(r^2) + eps)
+ *   x_dev, o_dev  dtype [num_tokens, hidden]; o_dev NULL: r = residual_scale * x
+ *   gate_dev      dtype, by gate_kind: QMOE_GATE_NONE (NULL; 1),
+ *                 _TOKEN [num_tokens], _CHANNEL [hidden], _FULL [num_tokens,
+ *                 hidden] with row stride ld_gate
+ *   w_post_dev    dtype [hidden], or NULL: n = o
+ *   w_pre_dev     dtype [hidden], or NULL: no h
+ *   r_dev, h_dev  outputs; r_dev may be NULL, h_dev is NULL iff w_pre_dev is
+ *   rstd_post_dev, rstd_pre_dev  float32 [num_tokens] for the gradient, or NULL
+ * hidden <= 16384 (UNSUPPORTED beyond).
+ */
+enum { QMOE_GATE_NONE = 0, QMOE_GATE_TOKEN = 1, QMOE_GATE_CHANNEL = 2, QMOE_GATE_FULL = 3 };
+qmoe_status qmoe_block_norm(const void* x_dev, int64_t ld_x, const void* o_dev, int64_t ld_o, const void* gate_dev,
+                            int gate_kind, int64_t ld_gate, const void* w_post_dev, const void* w_pre_dev,
+                            float residual_scale, float eps, int64_t num_tokens, int64_t hidden, int dtype, void* r_dev,
+                            void* h_dev, float* rstd_post_dev, float* rstd_pre_dev, void* stream);
+
+/* Bytes of workspace qmoe_block_norm_grad needs (0 for arguments it refuses). */
+size_t qmoe_block_norm_grad_workspace(int64_t num_tokens, int64_t hidden, int dtype);
+
+/*
+ * Its gradients.  dr_dev and dh_dev are the gradients of r and h (NULL: zero),
+ * x, o, gate, w_post, w_pre and residual_scale the forward's arguments,
+ * rstd_post and rstd_pre its statistics.  Outputs (any may be NULL), all in
+ * dtype: dx, do [num_tokens, hidden], dgate in the gate's shape (contiguous),
+ * dw_post and dw_pre [hidden]; sums in fp32, in an order that does not change
+ * from run to run.
+ */
+qmoe_status qmoe_block_norm_grad(const void* dr_dev, int64_t ld_dr, const void* dh_dev, int64_t ld_dh, const void* x_dev,
+                                 int64_t ld_x, const void* o_dev, int64_t ld_o, const void* gate_dev, int gate_kind,
+                                 int64_t ld_gate, const void* w_post_dev, const void* w_pre_dev,
+                                 const float* rstd_post_dev, const float* rstd_pre_dev, float residual_scale,
+                                 int64_t num_tokens, int64_t hidden, int dtype, void* dx_dev, void* do_dev,
+                                 void* dgate_dev, void* dw_post_dev, void* dw_pre_dev, void* workspace_dev,
+                                 size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,10 +28,14 @@ QMOE_TRACE_NUM_EVENTS = 5
 QMOE_PATH_NONE, QMOE_PATH_SEPARATE, QMOE_PATH_FUSED = 0, 1, 2
 QMOE_FUSED_OFF, QMOE_FUSED_ON, QMOE_FUSED_AUTO = 0, 1, 2
 QMOE_COMBINE_REDUCE, QMOE_COMBINE_ORDERED, QMOE_COMBINE_AUTO = 0, 1, 2
+QMOE_ACT_NONE = -1
+QMOE_GATE_NONE, QMOE_GATE_TOKEN, QMOE_GATE_CHANNEL, QMOE_GATE_FULL = 0, 1, 2, 3
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _i64 = ctypes.c_int64
+_f = ctypes.c_float
+_sz = ctypes.c_size_t
 _SIGS = {
     "qmoe_create": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_p)]),
     "qmoe_set_routing": (_i, [_p, _i]),
@@ -58,6 +62,23 @@ _SIGS = {
     "qmoe_last_error": (ctypes.c_char_p, [_p]),
     "qmoe_status_string": (ctypes.c_char_p, [_i]),
     "qmoe_destroy": (None, [_p]),
+    # operators around the layer
+    "qmoe_op_last_error": (ctypes.c_char_p, []),
+    "qmoe_op_poll_status": (_i, []),
+    "qmoe_op_set_wait_limit": (_i, [_i64]),
+    "qmoe_op_debug_inject_stall": (_i, [_i]),
+    "qmoe_expert_sort": (_i, [_p, _i, _i64, _i64, _i, _i, _p, _p, _p, _p]),
+    "qmoe_dispatch": (_i, [_p, _i64, _p, _p, _i64, _i, _i, _i64, _i, _p, _p]),
+    "qmoe_dispatch_grad": (_i, [_p, _i64, _p, _i64, _i, _i64, _i, _p, _p]),
+    "qmoe_combine": (_i, [_p, _i64, _p, _p, _i64, _i, _i64, _i, _p, _p]),
+    "qmoe_combine_grad": (_i, [_p, _i64, _p, _i64, _p, _p, _p, _i64, _i, _i, _i64, _i, _p, _p, _p]),
+    "qmoe_mx4_quantize": (_i, [_p, _i64, _i64, _i64, _i, _i, _p, _p, _i, _i, _i64, _p, _p, _p]),
+    "qmoe_mx4_dequantize": (_i, [_p, _p, _i64, _i64, _i64, _i, _p, _i64, _p]),
+    "qmoe_mx4_matmul": (_i, [_p, _p, _i64, _p, _p, _p, _i, _i64, _i64, _i, _p, _i64, _p]),
+    "qmoe_block_norm": (_i, [_p, _i64, _p, _i64, _p, _i, _i64, _p, _p, _f, _f, _i64, _i64, _i, _p, _p, _p, _p, _p]),
+    "qmoe_block_norm_grad_workspace": (_sz, [_i64, _i64, _i]),
+    "qmoe_block_norm_grad": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i, _i64, _p, _p, _p, _p, _f, _i64, _i64,
+                                  _i, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 
 _lib = None
@@ -203,3 +224,77 @@ def qmoe_status_string(status):
 
 def qmoe_destroy(layer):
     load().qmoe_destroy(layer)
+
+
+# --- operators around the layer ----------------------------------------------
+# Addresses are integers (0 or None = NULL), strides and sizes in elements, in
+# the order of include/qmoe.h.
+def qmoe_op_last_error():
+    return load().qmoe_op_last_error().decode()
+
+
+def qmoe_op_poll_status():
+    return load().qmoe_op_poll_status()
+
+
+def qmoe_op_set_wait_limit(iterations):
+    return load().qmoe_op_set_wait_limit(int(iterations))
+
+
+def qmoe_op_debug_inject_stall(enable):
+    return load().qmoe_op_debug_inject_stall(int(enable))
+
+
+def qmoe_expert_sort(ids, id_bytes, ld_ids, num_tokens, top_k, experts, perm, pos, offsets, stream):
+    return load().qmoe_expert_sort(ids, id_bytes, ld_ids, num_tokens, top_k, experts, perm, pos, offsets, stream)
+
+
+def qmoe_dispatch(x, ld_x, pos, offsets, num_tokens, top_k, experts, hidden, dtype, xs, stream):
+    return load().qmoe_dispatch(x, ld_x, pos, offsets, num_tokens, top_k, experts, hidden, dtype, xs, stream)
+
+
+def qmoe_dispatch_grad(dxs, ld_dxs, pos, num_tokens, top_k, hidden, dtype, dx, stream):
+    return load().qmoe_dispatch_grad(dxs, ld_dxs, pos, num_tokens, top_k, hidden, dtype, dx, stream)
+
+
+def qmoe_combine(y, ld_y, weights, pos, num_tokens, top_k, hidden, dtype, out, stream):
+    return load().qmoe_combine(y, ld_y, weights, pos, num_tokens, top_k, hidden, dtype, out, stream)
+
+
+def qmoe_combine_grad(dout, ld_dout, y, ld_y, weights, pos, offsets, num_tokens, top_k, experts, hidden, dtype, dy,
+                      dweights, stream):
+    return load().qmoe_combine_grad(dout, ld_dout, y, ld_y, weights, pos, offsets, num_tokens, top_k, experts, hidden,
+                                    dtype, dy, dweights, stream)
+
+
+def qmoe_mx4_quantize(x, ld_x, rows, cols, dtype, activation, pos, offsets, top_k, experts, panel_rows, codes, scales,
+                      stream):
+    return load().qmoe_mx4_quantize(x, ld_x, rows, cols, dtype, activation, pos, offsets, top_k, experts, panel_rows,
+                                    codes, scales, stream)
+
+
+def qmoe_mx4_dequantize(codes, scales, rows, cols, panel_rows, dtype, out, ld_out, stream):
+    return load().qmoe_mx4_dequantize(codes, scales, rows, cols, panel_rows, dtype, out, ld_out, stream)
+
+
+def qmoe_mx4_matmul(a_codes, a_scales, rows, w_codes, w_scales, offsets, experts, n, k, out_dtype, out, ld_out, stream):
+    return load().qmoe_mx4_matmul(a_codes, a_scales, rows, w_codes, w_scales, offsets, experts, n, k, out_dtype, out,
+                                  ld_out, stream)
+
+
+def qmoe_block_norm(x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre, residual_scale, eps, num_tokens, hidden,
+                    dtype, r, h, rstd_post, rstd_pre, stream):
+    return load().qmoe_block_norm(x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre, residual_scale, eps,
+                                  num_tokens, hidden, dtype, r, h, rstd_post, rstd_pre, stream)
+
+
+def qmoe_block_norm_grad_workspace(num_tokens, hidden, dtype):
+    return load().qmoe_block_norm_grad_workspace(num_tokens, hidden, dtype)
+
+
+def qmoe_block_norm_grad(dr, ld_dr, dh, ld_dh, x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre, rstd_post,
+                         rstd_pre, residual_scale, num_tokens, hidden, dtype, dx, do, dgate, dw_post, dw_pre, workspace,
+                         workspace_bytes, stream):
+    return load().qmoe_block_norm_grad(dr, ld_dr, dh, ld_dh, x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre,
+                                       rstd_post, rstd_pre, residual_scale, num_tokens, hidden, dtype, dx, do, dgate,
+                                       dw_post, dw_pre, workspace, workspace_bytes, stream)

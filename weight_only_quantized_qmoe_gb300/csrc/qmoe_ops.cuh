@@ -1,0 +1,230 @@
+// Operators around the expert layer: argument blocks and launchers shared by
+// their entry points (qmoe_ops_api.cu) and their kernels (qmoe_sort.cu,
+// qmoe_mx4.cu, qmoe_mx4_gemm.cu, qmoe_norm.cu).
+#pragma once
+
+#include "qmoe_internal.cuh"
+
+namespace qmoe {
+
+// Experts one sort handles (a warp's counters of all experts are held in
+// shared memory, 32 warps of them).
+constexpr int kSortMaxExperts = 1024;
+
+struct SortArgs {
+  const void* ids;          // int32 or int64 [T, k], rows ld_ids apart
+  int id_bytes;
+  int64_t ld_ids;
+  int64_t R;                // T * k
+  int k, E;
+  int* perm;                // [R]
+  int* pos;                 // [R]
+  int* offsets;             // [E + 1]
+};
+cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s);
+
+// Row copies and sums between token order and expert order.
+struct RowsArgs {
+  const void* src;          // dispatch: x [T, H]; combine / gather: y [R, H]; combine_grad: dout [T, H]
+  int64_t ld_src;
+  const void* y;            // combine_grad: y [R, H]
+  int64_t ld_y;
+  const float* w;           // [T, k] or null (all ones)
+  const int* pos;           // [T, k]
+  const int* offsets;       // [E + 1] (rows from offsets[E] on are written as zeros), or null
+  int64_t T, H;
+  int k, E, dtype;
+  void* dst;                // dispatch: xs [R, H]; combine: out [T, H]; combine_grad: dy [R, H] or null
+  float* dw;                // combine_grad: [T, k] or null
+};
+cudaError_t launch_dispatch(const RowsArgs& a, cudaStream_t s);
+cudaError_t launch_combine(const RowsArgs& a, cudaStream_t s);
+cudaError_t launch_combine_grad(const RowsArgs& a, cudaStream_t s);
+
+// Microscaled 4-bit rows.  Codes: [rows, 16 * nb] bytes, nb = ceil(cols / 32)
+// blocks a row, element d in byte d / 2 (even d in the low half).  Scales:
+// groups of `panel` rows, each [ceil(nb / 4), panel, 4] bytes.
+__host__ __device__ inline size_t mx4_scale_offset(int64_t row, int64_t q, int64_t panel, int64_t nq) {
+  const int64_t g = row / panel;
+  return (size_t)(((g * nq + q) * panel + (row - g * panel)) * 4);
+}
+
+struct Mx4QuantArgs {
+  const void* x;            // [rows, cols] (gated activation: [rows, 2 * cols], gate | up)
+  int64_t ld_x;
+  int64_t rows, cols;
+  int dtype;
+  ActParams act;            // act = -1: none
+  const int* pos;           // [rows, k]: the output rows of a row, or null: row i to row i
+  const int* offsets;       // with pos: rows from offsets[E] to rows * k are written as zeros
+  int k, E;
+  int64_t panel;            // rows of a scale panel of the output
+  uint8_t* codes;
+  uint8_t* scales;
+};
+cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s);
+
+struct Mx4DequantArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows, cols, panel;
+  int dtype;
+  void* out;                // [rows, cols]
+  int64_t ld_out;
+};
+cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, cudaStream_t s);
+
+struct Mx4MatmulArgs {
+  const uint8_t* a_codes;   // [R, 16 * nb]
+  const uint8_t* a_scales;  // one panel of R rows
+  const uint8_t* w_codes;   // [E, N, 16 * nb]
+  const uint8_t* w_scales;  // E panels of N rows
+  const int* offsets;       // [E + 1], or null: one group of R rows
+  int64_t R;
+  int E, N, K;
+  int out_dtype;
+  void* out;                // [R, N]
+  int64_t ld_out;
+  WaitCfg wait;
+};
+cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int inject_stall, cudaStream_t s);
+
+// Norms around a block.
+
+struct NormArgs {
+  const void* x;
+  int64_t ld_x;
+  const void* o;            // null: r = residual_scale * x
+  int64_t ld_o;
+  const void* gate;
+  int gate_kind;
+  int64_t ld_gate;          // QMOE_GATE_FULL
+  const void* w_post;       // null: the branch is not normalised
+  const void* w_pre;        // null: no h
+  float residual_scale, eps;
+  int64_t T, H;
+  int dtype;
+  // forward
+  void* r;
+  void* h;
+  float* rstd_post;
+  float* rstd_pre;
+  // backward
+  const void* dr;           // gradients of r and h (null: zero)
+  int64_t ld_dr;
+  const void* dh;
+  int64_t ld_dh;
+  void* dx;
+  void* d_o;
+  void* dgate;
+  void* dw_post;
+  void* dw_pre;
+  float* partial;           // [CTAs, sums, H]
+};
+cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s);
+// Longest row the norm kernels hold in registers.
+constexpr int64_t kNormMaxWidth = 16384;
+size_t block_norm_grad_workspace(int64_t T, int64_t H, int dtype);
+
+inline int dtype_size(int dtype) { return dtype == QMOE_F32 ? 4 : 2; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// Every row of a matrix starts on a 16-byte boundary.
+inline bool rows_aligned16(const void* p, int64_t ld, int dtype) {
+  return p == nullptr || (aligned16(p) && ld * dtype_size(dtype) % 16 == 0);
+}
+
+}  // namespace qmoe
+
+#ifdef __CUDACC__
+namespace qmoe {
+
+// VEC consecutive elements of type DT as floats: 16-byte accesses (VEC * size
+// a multiple of 16), or one element.
+template <int DT>
+struct ElemT;
+template <>
+struct ElemT<QMOE_F32> {
+  using t = float;
+};
+template <>
+struct ElemT<QMOE_F16> {
+  using t = __half;
+};
+template <>
+struct ElemT<QMOE_BF16> {
+  using t = __nv_bfloat16;
+};
+
+template <int DT>
+__device__ __forceinline__ void unpack2(uint32_t u, float& a, float& b) {
+  if constexpr (DT == QMOE_F16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+    a = f.x;
+    b = f.y;
+  } else {
+    a = __uint_as_float(u << 16);
+    b = __uint_as_float(u & 0xffff0000u);
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == QMOE_F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ void load_vec(const void* base, size_t i, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = load_d<DT>(base, i);
+  } else if constexpr (DT == QMOE_F32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) {
+      const float4 f = __ldg(p + q);
+      v[4 * q] = f.x;
+      v[4 * q + 1] = f.y;
+      v[4 * q + 2] = f.z;
+      v[4 * q + 3] = f.w;
+    }
+  } else {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+#pragma unroll
+    for (int q = 0; q < VEC / 8; ++q) {
+      const uint4 u = __ldg(p + q);
+      unpack2<DT>(u.x, v[8 * q], v[8 * q + 1]);
+      unpack2<DT>(u.y, v[8 * q + 2], v[8 * q + 3]);
+      unpack2<DT>(u.z, v[8 * q + 4], v[8 * q + 5]);
+      unpack2<DT>(u.w, v[8 * q + 6], v[8 * q + 7]);
+    }
+  }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ void store_vec(void* base, size_t i, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    store_d<DT>(base, i, v[0]);
+  } else if constexpr (DT == QMOE_F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  } else {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i);
+#pragma unroll
+    for (int q = 0; q < VEC / 8; ++q)
+      p[q] = make_uint4(pack2<DT>(v[8 * q], v[8 * q + 1]), pack2<DT>(v[8 * q + 2], v[8 * q + 3]),
+                        pack2<DT>(v[8 * q + 4], v[8 * q + 5]), pack2<DT>(v[8 * q + 6], v[8 * q + 7]));
+  }
+}
+
+// Elements of a 16-byte access.
+template <int DT>
+constexpr int kVec16 = DT == QMOE_F32 ? 4 : 8;
+
+}  // namespace qmoe
+#endif

@@ -1,0 +1,372 @@
+// Tokens sorted by expert and back, with weights applied, and the gradients.
+//
+//   sort:     route r = t * k + j goes to expert ids[t, j]; pos[r] is its row
+//             in the stable order by expert, perm the inverse, offsets[e] the
+//             first row of expert e.  A route whose id is outside [0, E) is
+//             dropped: pos -1, no row; rows past offsets[E] have perm -1.
+//   dispatch: xs[pos[t, j]] = x[t]
+//   combine:  out[t] = sum_j w[t, j] * y[pos[t, j]], in slot order, fp32
+//   their gradients: dx[t] = sum_j dxs[pos[t, j]] (combine with unit weights);
+//             dy[pos[t, j]] = w[t, j] * dout[t], dw[t, j] = <dout[t], y[pos[t, j]]>
+//
+// All of them run in token order: a token's row is read (or written) once and
+// its k rows in expert order once each, so every row crosses the memory
+// exactly once, whole.  No atomics: every result has one owner and one order.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "qmoe_ops.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace qmoe {
+
+// ----------------------------------------------------------------------------
+// Sort
+// ----------------------------------------------------------------------------
+// One launch of one cluster: every warp owns a contiguous run of routes, counts
+// it per expert in shared memory, the counts of all warps of all CTAs become
+// first rows (distributed shared memory between the CTAs), and the warps walk
+// their runs again in order.  No workspace and no second launch: at the sizes
+// a layer sorts (up to some 10^5 routes) the time is latency, not bandwidth.
+constexpr int kSortCluster = 8;
+
+template <typename ID>
+__global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
+  const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = a.E;
+  extern __shared__ int sort_smem[];
+  int* cnt = sort_smem;             // [W][E]: counts, then the next row of (warp, expert)
+  int* tot = cnt + (size_t)W * E;   // [E]: this CTA's counts (read by the other CTAs)
+  int* off = tot + E;               // [E + 1]: all counts, then first rows
+  for (int i = threadIdx.x; i < W * E; i += blockDim.x) cnt[i] = 0;
+  __syncthreads();
+
+  const ID* ids = static_cast<const ID*>(a.ids);
+  const bool dense = a.ld_ids == a.k;
+  auto id_of = [&](int64_t r) -> int {
+    const ID v = ids[dense ? r : (r / a.k) * a.ld_ids + r % a.k];
+    return v >= 0 && v < (ID)E ? (int)v : -1;
+  };
+  // routes [r0, r1) of this warp, a multiple of 32 each but the last
+  const int64_t per = ((a.R + (int64_t)C * W - 1) / ((int64_t)C * W) + 31) / 32 * 32;
+  const int64_t r0 = std::min<int64_t>(a.R, per * ((int64_t)c * W + warp)), r1 = std::min<int64_t>(a.R, r0 + per);
+  int* mine = cnt + (size_t)warp * E;
+  constexpr int U = 4;              // ids in flight per lane
+  for (int64_t b = r0; b < r1; b += 32 * U) {
+    int e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = b + 32 * u + lane;
+      e[u] = r < r1 ? id_of(r) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (e[u] >= 0) atomicAdd(mine + e[u], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int n = 0;
+    for (int w = 0; w < W; ++w) n += cnt[(size_t)w * E + e];
+    tot[e] = n;
+  }
+  cluster.sync();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int before = 0, all = 0;
+    for (int q = 0; q < C; ++q) {
+      const int n = cluster.map_shared_rank(tot, q)[e];
+      before += q < c ? n : 0;
+      all += n;
+    }
+    off[e] = all;
+    // counts -> rows of (warp, expert) within the expert
+    for (int w = 0; w < W; ++w) {
+      const int n = cnt[(size_t)w * E + e];
+      cnt[(size_t)w * E + e] = before;
+      before += n;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // exclusive scan of the expert counts: a contiguous run of experts a lane
+    const int per_lane = (E + 31) / 32, e0 = std::min(E, lane * per_lane), e1 = std::min(E, e0 + per_lane);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += off[e];
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    int first = run - sum;
+    for (int e = e0; e < e1; ++e) {
+      const int n = off[e];
+      off[e] = first;
+      first += n;
+    }
+    if (lane == 31) off[E] = run;
+  }
+  __syncthreads();
+  const int used = off[E];
+  if (c == 0)
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) a.offsets[e] = off[e];
+  // rows without a route
+  for (int64_t i = used + (int64_t)c * blockDim.x + threadIdx.x; i < a.R; i += (int64_t)C * blockDim.x) a.perm[i] = -1;
+
+  for (int64_t b = r0; b < r1; b += 32 * U) {
+    int e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = b + 32 * u + lane;
+      e[u] = r < r1 ? id_of(r) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = b + 32 * u + lane;
+      // lanes with the same expert take consecutive rows in lane order
+      const unsigned peers = __match_any_sync(0xffffffffu, e[u]);
+      const int rank = __popc(peers & ((1u << lane) - 1u));
+      int p = -1;
+      if (e[u] >= 0) p = off[e[u]] + mine[e[u]] + rank;
+      __syncwarp();
+      if (e[u] >= 0 && rank == 0) mine[e[u]] += __popc(peers);
+      __syncwarp();
+      if (r < r1) {
+        a.pos[r] = p;
+        if (p >= 0) a.perm[p] = (int)r;
+      }
+    }
+  }
+  cluster.sync();   // no CTA leaves while another may still read its counts
+}
+
+cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
+  // One CTA up to 1024 routes (a warp for each 32), else a cluster of eight:
+  // beyond one pass of a full CTA the extra CTAs' loads pay for the two
+  // cluster barriers.
+  const int C = a.R <= 1024 ? 1 : kSortCluster;
+  const int64_t passes = (a.R + 32 * C - 1) / (32 * C);
+  const int W = (int)std::max<int64_t>(1, std::min<int64_t>(32, passes));
+  const size_t smem = ((size_t)W * a.E + 2 * (size_t)a.E + 1) * sizeof(int);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)C, 1, 1};
+  cfg.gridDim = dim3(C);
+  cfg.blockDim = dim3(32 * W);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto run = [&](auto kern) {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, a);
+  };
+  return a.id_bytes == 8 ? run(expert_sort_kernel<long long>) : run(expert_sort_kernel<int>);
+}
+
+// ----------------------------------------------------------------------------
+// Row copies and sums
+// ----------------------------------------------------------------------------
+// A row takes blockDim.x threads (a power of two, 16 bytes or one element
+// each per step), blockDim.y rows a CTA.
+struct RowShape {
+  dim3 grid, block;
+};
+static RowShape row_shape(int64_t T, int64_t H, int vec) {
+  const int64_t n = (H + vec - 1) / vec;
+  int tpr = 8;
+  while (tpr < 256 && tpr < n) tpr *= 2;
+  const int rpb = 256 / tpr;
+  RowShape r;
+  r.block = dim3(tpr, rpb);
+  r.grid = dim3((unsigned)((T + rpb - 1) / rpb));
+  return r;
+}
+
+// The row of a slot, -1 where it has none.
+__device__ __forceinline__ int slot_row(const RowsArgs& a, int p) { return p < a.T * a.k ? p : -1; }
+
+// Rows offsets[E] .. T * k - 1 of dst, which no route fills: zeros, spread
+// over the rows of the grid.
+template <int DT, int VEC>
+__device__ __forceinline__ void zero_unused_rows(const RowsArgs& a, int64_t t) {
+  const int64_t R = a.T * a.k, used = max(a.offsets[a.E], 0);
+  float z[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) z[i] = 0.f;
+  for (int64_t i = used + t; i < R; i += a.T)
+    for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC)
+      store_vec<DT, VEC>(a.dst, (size_t)(i * a.H + c), z);
+}
+
+template <int DT, int VEC>
+__global__ void __launch_bounds__(256) dispatch_kernel(const RowsArgs a) {
+  const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+  if (t >= a.T) return;
+  const int* pos = a.pos + t * a.k;
+  for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC) {
+    float v[VEC];
+    load_vec<DT, VEC>(a.src, (size_t)(t * a.ld_src + c), v);
+    for (int j = 0; j < a.k; ++j) {
+      const int64_t p = slot_row(a, pos[j]);
+      if (p >= 0) store_vec<DT, VEC>(a.dst, (size_t)(p * a.H + c), v);
+    }
+  }
+  zero_unused_rows<DT, VEC>(a, t);
+}
+
+constexpr int kSlots = 8;   // slots whose rows are in flight together
+
+template <int DT, int VEC, bool WEIGHTED>
+__global__ void __launch_bounds__(256) combine_kernel(const RowsArgs a) {
+  const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+  if (t >= a.T) return;
+  const int* pos = a.pos + t * a.k;
+  for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC) {
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+      float v[kSlots][VEC], w[kSlots];
+      int p[kSlots];
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) p[u] = j0 + u < a.k ? slot_row(a, pos[j0 + u]) : -1;
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) {
+        if (p[u] >= 0) {
+          load_vec<DT, VEC>(a.src, (size_t)((int64_t)p[u] * a.ld_src + c), v[u]);
+          w[u] = WEIGHTED ? a.w[t * a.k + j0 + u] : 1.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u)
+        if (p[u] >= 0) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[i] = WEIGHTED ? fmaf(w[u], v[u][i], acc[i]) : acc[i] + v[u][i];
+        }
+    }
+    store_vec<DT, VEC>(a.dst, (size_t)(t * a.H + c), acc);
+  }
+}
+
+template <int DT, int VEC>
+__global__ void __launch_bounds__(256) combine_grad_kernel(const RowsArgs a) {
+  __shared__ float part[8][kSlots];
+  const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+  const bool live = t < a.T;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5;
+  const int* pos = a.pos + (live ? t : 0) * a.k;
+  for (int j0 = 0; j0 < a.k; j0 += kSlots) {
+    int p[kSlots];
+    float w[kSlots], dot[kSlots];
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u) {
+      p[u] = live && j0 + u < a.k ? slot_row(a, pos[j0 + u]) : -1;
+      w[u] = p[u] >= 0 && a.w ? a.w[t * a.k + j0 + u] : 1.f;
+      dot[u] = 0.f;
+    }
+    if (live) {
+      for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC) {
+        float g[VEC], v[kSlots][VEC];
+        load_vec<DT, VEC>(a.src, (size_t)(t * a.ld_src + c), g);
+        if (a.dw) {
+#pragma unroll
+          for (int u = 0; u < kSlots; ++u)
+            if (p[u] >= 0) load_vec<DT, VEC>(a.y, (size_t)((int64_t)p[u] * a.ld_y + c), v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u) {
+          if (p[u] < 0) continue;
+          if (a.dw) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dot[u] = fmaf(g[i], v[u][i], dot[u]);
+          }
+          if (a.dst) {
+            float d[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) d[i] = w[u] * g[i];
+            store_vec<DT, VEC>(a.dst, (size_t)((int64_t)p[u] * a.H + c), d);
+          }
+        }
+      }
+    }
+    if (a.dw) {
+      const int width = min((int)blockDim.x, 32);   // a row's lanes within its warp
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u)
+        for (int o = width >> 1; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+      if (blockDim.x > 32) {
+        if ((tid & 31) == 0) {
+#pragma unroll
+          for (int u = 0; u < kSlots; ++u) part[warp][u] = dot[u];
+        }
+        __syncthreads();
+        if (threadIdx.x < kSlots) {
+          float sum = 0.f;
+          const int nw = blockDim.x >> 5, w0 = threadIdx.y * nw;
+          for (int q = 0; q < nw; ++q) sum += part[w0 + q][threadIdx.x];
+          if (live && j0 + (int)threadIdx.x < a.k) a.dw[t * a.k + j0 + threadIdx.x] = sum;
+        }
+        __syncthreads();
+      } else if (threadIdx.x == 0 && live) {
+#pragma unroll
+        for (int u = 0; u < kSlots; ++u)
+          if (j0 + u < a.k) a.dw[t * a.k + j0 + u] = dot[u];
+      }
+    }
+  }
+  if (live && a.dst) zero_unused_rows<DT, VEC>(a, t);
+}
+
+template <typename F>
+static cudaError_t by_type(int dtype, bool vec, F&& f) {
+  if (dtype == QMOE_F32)
+    return vec ? f(std::integral_constant<int, QMOE_F32>{}, std::integral_constant<int, 4>{})
+               : f(std::integral_constant<int, QMOE_F32>{}, std::integral_constant<int, 1>{});
+  if (dtype == QMOE_F16)
+    return vec ? f(std::integral_constant<int, QMOE_F16>{}, std::integral_constant<int, 8>{})
+               : f(std::integral_constant<int, QMOE_F16>{}, std::integral_constant<int, 1>{});
+  return vec ? f(std::integral_constant<int, QMOE_BF16>{}, std::integral_constant<int, 8>{})
+             : f(std::integral_constant<int, QMOE_BF16>{}, std::integral_constant<int, 1>{});
+}
+
+// 16-byte accesses need every row of every operand on a 16-byte boundary and
+// whole vectors a row; anything else moves element by element.
+static bool rows_vec(const RowsArgs& a) {
+  return a.H % (16 / dtype_size(a.dtype)) == 0 && rows_aligned16(a.src, a.ld_src, a.dtype) &&
+         rows_aligned16(a.y, a.ld_y, a.dtype) && rows_aligned16(a.dst, a.H, a.dtype);
+}
+
+cudaError_t launch_dispatch(const RowsArgs& a, cudaStream_t s) {
+  return by_type(a.dtype, rows_vec(a), [&](auto dt, auto vec) {
+    const RowShape g = row_shape(a.T, a.H, vec);
+    dispatch_kernel<dt, vec><<<g.grid, g.block, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_combine(const RowsArgs& a, cudaStream_t s) {
+  return by_type(a.dtype, rows_vec(a), [&](auto dt, auto vec) {
+    const RowShape g = row_shape(a.T, a.H, vec);
+    if (a.w) combine_kernel<dt, vec, true><<<g.grid, g.block, 0, s>>>(a);
+    else combine_kernel<dt, vec, false><<<g.grid, g.block, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_combine_grad(const RowsArgs& a, cudaStream_t s) {
+  return by_type(a.dtype, rows_vec(a), [&](auto dt, auto vec) {
+    const RowShape g = row_shape(a.T, a.H, vec);
+    combine_grad_kernel<dt, vec><<<g.grid, g.block, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace qmoe
