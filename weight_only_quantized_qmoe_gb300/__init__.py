@@ -18,6 +18,12 @@ _ACT = {"swiglu": binding.QMOE_ACT_SWIGLU, "geglu": binding.QMOE_ACT_GEGLU_TANH,
         "identity": binding.QMOE_ACT_IDENTITY}
 
 
+def __getattr__(name):   # the operators' C names, which binding binds when first asked for
+    if name in binding._OPERATORS:
+        return getattr(binding, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 class QMoEError(RuntimeError):
     def __init__(self, status, msg):
         super().__init__(f"{binding.qmoe_status_string(status)}: {msg}")

@@ -227,74 +227,23 @@ def qmoe_destroy(layer):
 
 
 # --- operators around the layer ----------------------------------------------
-# Addresses are integers (0 or None = NULL), strides and sizes in elements, in
-# the order of include/qmoe.h.
+# The same names, bound to the C functions themselves when first asked for: a
+# wrapper of their own would be a good part of a small call's time.  Addresses
+# are integers (0 or None = NULL), strides and sizes in elements, in the order
+# of include/qmoe.h.
+_OPERATORS = frozenset((
+    "qmoe_op_poll_status", "qmoe_op_set_wait_limit", "qmoe_op_debug_inject_stall", "qmoe_expert_sort", "qmoe_dispatch",
+    "qmoe_dispatch_grad", "qmoe_combine", "qmoe_combine_grad", "qmoe_mx4_quantize", "qmoe_mx4_dequantize",
+    "qmoe_mx4_matmul", "qmoe_block_norm", "qmoe_block_norm_grad_workspace", "qmoe_block_norm_grad"))
+
+
 def qmoe_op_last_error():
     return load().qmoe_op_last_error().decode()
 
 
-def qmoe_op_poll_status():
-    return load().qmoe_op_poll_status()
-
-
-def qmoe_op_set_wait_limit(iterations):
-    return load().qmoe_op_set_wait_limit(int(iterations))
-
-
-def qmoe_op_debug_inject_stall(enable):
-    return load().qmoe_op_debug_inject_stall(int(enable))
-
-
-def qmoe_expert_sort(ids, id_bytes, ld_ids, num_tokens, top_k, experts, perm, pos, offsets, stream):
-    return load().qmoe_expert_sort(ids, id_bytes, ld_ids, num_tokens, top_k, experts, perm, pos, offsets, stream)
-
-
-def qmoe_dispatch(x, ld_x, pos, offsets, num_tokens, top_k, experts, hidden, dtype, xs, stream):
-    return load().qmoe_dispatch(x, ld_x, pos, offsets, num_tokens, top_k, experts, hidden, dtype, xs, stream)
-
-
-def qmoe_dispatch_grad(dxs, ld_dxs, pos, num_tokens, top_k, hidden, dtype, dx, stream):
-    return load().qmoe_dispatch_grad(dxs, ld_dxs, pos, num_tokens, top_k, hidden, dtype, dx, stream)
-
-
-def qmoe_combine(y, ld_y, weights, pos, num_tokens, top_k, hidden, dtype, out, stream):
-    return load().qmoe_combine(y, ld_y, weights, pos, num_tokens, top_k, hidden, dtype, out, stream)
-
-
-def qmoe_combine_grad(dout, ld_dout, y, ld_y, weights, pos, offsets, num_tokens, top_k, experts, hidden, dtype, dy,
-                      dweights, stream):
-    return load().qmoe_combine_grad(dout, ld_dout, y, ld_y, weights, pos, offsets, num_tokens, top_k, experts, hidden,
-                                    dtype, dy, dweights, stream)
-
-
-def qmoe_mx4_quantize(x, ld_x, rows, cols, dtype, activation, pos, offsets, top_k, experts, panel_rows, codes, scales,
-                      stream):
-    return load().qmoe_mx4_quantize(x, ld_x, rows, cols, dtype, activation, pos, offsets, top_k, experts, panel_rows,
-                                    codes, scales, stream)
-
-
-def qmoe_mx4_dequantize(codes, scales, rows, cols, panel_rows, dtype, out, ld_out, stream):
-    return load().qmoe_mx4_dequantize(codes, scales, rows, cols, panel_rows, dtype, out, ld_out, stream)
-
-
-def qmoe_mx4_matmul(a_codes, a_scales, rows, w_codes, w_scales, offsets, experts, n, k, out_dtype, out, ld_out, stream):
-    return load().qmoe_mx4_matmul(a_codes, a_scales, rows, w_codes, w_scales, offsets, experts, n, k, out_dtype, out,
-                                  ld_out, stream)
-
-
-def qmoe_block_norm(x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre, residual_scale, eps, num_tokens, hidden,
-                    dtype, r, h, rstd_post, rstd_pre, stream):
-    return load().qmoe_block_norm(x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre, residual_scale, eps,
-                                  num_tokens, hidden, dtype, r, h, rstd_post, rstd_pre, stream)
-
-
-def qmoe_block_norm_grad_workspace(num_tokens, hidden, dtype):
-    return load().qmoe_block_norm_grad_workspace(num_tokens, hidden, dtype)
-
-
-def qmoe_block_norm_grad(dr, ld_dr, dh, ld_dh, x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre, rstd_post,
-                         rstd_pre, residual_scale, num_tokens, hidden, dtype, dx, do, dgate, dw_post, dw_pre, workspace,
-                         workspace_bytes, stream):
-    return load().qmoe_block_norm_grad(dr, ld_dr, dh, ld_dh, x, ld_x, o, ld_o, gate, gate_kind, ld_gate, w_post, w_pre,
-                                       rstd_post, rstd_pre, residual_scale, num_tokens, hidden, dtype, dx, do, dgate,
-                                       dw_post, dw_pre, workspace, workspace_bytes, stream)
+def __getattr__(name):
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    fn = getattr(load(), name)
+    globals()[name] = fn
+    return fn

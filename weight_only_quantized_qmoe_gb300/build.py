@@ -20,7 +20,7 @@ SOURCES = ["qmoe_api.cu", "qmoe_route.cu", "qmoe_decode.cu", "qmoe_prefill.cu", 
            "qmoe_decode_b1.cu", "qmoe_fused.cu", "qmoe_fused_w22.cu", "qmoe_fused_w23.cu",
            "qmoe_fused_w24.cu", "qmoe_fused_w32.cu", "qmoe_fused_w33.cu", "qmoe_fused_w34.cu",
            "qmoe_fused_w42.cu", "qmoe_fused_w43.cu", "qmoe_fused_w44.cu",
-           "qmoe_ops_api.cu", "qmoe_sort.cu", "qmoe_mx4.cu", "qmoe_mx4_gemm.cu", "qmoe_norm.cu"]
+           "qmoe_ops_api.cu", "qmoe_sort.cu", "qmoe_mx4.cu", "qmoe_mx4_gemm.cu", "qmoe_norm.cu", "qmoe_norm_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE]

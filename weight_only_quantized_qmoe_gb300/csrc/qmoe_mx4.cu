@@ -15,6 +15,7 @@
 // to its rows in expert order: read once, quantised once, written k times at
 // 17/32 byte a value, instead of k 16-bit copies read again.
 #include <algorithm>
+#include <cstring>
 
 #include "qmoe_ops.cuh"
 
@@ -37,14 +38,74 @@ __device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Values c .. c + 7 of row src (length n), past the end 0.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void* src, size_t row0, int64_t c, int64_t n, float (&v)[8]) {
-  if (VEC && c + 8 <= n) {
-    load_vec<DT, 8>(src, row0 + c, v);
-  } else {
+// The eight elements from element `at` of x on, where `at` need not be on a
+// 16-byte boundary: the lane loads the aligned 16 bytes that hold the first of
+// them (32-bit types: also the next 16), takes the following ones from the
+// next lane, which starts 8 elements on, and shifts.  Whole warp; the tensor has
+// `hi` elements, and aligned words that are not wholly inside it are read
+// element by element.  Elements past n (of the row) become 0.
+template <int DT>
+__device__ __forceinline__ void load8_shifted(const void* x, int64_t at, int64_t hi, int n, float (&v)[8]) {
+  using T = typename ElemT<DT>::t;
+  constexpr int per = 16 / (int)sizeof(T);       // elements of 16 bytes
+  constexpr int words = DT == QMOE_F32 ? 8 : 4;  // 32-bit words a lane loads
+  const T* p = static_cast<const T*>(x) + at;
+  const int m = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));   // the same for the whole warp
+  uint32_t w[2 * words];
+  auto aligned = [&](int64_t from, uint32_t* out) {   // 16 bytes from element `from` (aligned)
+    if (from >= 0 && from + per <= hi) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(x) + from));
+      out[0] = u.x;
+      out[1] = u.y;
+      out[2] = u.z;
+      out[3] = u.w;
+    } else {
+      T e[per];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? load_d<DT>(src, row0 + c + i) : 0.f;
+      for (int i = 0; i < per; ++i) e[i] = from + i >= 0 && from + i < hi ? static_cast<const T*>(x)[from + i] : T(0.f);
+      memcpy(out, e, 16);
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < words / 4; ++q) aligned(at - m + q * per, w + 4 * q);
+#pragma unroll
+  for (int i = 0; i < words; ++i) w[words + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+  if ((threadIdx.x & 31) == 31 && m) aligned(at - m + 8, w + words);
+  if constexpr (DT == QMOE_F32) {
+    // shift by m words
+#pragma unroll
+    for (int i = 0; i < 10; ++i) w[i] = (m & 2) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __uint_as_float((m & 1) ? w[i + 1] : w[i]) : 0.f;
+  } else {
+    // shift by m halves of a word
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = (m & 4) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = (m & 2) ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = (m & 1) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+      unpack2<DT>(u, v[2 * i], v[2 * i + 1]);
+      if (2 * i >= n) v[2 * i] = 0.f;
+      if (2 * i + 1 >= n) v[2 * i + 1] = 0.f;
+    }
+  }
+}
+
+// Elements c .. c + 7 of the row that starts at element row0 and has n.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const void* x, int64_t row0, int64_t c, int64_t n, int64_t hi, float (&v)[8]) {
+  const int left = (int)max((int64_t)0, min((int64_t)8, n - c));
+  if constexpr (VEC) {
+    if (left == 8) {
+      load_vec<DT, 8>(x, (size_t)(row0 + c), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? load_d<DT>(x, (size_t)(row0 + c + i)) : 0.f;
+    }
+  } else {
+    load8_shifted<DT>(x, row0 + c, hi, left, v);
   }
 }
 
@@ -58,10 +119,12 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
   const int64_t c = (wid - row * nseg) * kQuantSeg + lane * 8;   // a multiple of 8; four lanes a block
   const bool in = c < nb * 32;
   float v[8];
-  load8<DT, VEC>(a.x, (size_t)(row * a.ld_x), c, a.cols, v);
+  const int64_t row0 = row * a.ld_x;
+  const int64_t hi = (a.rows - 1) * a.ld_x + (ACT ? 2 : 1) * a.cols;   // elements of x
+  load8<DT, VEC>(a.x, row0, c, a.cols, hi, v);
   if (ACT) {
     float u[8];
-    load8<DT, VEC>(a.x, (size_t)(row * a.ld_x + a.cols), c, a.cols, u);
+    load8<DT, VEC>(a.x, row0 + a.cols, c, a.cols, hi, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < a.cols ? glu(a.act, v[i], u[i]) : 0.f;
   }
@@ -120,48 +183,60 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s) {
   return pick(std::integral_constant<int, QMOE_BF16>{});
 }
 
-// The values of the codes, rounded once to D: a lane takes 8 of them.
-template <int DT, bool VEC>
+// The values of the codes, rounded once to D.  A lane writes 8 of them, from a
+// 16-byte boundary of the output on: where a row does not start on one, its
+// lanes start m elements early, so a lane's values come from two words of
+// codes and may belong to two blocks.
+template <int DT>
 __global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const Mx4DequantArgs a, int64_t nseg) {
+  using T = typename ElemT<DT>::t;
   const int64_t wid = blockIdx.x * (int64_t)kQuantWarps + (threadIdx.x >> 5);
   const int64_t nb = (a.cols + 31) / 32, nq = (nb + 3) / 4, pitch = nb * 16;
   const int64_t row = wid / nseg;
   if (row >= a.rows) return;
-  const int64_t c = (wid - row * nseg) * kQuantSeg + (threadIdx.x & 31) * 8;
+  const size_t row0 = (size_t)(row * a.ld_out);
+  const int m = (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + row0) & 15) / sizeof(T));
+  const int64_t g = (wid - row * nseg) * kQuantSeg + (threadIdx.x & 31) * 8;   // on the codes' grid
+  const int64_t c = g - m;
   if (c >= a.cols) return;
-  const uint32_t code = *reinterpret_cast<const uint32_t*>(a.codes + (size_t)row * pitch + (c >> 1));
-  const uint32_t e = a.scales[mx4_scale_offset(row, c >> 7, a.panel, nq) + ((c >> 5) & 3)];
-  // 2^(e - 127); e = 0 is the subnormal 2^-127, 255 is NaN
-  const float scale = __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(a.codes + (size_t)row * pitch);
+  const uint32_t hi = g < nb * 32 ? words[g >> 3] : 0u, lo = m && g > 0 ? words[(g >> 3) - 1] : 0u;
+  const uint32_t code = m ? __funnelshift_r(lo, hi, 32 - 4 * m) : hi;
+  const uint8_t* sc = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
+  auto scale_of = [&](int64_t x) {   // of the block of element x; 2^(e - 127), e = 0 is subnormal, 255 is NaN
+    const int64_t blk = min(max(x, (int64_t)0), a.cols - 1) >> 5;
+    const uint32_t e = sc[(size_t)(blk >> 2) * a.panel * 4 + (blk & 3)];
+    return __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
+  };
+  const float s0 = scale_of(c), s1 = m ? scale_of(c + 7) : s0;
+  const int change = m ? (int)((32 - (c & 31)) & 31) : 0;   // first element of the second block, if it is within 8
   float v[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = e2m1_values((code >> (8 * i)) & 0xffu);
-    v[2 * i] = f.x * scale;
-    v[2 * i + 1] = f.y * scale;
+    v[2 * i] = f.x * (change && 2 * i >= change ? s1 : s0);
+    v[2 * i + 1] = f.y * (change && 2 * i + 1 >= change ? s1 : s0);
   }
-  const size_t at = (size_t)(row * a.ld_out + c);
-  if (VEC && c + 8 <= a.cols) {
-    store_vec<DT, 8>(a.out, at, v);
+  if (c >= 0 && c + 8 <= a.cols) {
+    store_vec<DT, 8>(a.out, row0 + c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c + i < a.cols) store_d<DT>(a.out, at + i, v[i]);
+      if (c + i >= 0 && c + i < a.cols) store_d<DT>(a.out, row0 + c + i, v[i]);
   }
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, cudaStream_t s) {
-  const int64_t nseg = (a.cols + kQuantSeg - 1) / kQuantSeg;
+  const int64_t nseg = (a.cols + 7 + kQuantSeg - 1) / kQuantSeg;   // up to 7 elements early
   const int64_t blocks = (a.rows * nseg + kQuantWarps - 1) / kQuantWarps;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const bool vec = rows_aligned16(a.out, a.ld_out, a.dtype);
   auto run = [&](auto kern) {
     kern<<<(unsigned)blocks, 32 * kQuantWarps, 0, s>>>(a, nseg);
     return cudaGetLastError();
   };
-  if (a.dtype == QMOE_F32) return vec ? run(mx4_dequantize_kernel<QMOE_F32, true>) : run(mx4_dequantize_kernel<QMOE_F32, false>);
-  if (a.dtype == QMOE_F16) return vec ? run(mx4_dequantize_kernel<QMOE_F16, true>) : run(mx4_dequantize_kernel<QMOE_F16, false>);
-  return vec ? run(mx4_dequantize_kernel<QMOE_BF16, true>) : run(mx4_dequantize_kernel<QMOE_BF16, false>);
+  if (a.dtype == QMOE_F32) return run(mx4_dequantize_kernel<QMOE_F32>);
+  if (a.dtype == QMOE_F16) return run(mx4_dequantize_kernel<QMOE_F16>);
+  return run(mx4_dequantize_kernel<QMOE_BF16>);
 }
 
 }  // namespace qmoe

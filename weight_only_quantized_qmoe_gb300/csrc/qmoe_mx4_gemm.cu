@@ -18,7 +18,7 @@
 // that tcgen05.cp spreads over TMEM.
 //   warp 0    TMA producer (one elected lane)
 //   warp 1    MMA issuer: scales to TMEM, then four K = 64 MMAs a stage
-//   warp 2    scale loader
+//   warps 2-3 scale loaders
 //   warps 4-7 epilogue: TMEM -> registers -> shared memory -> whole rows
 // Two accumulators of BN columns alternate, so the epilogue of one tile runs
 // under the MMAs of the next.  CTAs are persistent over the (expert, row tile,
@@ -65,8 +65,8 @@ struct MxRing {
   static constexpr int sfb_off = sfa_off + stages * sfa_bytes;
   static constexpr int epi_off = sfb_off + stages * sfb_bytes;
   static constexpr int bar_off = epi_off + 4 * 32 * kMxEpiPitch;
-  static constexpr int tp_off = bar_off + 512;                    // first row tile of each expert
-  static constexpr int total = tp_off + (kMxMaxExperts + 2) * 4;
+  static constexpr int tp_off = bar_off + 512;                    // first row tile and first row of each expert
+  static constexpr int total = tp_off + 2 * (kMxMaxExperts + 2) * 4;
   // TMEM columns: two accumulators, then per stage the scales of A and W
   static constexpr int sf_col0 = 2 * BN;
   static constexpr int sf_cols = 8 + 8 * groups;
@@ -78,25 +78,66 @@ struct MxRing {
 // ----------------------------------------------------------------------------
 // Instructions
 // ----------------------------------------------------------------------------
-// One K = 64 MMA of E2M1 operands, E8M0 scales of 32 values, issued by one
-// elected lane.
-__device__ __forceinline__ void mx_mma_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                             uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-      : "memory");
-}
-// 512 bytes of scales (32 rows of 16 bytes) to four TMEM columns, the same in
-// each quarter of the lanes.
-__device__ __forceinline__ void mx_scales_to_tmem_elect(uint32_t taddr, uint64_t desc) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc)
-      : "memory");
+// One stage, issued by one elected lane: the scales of A (two chunks of 512
+// bytes) and of W (two per 128-row group) to TMEM, four columns each and the
+// same in every quarter of the lanes, then up to four K = 64 MMAs of E2M1
+// operands with E8M0 scales of 32 values, then the commit that frees the
+// stage.  One block of instructions with one elect: the issue of a stage has
+// to take less time than its MMAs (four of 96 cycles at 192 columns), and with
+// an elect and operand moves per instruction it took three times as long.
+template <int GROUPS>
+__device__ __forceinline__ void mx_stage_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sf, uint64_t sa,
+                                               uint64_t sb, uint32_t acc, int nk, uint64_t* empty) {
+  static_assert(GROUPS == 1 || GROUPS == 2, "row groups of W");
+  if constexpr (GROUPS == 2) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t"
+        ".reg .b32 t<6>, i2;\n\t.reg .b64 x<6>, y<4>, z<4>;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %7, 0;\n\tsetp.eq.b32 p1, %7, %7;\n\t"
+        "setp.gt.and.s32 q1, %8, 1, e;\n\tsetp.gt.and.s32 q2, %8, 2, e;\n\tsetp.gt.and.s32 q3, %8, 3, e;\n\t"
+        "add.u32 t1, %4, 4;\n\tadd.u32 t2, %4, 8;\n\tadd.u32 t3, %4, 12;\n\tadd.u32 t4, %4, 16;\n\tadd.u32 t5, %4, 20;\n\t"
+        "add.u64 x1, %5, 32;\n\tadd.u64 x3, %6, 32;\n\tadd.u64 x4, %6, 64;\n\tadd.u64 x5, %6, 96;\n\t"
+        "add.u64 y1, %1, 2;\n\tadd.u64 y2, %1, 4;\n\tadd.u64 y3, %1, 6;\n\t"
+        "add.u64 z1, %2, 2;\n\tadd.u64 z2, %2, 4;\n\tadd.u64 z3, %2, 6;\n\t"
+        "or.b32 i2, %3, 0x40000020;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %5;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t2], %6;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t3], x3;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t1], x1;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t4], x4;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t5], x5;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [t2], p0;\n\t"
+        "@q1 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], y1, z1, i2, [%4], [t2], p1;\n\t"
+        "@q2 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], y2, z2, %3, [t1], [t4], p1;\n\t"
+        "@q3 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], y3, z3, i2, [t1], [t4], p1;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%9];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sf), "l"(sa), "l"(sb), "r"(acc), "r"(nk), "r"(smem_u32(empty))
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t"
+        ".reg .b32 t<4>, i2;\n\t.reg .b64 x<4>, y<4>, z<4>;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %7, 0;\n\tsetp.eq.b32 p1, %7, %7;\n\t"
+        "setp.gt.and.s32 q1, %8, 1, e;\n\tsetp.gt.and.s32 q2, %8, 2, e;\n\tsetp.gt.and.s32 q3, %8, 3, e;\n\t"
+        "add.u32 t1, %4, 4;\n\tadd.u32 t2, %4, 8;\n\tadd.u32 t3, %4, 12;\n\t"
+        "add.u64 x1, %5, 32;\n\tadd.u64 x3, %6, 32;\n\t"
+        "add.u64 y1, %1, 2;\n\tadd.u64 y2, %1, 4;\n\tadd.u64 y3, %1, 6;\n\t"
+        "add.u64 z1, %2, 2;\n\tadd.u64 z2, %2, 4;\n\tadd.u64 z3, %2, 6;\n\t"
+        "or.b32 i2, %3, 0x40000020;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %5;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t2], %6;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t1], x1;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t3], x3;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [t2], p0;\n\t"
+        "@q1 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], y1, z1, i2, [%4], [t2], p1;\n\t"
+        "@q2 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], y2, z2, %3, [t1], [t3], p1;\n\t"
+        "@q3 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], y3, z3, i2, [t1], [t3], p1;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%9];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sf), "l"(sa), "l"(sb), "r"(acc), "r"(nk), "r"(smem_u32(empty))
+        : "memory");
+  }
 }
 __device__ __forceinline__ void tma_2d_elect(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -125,12 +166,11 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
   return d;
 }
 // Instruction descriptor, kind::mxf4: both operands E2M1, scales E8M0, M =
-// 128, K = 64.  The scale ids (the byte pair of a 32-bit scale word that an
-// MMA's two blocks use: 0 or 2) are added per MMA.
+// 128, K = 64.  The scale ids (bits 29-30 and 4-5) name the byte pair of a
+// 32-bit scale word that an MMA's two blocks use: 0, or 2 for every second MMA.
 __device__ __forceinline__ uint32_t idesc_mxf4(int N) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(kMxRows >> 7) << 27);
 }
-__device__ __forceinline__ uint32_t idesc_scale_ids(uint32_t id) { return (id << 29) | (id << 4); }
 
 // ----------------------------------------------------------------------------
 // Kernel
@@ -154,8 +194,8 @@ __device__ __forceinline__ int mx_first_row(const Mx4MatmulArgs& a, int e) {
 }
 
 // Tile index -> expert, rows and weight columns.  tp[e] is the first row tile
-// of group e, tp[E + 1] their number.
-__device__ __forceinline__ MxTile mx_tile(const Mx4MatmulArgs& a, const int* tp, int ntn, int bn, int tile) {
+// of group e, tp[E + 1] their number, and its first row is row0[e].
+__device__ __forceinline__ MxTile mx_tile(const Mx4MatmulArgs& a, const int* tp, const int* row0, int ntn, int bn, int tile) {
   const int mt = tile / ntn;
   int lo = 0, hi = a.E;
   while (lo < hi) {
@@ -165,8 +205,8 @@ __device__ __forceinline__ MxTile mx_tile(const Mx4MatmulArgs& a, const int* tp,
   }
   MxTile t;
   t.e = lo;
-  t.start = mx_first_row(a, lo) + (mt - tp[lo]) * kMxRows;
-  t.rows = min(kMxRows, mx_first_row(a, lo + 1) - t.start);
+  t.start = row0[lo] + (mt - tp[lo]) * kMxRows;
+  t.rows = min(kMxRows, row0[lo + 1] - t.start);
   t.n0 = (tile - mt * ntn) * bn;
   return t;
 }
@@ -189,12 +229,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* tp = reinterpret_cast<int*>(smem + RG::tp_off);
+  int* row0 = tp + kMxMaxExperts + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&sfull[i], 32);
+      mbar_init(&sfull[i], 64);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -219,6 +260,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       if (e <= a.E) {
         const int lo = mx_first_row(a, e), hi = mx_first_row(a, e + 1);
         n = hi > lo ? (hi - lo + kMxRows - 1) / kMxRows : 0;
+        row0[e] = lo;
       }
       int run = n;
 #pragma unroll
@@ -229,7 +271,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       if (e <= a.E) tp[e] = first + run - n;
       first += __shfl_sync(0xffffffffu, run, 31);
     }
-    if (lane == 0) tp[a.E + 1] = first;
+    if (lane == 0) {
+      tp[a.E + 1] = first;
+      row0[a.E + 1] = (int)a.R;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -245,7 +290,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     int it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_tile(a, tp, ntn, BN, tile);
+      const MxTile t = mx_tile(a, tp, row0, ntn, BN, tile);
       if (t.e == a.E) continue;
       const int boxes = (t.rows + kMxBoxRows - 1) / kMxBoxRows;
       for (int ks = 0; ks < ksteps; ++ks, ++it) {
@@ -270,39 +315,37 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
       }
     }
-  } else if (warp == 2) {
-    // ---------------- scale loader ----------------
+  } else if (warp == 2 || warp == 3) {
+    // ---------------- scale loaders: warp 2 + h takes the 128-value chunk h of each stage ----------------
+    // Row 32 j + lane of a 128-row group goes to bytes lane * 16 + j * 4 of its
+    // chunk.  Pointers are set up once a tile and step from panel to panel.
+    const int h = warp - 2;
+    const uint32_t sfa0 = smem_u32(smem + RG::sfa_off) + h * 512 + lane * 16;
+    const uint32_t sfb0 = smem_u32(smem + RG::sfb_off) + h * RG::groups * 512 + lane * 16;
+    const size_t step_a = (size_t)a.R * 8, step_w = (size_t)a.N * 8;   // two panels on
     int it = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_tile(a, tp, ntn, BN, tile);
+      const MxTile t = mx_tile(a, tp, row0, ntn, BN, tile);
       if (t.e == a.E) continue;
-      for (int ks = 0; ks < ksteps; ++ks, ++it) {
+      const uint8_t* pa = a.a_scales + ((size_t)h * a.R + t.start + lane) * 4;
+      const uint8_t* pw = a.w_scales + (((size_t)t.e * nq + h) * a.N + t.n0 + lane) * 4;
+      const int na = (int)a.R - t.start - lane, nw = a.N - t.n0 - lane;   // row 32 j exists: 32 j < n
+      for (int ks = 0; ks < ksteps; ++ks, ++it, pa += step_a, pw += step_w) {
         const int s = it % S;
         ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        // row 32 j + lane of a 128-row group: bytes lane * 16 + j * 4 of its chunk
-        const uint32_t sfa = smem_u32(smem + RG::sfa_off + s * RG::sfa_bytes) + lane * 16;
-        const uint32_t sfb = smem_u32(smem + RG::sfb_off + s * RG::sfb_bytes) + lane * 16;
+        const bool in = 2 * ks + h < nq;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int q = 2 * ks + h;
-          const bool in = q < nq;
-          const uint8_t* pa = a.a_scales + ((size_t)(in ? q : 0) * a.R) * 4;
-          const uint8_t* pw = a.w_scales + (((size_t)t.e * nq + (in ? q : 0)) * a.N) * 4;
+        for (int j = 0; j < kMxRows / 32; ++j) {
+          const bool real = in && 32 * j < na;
+          cp_async4(sfa0 + s * RG::sfa_bytes + j * 4, real ? pa + j * 128 : a.a_scales, real);
+        }
 #pragma unroll
-          for (int j = 0; j < kMxRows / 32; ++j) {
-            const int64_t row = (int64_t)t.start + 32 * j + lane;
-            const bool real = in && row < a.R;
-            cp_async4(sfa + h * 512 + j * 4, pa + (real ? row * 4 : 0), real);
-          }
-#pragma unroll
-          for (int j = 0; j < BN / 32; ++j) {
-            const int n = t.n0 + 32 * j + lane;
-            const bool real = in && n < a.N;
-            cp_async4(sfb + (h * RG::groups + j / 4) * 512 + (j & 3) * 4, pw + (real ? (size_t)n * 4 : 0), real);
-          }
+        for (int j = 0; j < BN / 32; ++j) {
+          const bool real = in && 32 * j < nw;
+          cp_async4(sfb0 + s * RG::sfb_bytes + (j / 4) * 512 + (j & 3) * 4, real ? pw + j * 128 : a.w_scales, real);
         }
         cp_async_arrive(&sfull[s]);
       }
@@ -310,56 +353,52 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
+    // The tiles that hold rows come first, so their number is all this warp
+    // needs to know.  The stage loop is unrolled over the ring: every stage's
+    // operands are compile-time offsets from a few bases.
     const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + RG::a_off));
     const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem + RG::b_off));
     const uint64_t sadesc0 = smem_desc_scales(smem_u32(smem + RG::sfa_off));
     const uint64_t sbdesc0 = smem_desc_scales(smem_u32(smem + RG::sfb_off));
     const uint32_t idesc = idesc_mxf4(BN);
-    int it = 0, tc = 0;
+    const int real = tp[a.E] * ntn;
+    const int tail = (nb * 32 - (ksteps - 1) * kMxStageK + 63) / 64;   // MMAs of a tile's last stage
+    int st = 0, tc = 0;
+    uint32_t ph = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_tile(a, tp, ntn, BN, tile);
-      if (t.e == a.E) continue;
+    for (int tile = blockIdx.x; tile < real && ok; tile += gridDim.x, ++tc) {
       const int ab = tc & 1;
       ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      tc_fence_after();
       const uint32_t dacc = tmem + ab * BN;
-      for (int ks = 0; ks < ksteps; ++ks, ++it) {
-        const int s = it % S;
-        const uint32_t par = (it / S) & 1;
-        if (!warp_test_wait(&full[s], par)) ok = spin_or_abort(&full[s], par, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (!warp_test_wait(&sfull[s], par)) ok = spin_or_abort(&sfull[s], par, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        fence_proxy_async_smem();   // the scale loader's copies are generic-proxy writes
-        __syncwarp();
-        const uint32_t sfa = tmem + RG::sf_col0 + s * RG::sf_cols, sfb = sfa + 8;
+      int ks = 0;
+      while (ks < ksteps && ok) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          mx_scales_to_tmem_elect(sfa + 4 * h, sadesc0 + (uint64_t)((s * RG::sfa_bytes + h * 512) >> 4));
-#pragma unroll
-          for (int g = 0; g < RG::groups; ++g)
-            mx_scales_to_tmem_elect(sfb + 4 * (h * RG::groups + g),
-                                    sbdesc0 + (uint64_t)((s * RG::sfb_bytes + (h * RG::groups + g) * 512) >> 4));
+        for (int u = 0; u < S; ++u) {
+          if (u == st && ks < ksteps && ok) {
+            if (!__all_sync(0xffffffffu, mbar_test_wait(&full[u], ph) && mbar_test_wait(&sfull[u], ph))) {
+              ok = spin_or_abort(&full[u], ph, a.wait, abort_flag) && spin_or_abort(&sfull[u], ph, a.wait, abort_flag);
+              ok = __all_sync(0xffffffffu, ok);
+            }
+            if (ok) {
+              tc_fence_after();
+              fence_proxy_async_smem();   // the scale loader's copies are generic-proxy writes
+              mx_stage_elect<RG::groups>(dacc, adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
+                                         bdesc0 + (uint64_t)((u * RG::b_bytes) >> 4), idesc,
+                                         tmem + RG::sf_col0 + u * RG::sf_cols, sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
+                                         sbdesc0 + (uint64_t)((u * RG::sfb_bytes) >> 4), ks != 0 ? 1u : 0u,
+                                         ks + 1 < ksteps ? 4 : tail, &empty[u]);
+              ++ks;
+              if (++st == S) {
+                st = 0;
+                ph ^= 1u;
+              }
+            }
+          }
         }
-        // MMAs of this stage that hold values (the copies fill the rest with zeros)
-        const int nk = min(4, (nb * 32 - ks * kMxStageK + 63) / 64);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j < nk)
-            mx_mma_elect(dacc, adesc0 + (uint64_t)((s * RG::a_bytes + j * 32) >> 4),
-                         bdesc0 + (uint64_t)((s * RG::b_bytes + j * 32) >> 4), idesc | idesc_scale_ids((j & 1) * 2),
-                         sfa + 4 * (j >> 1), sfb + 4 * RG::groups * (j >> 1), (ks | j) ? 1u : 0u);
-        }
-        tc_commit_elect(&empty[s]);
       }
       if (ok) tc_commit_elect(&acc_full[ab]);
-      ++tc;
     }
     tc_commit_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -373,7 +412,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     int tc = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_tile(a, tp, ntn, BN, tile);
+      const MxTile t = mx_tile(a, tp, row0, ntn, BN, tile);
       const bool zero = t.e == a.E;
       const int ab = tc & 1;
       if (!zero) {

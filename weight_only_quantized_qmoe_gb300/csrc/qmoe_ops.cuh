@@ -222,9 +222,95 @@ __device__ __forceinline__ void store_vec(void* base, size_t i, const float (&v)
   }
 }
 
-// Elements of a 16-byte access.
+// A thread's share of a row per step, kept as it is in memory until it is
+// used.  VECTOR: one aligned 16-byte access.  Otherwise, for rows that do not
+// start on 16-byte boundaries, four elements a row's thread count apart, so
+// that a warp's accesses stay side by side and four are in flight.
+template <int DT, bool VECTOR>
+struct Frag;
+
 template <int DT>
-constexpr int kVec16 = DT == QMOE_F32 ? 4 : 8;
+struct Frag<DT, true> {
+  static constexpr int n = DT == QMOE_F32 ? 4 : 8;   // elements
+  uint4 u;
+  // first element of a thread, elements of a step of all of a row's threads
+  __device__ static __forceinline__ int64_t first(int thread) { return (int64_t)thread * n; }
+  __device__ static __forceinline__ int64_t step(int threads) { return (int64_t)threads * n; }
+  __device__ static __forceinline__ bool any(int64_t c, int64_t H) { return c < H; }
+  __device__ __forceinline__ void load(const void* base, size_t row, int64_t c, int64_t, int) {
+    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const typename ElemT<DT>::t*>(base) + row + c));
+  }
+  __device__ __forceinline__ void get(float (&v)[n]) const {
+    if constexpr (DT == QMOE_F32) {
+      v[0] = __uint_as_float(u.x);
+      v[1] = __uint_as_float(u.y);
+      v[2] = __uint_as_float(u.z);
+      v[3] = __uint_as_float(u.w);
+    } else {
+      unpack2<DT>(u.x, v[0], v[1]);
+      unpack2<DT>(u.y, v[2], v[3]);
+      unpack2<DT>(u.z, v[4], v[5]);
+      unpack2<DT>(u.w, v[6], v[7]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&v)[n]) {
+    if constexpr (DT == QMOE_F32)
+      u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else
+      u = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+  }
+  __device__ __forceinline__ void store(void* base, size_t row, int64_t c, int64_t, int) const {
+    *reinterpret_cast<uint4*>(static_cast<typename ElemT<DT>::t*>(base) + row + c) = u;
+  }
+};
+
+template <int DT>
+struct Frag<DT, false> {
+  static constexpr int n = 4;
+  using T = typename ElemT<DT>::t;
+  T e[n];
+  __device__ static __forceinline__ int64_t first(int thread) { return thread; }
+  __device__ static __forceinline__ int64_t step(int threads) { return (int64_t)threads * n; }
+  __device__ static __forceinline__ bool any(int64_t c, int64_t H) { return c < H; }
+  __device__ __forceinline__ void load(const void* base, size_t row, int64_t c, int64_t H, int threads) {
+    const T* p = static_cast<const T*>(base) + row;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int64_t x = c + (int64_t)i * threads;
+      e[i] = x < H ? p[x] : T(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[n]) const {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = load_d<DT>(&e[i], 0);
+  }
+  __device__ __forceinline__ void set(const float (&v)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) store_d<DT>(&e[i], 0, v[i]);
+  }
+  __device__ __forceinline__ void store(void* base, size_t row, int64_t c, int64_t H, int threads) const {
+    T* p = static_cast<T*>(base) + row;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const int64_t x = c + (int64_t)i * threads;
+      if (x < H) p[x] = e[i];
+    }
+  }
+};
+
+// Threads of a row whose elements they take `per` at a time: as few steps as
+// 512 threads allow, whole warps (or 8 or 16 lanes for the shortest rows), so
+// that few threads idle in the last step; several short rows share a CTA.
+struct RowShape {
+  int tpr, rpb;
+};
+inline RowShape row_shape(int64_t H, int per, int most = 512) {
+  const int64_t n = (H + per - 1) / per, steps = (n + most - 1) / most, lanes = (n + steps - 1) / steps;
+  RowShape r;
+  r.tpr = lanes <= 8 ? 8 : lanes <= 16 ? 16 : (int)((lanes + 31) / 32 * 32);
+  r.rpb = r.tpr <= 128 ? 128 / r.tpr : 1;
+  return r;
+}
 
 }  // namespace qmoe
 #endif

@@ -174,197 +174,226 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
 // ----------------------------------------------------------------------------
 // Row copies and sums
 // ----------------------------------------------------------------------------
-// A row takes blockDim.x threads (a power of two, 16 bytes or one element
-// each per step), blockDim.y rows a CTA.
-struct RowShape {
-  dim3 grid, block;
-};
-static RowShape row_shape(int64_t T, int64_t H, int vec) {
-  const int64_t n = (H + vec - 1) / vec;
-  int tpr = 8;
-  while (tpr < 256 && tpr < n) tpr *= 2;
-  const int rpb = 256 / tpr;
-  RowShape r;
-  r.block = dim3(tpr, rpb);
-  r.grid = dim3((unsigned)((T + rpb - 1) / rpb));
-  return r;
-}
+// A row takes blockDim.x threads, blockDim.y rows a CTA (row_shape).  Rows are
+// held as they are in memory until they are added, and the slots of a token
+// (SLOTS of them, 1 to 8, the least that holds top_k; more than 8 in turns) are
+// in flight together: with eight rows unpacked to 32 bits ahead of their use
+// a thread took 128 registers and the sum ran at a quarter of the bandwidth.
 
 // The row of a slot, -1 where it has none.
 __device__ __forceinline__ int slot_row(const RowsArgs& a, int p) { return p < a.T * a.k ? p : -1; }
 
 // Rows offsets[E] .. T * k - 1 of dst, which no route fills: zeros, spread
 // over the rows of the grid.
-template <int DT, int VEC>
+template <int DT, bool VECTOR>
 __device__ __forceinline__ void zero_unused_rows(const RowsArgs& a, int64_t t) {
+  using F = Frag<DT, VECTOR>;
   const int64_t R = a.T * a.k, used = max(a.offsets[a.E], 0);
-  float z[VEC];
+  float z[F::n];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) z[i] = 0.f;
+  for (int i = 0; i < F::n; ++i) z[i] = 0.f;
+  F f;
+  f.set(z);
   for (int64_t i = used + t; i < R; i += a.T)
-    for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC)
-      store_vec<DT, VEC>(a.dst, (size_t)(i * a.H + c), z);
+    for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x))
+      f.store(a.dst, (size_t)(i * a.H), c, a.H, blockDim.x);
 }
 
-template <int DT, int VEC>
-__global__ void __launch_bounds__(256) dispatch_kernel(const RowsArgs a) {
+template <int DT, bool VECTOR>
+__global__ void __launch_bounds__(512) dispatch_kernel(const RowsArgs a) {
+  using F = Frag<DT, VECTOR>;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   if (t >= a.T) return;
   const int* pos = a.pos + t * a.k;
-  for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC) {
-    float v[VEC];
-    load_vec<DT, VEC>(a.src, (size_t)(t * a.ld_src + c), v);
+  for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x)) {
+    F f;
+    f.load(a.src, (size_t)(t * a.ld_src), c, a.H, blockDim.x);
     for (int j = 0; j < a.k; ++j) {
       const int64_t p = slot_row(a, pos[j]);
-      if (p >= 0) store_vec<DT, VEC>(a.dst, (size_t)(p * a.H + c), v);
+      if (p >= 0) f.store(a.dst, (size_t)(p * a.H), c, a.H, blockDim.x);
     }
   }
-  zero_unused_rows<DT, VEC>(a, t);
+  zero_unused_rows<DT, VECTOR>(a, t);
 }
 
-constexpr int kSlots = 8;   // slots whose rows are in flight together
-
-template <int DT, int VEC, bool WEIGHTED>
-__global__ void __launch_bounds__(256) combine_kernel(const RowsArgs a) {
+template <int DT, bool VECTOR, int SLOTS>
+__global__ void __launch_bounds__(512) combine_kernel(const RowsArgs a) {
+  using F = Frag<DT, VECTOR>;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   if (t >= a.T) return;
   const int* pos = a.pos + t * a.k;
-  for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC) {
-    float acc[VEC];
+  for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x)) {
+    float acc[F::n];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < a.k; j0 += kSlots) {
-      float v[kSlots][VEC], w[kSlots];
-      int p[kSlots];
+    for (int i = 0; i < F::n; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+      F f[SLOTS];
+      float w[SLOTS];
+      int p[SLOTS];
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u) p[u] = j0 + u < a.k ? slot_row(a, pos[j0 + u]) : -1;
-#pragma unroll
-      for (int u = 0; u < kSlots; ++u) {
-        if (p[u] >= 0) {
-          load_vec<DT, VEC>(a.src, (size_t)((int64_t)p[u] * a.ld_src + c), v[u]);
-          w[u] = WEIGHTED ? a.w[t * a.k + j0 + u] : 1.f;
-        }
+      for (int u = 0; u < SLOTS; ++u) {
+        p[u] = j0 + u < a.k ? slot_row(a, pos[j0 + u]) : -1;
+        w[u] = a.w && j0 + u < a.k ? a.w[t * a.k + j0 + u] : 1.f;
       }
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u)
-        if (p[u] >= 0) {
+      for (int u = 0; u < SLOTS; ++u)
+        if (p[u] >= 0) f[u].load(a.src, (size_t)((int64_t)p[u] * a.ld_src), c, a.H, blockDim.x);
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) acc[i] = WEIGHTED ? fmaf(w[u], v[u][i], acc[i]) : acc[i] + v[u][i];
+      for (int u = 0; u < SLOTS; ++u)
+        if (p[u] >= 0) {
+          float v[F::n];
+          f[u].get(v);
+#pragma unroll
+          for (int i = 0; i < F::n; ++i) acc[i] = fmaf(w[u], v[i], acc[i]);
         }
     }
-    store_vec<DT, VEC>(a.dst, (size_t)(t * a.H + c), acc);
+    F out;
+    out.set(acc);
+    out.store(a.dst, (size_t)(t * a.H), c, a.H, blockDim.x);
   }
 }
 
-template <int DT, int VEC>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const RowsArgs a) {
-  __shared__ float part[8][kSlots];
+// Sums v[0 .. N - 1] over the 32 lanes of a warp: lane l ends with the sum of
+// entry slot(l) in v[0].  Each of the first steps halves what a lane still
+// carries, so N sums take N + 4 - log2(N) exchanges or fewer instead of 5 N.
+template <int N>
+__device__ __forceinline__ int warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int slot = 0, o = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+    slot += up ? n : 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  for (; o >= 1; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return slot;
+}
+
+template <int DT, bool VECTOR, int SLOTS>
+__global__ void __launch_bounds__(512) combine_grad_kernel(const RowsArgs a) {
+  using F = Frag<DT, VECTOR>;
+  __shared__ float part[16][SLOTS];
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   const bool live = t < a.T;
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int* pos = a.pos + (live ? t : 0) * a.k;
-  for (int j0 = 0; j0 < a.k; j0 += kSlots) {
-    int p[kSlots];
-    float w[kSlots], dot[kSlots];
+  for (int j0 = 0; j0 < a.k; j0 += SLOTS) {
+    int p[SLOTS];
+    float w[SLOTS], dot[SLOTS];
 #pragma unroll
-    for (int u = 0; u < kSlots; ++u) {
+    for (int u = 0; u < SLOTS; ++u) {
       p[u] = live && j0 + u < a.k ? slot_row(a, pos[j0 + u]) : -1;
       w[u] = p[u] >= 0 && a.w ? a.w[t * a.k + j0 + u] : 1.f;
       dot[u] = 0.f;
     }
     if (live) {
-      for (int64_t c = (int64_t)threadIdx.x * VEC; c < a.H; c += (int64_t)blockDim.x * VEC) {
-        float g[VEC], v[kSlots][VEC];
-        load_vec<DT, VEC>(a.src, (size_t)(t * a.ld_src + c), g);
+      for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x)) {
+        F fg, f[SLOTS];
+        fg.load(a.src, (size_t)(t * a.ld_src), c, a.H, blockDim.x);
         if (a.dw) {
 #pragma unroll
-          for (int u = 0; u < kSlots; ++u)
-            if (p[u] >= 0) load_vec<DT, VEC>(a.y, (size_t)((int64_t)p[u] * a.ld_y + c), v[u]);
+          for (int u = 0; u < SLOTS; ++u)
+            if (p[u] >= 0) f[u].load(a.y, (size_t)((int64_t)p[u] * a.ld_y), c, a.H, blockDim.x);
         }
+        float g[F::n];
+        fg.get(g);
 #pragma unroll
-        for (int u = 0; u < kSlots; ++u) {
+        for (int u = 0; u < SLOTS; ++u) {
           if (p[u] < 0) continue;
+          float v[F::n];
           if (a.dw) {
+            f[u].get(v);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) dot[u] = fmaf(g[i], v[u][i], dot[u]);
+            for (int i = 0; i < F::n; ++i) dot[u] = fmaf(g[i], v[i], dot[u]);
           }
           if (a.dst) {
-            float d[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) d[i] = w[u] * g[i];
-            store_vec<DT, VEC>(a.dst, (size_t)((int64_t)p[u] * a.H + c), d);
+            for (int i = 0; i < F::n; ++i) v[i] = w[u] * g[i];
+            F out;
+            out.set(v);
+            out.store(a.dst, (size_t)((int64_t)p[u] * a.H), c, a.H, blockDim.x);
           }
         }
       }
     }
-    if (a.dw) {
-      const int width = min((int)blockDim.x, 32);   // a row's lanes within its warp
+    if (!a.dw) continue;
+    if (blockDim.x >= 32) {
+      const int slot = warp_sums<SLOTS>(dot);
+      if ((lane & (32 / SLOTS - 1)) == 0) part[warp][slot] = dot[0];
+      __syncthreads();
+      if (threadIdx.x < SLOTS) {
+        float sum = 0.f;
+        const int nw = blockDim.x >> 5, w0 = threadIdx.y * nw;
+        for (int q = 0; q < nw; ++q) sum += part[w0 + q][threadIdx.x];
+        if (live && j0 + (int)threadIdx.x < a.k) a.dw[t * a.k + j0 + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    } else {
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u)
-        for (int o = width >> 1; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-      if (blockDim.x > 32) {
-        if ((tid & 31) == 0) {
-#pragma unroll
-          for (int u = 0; u < kSlots; ++u) part[warp][u] = dot[u];
-        }
-        __syncthreads();
-        if (threadIdx.x < kSlots) {
-          float sum = 0.f;
-          const int nw = blockDim.x >> 5, w0 = threadIdx.y * nw;
-          for (int q = 0; q < nw; ++q) sum += part[w0 + q][threadIdx.x];
-          if (live && j0 + (int)threadIdx.x < a.k) a.dw[t * a.k + j0 + threadIdx.x] = sum;
-        }
-        __syncthreads();
-      } else if (threadIdx.x == 0 && live) {
-#pragma unroll
-        for (int u = 0; u < kSlots; ++u)
-          if (j0 + u < a.k) a.dw[t * a.k + j0 + u] = dot[u];
+      for (int u = 0; u < SLOTS; ++u) {
+        for (int o = blockDim.x >> 1; o > 0; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+        if (threadIdx.x == 0 && live && j0 + u < a.k) a.dw[t * a.k + j0 + u] = dot[u];
       }
     }
   }
-  if (live && a.dst) zero_unused_rows<DT, VEC>(a, t);
+  if (live && a.dst) zero_unused_rows<DT, VECTOR>(a, t);
 }
 
-template <typename F>
-static cudaError_t by_type(int dtype, bool vec, F&& f) {
-  if (dtype == QMOE_F32)
-    return vec ? f(std::integral_constant<int, QMOE_F32>{}, std::integral_constant<int, 4>{})
-               : f(std::integral_constant<int, QMOE_F32>{}, std::integral_constant<int, 1>{});
-  if (dtype == QMOE_F16)
-    return vec ? f(std::integral_constant<int, QMOE_F16>{}, std::integral_constant<int, 8>{})
-               : f(std::integral_constant<int, QMOE_F16>{}, std::integral_constant<int, 1>{});
-  return vec ? f(std::integral_constant<int, QMOE_BF16>{}, std::integral_constant<int, 8>{})
-             : f(std::integral_constant<int, QMOE_BF16>{}, std::integral_constant<int, 1>{});
+// Calls f(type, 16-byte accesses?, slots in flight).
+template <int DT, bool VECTOR, typename F>
+static cudaError_t by_slots(int k, F&& f) {
+  using D = std::integral_constant<int, DT>;
+  using V = std::integral_constant<bool, VECTOR>;
+  if (k <= 1) return f(D{}, V{}, std::integral_constant<int, 1>{});
+  if (k <= 2) return f(D{}, V{}, std::integral_constant<int, 2>{});
+  if (k <= 4) return f(D{}, V{}, std::integral_constant<int, 4>{});
+  return f(D{}, V{}, std::integral_constant<int, 8>{});
 }
-
 // 16-byte accesses need every row of every operand on a 16-byte boundary and
 // whole vectors a row; anything else moves element by element.
-static bool rows_vec(const RowsArgs& a) {
-  return a.H % (16 / dtype_size(a.dtype)) == 0 && rows_aligned16(a.src, a.ld_src, a.dtype) &&
-         rows_aligned16(a.y, a.ld_y, a.dtype) && rows_aligned16(a.dst, a.H, a.dtype);
+template <typename F>
+static cudaError_t by_rows(const RowsArgs& a, F&& f) {
+  const bool vec = a.H % (16 / dtype_size(a.dtype)) == 0 && rows_aligned16(a.src, a.ld_src, a.dtype) &&
+                   rows_aligned16(a.y, a.ld_y, a.dtype) && rows_aligned16(a.dst, a.H, a.dtype);
+  if (a.dtype == QMOE_F32) return vec ? by_slots<QMOE_F32, true>(a.k, f) : by_slots<QMOE_F32, false>(a.k, f);
+  if (a.dtype == QMOE_F16) return vec ? by_slots<QMOE_F16, true>(a.k, f) : by_slots<QMOE_F16, false>(a.k, f);
+  return vec ? by_slots<QMOE_BF16, true>(a.k, f) : by_slots<QMOE_BF16, false>(a.k, f);
+}
+template <int DT, bool VECTOR>
+static RowShape rows_of(const RowsArgs& a, dim3* grid) {
+  const RowShape r = row_shape(a.H, Frag<DT, VECTOR>::n);
+  *grid = dim3((unsigned)((a.T + r.rpb - 1) / r.rpb));
+  return r;
 }
 
 cudaError_t launch_dispatch(const RowsArgs& a, cudaStream_t s) {
-  return by_type(a.dtype, rows_vec(a), [&](auto dt, auto vec) {
-    const RowShape g = row_shape(a.T, a.H, vec);
-    dispatch_kernel<dt, vec><<<g.grid, g.block, 0, s>>>(a);
+  return by_rows(a, [&](auto dt, auto vec, auto) {
+    dim3 grid;
+    const RowShape r = rows_of<dt, vec>(a, &grid);
+    dispatch_kernel<dt, vec><<<grid, dim3(r.tpr, r.rpb), 0, s>>>(a);
     return cudaGetLastError();
   });
 }
 
 cudaError_t launch_combine(const RowsArgs& a, cudaStream_t s) {
-  return by_type(a.dtype, rows_vec(a), [&](auto dt, auto vec) {
-    const RowShape g = row_shape(a.T, a.H, vec);
-    if (a.w) combine_kernel<dt, vec, true><<<g.grid, g.block, 0, s>>>(a);
-    else combine_kernel<dt, vec, false><<<g.grid, g.block, 0, s>>>(a);
+  return by_rows(a, [&](auto dt, auto vec, auto slots) {
+    dim3 grid;
+    const RowShape r = rows_of<dt, vec>(a, &grid);
+    combine_kernel<dt, vec, slots><<<grid, dim3(r.tpr, r.rpb), 0, s>>>(a);
     return cudaGetLastError();
   });
 }
 
 cudaError_t launch_combine_grad(const RowsArgs& a, cudaStream_t s) {
-  return by_type(a.dtype, rows_vec(a), [&](auto dt, auto vec) {
-    const RowShape g = row_shape(a.T, a.H, vec);
-    combine_grad_kernel<dt, vec><<<g.grid, g.block, 0, s>>>(a);
+  return by_rows(a, [&](auto dt, auto vec, auto slots) {
+    dim3 grid;
+    const RowShape r = rows_of<dt, vec>(a, &grid);
+    combine_grad_kernel<dt, vec, slots><<<grid, dim3(r.tpr, r.rpb), 0, s>>>(a);
     return cudaGetLastError();
   });
 }

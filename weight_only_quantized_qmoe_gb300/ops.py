@@ -74,59 +74,66 @@ class NormGrads(NamedTuple):
 
 
 # --- argument handling --------------------------------------------------------
+# A call on small tensors is bound by this code, so every argument is looked at
+# once and the common case (contiguous tensors) takes the shortest way.
+_empty, _f32, _i32, _u8 = torch.empty, torch.float32, torch.int32, torch.uint8
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+
 def _refuse(msg):
     raise QMoEError(binding.QMOE_ERR_INVALID_ARG, msg)
 
 
-def _check(status):
-    if status != binding.QMOE_OK:
-        raise QMoEError(status, binding.qmoe_op_last_error())
+def _failed(status):
+    raise QMoEError(status, binding.qmoe_op_last_error())
 
 
-def _need(cond, msg):
-    if not cond:
-        _refuse(msg)
-
-
-def _cuda(t, name):
+def _first(t, name):
+    """(device index, dtype code) of the tensor that decides both."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        _refuse(f"{name} is on {t.device}, not on the current device")
-
-
-def _dtype(t, name):
     code = _DTYPES.get(t.dtype)
     if code is None:
         _refuse(f"{name} is {t.dtype}: float32, float16 or bfloat16")
-    return code
+    return _here(t, name), code
 
 
-def _rows(t, name, dtype=None):
+def _here(t, name):
+    dev = t.get_device()
+    if dev != _device():
+        _refuse(f"{name} is on {t.device}, not on the current device")
+    return dev
+
+
+def _not(t, name, dtype, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        _refuse(f"{name} is {t.dtype}, not {dtype}")
+    _refuse(f"{name} is on {t.device}, not on the current device")
+
+
+def _rows(t, name, dtype, dev):
     """A 2-D tensor with a contiguous last axis and rows at least its length
     apart, and that row stride."""
-    _cuda(t, name)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _not(t, name, dtype, dev)
     if t.dim() != 2:
         _refuse(f"{name} must be two-dimensional, not {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        _refuse(f"{name} is {t.dtype}, not {dtype}")
     n, width = t.shape
+    if t.is_contiguous():
+        return t, width or 1
     if (t.stride(1) != 1 and width > 1) or (t.stride(0) < width and n > 1):
-        t = t.contiguous()
+        return t.contiguous(), width
     return t, (t.stride(0) if n > 1 else max(width, 1))
 
 
-def _flat(t, name, dtype, numel=None):
-    _cuda(t, name)
-    if t.dtype != dtype:
-        _refuse(f"{name} is {t.dtype}, not {dtype}")
-    if numel is not None and t.numel() != numel:
+def _flat(t, name, dtype, numel, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _not(t, name, dtype, dev)
+    if t.numel() != numel:
         _refuse(f"{name} has {t.numel()} elements, not {numel}")
     return t if t.is_contiguous() else t.contiguous()
-
-
-def _stream():
-    return torch.cuda.current_stream().cuda_stream
 
 
 def _elsewhere(stream, call, *args, **kw):
@@ -140,19 +147,17 @@ def _elsewhere(stream, call, *args, **kw):
     return out
 
 
-def _plan(plan, tokens=None):
-    """(pos, offsets) of a plan, checked."""
+def _plan(plan, dev, tokens=None):
+    """(pos, offsets, tokens, k, experts) of a plan, checked."""
     if not isinstance(plan, ExpertPlan):
         _refuse("plan must be an ExpertPlan")
-    _need(plan.k >= 1 and plan.pos.numel() % plan.k == 0, "plan.pos does not hold whole tokens")
-    if tokens is not None and plan.tokens != tokens:
-        _refuse(f"the plan is of {plan.tokens} tokens, not {tokens}")
-    return (_flat(plan.pos, "plan.pos", torch.int32),
-            _flat(plan.offsets, "plan.offsets", torch.int32, plan.experts + 1))
-
-
-def _weights(weights, plan):
-    return None if weights is None else _flat(weights, "weights", torch.float32, plan.pos.numel())
+    _, pos, offsets, k, experts = plan
+    if k < 1 or pos.numel() % k:
+        _refuse("plan.pos does not hold whole tokens")
+    n = pos.numel() // k
+    if tokens is not None and n != tokens:
+        _refuse(f"the plan is of {n} tokens, not {tokens}")
+    return _flat(pos, "plan.pos", _i32, n * k, dev), _flat(offsets, "plan.offsets", _i32, experts + 1, dev), n, k, experts
 
 
 def _ptr(t):
@@ -171,26 +176,34 @@ def expert_sort(ids, experts, stream=None) -> ExpertPlan:
     outside [0, experts) drop their route."""
     if stream is not None:
         return _elsewhere(stream, expert_sort, ids, experts)
-    _cuda(ids, "ids")
-    _need(ids.dtype in (torch.int32, torch.int64), f"ids is {ids.dtype}: int32 or int64")
-    ids, ld = _rows(ids, "ids")
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        _refuse("ids must be a CUDA tensor")
+    dt = ids.dtype
+    if dt is not _i32 and dt is not torch.int64:
+        _refuse(f"ids is {dt}: int32 or int64")
+    dev = _here(ids, "ids")
+    ids, ld = _rows(ids, "ids", dt, dev)
     T, k = ids.shape
-    perm = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-    pos = torch.empty_like(perm)
-    offsets = torch.empty(max(int(experts), 0) + 1, dtype=torch.int32, device=ids.device)
-    _check(binding.qmoe_expert_sort(ids.data_ptr(), ids.element_size(), ld, T, k, experts, perm.data_ptr(),
-                                    pos.data_ptr(), offsets.data_ptr(), _stream()))
-    return ExpertPlan(perm, pos, offsets, k, int(experts))
+    R, device = T * k, ids.device
+    perm, pos = _empty(R, dtype=_i32, device=device), _empty(R, dtype=_i32, device=device)
+    offsets = _empty(max(experts, 0) + 1, dtype=_i32, device=device)
+    st = binding.qmoe_expert_sort(ids.data_ptr(), 4 if dt is _i32 else 8, ld, T, k, experts, perm.data_ptr(),
+                                  pos.data_ptr(), offsets.data_ptr(), _raw_stream(dev))
+    if st:
+        _failed(st)
+    return ExpertPlan(perm, pos, offsets, k, experts)
 
 
 def _dispatch(x, plan):
-    dt = _dtype(x, "x")
-    x, ld = _rows(x, "x")
+    dev, dt = _first(x, "x")
+    x, ld = _rows(x, "x", x.dtype, dev)
     T, H = x.shape
-    pos, offsets = _plan(plan, T)
-    xs = torch.empty((T * plan.k, H), dtype=x.dtype, device=x.device)
-    _check(binding.qmoe_dispatch(x.data_ptr(), ld, pos.data_ptr(), offsets.data_ptr(), T, plan.k, plan.experts, H, dt,
-                                 xs.data_ptr(), _stream()))
+    pos, offsets, _, k, experts = _plan(plan, dev, T)
+    xs = _empty((T * k, H), dtype=x.dtype, device=x.device)
+    st = binding.qmoe_dispatch(x.data_ptr(), ld, pos.data_ptr(), offsets.data_ptr(), T, k, experts, H, dt,
+                               xs.data_ptr(), _raw_stream(dev))
+    if st:
+        _failed(st)
     return xs
 
 
@@ -202,15 +215,20 @@ def dispatch_grad(dxs, plan, stream=None):
 
 
 def _combine(y, weights, plan, name="y"):
-    dt = _dtype(y, name)
-    y, ld = _rows(y, name)
-    pos, _ = _plan(plan)
-    T, H = plan.tokens, y.shape[1]
-    _need(y.shape[0] == pos.numel(), f"{name} has {y.shape[0]} rows, the plan {pos.numel()}")
-    weights = _weights(weights, plan)
-    out = torch.empty((T, H), dtype=y.dtype, device=y.device)
-    _check(binding.qmoe_combine(y.data_ptr(), ld, _ptr(weights), pos.data_ptr(), T, plan.k, H, dt, out.data_ptr(),
-                                _stream()))
+    dev, dt = _first(y, name)
+    y, ld = _rows(y, name, y.dtype, dev)
+    pos, _, T, k, _ = _plan(plan, dev)
+    R, H = y.shape
+    if R != T * k:
+        _refuse(f"{name} has {R} rows, the plan {T * k}")
+    w = 0
+    if weights is not None:
+        weights = _flat(weights, "weights", _f32, R, dev)
+        w = weights.data_ptr()
+    out = _empty((T, H), dtype=y.dtype, device=y.device)
+    st = binding.qmoe_combine(y.data_ptr(), ld, w, pos.data_ptr(), T, k, H, dt, out.data_ptr(), _raw_stream(dev))
+    if st:
+        _failed(st)
     return out
 
 
@@ -219,20 +237,24 @@ def combine_grad(dout, y, weights, plan, need_dy=True, need_dweights=True, strea
     of dout [T, H]; one that is not needed is None."""
     if stream is not None:
         return _elsewhere(stream, combine_grad, dout, y, weights, plan, need_dy, need_dweights)
-    dt = _dtype(dout, "dout")
-    dout, ld = _rows(dout, "dout")
+    dev, dt = _first(dout, "dout")
+    dout, ld = _rows(dout, "dout", dout.dtype, dev)
     T, H = dout.shape
-    pos, offsets = _plan(plan, T)
-    weights = _weights(weights, plan)
+    pos, offsets, _, k, experts = _plan(plan, dev, T)
+    if weights is not None:
+        weights = _flat(weights, "weights", _f32, T * k, dev)
     ld_y = H
     if need_dweights:
-        y, ld_y = _rows(y, "y", dout.dtype)
-        _need(tuple(y.shape) == (pos.numel(), H), f"y is {tuple(y.shape)}, not {(pos.numel(), H)}")
-    dy = torch.empty((T * plan.k, H), dtype=dout.dtype, device=dout.device) if need_dy else None
-    dw = torch.empty((T, plan.k), dtype=torch.float32, device=dout.device) if need_dweights else None
-    _check(binding.qmoe_combine_grad(dout.data_ptr(), ld, y.data_ptr() if need_dweights else 0, ld_y, _ptr(weights),
-                                     pos.data_ptr(), offsets.data_ptr(), T, plan.k, plan.experts, H, dt, _ptr(dy),
-                                     _ptr(dw), _stream()))
+        y, ld_y = _rows(y, "y", dout.dtype, dev)
+        if y.shape[0] != T * k or y.shape[1] != H:
+            _refuse(f"y is {tuple(y.shape)}, not {(T * k, H)}")
+    dy = _empty((T * k, H), dtype=dout.dtype, device=dout.device) if need_dy else None
+    dw = _empty((T, k), dtype=_f32, device=dout.device) if need_dweights else None
+    st = binding.qmoe_combine_grad(dout.data_ptr(), ld, y.data_ptr() if need_dweights else 0, ld_y, _ptr(weights),
+                                   pos.data_ptr(), offsets.data_ptr(), T, k, experts, H, dt, _ptr(dy), _ptr(dw),
+                                   _raw_stream(dev))
+    if st:
+        _failed(st)
     return dy, dw
 
 
@@ -263,7 +285,11 @@ class _CombineFn(torch.autograd.Function):
 
 
 def _differentiable(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def dispatch(x, plan, stream=None):
@@ -289,54 +315,71 @@ def mx4_quantize(x, plan=None, activation=None, stream=None) -> MX4Tensor:
     "geglu" a row holds gate | up (2 K values) and act(gate) * up is quantised."""
     if stream is not None:
         return _elsewhere(stream, mx4_quantize, x, plan, activation)
-    _cuda(x, "x")
-    dt = _dtype(x, "x")
-    _need(activation in _ACTIVATIONS, f"activation {activation!r}: None, 'swiglu' or 'geglu'")
-    _need(x.dim() >= 2, "x must have rows: two dimensions at least")
-    lead, n, width = x.shape[:-2], x.shape[-2], x.shape[-1]
+    dev, dt = _first(x, "x")
+    if x.dim() < 2:
+        _refuse("x must have rows: two dimensions at least")
+    *lead, n, width = x.shape
+    act, cols = binding.QMOE_ACT_NONE, width
     if activation is not None:
-        _need(width % 2 == 0, f"gate | up needs an even row length, not {width}")
-    cols = width if activation is None else width // 2
-    flat, ld = _rows(x if x.dim() == 2 else x.reshape(-1, width), "x")
+        act = _ACTIVATIONS.get(activation)
+        if act is None:
+            _refuse(f"activation {activation!r}: None, 'swiglu' or 'geglu'")
+        if width % 2:
+            _refuse(f"gate | up needs an even row length, not {width}")
+        cols = width // 2
+    flat, ld = _rows(x if not lead else x.reshape(-1, width), "x", x.dtype, dev)
     rows = flat.shape[0]
-    pos = offsets = None
+    pos = offsets = 0
     k = experts = 1
     if plan is not None:
-        _need(x.dim() == 2, "with a plan x is [T, K]")
-        pos, offsets = _plan(plan, rows)
-        k, experts, n = plan.k, plan.experts, rows * plan.k
-    nb = -(-cols // 32)
-    codes = torch.empty((*lead, n, nb * 16), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*lead, -(-nb // 4), n, 4), dtype=torch.uint8, device=x.device)
-    _check(binding.qmoe_mx4_quantize(flat.data_ptr(), ld, rows, cols, dt, _ACTIVATIONS[activation], _ptr(pos),
-                                     _ptr(offsets), k, experts, n, codes.data_ptr(), scales.data_ptr(), _stream()))
+        if lead:
+            _refuse("with a plan x is [T, K]")
+        tpos, toffsets, _, k, experts = _plan(plan, dev, rows)
+        pos, offsets, n = tpos.data_ptr(), toffsets.data_ptr(), rows * k
+    nb = (cols + 31) // 32
+    codes = _empty((*lead, n, nb * 16), dtype=_u8, device=x.device)
+    scales = _empty((*lead, (nb + 3) // 4, n, 4), dtype=_u8, device=x.device)
+    st = binding.qmoe_mx4_quantize(flat.data_ptr(), ld, rows, cols, dt, act, pos, offsets, k, experts, n,
+                                   codes.data_ptr(), scales.data_ptr(), _raw_stream(dev))
+    if st:
+        _failed(st)
     return MX4Tensor(codes, scales, cols)
 
 
 def _mx4(q, name):
-    """(codes, scales) of an MX4Tensor, checked and contiguous."""
+    """(codes, scales, shape of codes, device index) of an MX4Tensor, checked
+    and contiguous."""
     if not isinstance(q, MX4Tensor):
         _refuse(f"{name} must be an MX4Tensor")
-    codes, scales = _flat(q.codes, name + ".codes", torch.uint8), _flat(q.scales, name + ".scales", torch.uint8)
-    nb = -(-q.cols // 32)
-    if codes.dim() < 2 or codes.shape[-1] != nb * 16 or q.cols < 1:
-        _refuse(f"{name}.codes {tuple(codes.shape)} does not hold rows of {q.cols} values")
-    if tuple(scales.shape) != (*codes.shape[:-2], -(-nb // 4), codes.shape[-2], 4):
-        _refuse(f"{name}.scales {tuple(scales.shape)} does not belong to codes {tuple(codes.shape)}")
-    return codes, scales
+    codes, scales, cols = q
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        _refuse(f"{name}.codes must be a CUDA tensor")
+    dev = _here(codes, name + ".codes")
+    if codes.dtype is not _u8:
+        _refuse(f"{name}.codes is {codes.dtype}, not uint8")
+    nb, shape = (cols + 31) // 32, codes.shape
+    if len(shape) < 2 or shape[-1] != nb * 16 or cols < 1:
+        _refuse(f"{name}.codes {tuple(shape)} does not hold rows of {cols} values")
+    scales = _flat(scales, name + ".scales", _u8, codes.numel() // max(1, nb * 16) * ((nb + 3) // 4) * 4, dev)
+    if scales.shape != (*shape[:-2], (nb + 3) // 4, shape[-2], 4):
+        _refuse(f"{name}.scales {tuple(scales.shape)} does not belong to codes {tuple(shape)}")
+    return codes if codes.is_contiguous() else codes.contiguous(), scales, shape, dev
 
 
 def mx4_dequantize(q, dtype=torch.bfloat16, stream=None):
     """The values [..., N, cols] of an :class:`MX4Tensor`."""
     if stream is not None:
         return _elsewhere(stream, mx4_dequantize, q, dtype)
-    codes, scales = _mx4(q, "q")
-    _need(dtype in _DTYPES, f"dtype {dtype}: float32, float16 or bfloat16")
-    n = codes.shape[-2]
-    out = torch.empty((*codes.shape[:-1], q.cols), dtype=dtype, device=codes.device)
-    rows = out.numel() // q.cols
-    _check(binding.qmoe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, q.cols, n, _DTYPES[dtype],
-                                       out.data_ptr(), q.cols, _stream()))
+    codes, scales, shape, dev = _mx4(q, "q")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _refuse(f"dtype {dtype}: float32, float16 or bfloat16")
+    cols, n = q.cols, shape[-2]
+    out = _empty((*shape[:-1], cols), dtype=dtype, device=codes.device)
+    st = binding.qmoe_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), out.numel() // cols, cols, n, dt,
+                                     out.data_ptr(), cols, _raw_stream(dev))
+    if st:
+        _failed(st)
     return out
 
 
@@ -346,86 +389,95 @@ def mx4_matmul(a, w, plan=None, out_dtype=torch.bfloat16, stream=None):
     use).  Returns [R, N]."""
     if stream is not None:
         return _elsewhere(stream, mx4_matmul, a, w, plan, out_dtype)
-    a_codes, a_scales = _mx4(a, "a")
-    w_codes, w_scales = _mx4(w, "w")
-    _need(out_dtype in _DTYPES, f"out_dtype {out_dtype}: float32, float16 or bfloat16")
-    _need(a_codes.dim() == 2, "a must be [R, K]")
-    _need(a.cols == w.cols, f"a has rows of {a.cols} values, w of {w.cols}")
-    R, N = a_codes.shape[0], w_codes.shape[-2]
-    experts, offsets = 1, None
+    a_codes, a_scales, a_shape, dev = _mx4(a, "a")
+    w_codes, w_scales, w_shape, _ = _mx4(w, "w")
+    dt = _DTYPES.get(out_dtype)
+    if dt is None:
+        _refuse(f"out_dtype {out_dtype}: float32, float16 or bfloat16")
+    if len(a_shape) != 2:
+        _refuse("a must be [R, K]")
+    if a.cols != w.cols:
+        _refuse(f"a has rows of {a.cols} values, w of {w.cols}")
+    R, N = a_shape[0], w_shape[-2]
+    experts, offsets = 1, 0
     if plan is not None:
-        pos, offsets = _plan(plan)
-        experts = plan.experts
-        _need(pos.numel() == R, f"a has {R} rows, the plan {pos.numel()}")
-    if experts != w_codes.numel() // max(1, w_codes.shape[-2] * w_codes.shape[-1]) or w_codes.dim() > 3:
-        _refuse(f"w.codes {tuple(w_codes.shape)} does not hold {experts} expert(s)")
-    out = torch.empty((R, N), dtype=out_dtype, device=a_codes.device)
-    _check(binding.qmoe_mx4_matmul(a_codes.data_ptr(), a_scales.data_ptr(), R, w_codes.data_ptr(), w_scales.data_ptr(),
-                                   _ptr(offsets), experts, N, a.cols, _DTYPES[out_dtype], out.data_ptr(), N, _stream()))
+        _, toffsets, T, k, experts = _plan(plan, dev)
+        offsets = toffsets.data_ptr()
+        if T * k != R:
+            _refuse(f"a has {R} rows, the plan {T * k}")
+    if (w_shape[0] if len(w_shape) == 3 else 1) != experts or len(w_shape) > 3:
+        _refuse(f"w.codes {tuple(w_shape)} does not hold {experts} expert(s)")
+    out = _empty((R, N), dtype=out_dtype, device=a_codes.device)
+    st = binding.qmoe_mx4_matmul(a_codes.data_ptr(), a_scales.data_ptr(), R, w_codes.data_ptr(), w_scales.data_ptr(),
+                                 offsets, experts, N, a.cols, dt, out.data_ptr(), N, _raw_stream(dev))
+    if st:
+        _failed(st)
     return out
 
 
 # --- norms around a block ------------------------------------------------------
-class _Norm(NamedTuple):
-    """Checked arguments of a block norm, flattened to rows."""
-
-    shape: tuple
-    T: int
-    H: int
-    dt: int
-    x: torch.Tensor
-    ld_x: int
-    o: Optional[torch.Tensor]
-    ld_o: int
-    gate: Optional[torch.Tensor]
-    kind: int
-    ld_gate: int
-    w_post: Optional[torch.Tensor]
-    w_pre: Optional[torch.Tensor]
-
-
-def _flat_rows(t, name, H, shape, dtype):
-    _need(isinstance(t, torch.Tensor) and tuple(t.shape) == tuple(shape), f"{name} must have the shape {tuple(shape)}")
-    return _rows(t if t.dim() == 2 else t.reshape(-1, H), name, dtype)
+def _norm_rows(t, name, shape, dtype, dev):
+    if t.shape != shape:
+        _refuse(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _rows(t if len(shape) == 2 else t.reshape(-1, shape[-1]), name, dtype, dev)
 
 
 def _norm_args(x, o, gate, w_post, w_pre):
-    _cuda(x, "x")
-    dt = _dtype(x, "x")
-    _need(x.dim() >= 1 and x.shape[-1] >= 1, "x must have rows of at least one value")
-    shape, H = tuple(x.shape), x.shape[-1]
-    fx, ld_x = _flat_rows(x, "x", H, shape, x.dtype)
-    T = fx.shape[0]
-    fo, ld_o = (None, 0) if o is None else _flat_rows(o, "o", H, shape, x.dtype)
-    fg, kind, ld_g = None, binding.QMOE_GATE_NONE, 0
+    """The checked tensors of a block norm as rows (kept alive by the caller),
+    the device index, and the leading arguments of its C calls from x on."""
+    dev, dt = _first(x, "x")
+    shape, dtype = x.shape, x.dtype
+    if not shape or shape[-1] < 1:
+        _refuse("x must have rows of at least one value")
+    H = shape[-1]
+    x, ld_x = _norm_rows(x, "x", shape, dtype, dev)
+    po = ld_o = pg = kind = ld_g = pq = pp = 0
+    if o is not None:
+        o, ld_o = _norm_rows(o, "o", shape, dtype, dev)
+        po = o.data_ptr()
     if gate is not None:
-        _need(o is not None, "gate needs o")
-        g = tuple(gate.shape)
+        if o is None:
+            _refuse("gate needs o")
+        g = gate.shape
         if g == shape:
             kind = binding.QMOE_GATE_FULL
-            fg, ld_g = _flat_rows(gate, "gate", H, shape, x.dtype)
+            gate, ld_g = _norm_rows(gate, "gate", shape, dtype, dev)
         elif g == (H,):
             kind = binding.QMOE_GATE_CHANNEL
-            fg = _flat(gate, "gate", x.dtype)
-        elif g == shape[:-1] + (1,):
+            gate = _flat(gate, "gate", dtype, H, dev)
+        elif g == (*shape[:-1], 1):
             kind = binding.QMOE_GATE_TOKEN
-            fg = _flat(gate, "gate", x.dtype)
+            gate = _flat(gate, "gate", dtype, x.shape[0], dev)
         else:
-            _refuse(f"gate {g} is not {shape}, {(H,)} or {shape[:-1] + (1,)}")
-    wq = None if w_post is None else _flat(w_post, "w_post", x.dtype, H)
-    wp = None if w_pre is None else _flat(w_pre, "w_pre", x.dtype, H)
-    return _Norm(shape, T, H, dt, fx, ld_x, fo, ld_o, fg, kind, ld_g, wq, wp)
+            _refuse(f"gate {tuple(g)} is not {tuple(shape)}, {(H,)} or {(*shape[:-1], 1)}")
+        pg = gate.data_ptr()
+    if w_post is not None:
+        w_post = _flat(w_post, "w_post", dtype, H, dev)
+        pq = w_post.data_ptr()
+    if w_pre is not None:
+        w_pre = _flat(w_pre, "w_pre", dtype, H, dev)
+        pp = w_pre.data_ptr()
+    return (x, o, gate, w_post, w_pre), dev, (x.data_ptr(), ld_x, po, ld_o, pg, kind, ld_g, pq, pp), x.shape[0], H, dt
 
 
 def _block_norm(x, o, gate, w_post, w_pre, residual_scale, eps, stats):
-    a = _norm_args(x, o, gate, w_post, w_pre)
-    r = torch.empty(a.shape, dtype=x.dtype, device=x.device)
-    h = None if w_pre is None else torch.empty_like(r)
-    s1 = torch.empty(a.T, dtype=torch.float32, device=x.device) if stats and w_post is not None else None
-    s2 = torch.empty(a.T, dtype=torch.float32, device=x.device) if stats and w_pre is not None else None
-    _check(binding.qmoe_block_norm(a.x.data_ptr(), a.ld_x, _ptr(a.o), a.ld_o, _ptr(a.gate), a.kind, a.ld_gate,
-                                   _ptr(a.w_post), _ptr(a.w_pre), residual_scale, eps, a.T, a.H, a.dt, r.data_ptr(),
-                                   _ptr(h), _ptr(s1), _ptr(s2), _stream()))
+    keep, dev, args, T, H, dt = _norm_args(x, o, gate, w_post, w_pre)
+    r = _empty(x.shape, dtype=x.dtype, device=x.device)
+    h = s1 = s2 = None
+    ph = p1 = p2 = 0
+    if w_pre is not None:
+        h = _empty(x.shape, dtype=x.dtype, device=x.device)
+        ph = h.data_ptr()
+    if stats:
+        if w_post is not None:
+            s1 = _empty(T, dtype=_f32, device=x.device)
+            p1 = s1.data_ptr()
+        if w_pre is not None:
+            s2 = _empty(T, dtype=_f32, device=x.device)
+            p2 = s2.data_ptr()
+    st = binding.qmoe_block_norm(*args, residual_scale, eps, T, H, dt, r.data_ptr(), ph, p1, p2, _raw_stream(dev))
+    if st:
+        _failed(st)
     return r, h, NormStats(s1, s2)
 
 
@@ -437,23 +489,35 @@ def block_norm_grad(dr, dh, x, o, stats, gate=None, w_post=None, w_pre=None, res
     can be passed on)."""
     if stream is not None:
         return _elsewhere(stream, block_norm_grad, dr, dh, x, o, stats, gate, w_post, w_pre, residual_scale)
-    a = _norm_args(x, o, gate, w_post, w_pre)
-    _need(dh is None or w_pre is not None, "dh needs w_pre")
-    fr, ld_r = (None, 0) if dr is None else _flat_rows(dr, "dr", a.H, a.shape, x.dtype)
-    fh, ld_h = (None, 0) if dh is None else _flat_rows(dh, "dh", a.H, a.shape, x.dtype)
-    s1 = _flat(stats.rstd_post, "stats.rstd_post", torch.float32, a.T) if w_post is not None else None
-    s2 = _flat(stats.rstd_pre, "stats.rstd_pre", torch.float32, a.T) if w_pre is not None else None
+    keep, dev, args, T, H, dt = _norm_args(x, o, gate, w_post, w_pre)
+    dtype, device = x.dtype, x.device
+    pr = ld_r = ph = ld_h = p1 = p2 = 0
+    if dr is not None:
+        dr, ld_r = _norm_rows(dr, "dr", x.shape, dtype, dev)
+        pr = dr.data_ptr()
+    if dh is not None:
+        if w_pre is None:
+            _refuse("dh needs w_pre")
+        dh, ld_h = _norm_rows(dh, "dh", x.shape, dtype, dev)
+        ph = dh.data_ptr()
+    if w_post is not None:
+        s1 = _flat(stats.rstd_post, "stats.rstd_post", _f32, T, dev)
+        p1 = s1.data_ptr()
+    if w_pre is not None:
+        s2 = _flat(stats.rstd_pre, "stats.rstd_pre", _f32, T, dev)
+        p2 = s2.data_ptr()
 
     def like(t):
-        return None if t is None else torch.empty(t.shape, dtype=x.dtype, device=x.device)
+        return None if t is None else _empty(t.shape, dtype=dtype, device=device)
 
     dx, do, dgate, dwq, dwp = like(x), like(o), like(gate), like(w_post), like(w_pre)
-    nbytes = binding.qmoe_block_norm_grad_workspace(a.T, a.H, a.dt)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _check(binding.qmoe_block_norm_grad(_ptr(fr), ld_r, _ptr(fh), ld_h, a.x.data_ptr(), a.ld_x, _ptr(a.o), a.ld_o,
-                                        _ptr(a.gate), a.kind, a.ld_gate, _ptr(a.w_post), _ptr(a.w_pre), _ptr(s1),
-                                        _ptr(s2), residual_scale, a.T, a.H, a.dt, _ptr(dx), _ptr(do), _ptr(dgate),
-                                        _ptr(dwq), _ptr(dwp), work.data_ptr(), nbytes, _stream()))
+    nbytes = binding.qmoe_block_norm_grad_workspace(T, H, dt)
+    work = _empty(nbytes, dtype=_u8, device=device)
+    st = binding.qmoe_block_norm_grad(pr, ld_r, ph, ld_h, *args, p1, p2, residual_scale, T, H, dt, dx.data_ptr(),
+                                      _ptr(do), _ptr(dgate), _ptr(dwq), _ptr(dwp), work.data_ptr(), nbytes,
+                                      _raw_stream(dev))
+    if st:
+        _failed(st)
     return NormGrads(dx, do, dgate, dwq, dwp)
 
 
