@@ -477,7 +477,8 @@ qmoe_status qmoe_combine_grad(const void* dout_dev, int64_t ld_dout, const void*
  *   activation  QMOE_ACT_NONE, QMOE_ACT_SWIGLU or QMOE_ACT_GEGLU_TANH
  *   pos_dev     NULL, or int32 [rows, top_k] of qmoe_expert_sort: row t is
  *               then written to the rows pos[t, j] of a [rows * top_k, cols]
- *               output, whose rows from offsets[experts] on are zeros.
+ *               output (one panel), whose rows from offsets[experts] on are
+ *               zeros.
  *               offsets_dev, top_k and experts belong to pos_dev.
  * codes_dev must be 16-byte, scales_dev 4-byte aligned.
  */

@@ -109,68 +109,85 @@ __device__ __forceinline__ void load8(const void* x, int64_t row0, int64_t c, in
   }
 }
 
+// A row takes blockDim.y warps, 256 values each per step; blockDim.z rows a CTA.
 template <int DT, bool VEC, bool ACT>
-__global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx4QuantArgs a, int64_t nseg) {
-  const int64_t wid = blockIdx.x * (int64_t)kQuantWarps + (threadIdx.x >> 5);
-  const int64_t nb = (a.cols + 31) / 32, nq = (nb + 3) / 4, pitch = nb * 16;
-  const int64_t row = wid / nseg;
+__global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx4QuantArgs a) {
+  const int64_t row = blockIdx.x * (int64_t)blockDim.z + threadIdx.z;
   if (row >= a.rows) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t c = (wid - row * nseg) * kQuantSeg + lane * 8;   // a multiple of 8; four lanes a block
-  const bool in = c < nb * 32;
-  float v[8];
+  const int lane = threadIdx.x;
+  const int nb = (int)((a.cols + 31) / 32), nq = (nb + 3) / 4;
+  const int64_t pitch = (int64_t)nb * 16;
   const int64_t row0 = row * a.ld_x;
   const int64_t hi = (a.rows - 1) * a.ld_x + (ACT ? 2 : 1) * a.cols;   // elements of x
-  load8<DT, VEC>(a.x, row0, c, a.cols, hi, v);
-  if (ACT) {
-    float u[8];
-    load8<DT, VEC>(a.x, row0 + a.cols, c, a.cols, hi, u);
+  // the scale words of output row p start at its panel, 4 * panel bytes apart
+  uint8_t* scales0 = nullptr;
+  if (!a.pos) scales0 = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
+  const int64_t used = a.pos ? max(a.offsets[a.E], 0) : 0;
+  for (int64_t seg = threadIdx.y; seg * kQuantSeg < a.cols; seg += blockDim.y) {
+    const int64_t c = seg * kQuantSeg + lane * 8;   // four lanes a block
+    const bool in = c < (int64_t)nb * 32;
+    float v[8];
+    load8<DT, VEC>(a.x, row0, c, a.cols, hi, v);
+    if (ACT) {
+      float u[8];
+      load8<DT, VEC>(a.x, row0 + a.cols, c, a.cols, hi, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < a.cols ? glu(a.act, v[i], u[i]) : 0.f;
-  }
-  // the largest magnitude of the block, as its bits (they order like the
-  // values, NaN above infinity above every number)
-  uint32_t m = 0u;
+      for (int i = 0; i < 8; ++i) v[i] = c + i < a.cols ? glu(a.act, v[i], u[i]) : 0.f;
+    }
+    // the largest magnitude of the block, as its bits (they order like the
+    // values, NaN above infinity above every number)
+    uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const bool bad = m >= 0x7f800000u;
-  const int e = max((int)(m >> 23) - 2, 0);                       // biased exponent of the scale
-  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);   // 2^(127 - e): e <= 252
-  uint32_t code = 0u;
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const bool bad = m >= 0x7f800000u;
+    const int e = max((int)(m >> 23) - 2, 0);                       // biased exponent of the scale
+    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);   // 2^(127 - e): e <= 252
+    uint32_t code = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) code |= e2m1_pair(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
-  uint32_t sc = in ? (bad ? 255u : (uint32_t)e) : 0u;
-  if (bad) code = 0u;
-  // four blocks' scale bytes in one word, held by the first lane of each 16
-  sc |= __shfl_down_sync(0xffffffffu, sc, 4) << 8;
-  sc |= __shfl_down_sync(0xffffffffu, sc, 8) << 16;
-  const int64_t q = c >> 7;
-  const bool has_scale = (lane & 15) == 0 && q < nq;
-  auto put = [&](int64_t p, uint32_t codes, uint32_t scales) {
-    if (in) *reinterpret_cast<uint32_t*>(a.codes + (size_t)p * pitch + (c >> 1)) = codes;
-    if (has_scale) *reinterpret_cast<uint32_t*>(a.scales + mx4_scale_offset(p, q, a.panel, nq)) = scales;
-  };
-  if (!a.pos) {
-    put(row, code, sc);
-    return;
+    for (int i = 0; i < 4; ++i) code |= e2m1_pair(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+    uint32_t sc = in ? (bad ? 255u : (uint32_t)e) : 0u;
+    if (bad) code = 0u;
+    // four blocks' scale bytes in one word, held by the first lane of each 16
+    sc |= __shfl_down_sync(0xffffffffu, sc, 4) << 8;
+    sc |= __shfl_down_sync(0xffffffffu, sc, 8) << 16;
+    const int64_t q = c >> 7;
+    const bool has_scale = (lane & 15) == 0 && q < nq;
+    if (!a.pos) {
+      if (in) *reinterpret_cast<uint32_t*>(a.codes + (size_t)(row * pitch + (c >> 1))) = code;
+      if (has_scale) *reinterpret_cast<uint32_t*>(scales0 + (size_t)q * a.panel * 4) = sc;
+    } else {   // one panel of rows * k rows
+      uint8_t* codes = a.codes + (c >> 1);
+      uint8_t* scales = a.scales + (size_t)q * a.panel * 4;
+      for (int j = 0; j < a.k; ++j) {
+        const int64_t p = a.pos[row * a.k + j];
+        if (p < 0 || p >= a.panel) continue;
+        if (in) *reinterpret_cast<uint32_t*>(codes + (size_t)(p * pitch)) = code;
+        if (has_scale) *reinterpret_cast<uint32_t*>(scales + (size_t)p * 4) = sc;
+      }
+      for (int64_t p = used + row; p < a.panel; p += a.rows) {   // rows without a route
+        if (in) *reinterpret_cast<uint32_t*>(codes + (size_t)(p * pitch)) = 0u;
+        if (has_scale) *reinterpret_cast<uint32_t*>(scales + (size_t)p * 4) = 0u;
+      }
+    }
   }
-  for (int j = 0; j < a.k; ++j) {
-    const int p = a.pos[row * a.k + j];
-    if (p >= 0 && p < a.rows * a.k) put(p, code, sc);
-  }
-  for (int64_t p = max(a.offsets[a.E], 0) + row; p < a.rows * a.k; p += a.rows) put(p, 0u, 0u);   // rows without a route
+}
+
+// Warps of a row (the fewest steps eight warps allow) and rows of a CTA.
+static dim3 mx4_block(int64_t segs) {
+  const int64_t steps = (segs + kQuantWarps - 1) / kQuantWarps, warps = (segs + steps - 1) / steps;
+  return dim3(32, (unsigned)warps, (unsigned)(kQuantWarps / warps));
 }
 
 cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s) {
-  const int64_t nseg = (a.cols + kQuantSeg - 1) / kQuantSeg;
-  const int64_t blocks = (a.rows * nseg + kQuantWarps - 1) / kQuantWarps;
+  const dim3 block = mx4_block((a.cols + kQuantSeg - 1) / kQuantSeg);
+  const int64_t blocks = (a.rows + block.z - 1) / block.z;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const bool act = a.act.act >= 0;
   const bool vec = rows_aligned16(a.x, a.ld_x, a.dtype) && (!act || a.cols * dtype_size(a.dtype) % 16 == 0);
   auto run = [&](auto kern) {
-    kern<<<(unsigned)blocks, 32 * kQuantWarps, 0, s>>>(a, nseg);
+    kern<<<(unsigned)blocks, block, 0, s>>>(a);
     return cudaGetLastError();
   };
   auto pick = [&](auto dt) {
@@ -188,50 +205,49 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s) {
 // lanes start m elements early, so a lane's values come from two words of
 // codes and may belong to two blocks.
 template <int DT>
-__global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const Mx4DequantArgs a, int64_t nseg) {
+__global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const Mx4DequantArgs a) {
   using T = typename ElemT<DT>::t;
-  const int64_t wid = blockIdx.x * (int64_t)kQuantWarps + (threadIdx.x >> 5);
-  const int64_t nb = (a.cols + 31) / 32, nq = (nb + 3) / 4, pitch = nb * 16;
-  const int64_t row = wid / nseg;
+  const int64_t row = blockIdx.x * (int64_t)blockDim.z + threadIdx.z;
   if (row >= a.rows) return;
+  const int64_t nb = (a.cols + 31) / 32, nq = (nb + 3) / 4, pitch = nb * 16;
   const size_t row0 = (size_t)(row * a.ld_out);
   const int m = (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + row0) & 15) / sizeof(T));
-  const int64_t g = (wid - row * nseg) * kQuantSeg + (threadIdx.x & 31) * 8;   // on the codes' grid
-  const int64_t c = g - m;
-  if (c >= a.cols) return;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(a.codes + (size_t)row * pitch);
-  const uint32_t hi = g < nb * 32 ? words[g >> 3] : 0u, lo = m && g > 0 ? words[(g >> 3) - 1] : 0u;
-  const uint32_t code = m ? __funnelshift_r(lo, hi, 32 - 4 * m) : hi;
   const uint8_t* sc = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
   auto scale_of = [&](int64_t x) {   // of the block of element x; 2^(e - 127), e = 0 is subnormal, 255 is NaN
     const int64_t blk = min(max(x, (int64_t)0), a.cols - 1) >> 5;
     const uint32_t e = sc[(size_t)(blk >> 2) * a.panel * 4 + (blk & 3)];
     return __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
   };
-  const float s0 = scale_of(c), s1 = m ? scale_of(c + 7) : s0;
-  const int change = m ? (int)((32 - (c & 31)) & 31) : 0;   // first element of the second block, if it is within 8
-  float v[8];
+  for (int64_t g = ((int64_t)threadIdx.y * 32 + threadIdx.x) * 8; g - m < a.cols; g += (int64_t)blockDim.y * kQuantSeg) {
+    const int64_t c = g - m;   // g is on the codes' grid
+    const uint32_t hi = g < nb * 32 ? words[g >> 3] : 0u, lo = m && g > 0 ? words[(g >> 3) - 1] : 0u;
+    const uint32_t code = m ? __funnelshift_r(lo, hi, 32 - 4 * m) : hi;
+    const float s0 = scale_of(c), s1 = m ? scale_of(c + 7) : s0;
+    const int change = m ? (int)((32 - (c & 31)) & 31) : 0;   // first element of the second block, if it is within 8
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = e2m1_values((code >> (8 * i)) & 0xffu);
-    v[2 * i] = f.x * (change && 2 * i >= change ? s1 : s0);
-    v[2 * i + 1] = f.y * (change && 2 * i + 1 >= change ? s1 : s0);
-  }
-  if (c >= 0 && c + 8 <= a.cols) {
-    store_vec<DT, 8>(a.out, row0 + c, v);
-  } else {
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = e2m1_values((code >> (8 * i)) & 0xffu);
+      v[2 * i] = f.x * (change && 2 * i >= change ? s1 : s0);
+      v[2 * i + 1] = f.y * (change && 2 * i + 1 >= change ? s1 : s0);
+    }
+    if (c >= 0 && c + 8 <= a.cols) {
+      store_vec<DT, 8>(a.out, row0 + c, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i >= 0 && c + i < a.cols) store_d<DT>(a.out, row0 + c + i, v[i]);
+      for (int i = 0; i < 8; ++i)
+        if (c + i >= 0 && c + i < a.cols) store_d<DT>(a.out, row0 + c + i, v[i]);
+    }
   }
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, cudaStream_t s) {
-  const int64_t nseg = (a.cols + 7 + kQuantSeg - 1) / kQuantSeg;   // up to 7 elements early
-  const int64_t blocks = (a.rows * nseg + kQuantWarps - 1) / kQuantWarps;
+  const dim3 block = mx4_block((a.cols + 7 + kQuantSeg - 1) / kQuantSeg);   // up to 7 elements early
+  const int64_t blocks = (a.rows + block.z - 1) / block.z;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto run = [&](auto kern) {
-    kern<<<(unsigned)blocks, 32 * kQuantWarps, 0, s>>>(a, nseg);
+    kern<<<(unsigned)blocks, block, 0, s>>>(a);
     return cudaGetLastError();
   };
   if (a.dtype == QMOE_F32) return run(mx4_dequantize_kernel<QMOE_F32>);

@@ -7,10 +7,10 @@
 //   rh = r * rstd_pre,  rstd_pre = 1 / sqrt(mean(r^2) + eps)
 //   h  = rh * w_pre
 //
-// Memory-bound: a row stays in its threads' registers between the two sums,
-// so x and o are read once and r and h written once.  The two sums of a row
-// follow one another, so what decides is how many rows are on their way
-// meanwhile: CTAs stay and walk the rows, a ring of rows ahead of themselves.
+// Memory-bound: a row stays with its threads between the two sums, so x and o
+// are read once and r and h written once.  The two sums of a row follow one
+// another, so what decides is how many rows are on their way meanwhile: CTAs
+// stay and walk the rows, a ring of rows ahead of themselves.
 #include "qmoe_norm.cuh"
 
 namespace qmoe {
@@ -22,133 +22,138 @@ constexpr int norm_ahead(int vpt) { return vpt <= 2 ? 3 : vpt == 4 ? 2 : 0; }
 template <int DT, bool VECTOR, int VPT>
 __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   using F = Frag<DT, VECTOR>;
-  constexpr int N = F::n, kNormAhead = norm_ahead(VPT);
-  constexpr bool RING = VECTOR && kNormAhead > 0;
+  using T = typename ElemT<DT>::t;
+  constexpr int N2 = F::n / 2, AHEAD = norm_ahead(VPT);
+  constexpr bool RING = VECTOR && AHEAD > 0;
   __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
   const float inv_h = 1.f / (float)a.H;
-  const bool full = a.gate_kind == QMOE_GATE_FULL;
-  const int parts = 1 + (a.o ? 1 : 0) + (full ? 1 : 0);
+  const bool full = a.gate_kind == QMOE_GATE_FULL, branch = a.o != nullptr;
   const int64_t stride = gridDim.x * (int64_t)blockDim.y;
-  int turn = 0;
-  // slot of vector p of part q (x, o, gate) in ring row s
-  auto slot = [&](int s, int q, int p) { return norm_ring + (((size_t)s * parts + q) * VPT + p) * threads * 16 + tid * 16; };
-  auto fetch = [&](int64_t t, int s) {
+  int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+  int turn = 0, parts = 0;
+  const uint32_t ring = smem_u32(norm_ring);
+  Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts), o(a.o, a.ld_o, t, stride, ring, parts),
+      g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts);
+  const uint32_t row_bytes = (uint32_t)parts * VPT * blockDim.x * blockDim.y * 16;
+  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, a.H),
+      pre(a.w_pre, nullptr, a.H);
+  T* out_r = static_cast<T*>(a.r) + (a.r ? t * a.H : 0);
+  T* out_h = static_cast<T*>(a.h) + (a.h ? t * a.H : 0);
+  int64_t ahead = t;   // the row fetched next
+  auto fetch = [&](uint32_t at) {
     if constexpr (RING) {
-      if (t < a.T) {
-        using T = typename ElemT<DT>::t;
-#pragma unroll
-        for (int p = 0; p < VPT; ++p) {
-          const int64_t c = norm_column<DT, VECTOR>(p);
-          if (c < a.H) {
-            cp_async16(slot(s, 0, p), static_cast<const T*>(a.x) + t * a.ld_x + c);
-            if (a.o) cp_async16(slot(s, 1, p), static_cast<const T*>(a.o) + t * a.ld_o + c);
-            if (full) cp_async16(slot(s, 2, p), static_cast<const T*>(a.gate) + t * a.ld_gate + c);
-          }
-        }
+      if (ahead < a.T) {
+        x.fetch(at, a.H);
+        o.fetch(at, a.H);
+        g.fetch(at, a.H);
       }
+      x.advance();
+      o.advance();
+      g.advance();
+      ahead += stride;
       cp_async_commit();
     }
   };
-  auto part = [&](int s, int q, int p, const void* base, size_t row, int64_t c, float (&v)[N]) {
-    F f;
-    if constexpr (RING) f.u = *reinterpret_cast<const uint4*>(slot(s, q, p));
-    else f.load(base, row, c, a.H, blockDim.x);
-    f.get(v);
-  };
-
-  const int64_t first = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
 #pragma unroll
-  for (int s = 0; s + 1 < kNormAhead; ++s) fetch(first + s * stride, s);
-  int s = 0;
+  for (int s = 0; s + 1 < AHEAD; ++s) fetch(s * row_bytes);
+  const uint32_t last = (RING ? AHEAD - 1 : 0) * row_bytes;
+  uint32_t at = 0, to = last;
   // the rows of a block advance together (their sums share barriers)
-  for (int64_t t = first; t - threadIdx.y < a.T; t += stride) {
+  for (; t - threadIdx.y < a.T; t += stride, out_r += stride * a.H, out_h += stride * a.H) {
     const bool live = t < a.T;
-    fetch(t + (kNormAhead - 1) * stride, s == 0 ? kNormAhead - 1 : s - 1);
-    if constexpr (RING) cp_async_wait<kNormAhead - 1>();
-    float r[VPT][N], n[VPT][N];
-    float ss[1] = {0.f};
-#pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      const int64_t c = norm_column<DT, VECTOR>(p);
-      if (live && c < a.H) {
-        part(s, 0, p, a.x, (size_t)(t * a.ld_x), c, r[p]);
-        if (a.o) {
-          part(s, 1, p, a.o, (size_t)(t * a.ld_o), c, n[p]);
-#pragma unroll
-          for (int i = 0; i < N; ++i) ss[0] = fmaf(n[p][i], n[p][i], ss[0]);
-        }
-      }
+    if constexpr (RING) {
+      fetch(to);
+      cp_async_wait<AHEAD - 1>();
     }
     float rstd1 = 1.f;
-    if (a.o && a.w_post) {
-      row_sum<1>(ss, red, turn);
-      rstd1 = rsqrtf(ss[0] * inv_h + a.eps);
+    if (branch && a.w_post) {
+      float2 ss = both(0.f);
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+        const int64_t c = norm_column<DT, VECTOR>(p);
+        if (live && c < a.H) {
+          float2 v[N2];
+          o.get(at, p, c, a.H, v);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) ss = fma2(v[i], v[i], ss);
+        }
+      }
+      rstd1 = rsqrtf(row_sum(ss.x + ss.y, red, turn) * inv_h + a.eps);
     }
     const float token = live && a.gate_kind == QMOE_GATE_TOKEN ? load_d<DT>(a.gate, (size_t)t) : 1.f;
-    ss[0] = 0.f;
+    const float2 c1 = both(rstd1 * token), scale = both(a.residual_scale);
+    float2 r[VPT][N2], ss = both(0.f);
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
       const int64_t c = norm_column<DT, VECTOR>(p);
       if (live && c < a.H) {
-        if (a.o) {
-          float w[N], g[N];
-          load_columns<DT, VECTOR>(a.w_post, c, a.H, w);
-          if (full) {
-            part(s, 2, p, a.gate, (size_t)(t * a.ld_gate), c, g);
-          } else if (a.gate_kind == QMOE_GATE_CHANNEL) {
-            load_columns<DT, VECTOR>(a.gate, c, a.H, g);
-          } else {
+        x.get(at, p, c, a.H, r[p]);
 #pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = token;
+        for (int i = 0; i < N2; ++i) r[p][i] = mul2(r[p][i], scale);
+        if (branch) {
+          float2 v[N2], w[N2];
+          o.get(at, p, c, a.H, v);
+          post.get(p, c, w);
+          if (full) {
+            float2 q[N2];
+            g.get(at, p, c, a.H, q);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], q[i]);
           }
 #pragma unroll
-          for (int i = 0; i < N; ++i) r[p][i] = fmaf(g[i], n[p][i] * rstd1 * w[i], a.residual_scale * r[p][i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) r[p][i] *= a.residual_scale;
+          for (int i = 0; i < N2; ++i) r[p][i] = fma2(mul2(v[i], c1), w[i], r[p][i]);
         }
+        F f;
+        set2(f, r[p]);
+        if (a.r) f.store(out_r, 0, c, a.H, blockDim.x);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (VECTOR || c + (int64_t)i * blockDim.x < a.H) ss[0] = fmaf(r[p][i], r[p][i], ss[0]);
-        if (a.r) {
-          F f;
-          f.set(r[p]);
-          f.store(a.r, (size_t)(t * a.H), c, a.H, blockDim.x);
+        for (int i = 0; i < N2; ++i) {
+          if constexpr (!VECTOR) {   // past the row's end
+            if (c + (int64_t)(2 * i) * blockDim.x >= a.H) r[p][i].x = 0.f;
+            if (c + (int64_t)(2 * i + 1) * blockDim.x >= a.H) r[p][i].y = 0.f;
+          }
+          ss = fma2(r[p][i], r[p][i], ss);
         }
       }
     }
     if (a.rstd_post && live && threadIdx.x == 0) a.rstd_post[t] = rstd1;
     if (a.w_pre) {
-      row_sum<1>(ss, red, turn);
-      const float rstd2 = rsqrtf(ss[0] * inv_h + a.eps);
+      const float rstd2 = rsqrtf(row_sum(ss.x + ss.y, red, turn) * inv_h + a.eps);
       if (a.rstd_pre && live && threadIdx.x == 0) a.rstd_pre[t] = rstd2;
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
         const int64_t c = norm_column<DT, VECTOR>(p);
         if (live && c < a.H) {
-          float w[N];
-          load_columns<DT, VECTOR>(a.w_pre, c, a.H, w);
+          float2 w[N2];
+          pre.get(p, c, w);
 #pragma unroll
-          for (int i = 0; i < N; ++i) w[i] *= r[p][i] * rstd2;
+          for (int i = 0; i < N2; ++i) w[i] = mul2(mul2(r[p][i], both(rstd2)), w[i]);
           F f;
-          f.set(w);
-          f.store(a.h, (size_t)(t * a.H), c, a.H, blockDim.x);
+          set2(f, w);
+          f.store(out_h, 0, c, a.H, blockDim.x);
         }
       }
     }
-    if (++s == kNormAhead) s = 0;
+    if constexpr (RING) {
+      to = at;   // this row's place is the next to be filled
+      at = at == last ? 0 : at + row_bytes;
+    } else {
+      x.advance();
+      o.advance();
+      g.advance();
+    }
   }
   if constexpr (RING) cp_async_wait<0>();
 }
 
+// Threads of a row at most.
+constexpr int kNormThreads = 256;
+
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
   const bool vec = norm_vec(a);
   const int frag = norm_frag(a.dtype, vec);
-  // two fragments a thread up to 512 threads: enough rows at once, and few
-  // enough registers for two CTAs a multiprocessor
-  const RowShape g = row_shape(a.H, frag, a.H > 2 * 256 * frag ? 512 : 256);
+  const RowShape g = row_shape(a.H, frag, a.H > 2 * kNormThreads * frag ? 512 : kNormThreads);
   const int vpt = norm_vpt(a.H, frag, g.tpr);
   const int parts = 1 + (a.o ? 1 : 0) + (a.gate_kind == QMOE_GATE_FULL ? 1 : 0);
   const int threads = g.tpr * g.rpb;

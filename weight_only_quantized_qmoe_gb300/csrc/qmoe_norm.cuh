@@ -1,6 +1,6 @@
 // What the forward and the backward of the block norms share (qmoe_norm.cu,
-// qmoe_norm_grad.cu): the sums of a row, the ring of rows on their way, and
-// the choice of a kernel by type, alignment and row length.
+// qmoe_norm_grad.cu): the sum of a row, the rows on their way, the vectors over
+// the columns, and the choice of a kernel by type, alignment and row length.
 #pragma once
 
 #include <algorithm>
@@ -13,66 +13,172 @@ namespace qmoe {
 // are counted in them.
 constexpr int kNormSms = 152;
 
-// Sums of v over the threads of a row (blockDim.x of them: 8, 16 or whole
-// warps; every thread of the block calls it).  `red` holds 2 x 16 x N floats
-// and `turn` alternates between its halves: a half is written again only after
-// the barrier of the sum in between, which its readers have passed.
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& turn) {
+// Two fp32 values in one instruction.  The norms issue some thirty
+// instructions a value even so, close to what a multiprocessor can issue in the
+// time the value's bytes take.
+__device__ __forceinline__ uint64_t bits2(float2 a) { return *reinterpret_cast<uint64_t*>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// The pairs of a fragment.
+template <int DT, bool VECTOR>
+__device__ __forceinline__ void get2(const Frag<DT, VECTOR>& f, float2 (&v)[Frag<DT, VECTOR>::n / 2]) {
+  constexpr int N = Frag<DT, VECTOR>::n;
+  float e[N];
+  f.get(e);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[i] = make_float2(e[2 * i], e[2 * i + 1]);
+}
+template <int DT, bool VECTOR>
+__device__ __forceinline__ void set2(Frag<DT, VECTOR>& f, const float2 (&v)[Frag<DT, VECTOR>::n / 2]) {
+  constexpr int N = Frag<DT, VECTOR>::n;
+  float e[N];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    e[2 * i] = v[i].x;
+    e[2 * i + 1] = v[i].y;
+  }
+  f.set(e);
+}
+
+// Sum of v over the threads of a row (blockDim.x of them: 8, 16 or whole
+// warps; every thread of the block calls it).  `red` holds 2 x 16 floats and
+// `turn` alternates between its halves: a half is written again only after the
+// barrier of the sum in between, which its readers have passed.
+__device__ __forceinline__ float row_sum(float v, float* red, int& turn) {
   const int width = min((int)blockDim.x, 32);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    for (int o = width >> 1; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (blockDim.x <= 32) return;
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5;
-  const int nw = blockDim.x >> 5, w0 = threadIdx.y * nw;
-  float* half = red + turn * 16 * N;
+  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (blockDim.x <= 32) return v;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nw = blockDim.x >> 5, w0 = threadIdx.y * nw;   // at most 16 warps
+  float* half = red + turn * 16;
   turn ^= 1;
-  if ((tid & 31) == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) half[i * 16 + warp] = v[i];
-  }
+  if (lane == 0) half[warp] = v;
   __syncthreads();
+  v = lane < nw ? half[w0 + lane] : 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = 0.f;
-    for (int q = 0; q < nw; ++q) s += half[i * 16 + w0 + q];
-    v[i] = s;
-  }
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Rows on their way from memory.  With 16-byte rows a thread copies its own
-// vectors of the next rows into shared memory (cp.async) while it works on
-// this one; nobody else reads them, so there is no barrier to wait at.
-// Otherwise rows are loaded when they are used.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Column of a thread's vector p, and whether the row has it.
+// Column of a thread's fragment p.
 template <int DT, bool VECTOR>
 __device__ __forceinline__ int64_t norm_column(int p) {
   using F = Frag<DT, VECTOR>;
   return F::first(threadIdx.x) + p * F::step(blockDim.x);
 }
 
-// The weights or the channel gate of a thread's columns, or ones.
-template <int DT, bool VECTOR>
-__device__ __forceinline__ void load_columns(const void* p, int64_t c, int64_t H, float (&v)[Frag<DT, VECTOR>::n]) {
-  if (p) {
-    Frag<DT, VECTOR> f;
-    f.load(p, 0, c, H, blockDim.x);
-    f.get(v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < Frag<DT, VECTOR>::n; ++i) v[i] = 1.f;
+// The rows of one tensor as a thread sees them: its fragments of row after row
+// of a CTA.  With 16-byte rows (RING) a thread copies its own fragments of the
+// next rows into shared memory (cp.async) while it works on this one; nobody
+// else reads them, so there is no barrier to wait at.  Otherwise they are
+// loaded when they are used.
+template <int DT, bool VECTOR, int VPT, bool RING>
+struct Rows {
+  using F = Frag<DT, VECTOR>;
+  using T = typename ElemT<DT>::t;
+  const T* next;      // RING: the row to be fetched next, else the row in work
+  int64_t step;       // elements from a CTA's row to its next
+  uint32_t ring;      // shared address of this thread's fragment 0 in ring row 0
+  bool there;
+
+  // `slot` counts the tensors that are there: their fragments lie side by side
+  // in a ring row.
+  __device__ __forceinline__ Rows(const void* base, int64_t ld, int64_t row, int64_t rows, uint32_t ring0, int& slot) {
+    there = base != nullptr;
+    next = static_cast<const T*>(base) + row * ld;
+    step = rows * ld;
+    ring = ring0 + (uint32_t)slot * VPT * blockDim.x * blockDim.y * 16 + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+    slot += there ? 1 : 0;
   }
+  __device__ __forceinline__ void fetch(uint32_t at, int64_t H) const {   // `at`: byte offset of the ring row
+    if (!there) return;
+#pragma unroll
+    for (int p = 0; p < VPT; ++p) {
+      const int64_t c = norm_column<DT, VECTOR>(p);
+      if (c < H)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + at + p * blockDim.x * blockDim.y * 16), "l"(next + c)
+                     : "memory");
+    }
+  }
+  __device__ __forceinline__ void advance() { next += step; }
+  __device__ __forceinline__ void get(uint32_t at, int p, int64_t c, int64_t H, float2 (&v)[F::n / 2]) const {
+    F f;
+    if constexpr (RING) {
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(f.u.x), "=r"(f.u.y), "=r"(f.u.z), "=r"(f.u.w)
+                   : "r"(ring + at + p * blockDim.x * blockDim.y * 16)
+                   : "memory");
+    } else {
+      f.load(next, 0, c, H, blockDim.x);
+    }
+    get2(f, v);
+  }
+};
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// A product of up to two vectors over the columns (weight, channel gate), ones
+// where there are none.  It is the same for every row: a thread's only
+// fragment stays in registers as fp32, two as they are in memory, more are
+// loaded again (loaded for every row they came from the L2, time after time:
+// the rings leave little of the L1).
+template <int DT, bool VECTOR, int VPT>
+struct Columns {
+  using F = Frag<DT, VECTOR>;
+  static constexpr int N2 = F::n / 2;
+  const void *a, *b;
+  int64_t H;
+  float2 held[VPT == 1 ? N2 : 1];
+  F fa[VPT == 2 ? 2 : 1], fb[VPT == 2 ? 2 : 1];
+  __device__ __forceinline__ void compute(const F& x, const F& y, float2 (&v)[N2]) const {
+#pragma unroll
+    for (int i = 0; i < N2; ++i) v[i] = both(1.f);
+    if (a) get2(x, v);
+    if (b) {
+      float2 w[N2];
+      get2(y, w);
+#pragma unroll
+      for (int i = 0; i < N2; ++i) v[i] = a ? mul2(v[i], w[i]) : w[i];
+    }
+  }
+  __device__ __forceinline__ Columns(const void* a_, const void* b_, int64_t H_) : a(a_), b(b_), H(H_) {
+    if constexpr (VPT <= 2) {
+#pragma unroll
+      for (int q = 0; q < VPT; ++q) {
+        const int64_t c = norm_column<DT, VECTOR>(q);
+        if (a && c < H) fa[q].load(a, 0, c, H, blockDim.x);
+        if (b && c < H) fb[q].load(b, 0, c, H, blockDim.x);
+      }
+      if constexpr (VPT == 1) compute(fa[0], fb[0], held);
+    }
+  }
+  __device__ __forceinline__ void get(int q, int64_t c, float2 (&v)[N2]) const {
+    if constexpr (VPT == 1) {
+#pragma unroll
+      for (int i = 0; i < N2; ++i) v[i] = held[i];
+    } else if constexpr (VPT == 2) {
+      compute(fa[q], fb[q], v);
+    } else {
+      F x, y;
+      if (a) x.load(a, 0, c, H, blockDim.x);
+      if (b) y.load(b, 0, c, H, blockDim.x);
+      compute(x, y, v);
+    }
+  }
+};
 
 inline bool norm_vec(const NormArgs& a) {
   const void* whole[] = {a.w_post, a.w_pre, a.r, a.h, a.dx, a.d_o};

@@ -1,16 +1,22 @@
 // The norms before and after a block: gradients.  With the forward's names
 // (qmoe_norm.cu) and the incoming gradients dr, dh:
 //
-//   dr' = dr + rstd_pre * (dh w_pre - rh * mean(dh w_pre rh)),  dw_pre = sum_t dh rh
-//   dx  = residual_scale * dr';  dn = dr' gate;  dgate = dr' n (summed to the gate's shape)
-//   dw_post = sum_t dn oh;  do = rstd_post * (dn w_post - oh * mean(dn w_post oh))
+//   d   = dr + rstd_pre * (dh w_pre - rh * mean(dh w_pre rh)),  dw_pre = sum_t dh rh
+//   dx  = residual_scale * d;  dgate = d n (summed to the gate's shape)
+//   dw_post = sum_t d gate oh;  do = rstd_post * (u - oh * mean(u oh)), u = d gate w_post
 //
-// Memory-bound like the forward.  r is rebuilt in 32 bits from x and o (which
-// are read anyway) instead of reading the rounded r.  The sums over the rows
-// stay in the registers of the thread that owns the column while a CTA walks
-// its rows, a ring of rows ahead of itself; the CTAs' sums go through a small
-// fp32 workspace and a second launch adds them in order: no atomics, the
-// same bits every run.
+// With a gate that is the same for a whole row or a whole column these share
+// their sums: a token's dgate is the row's sum of d w_post oh, gate times which
+// is the sum in do; and S = sum_t d oh (times the token gate) gives dw_post =
+// gate S and a channel's dgate = w_post S.
+//
+// Memory-bound like the forward, with nearly as many instructions as the bytes
+// leave time for.  r is rebuilt in 32 bits from x and o (which are read anyway)
+// instead of reading the rounded r.  The sums over the rows stay in the
+// registers of the thread that owns the column while a CTA walks its rows, a
+// ring of rows ahead of itself; the CTAs' sums go through a small fp32
+// workspace and a second launch adds them in order: no atomics, the same bits
+// every run.
 #include "qmoe_norm.cuh"
 
 namespace qmoe {
@@ -19,177 +25,192 @@ namespace qmoe {
 constexpr int norm_grad_ahead(int vpt) { return vpt == 1 ? 3 : vpt == 2 ? 2 : 0; }
 
 // Sums over rows a CTA keeps, in this order in its slice of the workspace.
-enum { SUM_PRE = 0, SUM_POST = 1, SUM_GATE = 2, SUM_KINDS = 3 };
+enum { SUM_PRE = 0, SUM_POST = 1, SUM_KINDS = 2 };
 
-// CHANNEL: a channel gate, whose gradient is a sum over the rows too.
-template <int DT, bool VECTOR, int VPT, bool CHANNEL>
+template <int DT, bool VECTOR, int VPT>
 __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) {
   using F = Frag<DT, VECTOR>;
-  constexpr int N = F::n, kNormGradAhead = norm_grad_ahead(VPT);
-  constexpr bool RING = VECTOR && kNormGradAhead > 0;
-  __shared__ float red[2 * 16 * 2];
+  using T = typename ElemT<DT>::t;
+  constexpr int N2 = F::n / 2, AHEAD = norm_grad_ahead(VPT);
+  constexpr bool RING = VECTOR && AHEAD > 0;
+  __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
-  const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
   const float inv_h = 1.f / (float)a.H;
-  const bool full = !CHANNEL && a.gate_kind == QMOE_GATE_FULL;
+  const bool full = a.gate_kind == QMOE_GATE_FULL, branch = a.o != nullptr, pre_norm = a.dh != nullptr;
   const int64_t stride = gridDim.x * (int64_t)blockDim.y;
-  int turn = 0;
-  // parts of a ring row: x, o, dr, dh, gate, as far as they are there
-  const int q_o = 1, q_r = q_o + (a.o ? 1 : 0), q_h = q_r + (a.dr ? 1 : 0), q_g = q_h + (a.dh ? 1 : 0);
-  const int parts = q_g + (full ? 1 : 0);
-  auto slot = [&](int s, int q, int p) { return norm_ring + (((size_t)s * parts + q) * VPT + p) * threads * 16 + tid * 16; };
-  auto fetch = [&](int64_t t, int s) {
+  int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+  int turn = 0, parts = 0;
+  const uint32_t ring = smem_u32(norm_ring);
+  Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts), o(a.o, a.ld_o, t, stride, ring, parts),
+      dr(a.dr, a.ld_dr, t, stride, ring, parts), dh(a.dh, a.ld_dh, t, stride, ring, parts),
+      g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts);
+  const uint32_t row_bytes = (uint32_t)parts * VPT * blockDim.x * blockDim.y * 16;
+  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, a.H),
+      pre(a.w_pre, nullptr, a.H);
+  const int64_t out_step = stride * a.H;
+  int64_t out = t * a.H;
+  int64_t ahead = t;
+  auto fetch = [&](uint32_t at) {
     if constexpr (RING) {
-      if (t < a.T) {
-        using T = typename ElemT<DT>::t;
-#pragma unroll
-        for (int p = 0; p < VPT; ++p) {
-          const int64_t c = norm_column<DT, VECTOR>(p);
-          if (c < a.H) {
-            cp_async16(slot(s, 0, p), static_cast<const T*>(a.x) + t * a.ld_x + c);
-            if (a.o) cp_async16(slot(s, q_o, p), static_cast<const T*>(a.o) + t * a.ld_o + c);
-            if (a.dr) cp_async16(slot(s, q_r, p), static_cast<const T*>(a.dr) + t * a.ld_dr + c);
-            if (a.dh) cp_async16(slot(s, q_h, p), static_cast<const T*>(a.dh) + t * a.ld_dh + c);
-            if (full) cp_async16(slot(s, q_g, p), static_cast<const T*>(a.gate) + t * a.ld_gate + c);
-          }
-        }
+      if (ahead < a.T) {
+        x.fetch(at, a.H);
+        o.fetch(at, a.H);
+        dr.fetch(at, a.H);
+        dh.fetch(at, a.H);
+        g.fetch(at, a.H);
       }
+      ahead += stride;
       cp_async_commit();
     }
-  };
-  auto part = [&](int s, int q, int p, const void* base, size_t row, int64_t c, float (&v)[N]) {
-    F f;
-    if constexpr (RING) f.u = *reinterpret_cast<const uint4*>(slot(s, q, p));
-    else f.load(base, row, c, a.H, blockDim.x);
-    f.get(v);
+    x.advance();
+    o.advance();
+    dr.advance();
+    dh.advance();
+    g.advance();
   };
 
-  float s_pre[VPT][N], s_post[VPT][N], s_gate[CHANNEL ? VPT : 1][N];
+  float2 s_pre[VPT][N2], s_post[VPT][N2];
 #pragma unroll
   for (int p = 0; p < VPT; ++p)
 #pragma unroll
-    for (int i = 0; i < N; ++i) s_pre[p][i] = s_post[p][i] = s_gate[CHANNEL ? p : 0][i] = 0.f;
+    for (int i = 0; i < N2; ++i) s_pre[p][i] = s_post[p][i] = both(0.f);
 
-  const int64_t first = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
+  if constexpr (RING) {
 #pragma unroll
-  for (int s = 0; s + 1 < kNormGradAhead; ++s) fetch(first + s * stride, s);
-  int s = 0;
-  for (int64_t t = first; t - threadIdx.y < a.T; t += stride) {
+    for (int s = 0; s + 1 < AHEAD; ++s) fetch(s * row_bytes);
+  }
+  const uint32_t last = (RING ? AHEAD - 1 : 0) * row_bytes;
+  uint32_t at = 0, to = last;
+  for (; t - threadIdx.y < a.T; t += stride, out += out_step) {
     const bool live = t < a.T;
-    fetch(t + (kNormGradAhead - 1) * stride, s == 0 ? kNormGradAhead - 1 : s - 1);
-    const float rstd1 = live && a.o && a.w_post ? a.rstd_post[t] : 1.f;
-    const float rstd2 = live && a.w_pre ? a.rstd_pre[t] : 0.f;
+    const float rstd1 = live && branch && a.w_post ? a.rstd_post[t] : 1.f;
+    const float rstd2 = live && pre_norm ? a.rstd_pre[t] : 1.f;
     const float token = live && a.gate_kind == QMOE_GATE_TOKEN ? load_d<DT>(a.gate, (size_t)t) : 1.f;
-    auto gate = [&](int p, int64_t c, float (&g)[N]) {
-      if (CHANNEL) {
-        load_columns<DT, VECTOR>(a.gate, c, a.H, g);
-      } else if (full) {
-        part(s, q_g, p, a.gate, (size_t)(t * a.ld_gate), c, g);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = token;
-      }
-    };
-    if constexpr (RING) cp_async_wait<kNormGradAhead - 1>();
-    float oh[VPT][N], rh[VPT][N], d2[VPT][N];
-    float sum[1] = {0.f};
-#pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      const int64_t c = norm_column<DT, VECTOR>(p);
-      if (live && c < a.H) {
-        part(s, 0, p, a.x, (size_t)(t * a.ld_x), c, rh[p]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) rh[p][i] *= a.residual_scale;
-        if (a.o) {
-          float w[N], g[N];
-          part(s, q_o, p, a.o, (size_t)(t * a.ld_o), c, oh[p]);
-          load_columns<DT, VECTOR>(a.w_post, c, a.H, w);
-          gate(p, c, g);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            oh[p][i] *= rstd1;
-            rh[p][i] = fmaf(g[i], oh[p][i] * w[i], rh[p][i]);
-          }
-        }
-        if (a.dh) {
-          float w[N];
-          part(s, q_h, p, a.dh, (size_t)(t * a.ld_dh), c, d2[p]);
-          load_columns<DT, VECTOR>(a.w_pre, c, a.H, w);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            rh[p][i] *= rstd2;
-            s_pre[p][i] = fmaf(d2[p][i], rh[p][i], s_pre[p][i]);
-            d2[p][i] *= w[i];
-            sum[0] = fmaf(d2[p][i], rh[p][i], sum[0]);
-          }
-        }
-      }
+    if constexpr (RING) {
+      fetch(to);
+      cp_async_wait<AHEAD - 1>();
     }
-    if (a.dh) row_sum<1>(sum, red, turn);
-    const float m2 = sum[0] * inv_h;
-    float sums[2] = {0.f, 0.f};   // of dn w_post oh, and of dr' n (the gate of a token)
+    // rh and dh * w_pre, and the first sum
+    float2 rh[VPT][N2], dn[VPT][N2], sum2 = both(0.f);
+    if (pre_norm) {
+      const float2 cx = both(a.residual_scale * rstd2), co = both(rstd1 * token * rstd2);
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+        const int64_t c = norm_column<DT, VECTOR>(p);
+        if (live && c < a.H) {
+          float2 v[N2], w[N2];
+          x.get(at, p, c, a.H, rh[p]);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) rh[p][i] = mul2(rh[p][i], cx);
+          if (branch) {
+            o.get(at, p, c, a.H, v);
+            post.get(p, c, w);
+            if (full) {
+              float2 q[N2];
+              g.get(at, p, c, a.H, q);
+#pragma unroll
+              for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], q[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < N2; ++i) rh[p][i] = fma2(mul2(v[i], co), w[i], rh[p][i]);
+          }
+          dh.get(at, p, c, a.H, v);
+          pre.get(p, c, w);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) {
+            s_pre[p][i] = fma2(v[i], rh[p][i], s_pre[p][i]);
+            dn[p][i] = mul2(v[i], w[i]);
+            sum2 = fma2(dn[p][i], rh[p][i], sum2);
+          }
+        }
+      }
+      sum2.x = row_sum(sum2.x + sum2.y, red, turn) * inv_h * -rstd2;
+    }
+    const float2 m2 = both(sum2.x), k2 = both(rstd2);
+    // d and what follows from it: dx, u = d gate w_post (into dn), the second sum
+    float2 sum1 = both(0.f);
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
       const int64_t c = norm_column<DT, VECTOR>(p);
       if (live && c < a.H) {
-        float d[N], out[N];
+        float2 d[N2], v[N2], w[N2];
         if (a.dr) {
-          part(s, q_r, p, a.dr, (size_t)(t * a.ld_dr), c, d);
+          dr.get(at, p, c, a.H, d);
         } else {
 #pragma unroll
-          for (int i = 0; i < N; ++i) d[i] = 0.f;
+          for (int i = 0; i < N2; ++i) d[i] = both(0.f);
         }
+        if (pre_norm) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (a.dh) d[i] += rstd2 * (d2[p][i] - rh[p][i] * m2);
-          out[i] = a.residual_scale * d[i];
+          for (int i = 0; i < N2; ++i) d[i] = fma2(rh[p][i], m2, fma2(dn[p][i], k2, d[i]));
         }
         F f;
         if (a.dx) {
-          f.set(out);
-          f.store(a.dx, (size_t)(t * a.H), c, a.H, blockDim.x);
-        }
-        if (a.o) {
-          float w[N], g[N], dg[N];
-          load_columns<DT, VECTOR>(a.w_post, c, a.H, w);
-          gate(p, c, g);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            // past the row's end every factor here is zero (o was loaded so)
-            dg[i] = d[i] * (oh[p][i] * w[i]);
-            const float dn = d[i] * g[i];
-            s_post[p][i] = fmaf(dn, oh[p][i], s_post[p][i]);
-            if (CHANNEL) s_gate[p][i] += dg[i];
-            sums[1] += dg[i];
-            d2[p][i] = dn * w[i];
-            sums[0] = fmaf(d2[p][i], oh[p][i], sums[0]);
+          for (int i = 0; i < N2; ++i) v[i] = mul2(d[i], both(a.residual_scale));
+          set2(f, v);
+          f.store(static_cast<T*>(a.dx) + out, 0, c, a.H, blockDim.x);
+        }
+        if (branch) {
+          const float2 c1 = both(rstd1 * token);
+          o.get(at, p, c, a.H, v);
+          post.get(p, c, w);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) dn[p][i] = mul2(d[i], w[i]);
+          if (full) {
+            float2 q[N2], e[N2];
+            g.get(at, p, c, a.H, q);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              e[i] = mul2(mul2(dn[p][i], v[i]), both(rstd1));
+              dn[p][i] = mul2(dn[p][i], q[i]);
+              d[i] = mul2(d[i], q[i]);
+            }
+            if (a.dgate) {
+              set2(f, e);
+              f.store(static_cast<T*>(a.dgate) + out, 0, c, a.H, blockDim.x);
+            }
           }
-          if (full && a.dgate) {
-            f.set(dg);
-            f.store(a.dgate, (size_t)(t * a.H), c, a.H, blockDim.x);
+#pragma unroll
+          for (int i = 0; i < N2; ++i) {
+            if constexpr (!VECTOR) {   // past the row's end (an infinite factor would make NaN of its zeros)
+              if (c + (int64_t)(2 * i) * blockDim.x >= a.H) dn[p][i].x = d[i].x = 0.f;
+              if (c + (int64_t)(2 * i + 1) * blockDim.x >= a.H) dn[p][i].y = d[i].y = 0.f;
+            }
+            s_post[p][i] = fma2(mul2(d[i], c1), v[i], s_post[p][i]);
+            sum1 = fma2(dn[p][i], v[i], sum1);
           }
         }
       }
     }
-    if (a.o) {
-      row_sum<2>(sums, red, turn);
-      if (a.gate_kind == QMOE_GATE_TOKEN && a.dgate && live && threadIdx.x == 0) store_d<DT>(a.dgate, (size_t)t, sums[1]);
-      const float m1 = a.w_post ? sums[0] * inv_h : 0.f;
+    if (branch) {
+      // without w_post the branch is not normalised: do = u
+      float s1 = 0.f;
+      if (a.w_post || a.gate_kind == QMOE_GATE_TOKEN) s1 = row_sum(sum1.x + sum1.y, red, turn) * rstd1;
+      if (a.gate_kind == QMOE_GATE_TOKEN && a.dgate && live && threadIdx.x == 0) store_d<DT>(a.dgate, (size_t)t, s1);
       if (a.d_o) {
+        const float2 cu = both(rstd1 * token), co = both(a.w_post ? -s1 * token * inv_h * rstd1 * rstd1 : 0.f);
 #pragma unroll
         for (int p = 0; p < VPT; ++p) {
           const int64_t c = norm_column<DT, VECTOR>(p);
           if (live && c < a.H) {
+            float2 v[N2];
+            o.get(at, p, c, a.H, v);
 #pragma unroll
-            for (int i = 0; i < N; ++i) d2[p][i] = rstd1 * (d2[p][i] - oh[p][i] * m1);
+            for (int i = 0; i < N2; ++i) v[i] = a.w_post ? fma2(v[i], co, mul2(dn[p][i], cu)) : mul2(dn[p][i], cu);
             F f;
-            f.set(d2[p]);
-            f.store(a.d_o, (size_t)(t * a.H), c, a.H, blockDim.x);
+            set2(f, v);
+            f.store(static_cast<T*>(a.d_o) + out, 0, c, a.H, blockDim.x);
           }
         }
       }
     }
-    if (++s == kNormGradAhead) s = 0;
+    if constexpr (RING) {
+      to = at;
+      at = at == last ? 0 : at + row_bytes;
+    } else {
+      fetch(0);   // only steps to the next row
+    }
   }
   if constexpr (RING) cp_async_wait<0>();
   // a slice of the workspace for each row of the block
@@ -198,25 +219,25 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   for (int p = 0; p < VPT; ++p) {
     const int64_t c = norm_column<DT, VECTOR>(p);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int64_t x = VECTOR ? c + i : c + (int64_t)i * blockDim.x;
-      if (x >= a.H) continue;
-      if (a.dw_pre) mine[SUM_PRE * a.H + x] = s_pre[p][i];
-      if (a.dw_post) mine[SUM_POST * a.H + x] = s_post[p][i];
-      if (CHANNEL && a.dgate) mine[SUM_GATE * a.H + x] = s_gate[CHANNEL ? p : 0][i];
+    for (int i = 0; i < 2 * N2; ++i) {
+      const int64_t col = VECTOR ? c + i : c + (int64_t)i * blockDim.x;
+      if (col >= a.H) continue;
+      if (a.dw_pre) mine[SUM_PRE * a.H + col] = i & 1 ? s_pre[p][i / 2].y : s_pre[p][i / 2].x;
+      if (branch) mine[SUM_POST * a.H + col] = i & 1 ? s_post[p][i / 2].y : s_post[p][i / 2].x;
     }
   }
 }
 
 // Adds the slices of the workspace: 32 columns a CTA, its 16 rows of threads
-// take every 16th slice, then their sums in order.
+// take every 16th slice, then their sums in order.  SUM_POST gives both dw_post
+// and a channel gate's gradient.
 constexpr int kSumRows = 16;
 template <int DT>
 __global__ void __launch_bounds__(32 * kSumRows) block_norm_sums_kernel(const NormArgs a, int slices) {
   __shared__ float part[kSumRows][33];
   const int kind = blockIdx.y;
-  void* dst = kind == SUM_PRE ? a.dw_pre : kind == SUM_POST ? a.dw_post : (a.gate_kind == QMOE_GATE_CHANNEL ? a.dgate : nullptr);
-  if (!dst) return;
+  const bool channel = a.gate_kind == QMOE_GATE_CHANNEL;
+  if (kind == SUM_PRE ? !a.dw_pre : !a.dw_post && !(channel && a.dgate)) return;
   const int64_t c = blockIdx.x * (int64_t)32 + threadIdx.x;
   float s = 0.f;
   if (c < a.H) {
@@ -226,11 +247,15 @@ __global__ void __launch_bounds__(32 * kSumRows) block_norm_sums_kernel(const No
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && c < a.H) {
+  if (threadIdx.y != 0 || c >= a.H) return;
 #pragma unroll
-    for (int q = 1; q < kSumRows; ++q) s += part[q][threadIdx.x];
-    store_d<DT>(dst, (size_t)c, s);
+  for (int q = 1; q < kSumRows; ++q) s += part[q][threadIdx.x];
+  if (kind == SUM_PRE) {
+    store_d<DT>(a.dw_pre, (size_t)c, s);
+    return;
   }
+  if (a.dw_post) store_d<DT>(a.dw_post, (size_t)c, channel ? s * load_d<DT>(a.gate, (size_t)c) : s);
+  if (channel && a.dgate) store_d<DT>(a.dgate, (size_t)c, a.w_post ? s * load_d<DT>(a.w_post, (size_t)c) : s);
 }
 
 namespace {
@@ -263,16 +288,13 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
   const int64_t ctas = norm_grad_ctas(a.T, g);
   if (ctas > 0) {   // without rows the sums are zeros
     const cudaError_t e = by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
-      auto run = [&](auto kern) {
-        if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
-          const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
-          if (err != cudaSuccess) return err;
-        }
-        kern<<<(unsigned)ctas, dim3(g.tpr, g.rpb), ring, s>>>(a);
-        return cudaGetLastError();
-      };
-      return a.gate_kind == QMOE_GATE_CHANNEL ? run(block_norm_grad_kernel<dt, v, n, true>)
-                                              : run(block_norm_grad_kernel<dt, v, n, false>);
+      auto kern = block_norm_grad_kernel<dt, v, n>;
+      if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+        if (err != cudaSuccess) return err;
+      }
+      kern<<<(unsigned)ctas, dim3(g.tpr, g.rpb), ring, s>>>(a);
+      return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
   }

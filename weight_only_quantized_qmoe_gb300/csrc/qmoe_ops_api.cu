@@ -208,6 +208,8 @@ qmoe_status qmoe_mx4_quantize(const void* x_dev, int64_t ld_x, int64_t rows, int
     OP_TRY(check_routes(rows, top_k, experts));
     OP_CHECK(offsets_dev, "offsets is null beside pos");
     out_rows = rows * top_k;
+    OP_CHECK(panel_rows == out_rows, "panel_rows %lld: with pos the output is one panel of %lld rows", (long long)panel_rows,
+             (long long)out_rows);
   }
   OP_CHECK(panel_rows >= 1 || out_rows == 0, "panel_rows %lld is not positive", (long long)panel_rows);
   OP_CHECK(out_rows == 0 || out_rows % panel_rows == 0, "panel_rows %lld does not divide the %lld rows",

@@ -180,6 +180,14 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
 // in flight together: with eight rows unpacked to 32 bits ahead of their use
 // a thread took 128 registers and the sum ran at a quarter of the bandwidth.
 
+// Threads of a row at most, and CTAs a multiprocessor the registers are cut
+// for: many short CTAs, whose loads, sums and stores fall at different times
+// (gradient of 6001 x 4 rows of 2880: 56 us with 128 threads and 8 CTAs, 60
+// with 256 and 4, 91 with 256 and 2; eight slots need 85 registers, 4096 x 8
+// rows of 4096: 95 us with 6 CTAs, 107 with 8).
+constexpr int kRowThreads = 128;
+constexpr int row_ctas(int slots) { return slots == 8 ? 6 : 8; }
+
 // The row of a slot, -1 where it has none.
 __device__ __forceinline__ int slot_row(const RowsArgs& a, int p) { return p < a.T * a.k ? p : -1; }
 
@@ -200,7 +208,7 @@ __device__ __forceinline__ void zero_unused_rows(const RowsArgs& a, int64_t t) {
 }
 
 template <int DT, bool VECTOR>
-__global__ void __launch_bounds__(512) dispatch_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowsArgs a) {
   using F = Frag<DT, VECTOR>;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   if (t >= a.T) return;
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(512) dispatch_kernel(const RowsArgs a) {
 }
 
 template <int DT, bool VECTOR, int SLOTS>
-__global__ void __launch_bounds__(512) combine_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_kernel(const RowsArgs a) {
   using F = Frag<DT, VECTOR>;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   if (t >= a.T) return;
@@ -275,9 +283,9 @@ __device__ __forceinline__ int warp_sums(float (&v)[N]) {
 }
 
 template <int DT, bool VECTOR, int SLOTS>
-__global__ void __launch_bounds__(512) combine_grad_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_grad_kernel(const RowsArgs a) {
   using F = Frag<DT, VECTOR>;
-  __shared__ float part[16][SLOTS];
+  __shared__ float part[kRowThreads / 32][SLOTS];
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   const bool live = t < a.T;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -366,7 +374,7 @@ static cudaError_t by_rows(const RowsArgs& a, F&& f) {
 }
 template <int DT, bool VECTOR>
 static RowShape rows_of(const RowsArgs& a, dim3* grid) {
-  const RowShape r = row_shape(a.H, Frag<DT, VECTOR>::n);
+  const RowShape r = row_shape(a.H, Frag<DT, VECTOR>::n, kRowThreads);
   *grid = dim3((unsigned)((a.T + r.rpb - 1) / r.rpb));
   return r;
 }
