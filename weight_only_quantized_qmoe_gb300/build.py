@@ -1,7 +1,9 @@
-"""Build libqmoe.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libqmoe.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_ops_torch.so (the operators on torch tensors, a CPython module that calls the
+library) with g++ against torch's headers.
 
 Every translation unit is compiled in parallel; the objects go to
-``<repo>/_build`` and the library next to this file.  No cmake.
+``<repo>/_build`` and the libraries next to this file.  No cmake.
 """
 from __future__ import annotations
 
@@ -9,6 +11,8 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
+from importlib.util import find_spec
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +25,8 @@ SOURCES = ["qmoe_api.cu", "qmoe_route.cu", "qmoe_decode.cu", "qmoe_prefill.cu", 
            "qmoe_fused_w24.cu", "qmoe_fused_w32.cu", "qmoe_fused_w33.cu", "qmoe_fused_w34.cu",
            "qmoe_fused_w42.cu", "qmoe_fused_w43.cu", "qmoe_fused_w44.cu",
            "qmoe_ops_api.cu", "qmoe_sort.cu", "qmoe_mx4.cu", "qmoe_mx4_gemm.cu", "qmoe_norm.cu", "qmoe_norm_grad.cu"]
+TORCH_MODULE = os.path.join(HERE, "_ops_torch.so")
+TORCH_SOURCE = "qmoe_ops_torch.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE]
@@ -37,17 +43,40 @@ def nvcc_path() -> str:
 
 
 def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     files.append(os.path.join(INCLUDE, "qmoe.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(TORCH_MODULE)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_MODULE))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def torch_module_commands(nvcc: str, obj: str):
+    """The compile and the link command of the module on torch tensors."""
+    spec = find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found: its headers are needed for " + TORCH_SOURCE)
+    torch_dir = list(spec.submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc))
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-Wall", *[f"-I{d}" for d in inc], "-c",
+                   os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+    link_cmd = ["g++", "-shared", obj, "-o", TORCH_MODULE + ".tmp", "-L" + os.path.join(torch_dir, "lib"), "-lc10",
+                "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L" + HERE, "-l:libqmoe.so",
+                "-Wl,-rpath,$ORIGIN"]
+    return compile_cmd, link_cmd
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -69,14 +98,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    compile_torch, link_torch = torch_module_commands(nvcc, os.path.join(objdir, TORCH_SOURCE.replace(".cpp", ".o")))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_obj = ex.submit(_run, compile_torch, "g++ for " + TORCH_SOURCE)
         objs = list(ex.map(compile_one, SOURCES))
+        torch_obj.result()
     tmp = LIB_PATH + ".tmp"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcuda"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _run(link_torch, "link of " + os.path.basename(TORCH_MODULE))
+    os.replace(TORCH_MODULE + ".tmp", TORCH_MODULE)
     return LIB_PATH
 
 

@@ -520,7 +520,7 @@ bool encode_rows(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t pit
 }
 
 template <int BN, int OUT>
-cudaError_t launch_mx(const MxKernelArgs& args, int64_t tiles, int sms, cudaStream_t s) {
+cudaError_t launch_mx(const MxKernelArgs& args, int64_t tiles, cudaStream_t s) {
   const Mx4MatmulArgs& a = args.a;
   const int64_t pitch = (int64_t)((a.K + 31) / 32) * 16;
   CUtensorMap map_a, map_w;
@@ -535,7 +535,7 @@ cudaError_t launch_mx(const MxKernelArgs& args, int64_t tiles, int sms, cudaStre
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, sms));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, kSms));
   cfg.blockDim = dim3(kMxThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -553,21 +553,17 @@ int64_t most_tiles(const Mx4MatmulArgs& a, int bn) {
 }  // namespace
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int inject_stall, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
   MxKernelArgs args{a, inject_stall, 0};
   args.vec_out = rows_aligned16(a.out, a.ld_out, a.out_dtype) ? 1 : 0;
   const int64_t wide = most_tiles(a, 192);
   auto run = [&](auto bn, int64_t tiles) {
     constexpr int BN = decltype(bn)::value;
-    if (a.out_dtype == QMOE_F32) return launch_mx<BN, QMOE_F32>(args, tiles, sms, s);
-    if (a.out_dtype == QMOE_F16) return launch_mx<BN, QMOE_F16>(args, tiles, sms, s);
-    return launch_mx<BN, QMOE_BF16>(args, tiles, sms, s);
+    if (a.out_dtype == QMOE_F32) return launch_mx<BN, QMOE_F32>(args, tiles, s);
+    if (a.out_dtype == QMOE_F16) return launch_mx<BN, QMOE_F16>(args, tiles, s);
+    return launch_mx<BN, QMOE_BF16>(args, tiles, s);
   };
   // fewer wide tiles than multiprocessors: narrow ones
-  return wide >= sms ? run(std::integral_constant<int, 192>{}, wide)
+  return wide >= kSms ? run(std::integral_constant<int, 192>{}, wide)
                      : run(std::integral_constant<int, 64>{}, most_tiles(a, 64));
 }
 

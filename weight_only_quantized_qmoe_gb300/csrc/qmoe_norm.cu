@@ -33,20 +33,22 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   int turn = 0, parts = 0;
   const uint32_t ring = smem_u32(norm_ring);
-  Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts), o(a.o, a.ld_o, t, stride, ring, parts),
-      g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts);
-  const uint32_t row_bytes = (uint32_t)parts * VPT * blockDim.x * blockDim.y * 16;
-  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, a.H),
-      pre(a.w_pre, nullptr, a.H);
-  T* out_r = static_cast<T*>(a.r) + (a.r ? t * a.H : 0);
-  T* out_h = static_cast<T*>(a.h) + (a.h ? t * a.H : 0);
+  const Place<DT, VECTOR> me(a.H);
+  Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts, me), o(a.o, a.ld_o, t, stride, ring, parts, me),
+      g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts, me);
+  const uint32_t row_bytes = parts * VPT * me.frag_bytes;
+  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me),
+      pre(a.w_pre, nullptr, me);
+  const int64_t out_step = stride * a.H;
+  T* out_r = static_cast<T*>(a.r) + t * a.H + F::first(threadIdx.x);
+  T* out_h = static_cast<T*>(a.h) + t * a.H + F::first(threadIdx.x);
   int64_t ahead = t;   // the row fetched next
   auto fetch = [&](uint32_t at) {
     if constexpr (RING) {
       if (ahead < a.T) {
-        x.fetch(at, a.H);
-        o.fetch(at, a.H);
-        g.fetch(at, a.H);
+        x.fetch(at, me);
+        o.fetch(at, me);
+        g.fetch(at, me);
       }
       x.advance();
       o.advance();
@@ -59,8 +61,9 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   for (int s = 0; s + 1 < AHEAD; ++s) fetch(s * row_bytes);
   const uint32_t last = (RING ? AHEAD - 1 : 0) * row_bytes;
   uint32_t at = 0, to = last;
+  float next_token = a.gate_kind == QMOE_GATE_TOKEN && t < a.T ? load_d<DT>(a.gate, (size_t)t) : 1.f;   // a row ahead
   // the rows of a block advance together (their sums share barriers)
-  for (; t - threadIdx.y < a.T; t += stride, out_r += stride * a.H, out_h += stride * a.H) {
+  for (; t - threadIdx.y < a.T; t += stride, out_r += out_step, out_h += out_step) {
     const bool live = t < a.T;
     if constexpr (RING) {
       fetch(to);
@@ -71,47 +74,44 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
       float2 ss = both(0.f);
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
-        const int64_t c = norm_column<DT, VECTOR>(p);
-        if (live && c < a.H) {
+        if (live && me.has(p)) {
           float2 v[N2];
-          o.get(at, p, c, a.H, v);
+          o.get(at, p, me, v);
 #pragma unroll
           for (int i = 0; i < N2; ++i) ss = fma2(v[i], v[i], ss);
         }
       }
       rstd1 = rsqrtf(row_sum(ss.x + ss.y, red, turn) * inv_h + a.eps);
     }
-    const float token = live && a.gate_kind == QMOE_GATE_TOKEN ? load_d<DT>(a.gate, (size_t)t) : 1.f;
+    const float token = next_token;
+    if (a.gate_kind == QMOE_GATE_TOKEN && t + stride < a.T) next_token = load_d<DT>(a.gate, (size_t)(t + stride));
     const float2 c1 = both(rstd1 * token), scale = both(a.residual_scale);
     float2 r[VPT][N2], ss = both(0.f);
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      const int64_t c = norm_column<DT, VECTOR>(p);
-      if (live && c < a.H) {
-        x.get(at, p, c, a.H, r[p]);
+      if (live && me.has(p)) {
+        x.get(at, p, me, r[p]);
 #pragma unroll
         for (int i = 0; i < N2; ++i) r[p][i] = mul2(r[p][i], scale);
         if (branch) {
           float2 v[N2], w[N2];
-          o.get(at, p, c, a.H, v);
-          post.get(p, c, w);
+          o.get(at, p, me, v);
+          post.get(p, me, w);
           if (full) {
             float2 q[N2];
-            g.get(at, p, c, a.H, q);
+            g.get(at, p, me, q);
 #pragma unroll
             for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], q[i]);
           }
 #pragma unroll
           for (int i = 0; i < N2; ++i) r[p][i] = fma2(mul2(v[i], c1), w[i], r[p][i]);
         }
-        F f;
-        set2(f, r[p]);
-        if (a.r) f.store(out_r, 0, c, a.H, blockDim.x);
+        if (a.r) put<DT, VECTOR>(out_r, p, me, r[p]);
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
           if constexpr (!VECTOR) {   // past the row's end
-            if (c + (int64_t)(2 * i) * blockDim.x >= a.H) r[p][i].x = 0.f;
-            if (c + (int64_t)(2 * i + 1) * blockDim.x >= a.H) r[p][i].y = 0.f;
+            if (2 * i * me.threads >= me.left_of(p)) r[p][i].x = 0.f;
+            if ((2 * i + 1) * me.threads >= me.left_of(p)) r[p][i].y = 0.f;
           }
           ss = fma2(r[p][i], r[p][i], ss);
         }
@@ -123,15 +123,12 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
       if (a.rstd_pre && live && threadIdx.x == 0) a.rstd_pre[t] = rstd2;
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
-        const int64_t c = norm_column<DT, VECTOR>(p);
-        if (live && c < a.H) {
+        if (live && me.has(p)) {
           float2 w[N2];
-          pre.get(p, c, w);
+          pre.get(p, me, w);
 #pragma unroll
           for (int i = 0; i < N2; ++i) w[i] = mul2(mul2(r[p][i], both(rstd2)), w[i]);
-          F f;
-          set2(f, w);
-          f.store(out_h, 0, c, a.H, blockDim.x);
+          put<DT, VECTOR>(out_h, p, me, w);
         }
       }
     }
@@ -165,11 +162,11 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
       if (e != cudaSuccess) return e;
     }
     int64_t blocks = (a.T + g.rpb - 1) / g.rpb;
-    if (blocks > kNormSms) {   // as many as are resident at once
+    if (blocks > kSms) {   // as many as are resident at once
       int per = 0;
       const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, ring);
       if (e != cudaSuccess) return e;
-      blocks = std::min<int64_t>(blocks, (int64_t)kNormSms * std::max(1, per));
+      blocks = std::min<int64_t>(blocks, (int64_t)kSms * std::max(1, per));
     }
     kern<<<(unsigned)blocks, dim3(g.tpr, g.rpb), ring, s>>>(a);
     return cudaGetLastError();

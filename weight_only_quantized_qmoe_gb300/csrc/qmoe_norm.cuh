@@ -9,10 +9,6 @@
 
 namespace qmoe {
 
-// Multiprocessors of the one GPU these kernels are built for: persistent CTAs
-// are counted in them.
-constexpr int kNormSms = 152;
-
 // Two fp32 values in one instruction.  The norms issue some thirty
 // instructions a value even so, close to what a multiprocessor can issue in the
 // time the value's bytes take.
@@ -70,12 +66,23 @@ __device__ __forceinline__ float row_sum(float v, float* red, int& turn) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Column of a thread's fragment p.
+// What a thread needs to know of its place: the elements from its fragment p
+// to the row's end (none: it has no such fragment), and where that fragment
+// lies behind its first one, in memory and in a ring.
 template <int DT, bool VECTOR>
-__device__ __forceinline__ int64_t norm_column(int p) {
+struct Place {
   using F = Frag<DT, VECTOR>;
-  return F::first(threadIdx.x) + p * F::step(blockDim.x);
-}
+  int threads, left, step;
+  uint32_t frag_bytes;   // the fragments p of all of a CTA's threads in a ring
+  __device__ __forceinline__ explicit Place(int64_t H) {
+    threads = blockDim.x;
+    left = (int)H - F::first(threadIdx.x);
+    step = F::step(threads);
+    frag_bytes = blockDim.x * blockDim.y * 16;
+  }
+  __device__ __forceinline__ int left_of(int p) const { return left - p * step; }
+  __device__ __forceinline__ bool has(int p) const { return left_of(p) > 0; }
+};
 
 // The rows of one tensor as a thread sees them: its fragments of row after row
 // of a CTA.  With 16-byte rows (RING) a thread copies its own fragments of the
@@ -86,40 +93,39 @@ template <int DT, bool VECTOR, int VPT, bool RING>
 struct Rows {
   using F = Frag<DT, VECTOR>;
   using T = typename ElemT<DT>::t;
-  const T* next;      // RING: the row to be fetched next, else the row in work
+  const T* next;      // this thread's first element of the row to be fetched next, without RING of the row in work
   int64_t step;       // elements from a CTA's row to its next
-  uint32_t ring;      // shared address of this thread's fragment 0 in ring row 0
+  uint32_t ring;      // shared address of this thread's first fragment in ring row 0
   bool there;
 
   // `slot` counts the tensors that are there: their fragments lie side by side
   // in a ring row.
-  __device__ __forceinline__ Rows(const void* base, int64_t ld, int64_t row, int64_t rows, uint32_t ring0, int& slot) {
+  __device__ __forceinline__ Rows(const void* base, int64_t ld, int64_t row, int64_t rows, uint32_t ring0, int& slot,
+                                  const Place<DT, VECTOR>& at) {
     there = base != nullptr;
-    next = static_cast<const T*>(base) + row * ld;
+    next = static_cast<const T*>(base) + row * ld + F::first(threadIdx.x);
     step = rows * ld;
-    ring = ring0 + (uint32_t)slot * VPT * blockDim.x * blockDim.y * 16 + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+    ring = ring0 + slot * VPT * at.frag_bytes + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
     slot += there ? 1 : 0;
   }
-  __device__ __forceinline__ void fetch(uint32_t at, int64_t H) const {   // `at`: byte offset of the ring row
+  __device__ __forceinline__ void fetch(uint32_t row, const Place<DT, VECTOR>& at) const {   // `row`: offset of the ring row
     if (!there) return;
 #pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      const int64_t c = norm_column<DT, VECTOR>(p);
-      if (c < H)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + at + p * blockDim.x * blockDim.y * 16), "l"(next + c)
+    for (int p = 0; p < VPT; ++p)
+      if (at.has(p))
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + row + p * at.frag_bytes), "l"(next + p * at.step)
                      : "memory");
-    }
   }
   __device__ __forceinline__ void advance() { next += step; }
-  __device__ __forceinline__ void get(uint32_t at, int p, int64_t c, int64_t H, float2 (&v)[F::n / 2]) const {
+  __device__ __forceinline__ void get(uint32_t row, int p, const Place<DT, VECTOR>& at, float2 (&v)[F::n / 2]) const {
     F f;
     if constexpr (RING) {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(f.u.x), "=r"(f.u.y), "=r"(f.u.z), "=r"(f.u.w)
-                   : "r"(ring + at + p * blockDim.x * blockDim.y * 16)
+                   : "r"(ring + row + p * at.frag_bytes)
                    : "memory");
     } else {
-      f.load(next, 0, c, H, blockDim.x);
+      f.load(next + p * at.step, at.left_of(p), at.threads);
     }
     get2(f, v);
   }
@@ -138,47 +144,60 @@ __device__ __forceinline__ void cp_async_wait() {
 template <int DT, bool VECTOR, int VPT>
 struct Columns {
   using F = Frag<DT, VECTOR>;
+  using T = typename ElemT<DT>::t;
   static constexpr int N2 = F::n / 2;
-  const void *a, *b;
-  int64_t H;
+  const T *a, *b;
   float2 held[VPT == 1 ? N2 : 1];
   F fa[VPT == 2 ? 2 : 1], fb[VPT == 2 ? 2 : 1];
   __device__ __forceinline__ void compute(const F& x, const F& y, float2 (&v)[N2]) const {
+    if (a) {
+      get2(x, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N2; ++i) v[i] = both(1.f);
-    if (a) get2(x, v);
+      for (int i = 0; i < N2; ++i) v[i] = both(1.f);
+    }
     if (b) {
       float2 w[N2];
       get2(y, w);
 #pragma unroll
-      for (int i = 0; i < N2; ++i) v[i] = a ? mul2(v[i], w[i]) : w[i];
+      for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], w[i]);
     }
   }
-  __device__ __forceinline__ Columns(const void* a_, const void* b_, int64_t H_) : a(a_), b(b_), H(H_) {
+  __device__ __forceinline__ Columns(const void* a_, const void* b_, const Place<DT, VECTOR>& at) {
+    a = a_ ? static_cast<const T*>(a_) + F::first(threadIdx.x) : nullptr;
+    b = b_ ? static_cast<const T*>(b_) + F::first(threadIdx.x) : nullptr;
     if constexpr (VPT <= 2) {
 #pragma unroll
-      for (int q = 0; q < VPT; ++q) {
-        const int64_t c = norm_column<DT, VECTOR>(q);
-        if (a && c < H) fa[q].load(a, 0, c, H, blockDim.x);
-        if (b && c < H) fb[q].load(b, 0, c, H, blockDim.x);
+      for (int p = 0; p < VPT; ++p) {
+        if (a && at.has(p)) fa[p].load(a + p * at.step, at.left_of(p), at.threads);
+        if (b && at.has(p)) fb[p].load(b + p * at.step, at.left_of(p), at.threads);
       }
       if constexpr (VPT == 1) compute(fa[0], fb[0], held);
     }
   }
-  __device__ __forceinline__ void get(int q, int64_t c, float2 (&v)[N2]) const {
+  __device__ __forceinline__ void get(int p, const Place<DT, VECTOR>& at, float2 (&v)[N2]) const {
     if constexpr (VPT == 1) {
 #pragma unroll
       for (int i = 0; i < N2; ++i) v[i] = held[i];
     } else if constexpr (VPT == 2) {
-      compute(fa[q], fb[q], v);
+      compute(fa[p], fb[p], v);
     } else {
       F x, y;
-      if (a) x.load(a, 0, c, H, blockDim.x);
-      if (b) y.load(b, 0, c, H, blockDim.x);
+      if (a) x.load(a + p * at.step, at.left_of(p), at.threads);
+      if (b) y.load(b + p * at.step, at.left_of(p), at.threads);
       compute(x, y, v);
     }
   }
 };
+
+// A thread's fragment p of an output row (`out`: the thread's first element).
+template <int DT, bool VECTOR>
+__device__ __forceinline__ void put(typename ElemT<DT>::t* out, int p, const Place<DT, VECTOR>& at,
+                                    const float2 (&v)[Frag<DT, VECTOR>::n / 2]) {
+  Frag<DT, VECTOR> f;
+  set2(f, v);
+  f.store(out + p * at.step, at.left_of(p), at.threads);
+}
 
 inline bool norm_vec(const NormArgs& a) {
   const void* whole[] = {a.w_post, a.w_pre, a.r, a.h, a.dx, a.d_o};

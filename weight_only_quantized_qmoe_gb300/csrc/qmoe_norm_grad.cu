@@ -41,23 +41,24 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   int turn = 0, parts = 0;
   const uint32_t ring = smem_u32(norm_ring);
-  Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts), o(a.o, a.ld_o, t, stride, ring, parts),
-      dr(a.dr, a.ld_dr, t, stride, ring, parts), dh(a.dh, a.ld_dh, t, stride, ring, parts),
-      g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts);
-  const uint32_t row_bytes = (uint32_t)parts * VPT * blockDim.x * blockDim.y * 16;
-  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, a.H),
-      pre(a.w_pre, nullptr, a.H);
+  const Place<DT, VECTOR> me(a.H);
+  Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts, me), o(a.o, a.ld_o, t, stride, ring, parts, me),
+      dr(a.dr, a.ld_dr, t, stride, ring, parts, me), dh(a.dh, a.ld_dh, t, stride, ring, parts, me),
+      g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts, me);
+  const uint32_t row_bytes = parts * VPT * me.frag_bytes;
+  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me),
+      pre(a.w_pre, nullptr, me);
   const int64_t out_step = stride * a.H;
-  int64_t out = t * a.H;
+  int64_t out = t * a.H + F::first(threadIdx.x);
   int64_t ahead = t;
   auto fetch = [&](uint32_t at) {
     if constexpr (RING) {
       if (ahead < a.T) {
-        x.fetch(at, a.H);
-        o.fetch(at, a.H);
-        dr.fetch(at, a.H);
-        dh.fetch(at, a.H);
-        g.fetch(at, a.H);
+        x.fetch(at, me);
+        o.fetch(at, me);
+        dr.fetch(at, me);
+        dh.fetch(at, me);
+        g.fetch(at, me);
       }
       ahead += stride;
       cp_async_commit();
@@ -81,11 +82,19 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   }
   const uint32_t last = (RING ? AHEAD - 1 : 0) * row_bytes;
   uint32_t at = 0, to = last;
+  // a row's scalars, loaded a row ahead
+  float next1 = 1.f, next2 = 1.f, next_token = 1.f;
+  auto scalars = [&](int64_t row) {
+    if (row >= a.T) return;
+    if (branch && a.w_post) next1 = a.rstd_post[row];
+    if (pre_norm) next2 = a.rstd_pre[row];
+    if (a.gate_kind == QMOE_GATE_TOKEN) next_token = load_d<DT>(a.gate, (size_t)row);
+  };
+  scalars(t);
   for (; t - threadIdx.y < a.T; t += stride, out += out_step) {
     const bool live = t < a.T;
-    const float rstd1 = live && branch && a.w_post ? a.rstd_post[t] : 1.f;
-    const float rstd2 = live && pre_norm ? a.rstd_pre[t] : 1.f;
-    const float token = live && a.gate_kind == QMOE_GATE_TOKEN ? load_d<DT>(a.gate, (size_t)t) : 1.f;
+    const float rstd1 = next1, rstd2 = next2, token = next_token;
+    scalars(t + stride);
     if constexpr (RING) {
       fetch(to);
       cp_async_wait<AHEAD - 1>();
@@ -96,26 +105,25 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
       const float2 cx = both(a.residual_scale * rstd2), co = both(rstd1 * token * rstd2);
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
-        const int64_t c = norm_column<DT, VECTOR>(p);
-        if (live && c < a.H) {
+        if (live && me.has(p)) {
           float2 v[N2], w[N2];
-          x.get(at, p, c, a.H, rh[p]);
+          x.get(at, p, me, rh[p]);
 #pragma unroll
           for (int i = 0; i < N2; ++i) rh[p][i] = mul2(rh[p][i], cx);
           if (branch) {
-            o.get(at, p, c, a.H, v);
-            post.get(p, c, w);
+            o.get(at, p, me, v);
+            post.get(p, me, w);
             if (full) {
               float2 q[N2];
-              g.get(at, p, c, a.H, q);
+              g.get(at, p, me, q);
 #pragma unroll
               for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], q[i]);
             }
 #pragma unroll
             for (int i = 0; i < N2; ++i) rh[p][i] = fma2(mul2(v[i], co), w[i], rh[p][i]);
           }
-          dh.get(at, p, c, a.H, v);
-          pre.get(p, c, w);
+          dh.get(at, p, me, v);
+          pre.get(p, me, w);
 #pragma unroll
           for (int i = 0; i < N2; ++i) {
             s_pre[p][i] = fma2(v[i], rh[p][i], s_pre[p][i]);
@@ -131,11 +139,10 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
     float2 sum1 = both(0.f);
 #pragma unroll
     for (int p = 0; p < VPT; ++p) {
-      const int64_t c = norm_column<DT, VECTOR>(p);
-      if (live && c < a.H) {
+      if (live && me.has(p)) {
         float2 d[N2], v[N2], w[N2];
         if (a.dr) {
-          dr.get(at, p, c, a.H, d);
+          dr.get(at, p, me, d);
         } else {
 #pragma unroll
           for (int i = 0; i < N2; ++i) d[i] = both(0.f);
@@ -144,38 +151,33 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
 #pragma unroll
           for (int i = 0; i < N2; ++i) d[i] = fma2(rh[p][i], m2, fma2(dn[p][i], k2, d[i]));
         }
-        F f;
         if (a.dx) {
 #pragma unroll
           for (int i = 0; i < N2; ++i) v[i] = mul2(d[i], both(a.residual_scale));
-          set2(f, v);
-          f.store(static_cast<T*>(a.dx) + out, 0, c, a.H, blockDim.x);
+          put<DT, VECTOR>(static_cast<T*>(a.dx) + out, p, me, v);
         }
         if (branch) {
           const float2 c1 = both(rstd1 * token);
-          o.get(at, p, c, a.H, v);
-          post.get(p, c, w);
+          o.get(at, p, me, v);
+          post.get(p, me, w);
 #pragma unroll
           for (int i = 0; i < N2; ++i) dn[p][i] = mul2(d[i], w[i]);
           if (full) {
             float2 q[N2], e[N2];
-            g.get(at, p, c, a.H, q);
+            g.get(at, p, me, q);
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
               e[i] = mul2(mul2(dn[p][i], v[i]), both(rstd1));
               dn[p][i] = mul2(dn[p][i], q[i]);
               d[i] = mul2(d[i], q[i]);
             }
-            if (a.dgate) {
-              set2(f, e);
-              f.store(static_cast<T*>(a.dgate) + out, 0, c, a.H, blockDim.x);
-            }
+            if (a.dgate) put<DT, VECTOR>(static_cast<T*>(a.dgate) + out, p, me, e);
           }
 #pragma unroll
           for (int i = 0; i < N2; ++i) {
             if constexpr (!VECTOR) {   // past the row's end (an infinite factor would make NaN of its zeros)
-              if (c + (int64_t)(2 * i) * blockDim.x >= a.H) dn[p][i].x = d[i].x = 0.f;
-              if (c + (int64_t)(2 * i + 1) * blockDim.x >= a.H) dn[p][i].y = d[i].y = 0.f;
+              if (2 * i * me.threads >= me.left_of(p)) dn[p][i].x = d[i].x = 0.f;
+              if ((2 * i + 1) * me.threads >= me.left_of(p)) dn[p][i].y = d[i].y = 0.f;
             }
             s_post[p][i] = fma2(mul2(d[i], c1), v[i], s_post[p][i]);
             sum1 = fma2(dn[p][i], v[i], sum1);
@@ -192,15 +194,12 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
         const float2 cu = both(rstd1 * token), co = both(a.w_post ? -s1 * token * inv_h * rstd1 * rstd1 : 0.f);
 #pragma unroll
         for (int p = 0; p < VPT; ++p) {
-          const int64_t c = norm_column<DT, VECTOR>(p);
-          if (live && c < a.H) {
+          if (live && me.has(p)) {
             float2 v[N2];
-            o.get(at, p, c, a.H, v);
+            o.get(at, p, me, v);
 #pragma unroll
             for (int i = 0; i < N2; ++i) v[i] = a.w_post ? fma2(v[i], co, mul2(dn[p][i], cu)) : mul2(dn[p][i], cu);
-            F f;
-            set2(f, v);
-            f.store(static_cast<T*>(a.d_o) + out, 0, c, a.H, blockDim.x);
+            put<DT, VECTOR>(static_cast<T*>(a.d_o) + out, p, me, v);
           }
         }
       }
@@ -217,10 +216,9 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   float* mine = a.partial + ((size_t)blockIdx.x * blockDim.y + threadIdx.y) * SUM_KINDS * (size_t)a.H;
 #pragma unroll
   for (int p = 0; p < VPT; ++p) {
-    const int64_t c = norm_column<DT, VECTOR>(p);
 #pragma unroll
     for (int i = 0; i < 2 * N2; ++i) {
-      const int64_t col = VECTOR ? c + i : c + (int64_t)i * blockDim.x;
+      const int64_t col = F::first(threadIdx.x) + p * me.step + (VECTOR ? i : i * me.threads);
       if (col >= a.H) continue;
       if (a.dw_pre) mine[SUM_PRE * a.H + col] = i & 1 ? s_pre[p][i / 2].y : s_pre[p][i / 2].x;
       if (branch) mine[SUM_POST * a.H + col] = i & 1 ? s_post[p][i / 2].y : s_post[p][i / 2].x;
@@ -263,7 +261,7 @@ namespace {
 // CTAs: 512 threads a multiprocessor (their sums' workspace grows with them),
 // no more than there are rows.
 int64_t norm_grad_ctas(int64_t T, const RowShape& g) {
-  return std::min<int64_t>((int64_t)kNormSms * std::max(1, 512 / (g.tpr * g.rpb)), (T + g.rpb - 1) / g.rpb);
+  return std::min<int64_t>((int64_t)kSms * std::max(1, 512 / (g.tpr * g.rpb)), (T + g.rpb - 1) / g.rpb);
 }
 
 }  // namespace

@@ -7,6 +7,10 @@
 
 namespace qmoe {
 
+// Multiprocessors of the one GPU these kernels are built for: persistent CTAs
+// are counted in them.
+constexpr int kSms = 152;
+
 // Experts one sort handles (a warp's counters of all experts are held in
 // shared memory, 32 warps of them).
 constexpr int kSortMaxExperts = 1024;
@@ -234,11 +238,11 @@ struct Frag<DT, true> {
   static constexpr int n = DT == QMOE_F32 ? 4 : 8;   // elements
   uint4 u;
   // first element of a thread, elements of a step of all of a row's threads
-  __device__ static __forceinline__ int64_t first(int thread) { return (int64_t)thread * n; }
-  __device__ static __forceinline__ int64_t step(int threads) { return (int64_t)threads * n; }
-  __device__ static __forceinline__ bool any(int64_t c, int64_t H) { return c < H; }
-  __device__ __forceinline__ void load(const void* base, size_t row, int64_t c, int64_t, int) {
-    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const typename ElemT<DT>::t*>(base) + row + c));
+  __device__ static __forceinline__ int first(int thread) { return thread * n; }
+  __device__ static __forceinline__ int step(int threads) { return threads * n; }
+  // from the thread's first element, `left` elements before the row's end
+  __device__ __forceinline__ void load(const typename ElemT<DT>::t* p, int, int) {
+    u = __ldg(reinterpret_cast<const uint4*>(p));
   }
   __device__ __forceinline__ void get(float (&v)[n]) const {
     if constexpr (DT == QMOE_F32) {
@@ -259,9 +263,7 @@ struct Frag<DT, true> {
     else
       u = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
   }
-  __device__ __forceinline__ void store(void* base, size_t row, int64_t c, int64_t, int) const {
-    *reinterpret_cast<uint4*>(static_cast<typename ElemT<DT>::t*>(base) + row + c) = u;
-  }
+  __device__ __forceinline__ void store(typename ElemT<DT>::t* p, int, int) const { *reinterpret_cast<uint4*>(p) = u; }
 };
 
 template <int DT>
@@ -269,16 +271,11 @@ struct Frag<DT, false> {
   static constexpr int n = 4;
   using T = typename ElemT<DT>::t;
   T e[n];
-  __device__ static __forceinline__ int64_t first(int thread) { return thread; }
-  __device__ static __forceinline__ int64_t step(int threads) { return (int64_t)threads * n; }
-  __device__ static __forceinline__ bool any(int64_t c, int64_t H) { return c < H; }
-  __device__ __forceinline__ void load(const void* base, size_t row, int64_t c, int64_t H, int threads) {
-    const T* p = static_cast<const T*>(base) + row;
+  __device__ static __forceinline__ int first(int thread) { return thread; }
+  __device__ static __forceinline__ int step(int threads) { return threads * n; }
+  __device__ __forceinline__ void load(const T* p, int left, int threads) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int64_t x = c + (int64_t)i * threads;
-      e[i] = x < H ? p[x] : T(0.f);
-    }
+    for (int i = 0; i < n; ++i) e[i] = i * threads < left ? p[i * threads] : T(0.f);
   }
   __device__ __forceinline__ void get(float (&v)[n]) const {
 #pragma unroll
@@ -288,13 +285,10 @@ struct Frag<DT, false> {
 #pragma unroll
     for (int i = 0; i < n; ++i) store_d<DT>(&e[i], 0, v[i]);
   }
-  __device__ __forceinline__ void store(void* base, size_t row, int64_t c, int64_t H, int threads) const {
-    T* p = static_cast<T*>(base) + row;
+  __device__ __forceinline__ void store(T* p, int left, int threads) const {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int64_t x = c + (int64_t)i * threads;
-      if (x < H) p[x] = e[i];
-    }
+    for (int i = 0; i < n; ++i)
+      if (i * threads < left) p[i * threads] = e[i];
   }
 };
 

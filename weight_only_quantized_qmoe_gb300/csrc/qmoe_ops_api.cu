@@ -58,7 +58,7 @@ qmoe_status check_routes(int64_t T, int k, int E) {
 }
 qmoe_status check_rows(int64_t H, int64_t ld, int dtype) {
   OP_CHECK(dtype_ok(dtype), "dtype %d is not QMOE_F32, QMOE_F16 or QMOE_BF16", dtype);
-  OP_CHECK(H >= 1 && H < INT_MAX, "row length %lld is out of range", (long long)H);
+  OP_CHECK(H >= 1 && H <= (1 << 30), "row length %lld is out of range", (long long)H);
   OP_CHECK(ld >= H, "row stride %lld is below the row length %lld", (long long)ld, (long long)H);
   return QMOE_OK;
 }
@@ -201,7 +201,7 @@ qmoe_status qmoe_mx4_quantize(const void* x_dev, int64_t ld_x, int64_t rows, int
   OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
   OP_CHECK(activation == QMOE_ACT_NONE || activation == QMOE_ACT_SWIGLU || activation == QMOE_ACT_GEGLU_TANH,
            "activation %d is not QMOE_ACT_NONE or a gated one", activation);
-  OP_CHECK(cols >= 1 && cols < INT_MAX / 2, "cols %lld is out of range", (long long)cols);
+  OP_CHECK(cols >= 1 && cols <= (1 << 29), "cols %lld is out of range", (long long)cols);
   OP_TRY(check_rows(activation == QMOE_ACT_NONE ? cols : 2 * cols, ld_x, dtype));
   int64_t out_rows = rows;
   if (pos_dev) {

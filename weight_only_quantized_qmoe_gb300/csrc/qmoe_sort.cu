@@ -160,7 +160,7 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = C > 1 ? 1 : 0;   // a single CTA is its own cluster
   auto run = [&](auto kern) {
     if (smem > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -196,6 +196,7 @@ __device__ __forceinline__ int slot_row(const RowsArgs& a, int p) { return p < a
 template <int DT, bool VECTOR>
 __device__ __forceinline__ void zero_unused_rows(const RowsArgs& a, int64_t t) {
   using F = Frag<DT, VECTOR>;
+  const int H = (int)a.H;
   const int64_t R = a.T * a.k, used = max(a.offsets[a.E], 0);
   float z[F::n];
 #pragma unroll
@@ -203,22 +204,23 @@ __device__ __forceinline__ void zero_unused_rows(const RowsArgs& a, int64_t t) {
   F f;
   f.set(z);
   for (int64_t i = used + t; i < R; i += a.T)
-    for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x))
-      f.store(a.dst, (size_t)(i * a.H), c, a.H, blockDim.x);
+    for (int c = F::first(threadIdx.x); c < H; c += F::step(blockDim.x))
+      f.store(static_cast<typename ElemT<DT>::t*>(a.dst) + i * a.H + c, H - c, blockDim.x);
 }
 
 template <int DT, bool VECTOR>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowsArgs a) {
   using F = Frag<DT, VECTOR>;
+  const int H = (int)a.H;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   if (t >= a.T) return;
   const int* pos = a.pos + t * a.k;
-  for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x)) {
+  for (int c = F::first(threadIdx.x); c < H; c += F::step(blockDim.x)) {
     F f;
-    f.load(a.src, (size_t)(t * a.ld_src), c, a.H, blockDim.x);
+    f.load(static_cast<const typename ElemT<DT>::t*>(a.src) + t * a.ld_src + c, H - c, blockDim.x);
     for (int j = 0; j < a.k; ++j) {
       const int64_t p = slot_row(a, pos[j]);
-      if (p >= 0) f.store(a.dst, (size_t)(p * a.H), c, a.H, blockDim.x);
+      if (p >= 0) f.store(static_cast<typename ElemT<DT>::t*>(a.dst) + p * a.H + c, H - c, blockDim.x);
     }
   }
   zero_unused_rows<DT, VECTOR>(a, t);
@@ -227,10 +229,11 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowsArgs a)
 template <int DT, bool VECTOR, int SLOTS>
 __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_kernel(const RowsArgs a) {
   using F = Frag<DT, VECTOR>;
+  const int H = (int)a.H;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   if (t >= a.T) return;
   const int* pos = a.pos + t * a.k;
-  for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x)) {
+  for (int c = F::first(threadIdx.x); c < H; c += F::step(blockDim.x)) {
     float acc[F::n];
 #pragma unroll
     for (int i = 0; i < F::n; ++i) acc[i] = 0.f;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_kernel(c
       }
 #pragma unroll
       for (int u = 0; u < SLOTS; ++u)
-        if (p[u] >= 0) f[u].load(a.src, (size_t)((int64_t)p[u] * a.ld_src), c, a.H, blockDim.x);
+        if (p[u] >= 0) f[u].load(static_cast<const typename ElemT<DT>::t*>(a.src) + (int64_t)p[u] * a.ld_src + c, H - c, blockDim.x);
 #pragma unroll
       for (int u = 0; u < SLOTS; ++u)
         if (p[u] >= 0) {
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_kernel(c
     }
     F out;
     out.set(acc);
-    out.store(a.dst, (size_t)(t * a.H), c, a.H, blockDim.x);
+    out.store(static_cast<typename ElemT<DT>::t*>(a.dst) + t * a.H + c, H - c, blockDim.x);
   }
 }
 
@@ -285,6 +288,7 @@ __device__ __forceinline__ int warp_sums(float (&v)[N]) {
 template <int DT, bool VECTOR, int SLOTS>
 __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_grad_kernel(const RowsArgs a) {
   using F = Frag<DT, VECTOR>;
+  const int H = (int)a.H;
   __shared__ float part[kRowThreads / 32][SLOTS];
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   const bool live = t < a.T;
@@ -300,13 +304,13 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_grad_ker
       dot[u] = 0.f;
     }
     if (live) {
-      for (int64_t c = F::first(threadIdx.x); c < a.H; c += F::step(blockDim.x)) {
+      for (int c = F::first(threadIdx.x); c < H; c += F::step(blockDim.x)) {
         F fg, f[SLOTS];
-        fg.load(a.src, (size_t)(t * a.ld_src), c, a.H, blockDim.x);
+        fg.load(static_cast<const typename ElemT<DT>::t*>(a.src) + t * a.ld_src + c, H - c, blockDim.x);
         if (a.dw) {
 #pragma unroll
           for (int u = 0; u < SLOTS; ++u)
-            if (p[u] >= 0) f[u].load(a.y, (size_t)((int64_t)p[u] * a.ld_y), c, a.H, blockDim.x);
+            if (p[u] >= 0) f[u].load(static_cast<const typename ElemT<DT>::t*>(a.y) + (int64_t)p[u] * a.ld_y + c, H - c, blockDim.x);
         }
         float g[F::n];
         fg.get(g);
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_grad_ker
             for (int i = 0; i < F::n; ++i) v[i] = w[u] * g[i];
             F out;
             out.set(v);
-            out.store(a.dst, (size_t)((int64_t)p[u] * a.H), c, a.H, blockDim.x);
+            out.store(static_cast<typename ElemT<DT>::t*>(a.dst) + (int64_t)p[u] * a.H + c, H - c, blockDim.x);
           }
         }
       }
