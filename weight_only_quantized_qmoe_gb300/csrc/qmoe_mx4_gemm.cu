@@ -43,13 +43,14 @@
 namespace qmoe {
 
 constexpr int kMxRows = 128;                   // rows of A a tile
-constexpr int kMxBoxRows = 32;                 // rows of A a copy
+constexpr int kMxBoxRows = 32;                 // rows of A a copy where a tile is not full
 constexpr int kMxStageK = 256;                 // values along K a stage
 constexpr int kMxRowBytes = kMxStageK / 2;     // 128: one swizzle atom
 constexpr int kMxTmemCols = 512;
 constexpr int kMxThreads = 256;
 constexpr int kMxEpiPitch = 144;               // bytes of a staged output row (128 + 16: banks)
 constexpr int kMxMaxExperts = 1024;
+constexpr long long kMxDrainPolls = 4096;      // parked polls (about 4 ms) a copy in flight is given to land
 
 template <int BN>
 struct MxRing {
@@ -147,8 +148,11 @@ __device__ __forceinline__ void tma_2d_elect(void* dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-// Four bytes global -> shared, or four zero bytes.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool real) {
+// Four bytes global -> shared; or four zero bytes.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
@@ -213,16 +217,15 @@ __device__ __forceinline__ MxTile mx_tile(const Mx4MatmulArgs& a, const int* tp,
 
 template <int BN, int OUT>
 __global__ void __launch_bounds__(kMxThreads, 1)
-    mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-                      const MxKernelArgs args) {
+    mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a32,
+                      const __grid_constant__ CUtensorMap map_w, const MxKernelArgs args) {
   using RG = MxRing<BN>;
   constexpr int S = RG::stages;
   extern __shared__ __align__(1024) uint8_t mx_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mx_smem_raw) + 1023) & ~uintptr_t(1023));
   const Mx4MatmulArgs& a = args.a;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + RG::bar_off);
-  uint64_t* sfull = full + S;
-  uint64_t* empty = sfull + S;
+  uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain_bar = acc_empty + 2;
@@ -234,8 +237,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&sfull[i], 64);
+      // one barrier tells the MMA warp that a stage is there (a poll takes 120
+      // cycles, a stage's MMAs 384): the announced bytes and the 64 lanes of the
+      // scale loaders
+      mbar_init(&full[i], 1 + 64);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -292,7 +297,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       const MxTile t = mx_tile(a, tp, row0, ntn, BN, tile);
       if (t.e == a.E) continue;
-      const int boxes = (t.rows + kMxBoxRows - 1) / kMxBoxRows;
+      // the rows in one copy if they are many, else in copies of 32
+      const int boxes = (max(t.rows, 0) + kMxBoxRows - 1) / kMxBoxRows;
       for (int ks = 0; ks < ksteps; ++ks, ++it) {
         const int s = it % S;
         ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
@@ -301,19 +307,21 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         mbar_arrive_expect_tx_elect(&full[s], (uint32_t)(boxes * kMxBoxRows * kMxRowBytes + RG::b_bytes));
         // Test hook: the first stage's barrier is armed, its copies are never issued.
         if (args.inject_stall && it == 0) continue;
-        for (int b = 0; b < boxes; ++b)
-          tma_2d_elect(smem + RG::a_off + s * RG::a_bytes + b * kMxBoxRows * kMxRowBytes, &map_a, ks * kMxRowBytes,
-                       t.start + b * kMxBoxRows, &full[s]);
+        if (boxes == kMxRows / kMxBoxRows)
+          tma_2d_elect(smem + RG::a_off + s * RG::a_bytes, &map_a, ks * kMxRowBytes, t.start, &full[s]);
+        else
+          for (int b = 0; b < boxes; ++b)
+            tma_2d_elect(smem + RG::a_off + s * RG::a_bytes + b * kMxBoxRows * kMxRowBytes, &map_a32, ks * kMxRowBytes,
+                         t.start + b * kMxBoxRows, &full[s]);
         tma_2d_elect(smem + RG::b_off + s * RG::b_bytes, &map_w, ks * kMxRowBytes, t.e * a.N + t.n0, &full[s]);
       }
     }
     if (!ok) {
-      // the copies of the last S stages must land before the CTA leaves
-      const WaitCfg drain{a.wait.status, kDrainWaitLimit};
-      for (int i = it > S ? it - S : 0; i < it; ++i) {
-        if (args.inject_stall && i == 0) continue;
-        mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
-      }
+      // After a wait that ran out the copies in flight must land before the CTA
+      // leaves: wait for the last stages' barriers, with a limit, as the scale
+      // loaders may have left them short.
+      const WaitCfg drain{a.wait.status, kMxDrainPolls};
+      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
     }
   } else if (warp == 2 || warp == 3) {
     // ---------------- scale loaders: warp 2 + h takes the 128-value chunk h of each stage ----------------
@@ -331,23 +339,32 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       const uint8_t* pa = a.a_scales + ((size_t)h * a.R + t.start + lane) * 4;
       const uint8_t* pw = a.w_scales + (((size_t)t.e * nq + h) * a.N + t.n0 + lane) * 4;
       const int na = (int)a.R - t.start - lane, nw = a.N - t.n0 - lane;   // row 32 j exists: 32 j < n
+      const bool inside = t.start + kMxRows <= (int)a.R && t.n0 + BN <= a.N;
       for (int ks = 0; ks < ksteps; ++ks, ++it, pa += step_a, pw += step_w) {
         const int s = it % S;
         ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const bool in = 2 * ks + h < nq;
+        const uint32_t da = sfa0 + s * RG::sfa_bytes, db = sfb0 + s * RG::sfb_bytes;
+        if (inside && 2 * ks + h < nq) {   // every row exists: no tests between the copies
 #pragma unroll
-        for (int j = 0; j < kMxRows / 32; ++j) {
-          const bool real = in && 32 * j < na;
-          cp_async4(sfa0 + s * RG::sfa_bytes + j * 4, real ? pa + j * 128 : a.a_scales, real);
-        }
+          for (int j = 0; j < kMxRows / 32; ++j) cp_async4(da + j * 4, pa + j * 128);
 #pragma unroll
-        for (int j = 0; j < BN / 32; ++j) {
-          const bool real = in && 32 * j < nw;
-          cp_async4(sfb0 + s * RG::sfb_bytes + (j / 4) * 512 + (j & 3) * 4, real ? pw + j * 128 : a.w_scales, real);
+          for (int j = 0; j < BN / 32; ++j) cp_async4(db + (j / 4) * 512 + (j & 3) * 4, pw + j * 128);
+        } else {
+          const bool in = 2 * ks + h < nq;
+#pragma unroll
+          for (int j = 0; j < kMxRows / 32; ++j) {
+            const bool real = in && 32 * j < na;
+            cp_async4_or_zero(da + j * 4, real ? pa + j * 128 : a.a_scales, real);
+          }
+#pragma unroll
+          for (int j = 0; j < BN / 32; ++j) {
+            const bool real = in && 32 * j < nw;
+            cp_async4_or_zero(db + (j / 4) * 512 + (j & 3) * 4, real ? pw + j * 128 : a.w_scales, real);
+          }
         }
-        cp_async_arrive(&sfull[s]);
+        cp_async_arrive(&full[s]);
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -377,8 +394,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 #pragma unroll
         for (int u = 0; u < S; ++u) {
           if (u == st && ks < ksteps && ok) {
-            if (!__all_sync(0xffffffffu, mbar_test_wait(&full[u], ph) && mbar_test_wait(&sfull[u], ph))) {
-              ok = spin_or_abort(&full[u], ph, a.wait, abort_flag) && spin_or_abort(&sfull[u], ph, a.wait, abort_flag);
+            if (!warp_test_wait(&full[u], ph)) {
+              ok = spin_or_abort(&full[u], ph, a.wait, abort_flag);
               ok = __all_sync(0xffffffffu, ok);
             }
             if (ok) {
@@ -515,7 +532,7 @@ bool encode_rows(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t pit
   const cuuint32_t box[2] = {(cuuint32_t)kMxRowBytes, (cuuint32_t)box_rows};
   const cuuint32_t ones[2] = {1, 1};
   return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, ones,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -523,8 +540,8 @@ template <int BN, int OUT>
 cudaError_t launch_mx(const MxKernelArgs& args, int64_t tiles, cudaStream_t s) {
   const Mx4MatmulArgs& a = args.a;
   const int64_t pitch = (int64_t)((a.K + 31) / 32) * 16;
-  CUtensorMap map_a, map_w;
-  if (!encode_rows(&map_a, a.a_codes, a.R, pitch, kMxBoxRows) ||
+  CUtensorMap map_a, map_a32, map_w;
+  if (!encode_rows(&map_a, a.a_codes, a.R, pitch, kMxRows) || !encode_rows(&map_a32, a.a_codes, a.R, pitch, kMxBoxRows) ||
       !encode_rows(&map_w, a.w_codes, (int64_t)a.E * a.N, pitch, BN))
     return cudaErrorInvalidValue;
   constexpr int smem = MxRing<BN>::total + 1024;   // + alignment slack
@@ -541,7 +558,7 @@ cudaError_t launch_mx(const MxKernelArgs& args, int64_t tiles, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, map_a, map_w, args);
+  return cudaLaunchKernelEx(&cfg, kern, map_a, map_a32, map_w, args);
 }
 
 // Output tiles there can be at most (the device offsets decide how many there are).
