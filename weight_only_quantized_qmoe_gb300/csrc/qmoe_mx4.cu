@@ -38,23 +38,23 @@ __device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The eight elements from element `at` of x on, where `at` need not be on a
-// 16-byte boundary: the lane loads the aligned 16 bytes that hold the first of
-// them (32-bit types: also the next 16), takes the following ones from the
-// next lane, which starts 8 elements on, and shifts.  Whole warp; the tensor has
-// `hi` elements, and aligned words that are not wholly inside it are read
-// element by element.  Elements past n (of the row) become 0.
-template <int DT>
-__device__ __forceinline__ void load8_shifted(const void* x, int64_t at, int64_t hi, int n, float (&v)[8]) {
+// Eight elements of a row a lane, c .. c + 7, loaded in two steps so that the
+// next ones are on their way while these are worked on.  VEC: the rows start on
+// 16-byte boundaries, and so do the lane's elements.  Otherwise the lane loads
+// the aligned 16 bytes that hold the first of them (32-bit types: also the next
+// 16), takes the following ones from the next lane, which starts 8 elements on,
+// and shifts.  `size` is the number of elements of the tensor: aligned words
+// that are not wholly inside it are read element by element.
+template <int DT, bool VEC>
+struct Load8 {
   using T = typename ElemT<DT>::t;
-  constexpr int per = 16 / (int)sizeof(T);       // elements of 16 bytes
-  constexpr int words = DT == QMOE_F32 ? 8 : 4;  // 32-bit words a lane loads
-  const T* p = static_cast<const T*>(x) + at;
-  const int m = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));   // the same for the whole warp
-  uint32_t w[2 * words];
-  auto aligned = [&](int64_t from, uint32_t* out) {   // 16 bytes from element `from` (aligned)
-    if (from >= 0 && from + per <= hi) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(x) + from));
+  static constexpr int per = 16 / (int)sizeof(T);       // elements of 16 bytes
+  static constexpr int words = DT == QMOE_F32 ? 8 : 4;  // 32-bit words of 8 elements
+  uint32_t w[words], over[4];                           // over: lane 31's, what the next lane would have
+
+  __device__ static __forceinline__ void aligned(const T* x, int64_t from, int64_t size, uint32_t* out) {
+    if (from >= 0 && from + per <= size) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + from));
       out[0] = u.x;
       out[1] = u.y;
       out[2] = u.z;
@@ -62,56 +62,65 @@ __device__ __forceinline__ void load8_shifted(const void* x, int64_t at, int64_t
     } else {
       T e[per];
 #pragma unroll
-      for (int i = 0; i < per; ++i) e[i] = from + i >= 0 && from + i < hi ? static_cast<const T*>(x)[from + i] : T(0.f);
+      for (int i = 0; i < per; ++i) e[i] = from + i >= 0 && from + i < size ? x[from + i] : T(0.f);
       memcpy(out, e, 16);
     }
-  };
-#pragma unroll
-  for (int q = 0; q < words / 4; ++q) aligned(at - m + q * per, w + 4 * q);
-#pragma unroll
-  for (int i = 0; i < words; ++i) w[words + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
-  if ((threadIdx.x & 31) == 31 && m) aligned(at - m + 8, w + words);
-  if constexpr (DT == QMOE_F32) {
-    // shift by m words
-#pragma unroll
-    for (int i = 0; i < 10; ++i) w[i] = (m & 2) ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? __uint_as_float((m & 1) ? w[i + 1] : w[i]) : 0.f;
-  } else {
-    // shift by m halves of a word
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = (m & 4) ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = (m & 2) ? w[i + 1] : w[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = (m & 1) ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-      unpack2<DT>(u, v[2 * i], v[2 * i + 1]);
-      if (2 * i >= n) v[2 * i] = 0.f;
-      if (2 * i + 1 >= n) v[2 * i + 1] = 0.f;
-    }
   }
-}
-
-// Elements c .. c + 7 of the row that starts at element row0 and has n.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void* x, int64_t row0, int64_t c, int64_t n, int64_t hi, float (&v)[8]) {
-  const int left = (int)max((int64_t)0, min((int64_t)8, n - c));
-  if constexpr (VEC) {
-    if (left == 8) {
-      load_vec<DT, 8>(x, (size_t)(row0 + c), v);
+  // Elements before the lane's first one in its aligned 16 bytes: the same for
+  // every lane and step of a row.
+  __device__ static __forceinline__ int early(const void* x, int64_t row0) {
+    return VEC ? 0 : (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(x) + row0) & 15) / sizeof(T));
+  }
+  __device__ __forceinline__ void load(const void* base, int64_t at, int m, int64_t size) {
+    const T* x = static_cast<const T*>(base);
+#pragma unroll
+    for (int q = 0; q < words / 4; ++q) aligned(x, at - m + q * per, size, w + 4 * q);
+    if (!VEC && m && (threadIdx.x & 31) == 31) aligned(x, at - m + 8, size, over);
+  }
+  // The elements, past the row's last (left of them) 0.  Whole warp.
+  __device__ __forceinline__ void get(int m, int left, float (&v)[8]) {
+    if constexpr (!VEC) {
+      uint32_t u[words + 4];
+#pragma unroll
+      for (int i = 0; i < words; ++i) u[i] = w[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t next = __shfl_down_sync(0xffffffffu, w[i], 1);
+        u[words + i] = (threadIdx.x & 31) == 31 ? over[i] : next;
+      }
+      if constexpr (DT == QMOE_F32) {   // by m words
+#pragma unroll
+        for (int i = 0; i < 10; ++i) u[i] = (m & 2) ? u[i + 2] : u[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = (m & 1) ? u[i + 1] : u[i];
+      } else {                          // by m halves of a word
+#pragma unroll
+        for (int i = 0; i < 6; ++i) u[i] = (m & 4) ? u[i + 2] : u[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) u[i] = (m & 2) ? u[i + 1] : u[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (m & 1) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+      }
+    }
+    if constexpr (DT == QMOE_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < left ? load_d<DT>(x, (size_t)(row0 + c + i)) : 0.f;
+      for (int i = 0; i < 4; ++i) unpack2<DT>(w[i], v[2 * i], v[2 * i + 1]);
     }
-  } else {
-    load8_shifted<DT>(x, row0 + c, hi, left, v);
+    if (left < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= left) v[i] = 0.f;
+    }
   }
-}
+};
 
 // A row takes blockDim.y warps, 256 values each per step; blockDim.z rows a CTA.
 template <int DT, bool VEC, bool ACT>
 __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx4QuantArgs a) {
+  op_begin();
   const int64_t row = blockIdx.x * (int64_t)blockDim.z + threadIdx.z;
   if (row >= a.rows) return;
   const int lane = threadIdx.x;
@@ -123,16 +132,27 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
   uint8_t* scales0 = nullptr;
   if (!a.pos) scales0 = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
   const int64_t used = a.pos ? max(a.offsets[a.E], 0) : 0;
+  const int m0 = Load8<DT, VEC>::early(a.x, row0), m1 = ACT ? Load8<DT, VEC>::early(a.x, row0 + a.cols) : 0;
+  Load8<DT, VEC> next, next_up;
+  auto fetch = [&](int64_t seg) {
+    const int64_t c = seg * kQuantSeg + lane * 8;
+    next.load(a.x, row0 + c, m0, hi);
+    if (ACT) next_up.load(a.x, row0 + a.cols + c, m1, hi);
+  };
+  fetch(threadIdx.y);
   for (int64_t seg = threadIdx.y; seg * kQuantSeg < a.cols; seg += blockDim.y) {
     const int64_t c = seg * kQuantSeg + lane * 8;   // four lanes a block
     const bool in = c < (int64_t)nb * 32;
+    const int left = (int)max((int64_t)0, min((int64_t)8, a.cols - c));
+    Load8<DT, VEC> here = next, up = next_up;
+    if ((seg + blockDim.y) * kQuantSeg < a.cols) fetch(seg + blockDim.y);
     float v[8];
-    load8<DT, VEC>(a.x, row0, c, a.cols, hi, v);
+    here.get(m0, left, v);
     if (ACT) {
       float u[8];
-      load8<DT, VEC>(a.x, row0 + a.cols, c, a.cols, hi, u);
+      up.get(m1, left, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < a.cols ? glu(a.act, v[i], u[i]) : 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? glu(a.act, v[i], u[i]) : 0.f;
     }
     // the largest magnitude of the block, as its bits (they order like the
     // values, NaN above infinity above every number)
@@ -187,8 +207,7 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s) {
   const bool act = a.act.act >= 0;
   const bool vec = rows_aligned16(a.x, a.ld_x, a.dtype) && (!act || a.cols * dtype_size(a.dtype) % 16 == 0);
   auto run = [&](auto kern) {
-    kern<<<(unsigned)blocks, block, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_op(kern, dim3((unsigned)blocks), block, 0, s, a);
   };
   auto pick = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
@@ -206,6 +225,7 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s) {
 // codes and may belong to two blocks.
 template <int DT>
 __global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const Mx4DequantArgs a) {
+  op_begin();
   using T = typename ElemT<DT>::t;
   const int64_t row = blockIdx.x * (int64_t)blockDim.z + threadIdx.z;
   if (row >= a.rows) return;
@@ -214,16 +234,29 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const 
   const int m = (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + row0) & 15) / sizeof(T));
   const uint32_t* words = reinterpret_cast<const uint32_t*>(a.codes + (size_t)row * pitch);
   const uint8_t* sc = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
-  auto scale_of = [&](int64_t x) {   // of the block of element x; 2^(e - 127), e = 0 is subnormal, 255 is NaN
+  auto scale_byte = [&](int64_t x) -> uint32_t {   // of the block of element x
     const int64_t blk = min(max(x, (int64_t)0), a.cols - 1) >> 5;
-    const uint32_t e = sc[(size_t)(blk >> 2) * a.panel * 4 + (blk & 3)];
+    return sc[(size_t)(blk >> 2) * a.panel * 4 + (blk & 3)];
+  };
+  auto scale_of = [](uint32_t e) {   // 2^(e - 127); e = 0 is subnormal, 255 is NaN
     return __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
   };
-  for (int64_t g = ((int64_t)threadIdx.y * 32 + threadIdx.x) * 8; g - m < a.cols; g += (int64_t)blockDim.y * kQuantSeg) {
+  // codes and scale bytes of a step, loaded a step ahead
+  uint32_t next_hi = 0, next_lo = 0, next_e0 = 0, next_e1 = 0;
+  auto fetch = [&](int64_t g) {
+    next_hi = g < nb * 32 ? words[g >> 3] : 0u;
+    next_lo = m && g > 0 ? words[(g >> 3) - 1] : 0u;
+    next_e0 = scale_byte(g - m);
+    next_e1 = m ? scale_byte(g - m + 7) : next_e0;
+  };
+  const int64_t first = ((int64_t)threadIdx.y * 32 + threadIdx.x) * 8, step = (int64_t)blockDim.y * kQuantSeg;
+  if (first - m < a.cols) fetch(first);
+  for (int64_t g = first; g - m < a.cols; g += step) {
     const int64_t c = g - m;   // g is on the codes' grid
-    const uint32_t hi = g < nb * 32 ? words[g >> 3] : 0u, lo = m && g > 0 ? words[(g >> 3) - 1] : 0u;
+    const uint32_t hi = next_hi, lo = next_lo;
     const uint32_t code = m ? __funnelshift_r(lo, hi, 32 - 4 * m) : hi;
-    const float s0 = scale_of(c), s1 = m ? scale_of(c + 7) : s0;
+    const float s0 = scale_of(next_e0), s1 = scale_of(next_e1);
+    if (c + step < a.cols) fetch(g + step);
     const int change = m ? (int)((32 - (c & 31)) & 31) : 0;   // first element of the second block, if it is within 8
     float v[8];
 #pragma unroll
@@ -247,8 +280,7 @@ cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, cudaStream_t s) {
   const int64_t blocks = (a.rows + block.z - 1) / block.z;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto run = [&](auto kern) {
-    kern<<<(unsigned)blocks, block, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_op(kern, dim3((unsigned)blocks), block, 0, s, a);
   };
   if (a.dtype == QMOE_F32) return run(mx4_dequantize_kernel<QMOE_F32>);
   if (a.dtype == QMOE_F16) return run(mx4_dequantize_kernel<QMOE_F16>);

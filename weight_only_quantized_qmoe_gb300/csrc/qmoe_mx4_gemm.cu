@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     tmem_alloc(tmem_holder, kMxTmemCols);
     tmem_relinquish();
   }
-  pdl_wait();   // the operands and offsets may come from the kernel before
+  op_begin();   // the operands and offsets may come from the kernel before
   if (warp == 3) {
     // first row tile of each group: E experts, then the rows without a route
     int first = 0;
@@ -492,7 +492,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_launch_dependents();
   if (warp == 1) tmem_dealloc(tmem, kMxTmemCols);
 }
 

@@ -21,10 +21,11 @@ constexpr int norm_ahead(int vpt) { return vpt <= 2 ? 3 : vpt == 4 ? 2 : 0; }
 
 template <int DT, bool VECTOR, int VPT>
 __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
+  op_begin();
   using F = Frag<DT, VECTOR>;
   using T = typename ElemT<DT>::t;
   constexpr int N2 = F::n / 2, AHEAD = norm_ahead(VPT);
-  constexpr bool RING = VECTOR && AHEAD > 0;
+  constexpr bool RING = kCopies<DT, VECTOR> && AHEAD > 0;
   __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
   const float inv_h = 1.f / (float)a.H;
@@ -154,7 +155,7 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
   const int vpt = norm_vpt(a.H, frag, g.tpr);
   const int parts = 1 + (a.o ? 1 : 0) + (a.gate_kind == QMOE_GATE_FULL ? 1 : 0);
   const int threads = g.tpr * g.rpb;
-  const size_t ring = vec ? (size_t)norm_ahead(vpt) * parts * vpt * threads * 16 : 0;
+  const size_t ring = vec || a.dtype == QMOE_F32 ? (size_t)norm_ahead(vpt) * parts * vpt * threads * 16 : 0;
   return by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
     auto kern = block_norm_kernel<dt, v, n>;
     if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
@@ -168,8 +169,7 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
       if (e != cudaSuccess) return e;
       blocks = std::min<int64_t>(blocks, (int64_t)kSms * std::max(1, per));
     }
-    kern<<<(unsigned)blocks, dim3(g.tpr, g.rpb), ring, s>>>(a);
-    return cudaGetLastError();
+    return launch_op(kern, dim3((unsigned)blocks), dim3(g.tpr, g.rpb), ring, s, a);
   });
 }
 

@@ -84,11 +84,16 @@ struct Place {
   __device__ __forceinline__ bool has(int p) const { return left_of(p) > 0; }
 };
 
+// Whether rows can be copied ahead: 16 bytes at a time, or for 32-bit rows on
+// any boundary 4 (cp.async knows no 2).
+template <int DT, bool VECTOR>
+constexpr bool kCopies = VECTOR || DT == QMOE_F32;
+
 // The rows of one tensor as a thread sees them: its fragments of row after row
-// of a CTA.  With 16-byte rows (RING) a thread copies its own fragments of the
-// next rows into shared memory (cp.async) while it works on this one; nobody
-// else reads them, so there is no barrier to wait at.  Otherwise they are
-// loaded when they are used.
+// of a CTA.  With a RING a thread copies its own fragments of the next rows into
+// shared memory (cp.async) while it works on this one; nobody else reads them,
+// so there is no barrier to wait at.  Otherwise they are loaded when they are
+// used.
 template <int DT, bool VECTOR, int VPT, bool RING>
 struct Rows {
   using F = Frag<DT, VECTOR>;
@@ -111,19 +116,39 @@ struct Rows {
   __device__ __forceinline__ void fetch(uint32_t row, const Place<DT, VECTOR>& at) const {   // `row`: offset of the ring row
     if (!there) return;
 #pragma unroll
-    for (int p = 0; p < VPT; ++p)
-      if (at.has(p))
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + row + p * at.frag_bytes), "l"(next + p * at.step)
-                     : "memory");
+    for (int p = 0; p < VPT; ++p) {
+      const uint32_t to = ring + row + p * at.frag_bytes;
+      const T* from = next + p * at.step;
+      if constexpr (VECTOR) {
+        if (at.has(p)) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+      } else {
+#pragma unroll
+        for (int i = 0; i < F::n; ++i) {   // zeros past the row's end
+          const bool in = i * at.threads < at.left_of(p);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * i), "l"(in ? from + i * at.threads : next),
+                       "r"(in ? 4 : 0)
+                       : "memory");
+        }
+      }
+    }
   }
   __device__ __forceinline__ void advance() { next += step; }
   __device__ __forceinline__ void get(uint32_t row, int p, const Place<DT, VECTOR>& at, float2 (&v)[F::n / 2]) const {
     F f;
     if constexpr (RING) {
+      uint4 u;
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(f.u.x), "=r"(f.u.y), "=r"(f.u.z), "=r"(f.u.w)
+                   : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                    : "r"(ring + row + p * at.frag_bytes)
                    : "memory");
+      if constexpr (VECTOR) {
+        f.u = u;
+      } else {
+        f.e[0] = __uint_as_float(u.x);
+        f.e[1] = __uint_as_float(u.y);
+        f.e[2] = __uint_as_float(u.z);
+        f.e[3] = __uint_as_float(u.w);
+      }
     } else {
       f.load(next + p * at.step, at.left_of(p), at.threads);
     }

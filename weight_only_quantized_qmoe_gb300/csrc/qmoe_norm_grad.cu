@@ -29,10 +29,11 @@ enum { SUM_PRE = 0, SUM_POST = 1, SUM_KINDS = 2 };
 
 template <int DT, bool VECTOR, int VPT>
 __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) {
+  op_begin();
   using F = Frag<DT, VECTOR>;
   using T = typename ElemT<DT>::t;
   constexpr int N2 = F::n / 2, AHEAD = norm_grad_ahead(VPT);
-  constexpr bool RING = VECTOR && AHEAD > 0;
+  constexpr bool RING = kCopies<DT, VECTOR> && AHEAD > 0;
   __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
   const float inv_h = 1.f / (float)a.H;
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
 constexpr int kSumRows = 16;
 template <int DT>
 __global__ void __launch_bounds__(32 * kSumRows) block_norm_sums_kernel(const NormArgs a, int slices) {
+  op_begin();
   __shared__ float part[kSumRows][33];
   const int kind = blockIdx.y;
   const bool channel = a.gate_kind == QMOE_GATE_CHANNEL;
@@ -282,7 +284,7 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
   const RowShape g = row_shape(a.H, frag);
   const int vpt = norm_vpt(a.H, frag, g.tpr);
   const int parts = 1 + (a.o ? 1 : 0) + (a.dr ? 1 : 0) + (a.dh ? 1 : 0) + (a.gate_kind == QMOE_GATE_FULL ? 1 : 0);
-  const size_t ring = vec ? (size_t)norm_grad_ahead(vpt) * parts * vpt * g.tpr * g.rpb * 16 : 0;
+  const size_t ring = vec || a.dtype == QMOE_F32 ? (size_t)norm_grad_ahead(vpt) * parts * vpt * g.tpr * g.rpb * 16 : 0;
   const int64_t ctas = norm_grad_ctas(a.T, g);
   if (ctas > 0) {   // without rows the sums are zeros
     const cudaError_t e = by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
@@ -291,17 +293,15 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
         const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
         if (err != cudaSuccess) return err;
       }
-      kern<<<(unsigned)ctas, dim3(g.tpr, g.rpb), ring, s>>>(a);
-      return cudaGetLastError();
+      return launch_op(kern, dim3((unsigned)ctas), dim3(g.tpr, g.rpb), ring, s, a);
     });
     if (e != cudaSuccess) return e;
   }
   const dim3 grid((unsigned)((a.H + 31) / 32), SUM_KINDS), block(32, kSumRows);
   const int slices = (int)(ctas * g.rpb);
-  if (a.dtype == QMOE_F32) block_norm_sums_kernel<QMOE_F32><<<grid, block, 0, s>>>(a, slices);
-  else if (a.dtype == QMOE_F16) block_norm_sums_kernel<QMOE_F16><<<grid, block, 0, s>>>(a, slices);
-  else block_norm_sums_kernel<QMOE_BF16><<<grid, block, 0, s>>>(a, slices);
-  return cudaGetLastError();
+  if (a.dtype == QMOE_F32) return launch_op(block_norm_sums_kernel<QMOE_F32>, grid, block, 0, s, a, slices);
+  if (a.dtype == QMOE_F16) return launch_op(block_norm_sums_kernel<QMOE_F16>, grid, block, 0, s, a, slices);
+  return launch_op(block_norm_sums_kernel<QMOE_BF16>, grid, block, 0, s, a, slices);
 }
 
 }  // namespace qmoe

@@ -3,6 +3,8 @@
 // qmoe_mx4.cu, qmoe_mx4_gemm.cu, qmoe_norm.cu).
 #pragma once
 
+#include <utility>
+
 #include "qmoe_internal.cuh"
 
 namespace qmoe {
@@ -142,6 +144,32 @@ inline bool rows_aligned16(const void* p, int64_t ld, int dtype) {
 
 #ifdef __CUDACC__
 namespace qmoe {
+
+// Launches with programmatic dependent launch: the kernel may start while the
+// one before it on the stream ends, and waits (op_begin) before it touches
+// memory.  Small calls follow one another at launch latency; this takes its
+// greater part off.
+template <typename... Params, typename... Args>
+cudaError_t launch_op(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+// First thing in an operator's kernel: lets the next one start (once every CTA
+// of this one has), and waits for the ones before.  What follows sees their
+// memory, and as every operator waits, theirs before them too.
+__device__ __forceinline__ void op_begin() {
+  pdl_launch_dependents();
+  pdl_wait();
+}
 
 // VEC consecutive elements of type DT as floats: 16-byte accesses (VEC * size
 // a multiple of 16), or one element.

@@ -37,12 +37,14 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
   const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = a.E;
+  const int E = a.E, pitch = E | 1;    // an odd pitch: a warp reads a column of counters without bank conflicts
   extern __shared__ int sort_smem[];
-  int* cnt = sort_smem;             // [W][E]: counts, then the next row of (warp, expert)
-  int* tot = cnt + (size_t)W * E;   // [E]: this CTA's counts (read by the other CTAs)
-  int* off = tot + E;               // [E + 1]: all counts, then first rows
-  for (int i = threadIdx.x; i < W * E; i += blockDim.x) cnt[i] = 0;
+  int* cnt = sort_smem;                 // [W][pitch]: counts, then the warp's next rank within the CTA
+  int* tot = cnt + (size_t)W * pitch;   // [E]: this CTA's counts (read by the other CTAs)
+  int* base = tot + E;                  // [E]: routes of earlier CTAs
+  int* off = base + E;                  // [E + 1]: all counts, then first rows
+  for (int i = threadIdx.x; i < W * pitch; i += blockDim.x) cnt[i] = 0;
+  op_begin();
   __syncthreads();
 
   const ID* ids = static_cast<const ID*>(a.ids);
@@ -54,47 +56,59 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
   // routes [r0, r1) of this warp, a multiple of 32 each but the last
   const int64_t per = ((a.R + (int64_t)C * W - 1) / ((int64_t)C * W) + 31) / 32 * 32;
   const int64_t r0 = std::min<int64_t>(a.R, per * ((int64_t)c * W + warp)), r1 = std::min<int64_t>(a.R, r0 + per);
-  int* mine = cnt + (size_t)warp * E;
-  constexpr int U = 4;              // ids in flight per lane
-  for (int64_t b = r0; b < r1; b += 32 * U) {
-    int e[U];
+  int* mine = cnt + (size_t)warp * pitch;
+  constexpr int U = 4;                  // ids in flight per lane
+  int e[U];
+  auto fetch = [&](int64_t b) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = b + 32 * u + lane;
       e[u] = r < r1 ? id_of(r) : -1;
     }
+  };
+  for (int64_t b = r0; b < r1; b += 32 * U) {
+    fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (e[u] >= 0) atomicAdd(mine + e[u], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int n = 0;
-    for (int w = 0; w < W; ++w) n += cnt[(size_t)w * E + e];
-    tot[e] = n;
+  // a warp takes an expert at a time, a lane the counter of a warp: counts
+  // become ranks within the CTA
+  for (int x = warp; x < E; x += W) {
+    const int n = lane < W ? cnt[(size_t)lane * pitch + x] : 0;
+    int run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    if (lane < W) cnt[(size_t)lane * pitch + x] = run - n;
+    if (lane == 31) tot[x] = run;
   }
-  cluster.sync();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+  if (C > 1) cluster.sync();
+  else __syncthreads();
+  for (int x = threadIdx.x; x < E; x += blockDim.x) {
     int before = 0, all = 0;
-    for (int q = 0; q < C; ++q) {
-      const int n = cluster.map_shared_rank(tot, q)[e];
-      before += q < c ? n : 0;
-      all += n;
+    if (C > 1) {
+#pragma unroll
+      for (int q = 0; q < kSortCluster; ++q) {
+        const int n = cluster.map_shared_rank(tot, q)[x];
+        before += q < c ? n : 0;
+        all += n;
+      }
+    } else {
+      all = tot[x];
     }
-    off[e] = all;
-    // counts -> rows of (warp, expert) within the expert
-    for (int w = 0; w < W; ++w) {
-      const int n = cnt[(size_t)w * E + e];
-      cnt[(size_t)w * E + e] = before;
-      before += n;
-    }
+    base[x] = before;
+    off[x] = all;
   }
   __syncthreads();
   if (warp == 0) {
     // exclusive scan of the expert counts: a contiguous run of experts a lane
     const int per_lane = (E + 31) / 32, e0 = std::min(E, lane * per_lane), e1 = std::min(E, e0 + per_lane);
     int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += off[e];
+    for (int x = e0; x < e1; ++x) sum += off[x];
     int run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -102,9 +116,9 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
       if (lane >= o) run += up;
     }
     int first = run - sum;
-    for (int e = e0; e < e1; ++e) {
-      const int n = off[e];
-      off[e] = first;
+    for (int x = e0; x < e1; ++x) {
+      const int n = off[x];
+      off[x] = first;
       first += n;
     }
     if (lane == 31) off[E] = run;
@@ -112,17 +126,13 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
   __syncthreads();
   const int used = off[E];
   if (c == 0)
-    for (int e = threadIdx.x; e <= E; e += blockDim.x) a.offsets[e] = off[e];
+    for (int x = threadIdx.x; x <= E; x += blockDim.x) a.offsets[x] = off[x];
   // rows without a route
   for (int64_t i = used + (int64_t)c * blockDim.x + threadIdx.x; i < a.R; i += (int64_t)C * blockDim.x) a.perm[i] = -1;
 
+  const bool again = r1 - r0 > 32 * U;  // else the ids are still in registers
   for (int64_t b = r0; b < r1; b += 32 * U) {
-    int e[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = b + 32 * u + lane;
-      e[u] = r < r1 ? id_of(r) : -1;
-    }
+    if (again) fetch(b);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t r = b + 32 * u + lane;
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
       const unsigned peers = __match_any_sync(0xffffffffu, e[u]);
       const int rank = __popc(peers & ((1u << lane) - 1u));
       int p = -1;
-      if (e[u] >= 0) p = off[e[u]] + mine[e[u]] + rank;
+      if (e[u] >= 0) p = off[e[u]] + base[e[u]] + mine[e[u]] + rank;
       __syncwarp();
       if (e[u] >= 0 && rank == 0) mine[e[u]] += __popc(peers);
       __syncwarp();
@@ -140,7 +150,7 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
       }
     }
   }
-  cluster.sync();   // no CTA leaves while another may still read its counts
+  if (C > 1) cluster.sync();   // no CTA leaves while another may still read its counts
 }
 
 cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
@@ -150,21 +160,23 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
   const int C = a.R <= 1024 ? 1 : kSortCluster;
   const int64_t passes = (a.R + 32 * C - 1) / (32 * C);
   const int W = (int)std::max<int64_t>(1, std::min<int64_t>(32, passes));
-  const size_t smem = ((size_t)W * a.E + 2 * (size_t)a.E + 1) * sizeof(int);
+  const size_t smem = ((size_t)W * (a.E | 1) + 3 * (size_t)a.E + 1) * sizeof(int);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)C, 1, 1};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)C, 1, 1};
   cfg.gridDim = dim3(C);
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;   // a single CTA is its own cluster
+  cfg.numAttrs = C > 1 ? 2 : 1;   // a single CTA is its own cluster
   auto run = [&](auto kern) {
     if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
+      const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (err != cudaSuccess) return err;
     }
     return cudaLaunchKernelEx(&cfg, kern, a);
   };
@@ -210,6 +222,7 @@ __device__ __forceinline__ void zero_unused_rows(const RowsArgs& a, int64_t t) {
 
 template <int DT, bool VECTOR>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowsArgs a) {
+  op_begin();
   using F = Frag<DT, VECTOR>;
   const int H = (int)a.H;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
@@ -228,6 +241,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowsArgs a)
 
 template <int DT, bool VECTOR, int SLOTS>
 __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_kernel(const RowsArgs a) {
+  op_begin();
   using F = Frag<DT, VECTOR>;
   const int H = (int)a.H;
   const int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
@@ -287,6 +301,7 @@ __device__ __forceinline__ int warp_sums(float (&v)[N]) {
 
 template <int DT, bool VECTOR, int SLOTS>
 __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_grad_kernel(const RowsArgs a) {
+  op_begin();
   using F = Frag<DT, VECTOR>;
   const int H = (int)a.H;
   __shared__ float part[kRowThreads / 32][SLOTS];
@@ -387,8 +402,7 @@ cudaError_t launch_dispatch(const RowsArgs& a, cudaStream_t s) {
   return by_rows(a, [&](auto dt, auto vec, auto) {
     dim3 grid;
     const RowShape r = rows_of<dt, vec>(a, &grid);
-    dispatch_kernel<dt, vec><<<grid, dim3(r.tpr, r.rpb), 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_op(dispatch_kernel<dt, vec>, grid, dim3(r.tpr, r.rpb), 0, s, a);
   });
 }
 
@@ -396,8 +410,7 @@ cudaError_t launch_combine(const RowsArgs& a, cudaStream_t s) {
   return by_rows(a, [&](auto dt, auto vec, auto slots) {
     dim3 grid;
     const RowShape r = rows_of<dt, vec>(a, &grid);
-    combine_kernel<dt, vec, slots><<<grid, dim3(r.tpr, r.rpb), 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_op(combine_kernel<dt, vec, slots>, grid, dim3(r.tpr, r.rpb), 0, s, a);
   });
 }
 
@@ -405,8 +418,7 @@ cudaError_t launch_combine_grad(const RowsArgs& a, cudaStream_t s) {
   return by_rows(a, [&](auto dt, auto vec, auto slots) {
     dim3 grid;
     const RowShape r = rows_of<dt, vec>(a, &grid);
-    combine_grad_kernel<dt, vec, slots><<<grid, dim3(r.tpr, r.rpb), 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_op(combine_grad_kernel<dt, vec, slots>, grid, dim3(r.tpr, r.rpb), 0, s, a);
   });
 }
 
