@@ -115,40 +115,37 @@ struct Rows {
   }
   __device__ __forceinline__ void fetch(uint32_t row, const Place<DT, VECTOR>& at) const {   // `row`: offset of the ring row
     if (!there) return;
+    if constexpr (VECTOR) {
 #pragma unroll
-    for (int p = 0; p < VPT; ++p) {
-      const uint32_t to = ring + row + p * at.frag_bytes;
-      const T* from = next + p * at.step;
-      if constexpr (VECTOR) {
-        if (at.has(p)) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-      } else {
+      for (int p = 0; p < VPT; ++p)
+        if (at.has(p))
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + row + p * at.frag_bytes), "l"(next + p * at.step)
+                       : "memory");
+    } else {
+#pragma unroll
+      for (int p = 0; p < VPT; ++p)
 #pragma unroll
         for (int i = 0; i < F::n; ++i) {   // zeros past the row's end
           const bool in = i * at.threads < at.left_of(p);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * i), "l"(in ? from + i * at.threads : next),
-                       "r"(in ? 4 : 0)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ring + row + p * at.frag_bytes + 4 * i),
+                       "l"(in ? next + p * at.step + i * at.threads : next), "r"(in ? 4 : 0)
                        : "memory");
         }
-      }
     }
   }
   __device__ __forceinline__ void advance() { next += step; }
   __device__ __forceinline__ void get(uint32_t row, int p, const Place<DT, VECTOR>& at, float2 (&v)[F::n / 2]) const {
     F f;
-    if constexpr (RING) {
-      uint4 u;
+    if constexpr (RING && VECTOR) {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                   : "=r"(f.u.x), "=r"(f.u.y), "=r"(f.u.z), "=r"(f.u.w)
                    : "r"(ring + row + p * at.frag_bytes)
                    : "memory");
-      if constexpr (VECTOR) {
-        f.u = u;
-      } else {
-        f.e[0] = __uint_as_float(u.x);
-        f.e[1] = __uint_as_float(u.y);
-        f.e[2] = __uint_as_float(u.z);
-        f.e[3] = __uint_as_float(u.w);
-      }
+    } else if constexpr (RING) {
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(f.e[0]), "=f"(f.e[1]), "=f"(f.e[2]), "=f"(f.e[3])
+                   : "r"(ring + row + p * at.frag_bytes)
+                   : "memory");
     } else {
       f.load(next + p * at.step, at.left_of(p), at.threads);
     }
