@@ -132,20 +132,22 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
   uint8_t* scales0 = nullptr;
   if (!a.pos) scales0 = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
   const int64_t used = a.pos ? max(a.offsets[a.E], 0) : 0;
+  // a routed row's output rows, a lane each, known before its values are
+  const int first_rows = a.pos && lane < a.k ? a.pos[row * a.k + lane] : -1;
+  const int cols = (int)a.cols, step = blockDim.y * kQuantSeg;
   const int m0 = Load8<DT, VEC>::early(a.x, row0), m1 = ACT ? Load8<DT, VEC>::early(a.x, row0 + a.cols) : 0;
   Load8<DT, VEC> next, next_up;
-  auto fetch = [&](int64_t seg) {
-    const int64_t c = seg * kQuantSeg + lane * 8;
+  auto fetch = [&](int c) {
     next.load(a.x, row0 + c, m0, hi);
     if (ACT) next_up.load(a.x, row0 + a.cols + c, m1, hi);
   };
-  fetch(threadIdx.y);
-  for (int64_t seg = threadIdx.y; seg * kQuantSeg < a.cols; seg += blockDim.y) {
-    const int64_t c = seg * kQuantSeg + lane * 8;   // four lanes a block
-    const bool in = c < (int64_t)nb * 32;
-    const int left = (int)max((int64_t)0, min((int64_t)8, a.cols - c));
+  const int c0 = (int)threadIdx.y * kQuantSeg + lane * 8;   // four lanes a block
+  fetch(c0);
+  for (int c = c0; c - lane * 8 < cols; c += step) {
+    const bool in = c < nb * 32;
+    const int left = max(0, min(8, cols - c));
     Load8<DT, VEC> here = next, up = next_up;
-    if ((seg + blockDim.y) * kQuantSeg < a.cols) fetch(seg + blockDim.y);
+    if (c - lane * 8 + step < cols) fetch(c + step);
     float v[8];
     here.get(m0, left, v);
     if (ACT) {
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
     // four blocks' scale bytes in one word, held by the first lane of each 16
     sc |= __shfl_down_sync(0xffffffffu, sc, 4) << 8;
     sc |= __shfl_down_sync(0xffffffffu, sc, 8) << 16;
-    const int64_t q = c >> 7;
+    const int q = c >> 7;
     const bool has_scale = (lane & 15) == 0 && q < nq;
     if (!a.pos) {
       if (in) *reinterpret_cast<uint32_t*>(a.codes + (size_t)(row * pitch + (c >> 1))) = code;
@@ -180,16 +182,15 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
     } else {   // one panel of rows * k rows
       uint8_t* codes = a.codes + (c >> 1);
       uint8_t* scales = a.scales + (size_t)q * a.panel * 4;
+      auto put = [&](int64_t p, uint32_t code_word, uint32_t scale_word) {
+        if (in) *reinterpret_cast<uint32_t*>(codes + (size_t)(p * pitch)) = code_word;
+        if (has_scale) *reinterpret_cast<uint32_t*>(scales + (size_t)p * 4) = scale_word;
+      };
       for (int j = 0; j < a.k; ++j) {
-        const int64_t p = a.pos[row * a.k + j];
-        if (p < 0 || p >= a.panel) continue;
-        if (in) *reinterpret_cast<uint32_t*>(codes + (size_t)(p * pitch)) = code;
-        if (has_scale) *reinterpret_cast<uint32_t*>(scales + (size_t)p * 4) = sc;
+        const int p = j < 32 ? __shfl_sync(0xffffffffu, first_rows, j) : a.pos[row * a.k + j];
+        if (p >= 0 && p < a.panel) put(p, code, sc);
       }
-      for (int64_t p = used + row; p < a.panel; p += a.rows) {   // rows without a route
-        if (in) *reinterpret_cast<uint32_t*>(codes + (size_t)(p * pitch)) = 0u;
-        if (has_scale) *reinterpret_cast<uint32_t*>(scales + (size_t)p * 4) = 0u;
-      }
+      for (int64_t p = used + row; p < a.panel; p += a.rows) put(p, 0u, 0u);   // rows without a route
     }
   }
 }
@@ -229,34 +230,37 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const 
   using T = typename ElemT<DT>::t;
   const int64_t row = blockIdx.x * (int64_t)blockDim.z + threadIdx.z;
   if (row >= a.rows) return;
-  const int64_t nb = (a.cols + 31) / 32, nq = (nb + 3) / 4, pitch = nb * 16;
+  const int nb = (int)((a.cols + 31) / 32), nq = (nb + 3) / 4;
+  const int64_t pitch = (int64_t)nb * 16;
   const size_t row0 = (size_t)(row * a.ld_out);
   const int m = (int)((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + row0) & 15) / sizeof(T));
   const uint32_t* words = reinterpret_cast<const uint32_t*>(a.codes + (size_t)row * pitch);
   const uint8_t* sc = a.scales + mx4_scale_offset(row, 0, a.panel, nq);
-  auto scale_byte = [&](int64_t x) -> uint32_t {   // of the block of element x
-    const int64_t blk = min(max(x, (int64_t)0), a.cols - 1) >> 5;
-    return sc[(size_t)(blk >> 2) * a.panel * 4 + (blk & 3)];
+  const int cols = (int)a.cols;
+  const size_t panel_bytes = 4 * (size_t)a.panel;
+  auto scale_byte = [&](int x) -> uint32_t {   // of the block of element x
+    const int blk = min(max(x, 0), cols - 1) >> 5;
+    return sc[(size_t)(blk >> 2) * panel_bytes + (blk & 3)];
   };
   auto scale_of = [](uint32_t e) {   // 2^(e - 127); e = 0 is subnormal, 255 is NaN
     return __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7fc00000u : e << 23));
   };
   // codes and scale bytes of a step, loaded a step ahead
   uint32_t next_hi = 0, next_lo = 0, next_e0 = 0, next_e1 = 0;
-  auto fetch = [&](int64_t g) {
+  auto fetch = [&](int g) {
     next_hi = g < nb * 32 ? words[g >> 3] : 0u;
     next_lo = m && g > 0 ? words[(g >> 3) - 1] : 0u;
     next_e0 = scale_byte(g - m);
     next_e1 = m ? scale_byte(g - m + 7) : next_e0;
   };
-  const int64_t first = ((int64_t)threadIdx.y * 32 + threadIdx.x) * 8, step = (int64_t)blockDim.y * kQuantSeg;
-  if (first - m < a.cols) fetch(first);
-  for (int64_t g = first; g - m < a.cols; g += step) {
-    const int64_t c = g - m;   // g is on the codes' grid
+  const int first = ((int)threadIdx.y * 32 + threadIdx.x) * 8, step = blockDim.y * kQuantSeg;
+  if (first - m < cols) fetch(first);
+  for (int g = first; g - m < cols; g += step) {
+    const int c = g - m;   // g is on the codes' grid
     const uint32_t hi = next_hi, lo = next_lo;
     const uint32_t code = m ? __funnelshift_r(lo, hi, 32 - 4 * m) : hi;
     const float s0 = scale_of(next_e0), s1 = scale_of(next_e1);
-    if (c + step < a.cols) fetch(g + step);
+    if (c + step < cols) fetch(g + step);
     const int change = m ? (int)((32 - (c & 31)) & 31) : 0;   // first element of the second block, if it is within 8
     float v[8];
 #pragma unroll
@@ -265,12 +269,12 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const 
       v[2 * i] = f.x * (change && 2 * i >= change ? s1 : s0);
       v[2 * i + 1] = f.y * (change && 2 * i + 1 >= change ? s1 : s0);
     }
-    if (c >= 0 && c + 8 <= a.cols) {
+    if (c >= 0 && c + 8 <= cols) {
       store_vec<DT, 8>(a.out, row0 + c, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c + i >= 0 && c + i < a.cols) store_d<DT>(a.out, row0 + c + i, v[i]);
+        if (c + i >= 0 && c + i < cols) store_d<DT>(a.out, row0 + c + i, v[i]);
     }
   }
 }
