@@ -24,11 +24,13 @@
 // under the MMAs of the next.  CTAs are persistent over the (expert, row tile,
 // weight tile) list, which every CTA derives from the device offsets.
 //
-// Bound: at few rows an expert the weight bytes (17/32 byte a weight); at many
-// the output bytes and the tensor pipe together.  BN = 192 needs 10 KB of
-// shared-memory operand reads per 96 cycles of MMA (below its 128 B / cycle);
-// BN = 64 serves products with fewer tiles than multiprocessors, where more,
-// smaller tiles put more of the machine's copy bandwidth to work.
+// Bound: at few rows an expert the weight bytes (17/32 byte a weight; 256 rows
+// of 2048 to 1536 over 128 experts: 34 us, 6.3 TB/s); at many the way of a stage
+// round the ring, about 4000 cycles for four stages of 384 cycles of MMAs
+// (32768 rows of 1536 to 4096 over 64 experts: 125 us, 3.3 PFLOP/s, 4.1 TB/s of
+// its bytes; the same copies without MMAs, scales and stores take 107).  BN =
+// 192 is what two accumulators and the scales leave of TMEM; BN = 64 puts more
+// multiprocessors to work where there are few tiles.
 //
 // Every wait is bounded; a timeout aborts all roles, drains what is in
 // flight, frees TMEM and is reported by qmoe_op_poll_status.
@@ -571,16 +573,19 @@ int64_t most_tiles(const Mx4MatmulArgs& a, int bn) {
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int inject_stall, cudaStream_t s) {
   MxKernelArgs args{a, inject_stall, 0};
   args.vec_out = rows_aligned16(a.out, a.ld_out, a.out_dtype) ? 1 : 0;
-  const int64_t wide = most_tiles(a, 192);
   auto run = [&](auto bn, int64_t tiles) {
     constexpr int BN = decltype(bn)::value;
     if (a.out_dtype == QMOE_F32) return launch_mx<BN, QMOE_F32>(args, tiles, s);
     if (a.out_dtype == QMOE_F16) return launch_mx<BN, QMOE_F16>(args, tiles, s);
     return launch_mx<BN, QMOE_BF16>(args, tiles, s);
   };
-  // fewer wide tiles than multiprocessors: narrow ones
-  return wide >= kSms ? run(std::integral_constant<int, 192>{}, wide)
-                     : run(std::integral_constant<int, 64>{}, most_tiles(a, 64));
+  // narrow tiles while they are all under way at once, wide ones from then on
+  // (us, narrow / wide: 64 x 4096 x 4096, 64 narrow tiles, 9.4 / 10.3; 1 x 8192 x
+  // 2048, 128, 7.9 / 8.0; 512 x 4096 x 4096, 320, 13.9 / 9.9; 2048 x 4096 x 4096,
+  // 1088, 38.9 / 20.8)
+  const int64_t narrow = most_tiles(a, 64);
+  return narrow <= kSms ? run(std::integral_constant<int, 64>{}, narrow)
+                        : run(std::integral_constant<int, 192>{}, most_tiles(a, 192));
 }
 
 }  // namespace qmoe
