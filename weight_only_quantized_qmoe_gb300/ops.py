@@ -27,6 +27,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import QMoEError, binding
 
@@ -137,6 +138,7 @@ class _DispatchFn(torch.autograd.Function):
         return _c.dispatch(x, plan)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dxs):
         return dispatch_grad(dxs, ctx.plan), None
 
@@ -149,6 +151,7 @@ class _CombineFn(torch.autograd.Function):
         return _c.combine(y, weights, plan)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         y, weights = ctx.saved_tensors
         dy, dw = combine_grad(dout, y, weights, ctx.plan, ctx.needs_input_grad[0],
@@ -227,6 +230,7 @@ class _BlockNormFn(torch.autograd.Function):
         return r, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dr, dh):
         x, o, gate, w_post, w_pre, s1, s2 = ctx.saved_tensors
         g = _c.block_norm_grad(x, o, gate, w_post, w_pre, dr, dh, s1, s2, ctx.residual_scale)
