@@ -272,6 +272,8 @@ struct Frag<DT, true> {
   __device__ __forceinline__ void load(const typename ElemT<DT>::t* p, int, int) {
     u = __ldg(reinterpret_cast<const uint4*>(p));
   }
+  // the same for rows that are read once: they do not pass through the L1
+  __device__ __forceinline__ void load_once(const typename ElemT<DT>::t* p, int, int) { u = ld_nc_v4(p); }
   __device__ __forceinline__ void get(float (&v)[n]) const {
     if constexpr (DT == QMOE_F32) {
       v[0] = __uint_as_float(u.x);
@@ -305,6 +307,7 @@ struct Frag<DT, false> {
 #pragma unroll
     for (int i = 0; i < n; ++i) e[i] = i * threads < left ? p[i * threads] : T(0.f);
   }
+  __device__ __forceinline__ void load_once(const T* p, int left, int threads) { load(p, left, threads); }
   __device__ __forceinline__ void get(float (&v)[n]) const {
 #pragma unroll
     for (int i = 0; i < n; ++i) v[i] = load_d<DT>(&e[i], 0);

@@ -13,7 +13,7 @@
 // its k rows in expert order once each, so every row crosses the memory
 // exactly once, whole.  No atomics: every result has one owner and one order.
 // Bound by those bytes (bf16, 4096 tokens to 8 experts, rows of 4096: dispatch
-// 45 us, 6.7 TB/s; combine 61 us, 5.0 TB/s; 6001 to 4, rows of 2880: gradient of
+// 45 us, 6.7 TB/s; combine 56 us, 5.4 TB/s; 6001 to 4, rows of 2880: gradient of
 // the combine 50 us, 6.2 TB/s).
 #include <cooperative_groups.h>
 
@@ -194,6 +194,8 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
 // (SLOTS of them, 1 to 8, the least that holds top_k; more than 8 in turns) are
 // in flight together: with eight rows unpacked to 32 bits ahead of their use
 // a thread took 128 registers and the sum ran at a quarter of the bandwidth.
+// Rows pass by the L1, as each is read once (sum of 4096 x 8 rows of 4096: 56 us,
+// through it 60).
 
 // Threads of a row at most, and CTAs a multiprocessor the registers are cut
 // for: many short CTAs, whose loads, sums and stores fall at different times
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowsArgs a)
   const int* pos = a.pos + t * a.k;
   for (int c = F::first(threadIdx.x); c < H; c += F::step(blockDim.x)) {
     F f;
-    f.load(static_cast<const typename ElemT<DT>::t*>(a.src) + t * a.ld_src + c, H - c, blockDim.x);
+    f.load_once(static_cast<const typename ElemT<DT>::t*>(a.src) + t * a.ld_src + c, H - c, blockDim.x);
     for (int j = 0; j < a.k; ++j) {
       const int64_t p = slot_row(a, pos[j]);
       if (p >= 0) f.store(static_cast<typename ElemT<DT>::t*>(a.dst) + p * a.H + c, H - c, blockDim.x);
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_kernel(c
       }
 #pragma unroll
       for (int u = 0; u < SLOTS; ++u)
-        if (p[u] >= 0) f[u].load(static_cast<const typename ElemT<DT>::t*>(a.src) + (int64_t)p[u] * a.ld_src + c, H - c, blockDim.x);
+        if (p[u] >= 0) f[u].load_once(static_cast<const typename ElemT<DT>::t*>(a.src) + (int64_t)p[u] * a.ld_src + c, H - c, blockDim.x);
 #pragma unroll
       for (int u = 0; u < SLOTS; ++u)
         if (p[u] >= 0) {
@@ -324,11 +326,11 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(SLOTS)) combine_grad_ker
     if (live) {
       for (int c = F::first(threadIdx.x); c < H; c += F::step(blockDim.x)) {
         F fg, f[SLOTS];
-        fg.load(static_cast<const typename ElemT<DT>::t*>(a.src) + t * a.ld_src + c, H - c, blockDim.x);
+        fg.load_once(static_cast<const typename ElemT<DT>::t*>(a.src) + t * a.ld_src + c, H - c, blockDim.x);
         if (a.dw) {
 #pragma unroll
           for (int u = 0; u < SLOTS; ++u)
-            if (p[u] >= 0) f[u].load(static_cast<const typename ElemT<DT>::t*>(a.y) + (int64_t)p[u] * a.ld_y + c, H - c, blockDim.x);
+            if (p[u] >= 0) f[u].load_once(static_cast<const typename ElemT<DT>::t*>(a.y) + (int64_t)p[u] * a.ld_y + c, H - c, blockDim.x);
         }
         float g[F::n];
         fg.get(g);
