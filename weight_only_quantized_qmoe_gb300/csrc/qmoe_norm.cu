@@ -11,7 +11,7 @@
 // are read once and r and h written once.  The two sums of a row follow one
 // another, so what decides is how many rows are on their way meanwhile: CTAs
 // stay and walk the rows, a ring of rows ahead of themselves.  (bf16, 4096 rows
-// of 4096: 31 us, 4.3 TB/s; rows loaded when they are used took 50.)
+// of 4096: 29 us, 4.6 TB/s; rows loaded when they are used took 50.)
 #include "qmoe_norm.cuh"
 
 namespace qmoe {
@@ -20,7 +20,11 @@ namespace qmoe {
 // allows; 0: rows are loaded when they are used.
 constexpr int norm_ahead(int vpt) { return vpt <= 2 ? 3 : vpt == 4 ? 2 : 0; }
 
-template <int DT, bool VECTOR, int VPT>
+// ALL: both norms and r are there, and no gate of its own for every value.
+// Known when the kernel is compiled, the tests for each tensor leave the loop
+// over the rows (bf16, with / without, 4096 rows of 4096: 29 / 33 us, 8192 of
+// 2048: 36 / 45, 4096 of 8192: 52 / 58).
+template <int DT, bool VECTOR, int VPT, bool ALL>
 __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   op_begin();
   using F = Frag<DT, VECTOR>;
@@ -30,7 +34,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
   const float inv_h = 1.f / (float)a.H;
-  const bool full = a.gate_kind == QMOE_GATE_FULL, branch = a.o != nullptr;
+  const bool full = !ALL && a.gate_kind == QMOE_GATE_FULL, branch = ALL || a.o;
   const int64_t stride = gridDim.x * (int64_t)blockDim.y;
   int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   int turn = 0, parts = 0;
@@ -39,8 +43,9 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
   Rows<DT, VECTOR, VPT, RING> x(a.x, a.ld_x, t, stride, ring, parts, me), o(a.o, a.ld_o, t, stride, ring, parts, me),
       g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts, me);
   const uint32_t row_bytes = parts * VPT * me.frag_bytes;
-  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me),
-      pre(a.w_pre, nullptr, me);
+  uint32_t cols = 0;   // none in shared memory
+  const Columns<DT, VECTOR, VPT, false> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me, cols),
+      pre(a.w_pre, nullptr, me, cols);
   const int64_t out_step = stride * a.H;
   T* out_r = static_cast<T*>(a.r) + t * a.H + F::first(threadIdx.x);
   T* out_h = static_cast<T*>(a.h) + t * a.H + F::first(threadIdx.x);
@@ -72,7 +77,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
       cp_async_wait<AHEAD - 1>();
     }
     float rstd1 = 1.f;
-    if (branch && a.w_post) {
+    if (ALL || (branch && a.w_post)) {
       float2 ss = both(0.f);
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
 #pragma unroll
           for (int i = 0; i < N2; ++i) r[p][i] = fma2(mul2(v[i], c1), w[i], r[p][i]);
         }
-        if (a.r) put<DT, VECTOR>(out_r, p, me, r[p]);
+        if (ALL || a.r) put<DT, VECTOR>(out_r, p, me, r[p]);
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
           if constexpr (!VECTOR) {   // past the row's end
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
       }
     }
     if (a.rstd_post && live && threadIdx.x == 0) a.rstd_post[t] = rstd1;
-    if (a.w_pre) {
+    if (ALL || a.w_pre) {
       const float rstd2 = rsqrtf(row_sum(ss.x + ss.y, red, turn) * inv_h + a.eps);
       if (a.rstd_pre && live && threadIdx.x == 0) a.rstd_pre[t] = rstd2;
 #pragma unroll
@@ -156,9 +161,10 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
   const int vpt = norm_vpt(a.H, frag, g.tpr);
   const int parts = 1 + (a.o ? 1 : 0) + (a.gate_kind == QMOE_GATE_FULL ? 1 : 0);
   const int threads = g.tpr * g.rpb;
+  const bool all = a.o && a.w_post && a.w_pre && a.r && a.gate_kind != QMOE_GATE_FULL;
   const size_t ring = vec || a.dtype == QMOE_F32 ? (size_t)norm_ahead(vpt) * parts * vpt * threads * 16 : 0;
   return by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
-    auto kern = block_norm_kernel<dt, v, n>;
+    auto kern = all ? block_norm_kernel<dt, v, n, true> : block_norm_kernel<dt, v, n, false>;
     if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
       if (e != cudaSuccess) return e;

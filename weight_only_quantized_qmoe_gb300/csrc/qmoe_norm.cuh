@@ -162,15 +162,17 @@ __device__ __forceinline__ void cp_async_wait() {
 // where there are none.  It is the same for every row: a thread's only
 // fragment stays in registers as fp32, two as they are in memory, more are
 // loaded again (loaded for every row they came from the L2, time after time:
-// the rings leave little of the L1).
-template <int DT, bool VECTOR, int VPT>
+// the rings leave little of the L1).  SHARED: a thread keeps its fragments in
+// shared memory, behind the ring, where the registers are needed otherwise.
+template <int DT, bool VECTOR, int VPT, bool SHARED>
 struct Columns {
   using F = Frag<DT, VECTOR>;
   using T = typename ElemT<DT>::t;
   static constexpr int N2 = F::n / 2;
   const T *a, *b;
   float2 held[VPT == 1 ? N2 : 1];
-  F fa[VPT == 2 ? 2 : 1], fb[VPT == 2 ? 2 : 1];
+  F fa[VPT == 2 && !SHARED ? 2 : 1], fb[VPT == 2 && !SHARED ? 2 : 1];
+  uint32_t place, part;   // SHARED: this thread's first fragment of `a`, bytes from there to the one of `b`
   __device__ __forceinline__ void compute(const F& x, const F& y, float2 (&v)[N2]) const {
     if (a) {
       get2(x, v);
@@ -185,10 +187,41 @@ struct Columns {
       for (int i = 0; i < N2; ++i) v[i] = mul2(v[i], w[i]);
     }
   }
-  __device__ __forceinline__ Columns(const void* a_, const void* b_, const Place<DT, VECTOR>& at) {
+  // fragments of 16 bytes in shared memory, read by the thread that wrote them
+  static __device__ __forceinline__ void keep(uint32_t to, const F& f) {
+    static_assert(sizeof(F) == 16);
+    const uint4 u = *reinterpret_cast<const uint4*>(&f);
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+  }
+  static __device__ __forceinline__ void kept(uint32_t from, F& f) {
+    uint4 u;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(from)
+                 : "memory");
+    *reinterpret_cast<uint4*>(&f) = u;
+  }
+  // `shared`: where the fragments go if they are kept there, moved past them
+  __device__ __forceinline__ Columns(const void* a_, const void* b_, const Place<DT, VECTOR>& at, uint32_t& shared) {
+    place = shared + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+    part = VPT * at.frag_bytes;
     a = a_ ? static_cast<const T*>(a_) + F::first(threadIdx.x) : nullptr;
     b = b_ ? static_cast<const T*>(b_) + F::first(threadIdx.x) : nullptr;
-    if constexpr (VPT <= 2) {
+    if constexpr (SHARED) {
+#pragma unroll
+      for (int p = 0; p < VPT; ++p) {
+        F x;
+        if (a && at.has(p)) {
+          x.load(a + p * at.step, at.left_of(p), at.threads);
+          keep(place + p * at.frag_bytes, x);
+        }
+        if (b && at.has(p)) {
+          x.load(b + p * at.step, at.left_of(p), at.threads);
+          keep(place + part + p * at.frag_bytes, x);
+        }
+      }
+      shared += part * (b ? 2 : 1);
+    } else if constexpr (VPT <= 2) {
 #pragma unroll
       for (int p = 0; p < VPT; ++p) {
         if (a && at.has(p)) fa[p].load(a + p * at.step, at.left_of(p), at.threads);
@@ -198,7 +231,12 @@ struct Columns {
     }
   }
   __device__ __forceinline__ void get(int p, const Place<DT, VECTOR>& at, float2 (&v)[N2]) const {
-    if constexpr (VPT == 1) {
+    if constexpr (SHARED) {
+      F x, y;
+      if (a) kept(place + p * at.frag_bytes, x);
+      if (b) kept(place + part + p * at.frag_bytes, y);
+      compute(x, y, v);
+    } else if constexpr (VPT == 1) {
 #pragma unroll
       for (int i = 0; i < N2; ++i) v[i] = held[i];
     } else if constexpr (VPT == 2) {

@@ -16,9 +16,9 @@
 // registers of the thread that owns the column while a CTA walks its rows, a
 // ring of rows ahead of itself; the CTAs' sums go through a small fp32
 // workspace and a second launch adds them in order: no atomics, the same bits
-// every run.  (bf16, 4096 rows of 4096 with a channel gate: 58 us, 3.5 TB/s, half
-// of the issue slots in use; one CTA a multiprocessor, as the sums and a row's
-// values take 118 registers of 512 threads.)
+// every run.  (bf16, 4096 rows of 4096 with a channel gate: 49 us alone, 4.1 TB/s,
+// half of the issue slots in use; one CTA a multiprocessor, as the sums and a
+// row's values take 112 registers of 512 threads.)
 #include "qmoe_norm.cuh"
 
 namespace qmoe {
@@ -29,7 +29,12 @@ constexpr int norm_grad_ahead(int vpt) { return vpt == 1 ? 3 : vpt == 2 ? 2 : 0;
 // Sums over rows a CTA keeps, in this order in its slice of the workspace.
 enum { SUM_PRE = 0, SUM_POST = 1, SUM_KINDS = 2 };
 
-template <int DT, bool VECTOR, int VPT>
+// ALL: both norms and every row gradient are there, and no gate of its own for
+// every value, as in a training step.  Known when the kernel is compiled, the
+// tests for each tensor leave the loop over the rows (bf16, with / without,
+// 4096 rows of 4096: 56 / 62 us, 8192 of 2048: 63 / 68; a gate for every value
+// gained nothing by it: 66 / 66).
+template <int DT, bool VECTOR, int VPT, bool ALL>
 __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) {
   op_begin();
   using F = Frag<DT, VECTOR>;
@@ -39,7 +44,8 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
   const float inv_h = 1.f / (float)a.H;
-  const bool full = a.gate_kind == QMOE_GATE_FULL, branch = a.o != nullptr, pre_norm = a.dh != nullptr;
+  const bool full = !ALL && a.gate_kind == QMOE_GATE_FULL;
+  const bool branch = ALL || a.o, pre_norm = ALL || a.dh, post_norm = ALL || a.w_post;
   const int64_t stride = gridDim.x * (int64_t)blockDim.y;
   int64_t t = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
   int turn = 0, parts = 0;
@@ -49,8 +55,12 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
       dr(a.dr, a.ld_dr, t, stride, ring, parts, me), dh(a.dh, a.ld_dh, t, stride, ring, parts, me),
       g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts, me);
   const uint32_t row_bytes = parts * VPT * me.frag_bytes;
-  const Columns<DT, VECTOR, VPT> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me),
-      pre(a.w_pre, nullptr, me);
+  // two fragments a thread: their sums and values fill the registers, so the
+  // columns are in shared memory (bf16, 4096 rows of 8192: 121 us, in registers 159)
+  constexpr bool SHARED = RING && VPT == 2;
+  uint32_t cols = ring + AHEAD * row_bytes;
+  const Columns<DT, VECTOR, VPT, SHARED> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me, cols),
+      pre(a.w_pre, nullptr, me, cols);
   const int64_t out_step = stride * a.H;
   int64_t out = t * a.H + F::first(threadIdx.x);
   int64_t ahead = t;
@@ -89,7 +99,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   float next1 = 1.f, next2 = 1.f, next_token = 1.f;
   auto scalars = [&](int64_t row) {
     if (row >= a.T) return;
-    if (branch && a.w_post) next1 = a.rstd_post[row];
+    if (branch && post_norm) next1 = a.rstd_post[row];
     if (pre_norm) next2 = a.rstd_pre[row];
     if (a.gate_kind == QMOE_GATE_TOKEN) next_token = load_d<DT>(a.gate, (size_t)row);
   };
@@ -144,7 +154,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
     for (int p = 0; p < VPT; ++p) {
       if (live && me.has(p)) {
         float2 d[N2], v[N2], w[N2];
-        if (a.dr) {
+        if (ALL || a.dr) {
           dr.get(at, p, me, d);
         } else {
 #pragma unroll
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
 #pragma unroll
           for (int i = 0; i < N2; ++i) d[i] = fma2(rh[p][i], m2, fma2(dn[p][i], k2, d[i]));
         }
-        if (a.dx) {
+        if (ALL || a.dx) {
 #pragma unroll
           for (int i = 0; i < N2; ++i) v[i] = mul2(d[i], both(a.residual_scale));
           put<DT, VECTOR>(static_cast<T*>(a.dx) + out, p, me, v);
@@ -191,17 +201,17 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
     if (branch) {
       // without w_post the branch is not normalised: do = u
       float s1 = 0.f;
-      if (a.w_post || a.gate_kind == QMOE_GATE_TOKEN) s1 = row_sum(sum1.x + sum1.y, red, turn) * rstd1;
+      if (post_norm || a.gate_kind == QMOE_GATE_TOKEN) s1 = row_sum(sum1.x + sum1.y, red, turn) * rstd1;
       if (a.gate_kind == QMOE_GATE_TOKEN && a.dgate && live && threadIdx.x == 0) store_d<DT>(a.dgate, (size_t)t, s1);
-      if (a.d_o) {
-        const float2 cu = both(rstd1 * token), co = both(a.w_post ? -s1 * token * inv_h * rstd1 * rstd1 : 0.f);
+      if (ALL || a.d_o) {
+        const float2 cu = both(rstd1 * token), co = both(post_norm ? -s1 * token * inv_h * rstd1 * rstd1 : 0.f);
 #pragma unroll
         for (int p = 0; p < VPT; ++p) {
           if (live && me.has(p)) {
             float2 v[N2];
             o.get(at, p, me, v);
 #pragma unroll
-            for (int i = 0; i < N2; ++i) v[i] = a.w_post ? fma2(v[i], co, mul2(dn[p][i], cu)) : mul2(dn[p][i], cu);
+            for (int i = 0; i < N2; ++i) v[i] = post_norm ? fma2(v[i], co, mul2(dn[p][i], cu)) : mul2(dn[p][i], cu);
             put<DT, VECTOR>(static_cast<T*>(a.d_o) + out, p, me, v);
           }
         }
@@ -286,11 +296,14 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
   const RowShape g = row_shape(a.H, frag);
   const int vpt = norm_vpt(a.H, frag, g.tpr);
   const int parts = 1 + (a.o ? 1 : 0) + (a.dr ? 1 : 0) + (a.dh ? 1 : 0) + (a.gate_kind == QMOE_GATE_FULL ? 1 : 0);
-  const size_t ring = vec || a.dtype == QMOE_F32 ? (size_t)norm_grad_ahead(vpt) * parts * vpt * g.tpr * g.rpb * 16 : 0;
+  const int columns = vpt == 2 ? 3 : 0;   // kept in shared memory
+  const size_t ring =
+      vec || a.dtype == QMOE_F32 ? (size_t)(norm_grad_ahead(vpt) * parts + columns) * vpt * g.tpr * g.rpb * 16 : 0;
   const int64_t ctas = norm_grad_ctas(a.T, g);
+  const bool all = a.o && a.w_post && a.dr && a.dh && a.dx && a.d_o && a.gate_kind != QMOE_GATE_FULL;
   if (ctas > 0) {   // without rows the sums are zeros
     const cudaError_t e = by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
-      auto kern = block_norm_grad_kernel<dt, v, n>;
+      auto kern = all ? block_norm_grad_kernel<dt, v, n, true> : block_norm_grad_kernel<dt, v, n, false>;
       if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
         const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
         if (err != cudaSuccess) return err;
