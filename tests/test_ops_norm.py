@@ -230,3 +230,10 @@ def test_refusals(ops):
     with pytest.raises(QMoEError) as e:
         ops.block_norm(torch.zeros((2, 16385), device="cuda"))
     assert e.value.status == binding.QMOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,H", [(5, 4104), (3, 6000), (4, 8192), (160, 8192)])
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_two_fragments_of_16_bit_rows(ops, T, H, gate, dtype):
+    test_forward_and_gradients(ops, T, H, gate, dtype)

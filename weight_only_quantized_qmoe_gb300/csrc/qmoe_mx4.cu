@@ -14,8 +14,8 @@
 // and the lane writes four bytes of codes.  With a plan the row goes straight
 // to its rows in expert order: read once, quantised once, written k times at
 // 17/32 byte a value, instead of k 16-bit copies read again.  (bf16, rows of
-// 4127 that start anywhere: 2880 of them in 15 us, read back in 12; 4096 rows of
-// 1536 to eight places each 15 us.)
+// 4127 that start anywhere: 2880 of them in 12 us, read back in 10; 4096 rows of
+// 1536 to eight places each 12 us.)
 #include <algorithm>
 #include <cstring>
 
@@ -197,14 +197,22 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
   }
 }
 
-// Warps of a row (the fewest steps eight warps allow) and rows of a CTA.
-static dim3 mx4_block(int64_t segs) {
-  const int64_t steps = (segs + kQuantWarps - 1) / kQuantWarps, warps = (segs + steps - 1) / steps;
-  return dim3(32, (unsigned)warps, (unsigned)(kQuantWarps / warps));
+// Warps of a row and rows of a CTA.  A warp that walks some steps of its row has
+// the next one's loads in flight while it works, which one that ends after a
+// step has not: up to `most` steps while every multiprocessor still gets 32
+// warps, more where a row's kQuantWarps warps need them.  (Quantise and back,
+// us, with 6 / as few as possible: 8192 x 2048 f16 11.8 + 11.2 / 17.7 + 13.2,
+// 20000 x 704 bf16 11.9 + 10.6 / 17.1 + 14.0, 2880 x 4127 bf16 12.3 + 9.6 /
+// 13.5 + 10.3; but 32-bit rows written, 2880 x 4128: 13.5 / 11.0 with 3.)
+static dim3 mx4_block(int64_t segs, int64_t rows, int64_t most) {
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, rows * segs / (kSms * 32)));
+  const int64_t at_most = std::min<int64_t>(kQuantWarps, (segs + want - 1) / want);
+  const int64_t steps = (segs + at_most - 1) / at_most, warps = (segs + steps - 1) / steps;
+  return dim3(32, (unsigned)warps, (unsigned)std::max<int64_t>(1, kQuantWarps / 2 / warps));
 }
 
 cudaError_t launch_mx4_quantize(const Mx4QuantArgs& a, cudaStream_t s) {
-  const dim3 block = mx4_block((a.cols + kQuantSeg - 1) / kQuantSeg);
+  const dim3 block = mx4_block((a.cols + kQuantSeg - 1) / kQuantSeg, a.rows, 6);
   const int64_t blocks = (a.rows + block.z - 1) / block.z;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const bool act = a.act.act >= 0;
@@ -282,7 +290,8 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_dequantize_kernel(const 
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4DequantArgs& a, cudaStream_t s) {
-  const dim3 block = mx4_block((a.cols + 7 + kQuantSeg - 1) / kQuantSeg);   // up to 7 elements early
+  // up to 7 elements early
+  const dim3 block = mx4_block((a.cols + 7 + kQuantSeg - 1) / kQuantSeg, a.rows, a.dtype == QMOE_F32 ? 3 : 6);
   const int64_t blocks = (a.rows + block.z - 1) / block.z;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto run = [&](auto kern) {
