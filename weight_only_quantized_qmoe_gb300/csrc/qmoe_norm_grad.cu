@@ -18,7 +18,7 @@
 // workspace and a second launch adds them in order: no atomics, the same bits
 // every run.  (bf16, 4096 rows of 4096 with a channel gate: 49 us alone, 4.1 TB/s,
 // half of the issue slots in use; one CTA a multiprocessor, as the sums and a
-// row's values take 112 registers of 512 threads.)
+// row's values take 116 registers of 512 threads.)
 #include "qmoe_norm.cuh"
 
 namespace qmoe {
@@ -239,14 +239,13 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   }
 }
 
-// Adds the slices of the workspace: 32 columns a CTA, its 16 rows of threads
-// take every 16th slice, then their sums in order.  SUM_POST gives both dw_post
-// and a channel gate's gradient.
-constexpr int kSumRows = 16;
-template <int DT>
-__global__ void __launch_bounds__(32 * kSumRows) block_norm_sums_kernel(const NormArgs a, int slices) {
+// Adds the slices of the workspace: 32 columns a CTA, its ROWS rows of threads
+// take every ROWS-th slice, then their sums in order.  SUM_POST gives both
+// dw_post and a channel gate's gradient.
+template <int DT, int ROWS, int AHEAD>
+__global__ void __launch_bounds__(32 * ROWS) block_norm_sums_kernel(const NormArgs a, int slices) {
   op_begin();
-  __shared__ float part[kSumRows][33];
+  __shared__ float part[ROWS][33];
   const int kind = blockIdx.y;
   const bool channel = a.gate_kind == QMOE_GATE_CHANNEL;
   if (kind == SUM_PRE ? !a.dw_pre : !a.dw_post && !(channel && a.dgate)) return;
@@ -254,14 +253,14 @@ __global__ void __launch_bounds__(32 * kSumRows) block_norm_sums_kernel(const No
   float s = 0.f;
   if (c < a.H) {
     const float* p = a.partial + kind * (size_t)a.H + c;
-#pragma unroll 4
-    for (int q = threadIdx.y; q < slices; q += kSumRows) s += p[(size_t)q * SUM_KINDS * a.H];
+#pragma unroll AHEAD
+    for (int q = threadIdx.y; q < slices; q += ROWS) s += p[(size_t)q * SUM_KINDS * a.H];
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= a.H) return;
 #pragma unroll
-  for (int q = 1; q < kSumRows; ++q) s += part[q][threadIdx.x];
+  for (int q = 1; q < ROWS; ++q) s += part[q][threadIdx.x];
   if (kind == SUM_PRE) {
     store_d<DT>(a.dw_pre, (size_t)c, s);
     return;
@@ -312,11 +311,17 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
     });
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid((unsigned)((a.H + 31) / 32), SUM_KINDS), block(32, kSumRows);
+  // (both launches, us, 16 rows of threads / 32: 64 slices 10.9 / 11.8, 152 of
+  // 2048 columns 57.4 / 56.4, 304 of 1001 18.8 / 17.6, 1216 of 512 35.5 / 32.6)
   const int slices = (int)(ctas * g.rpb);
-  if (a.dtype == QMOE_F32) return launch_op(block_norm_sums_kernel<QMOE_F32>, grid, block, 0, s, a, slices);
-  if (a.dtype == QMOE_F16) return launch_op(block_norm_sums_kernel<QMOE_F16>, grid, block, 0, s, a, slices);
-  return launch_op(block_norm_sums_kernel<QMOE_BF16>, grid, block, 0, s, a, slices);
+  const dim3 grid((unsigned)((a.H + 31) / 32), SUM_KINDS);
+  auto sums = [&](auto dt) {
+    return slices < 128 ? launch_op(block_norm_sums_kernel<dt, 16, 4>, grid, dim3(32, 16), 0, s, a, slices)
+                        : launch_op(block_norm_sums_kernel<dt, 32, 8>, grid, dim3(32, 32), 0, s, a, slices);
+  };
+  if (a.dtype == QMOE_F32) return sums(std::integral_constant<int, QMOE_F32>{});
+  if (a.dtype == QMOE_F16) return sums(std::integral_constant<int, QMOE_F16>{});
+  return sums(std::integral_constant<int, QMOE_BF16>{});
 }
 
 }  // namespace qmoe
