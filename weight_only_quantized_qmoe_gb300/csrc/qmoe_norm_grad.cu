@@ -26,6 +26,13 @@ namespace qmoe {
 // Rows in the ring of a CTA (see norm_ahead); up to five tensors a row here.
 constexpr int norm_grad_ahead(int vpt) { return vpt == 1 ? 3 : vpt == 2 ? 2 : 0; }
 
+// Whether a thread's columns are in shared memory instead of its registers: with
+// two fragments a thread, whose sums and values fill the registers (bf16, 4096
+// rows of 8192: 121 us, in registers 159), and where more would be loaded for
+// every row element by element (f32, 2048 rows of 8191: 178 us, loaded 238; 16
+// bytes at a time, rows of 8192: 132, loaded 124).
+constexpr bool columns_shared(int vpt, bool vector) { return vpt == 2 || (vpt > 2 && !vector); }
+
 // Sums over rows a CTA keeps, in this order in its slice of the workspace.
 enum { SUM_PRE = 0, SUM_POST = 1, SUM_KINDS = 2 };
 
@@ -55,9 +62,7 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
       dr(a.dr, a.ld_dr, t, stride, ring, parts, me), dh(a.dh, a.ld_dh, t, stride, ring, parts, me),
       g(full ? a.gate : nullptr, a.ld_gate, t, stride, ring, parts, me);
   const uint32_t row_bytes = parts * VPT * me.frag_bytes;
-  // two fragments a thread: their sums and values fill the registers, so the
-  // columns are in shared memory (bf16, 4096 rows of 8192: 121 us, in registers 159)
-  constexpr bool SHARED = RING && VPT == 2;
+  constexpr bool SHARED = columns_shared(VPT, VECTOR) && kCopies<DT, VECTOR>;
   uint32_t cols = ring + AHEAD * row_bytes;
   const Columns<DT, VECTOR, VPT, SHARED> post(a.w_post, a.gate_kind == QMOE_GATE_CHANNEL ? a.gate : nullptr, me, cols),
       pre(a.w_pre, nullptr, me, cols);
@@ -295,7 +300,7 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
   const RowShape g = row_shape(a.H, frag);
   const int vpt = norm_vpt(a.H, frag, g.tpr);
   const int parts = 1 + (a.o ? 1 : 0) + (a.dr ? 1 : 0) + (a.dh ? 1 : 0) + (a.gate_kind == QMOE_GATE_FULL ? 1 : 0);
-  const int columns = vpt == 2 ? 3 : 0;   // kept in shared memory
+  const int columns = columns_shared(vpt, vec) ? 3 : 0;   // kept in shared memory
   const size_t ring =
       vec || a.dtype == QMOE_F32 ? (size_t)(norm_grad_ahead(vpt) * parts + columns) * vpt * g.tpr * g.rpb * 16 : 0;
   const int64_t ctas = norm_grad_ctas(a.T, g);
