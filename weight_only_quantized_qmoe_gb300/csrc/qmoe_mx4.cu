@@ -56,7 +56,7 @@ struct Load8 {
 
   __device__ static __forceinline__ void aligned(const T* x, int64_t from, int64_t size, uint32_t* out) {
     if (from >= 0 && from + per <= size) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + from));
+      const uint4 u = *reinterpret_cast<const uint4*>(x + from);
       out[0] = u.x;
       out[1] = u.y;
       out[2] = u.z;

@@ -28,9 +28,9 @@ constexpr int norm_grad_ahead(int vpt) { return vpt == 1 ? 3 : vpt == 2 ? 2 : 0;
 
 // Whether a thread's columns are in shared memory instead of its registers: with
 // two fragments a thread, whose sums and values fill the registers (bf16, 4096
-// rows of 8192: 121 us, in registers 159), and where more would be loaded for
-// every row element by element (f32, 2048 rows of 8191: 178 us, loaded 238; 16
-// bytes at a time, rows of 8192: 132, loaded 124).
+// rows of 8192: 113 us; when this was chosen 121, in registers 159), and where
+// more would be loaded for every row element by element (f32, 2048 rows of 8191:
+// 153 us, loaded 197; 16 bytes at a time, rows of 8192: 136, loaded 124).
 constexpr bool columns_shared(int vpt, bool vector) { return vpt == 2 || (vpt > 2 && !vector); }
 
 // Sums over rows a CTA keeps, in this order in its slice of the workspace.
@@ -48,6 +48,10 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
   using T = typename ElemT<DT>::t;
   constexpr int N2 = F::n / 2, AHEAD = norm_grad_ahead(VPT);
   constexpr bool RING = kCopies<DT, VECTOR> && AHEAD > 0;
+  // rows that are loaded when they are used: a load does not pass a store that
+  // the source has before it (f32, 2048 rows of 8192 / 8191: 124 / 153 us, after
+  // it 135 / 183; 8191 with a gate for every value 292, after it 243)
+  constexpr bool EARLY = ALL && !RING;
   __shared__ float red[2 * 16];
   extern __shared__ __align__(16) uint8_t norm_ring[];
   const float inv_h = 1.f / (float)a.H;
@@ -169,15 +173,22 @@ __global__ void __launch_bounds__(512) block_norm_grad_kernel(const NormArgs a) 
 #pragma unroll
           for (int i = 0; i < N2; ++i) d[i] = fma2(rh[p][i], m2, fma2(dn[p][i], k2, d[i]));
         }
+        if constexpr (EARLY) {
+          o.get(at, p, me, v);
+          post.get(p, me, w);
+        }
         if (ALL || a.dx) {
+          float2 e[N2];
 #pragma unroll
-          for (int i = 0; i < N2; ++i) v[i] = mul2(d[i], both(a.residual_scale));
-          put<DT, VECTOR>(static_cast<T*>(a.dx) + out, p, me, v);
+          for (int i = 0; i < N2; ++i) e[i] = mul2(d[i], both(a.residual_scale));
+          put<DT, VECTOR>(static_cast<T*>(a.dx) + out, p, me, e);
         }
         if (branch) {
           const float2 c1 = both(rstd1 * token);
-          o.get(at, p, me, v);
-          post.get(p, me, w);
+          if constexpr (!EARLY) {
+            o.get(at, p, me, v);
+            post.get(p, me, w);
+          }
 #pragma unroll
           for (int i = 0; i < N2; ++i) dn[p][i] = mul2(d[i], w[i]);
           if (full) {

@@ -165,14 +165,24 @@ cudaError_t launch_op(void (*kern)(Params...), dim3 grid, dim3 block, size_t sme
 }
 // First thing in an operator's kernel: lets the next one start (once every CTA
 // of this one has), and waits for the ones before.  What follows sees their
-// memory, and as every operator waits, theirs before them too.
+// memory, and as every operator waits, theirs before them too.  Tensors are read
+// by plain loads only: they may still be written when this kernel starts, so
+// the non-coherent path, which asks that memory is not written during the
+// kernel's life (and whose loads may be moved ahead of the wait), is not open.
 __device__ __forceinline__ void op_begin() {
   pdl_launch_dependents();
   pdl_wait();
 }
+// 16 bytes of a row that is read once: past the L1.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
 
-// VEC consecutive elements of type DT as floats: 16-byte accesses (VEC * size
-// a multiple of 16), or one element.
 template <int DT>
 struct ElemT;
 template <>
@@ -210,38 +220,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-template <int DT, int VEC>
-__device__ __forceinline__ void load_vec(const void* base, size_t i, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = load_d<DT>(base, i);
-  } else if constexpr (DT == QMOE_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-#pragma unroll
-    for (int q = 0; q < VEC / 4; ++q) {
-      const float4 f = __ldg(p + q);
-      v[4 * q] = f.x;
-      v[4 * q + 1] = f.y;
-      v[4 * q + 2] = f.z;
-      v[4 * q + 3] = f.w;
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-#pragma unroll
-    for (int q = 0; q < VEC / 8; ++q) {
-      const uint4 u = __ldg(p + q);
-      unpack2<DT>(u.x, v[8 * q], v[8 * q + 1]);
-      unpack2<DT>(u.y, v[8 * q + 2], v[8 * q + 3]);
-      unpack2<DT>(u.z, v[8 * q + 4], v[8 * q + 5]);
-      unpack2<DT>(u.w, v[8 * q + 6], v[8 * q + 7]);
-    }
-  }
-}
-
+// VEC consecutive values as elements of type DT, in 16-byte accesses (VEC *
+// size a multiple of 16).
 template <int DT, int VEC>
 __device__ __forceinline__ void store_vec(void* base, size_t i, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    store_d<DT>(base, i, v[0]);
-  } else if constexpr (DT == QMOE_F32) {
+  if constexpr (DT == QMOE_F32) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
 #pragma unroll
     for (int q = 0; q < VEC / 4; ++q) p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
@@ -270,10 +253,10 @@ struct Frag<DT, true> {
   __device__ static __forceinline__ int step(int threads) { return threads * n; }
   // from the thread's first element, `left` elements before the row's end
   __device__ __forceinline__ void load(const typename ElemT<DT>::t* p, int, int) {
-    u = __ldg(reinterpret_cast<const uint4*>(p));
+    u = *reinterpret_cast<const uint4*>(p);
   }
   // the same for rows that are read once: they do not pass through the L1
-  __device__ __forceinline__ void load_once(const typename ElemT<DT>::t* p, int, int) { u = ld_nc_v4(p); }
+  __device__ __forceinline__ void load_once(const typename ElemT<DT>::t* p, int, int) { u = ld_once_v4(p); }
   __device__ __forceinline__ void get(float (&v)[n]) const {
     if constexpr (DT == QMOE_F32) {
       v[0] = __uint_as_float(u.x);
