@@ -499,7 +499,8 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_
  * on are zeros.  offsets_dev NULL: one expert, all rows.
  *   a  [rows, k], one panel of rows;  w  [experts, n, k], panel_rows = n
  *   out_dev  out_dtype [rows, n], row stride ld_out
- * Both codes must be 16-byte aligned; experts <= 1024.
+ * Both codes must be 16-byte aligned; experts <= 1024; rows and experts * n
+ * have to be below 2^31 - 512 (a tile's last rows are indexed past them).
  */
 qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
                             const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,

@@ -259,13 +259,16 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_
 qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
                             const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,
                             int experts, int64_t n, int64_t k, int out_dtype, void* out_dev, int64_t ld_out, void* stream) {
-  OP_CHECK(rows >= 0 && rows < INT_MAX, "rows %lld is out of range", (long long)rows);
+  // a tile's rows, of either operand, may reach past the last one by less than this
+  constexpr int reach = 256;
+  OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
+  OP_CHECK(rows < INT_MAX - reach, "rows %lld do not fit 31 bits", (long long)rows);
   OP_CHECK(experts >= 1, "experts %d is not positive", experts);
   OP_SUPPORTED(experts <= kSortMaxExperts, "experts %d: at most %d", experts, kSortMaxExperts);
   OP_CHECK(offsets_dev || experts == 1, "%d experts need offsets", experts);
   OP_TRY(check_rows(n, ld_out, out_dtype));
   OP_CHECK(k >= 1 && k < (1LL << 30), "reduction length %lld is out of range", (long long)k);
-  OP_CHECK(n <= INT_MAX / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
+  OP_CHECK(n < (INT_MAX - reach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
   if (rows == 0) return QMOE_OK;
   OP_CHECK(a_codes_dev && a_scales_dev && w_codes_dev && w_scales_dev && out_dev, "an operand or out is null");
   OP_CHECK(aligned16(a_codes_dev) && aligned16(w_codes_dev), "codes must be 16-byte aligned");
