@@ -397,8 +397,9 @@ void qmoe_destroy(qmoe_layer* layer);
  * nothing between calls and allocate nothing, so any number may run on any
  * streams at once and all may be captured into a CUDA graph.  Matrices are
  * row-major with a row stride ld in elements (at least the row length; the
- * last axis is contiguous); 16-byte aligned rows run fastest, any alignment
- * is right.  Outputs without an ld are contiguous and may not overlap inputs.
+ * last axis is contiguous); 16-byte aligned rows run fastest, rows on any
+ * element are right.  An address that is not a multiple of its element's size
+ * is refused.  Outputs without an ld are contiguous and may not overlap inputs.
  * Zero tokens or rows are OK and launch nothing (sums over rows are written
  * as zeros).  A failed call's message: qmoe_op_last_error, of the calling
  * thread.

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "qmoe_ops.cuh"
 
@@ -45,6 +46,24 @@ qmoe_status done(cudaError_t e, const char* what) {
     if (!(cond)) return fail(QMOE_ERR_UNSUPPORTED, __VA_ARGS__); \
   } while (0)
 
+#define OP_TRY(call)                    \
+  do {                                  \
+    const qmoe_status st_ = (call);     \
+    if (st_ != QMOE_OK) return st_;     \
+  } while (0)
+
+// Every address is a multiple of the size of what it points to (null is one).
+struct Address {
+  const void* p;
+  int bytes;
+  const char* name;
+};
+qmoe_status check_addresses(std::initializer_list<Address> all) {
+  for (const Address& a : all)
+    OP_CHECK((reinterpret_cast<uintptr_t>(a.p) & (uintptr_t)(a.bytes - 1)) == 0, "%s is not aligned to %d bytes", a.name, a.bytes);
+  return QMOE_OK;
+}
+
 bool dtype_ok(int d) { return d == QMOE_F32 || d == QMOE_F16 || d == QMOE_BF16; }
 
 // Shapes every routed operator shares.
@@ -62,11 +81,6 @@ qmoe_status check_rows(int64_t H, int64_t ld, int dtype) {
   OP_CHECK(ld >= H, "row stride %lld is below the row length %lld", (long long)ld, (long long)H);
   return QMOE_OK;
 }
-#define OP_TRY(call)                    \
-  do {                                  \
-    const qmoe_status st_ = (call);     \
-    if (st_ != QMOE_OK) return st_;     \
-  } while (0)
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -108,6 +122,7 @@ qmoe_status qmoe_expert_sort(const void* ids_dev, int id_bytes, int64_t ld_ids, 
   if (num_tokens == 0)
     return done(cudaMemsetAsync(offsets_dev, 0, ((size_t)experts + 1) * sizeof(int32_t), as_stream(stream)), "clear offsets");
   OP_CHECK(ids_dev && perm_dev && pos_dev, "ids, perm or pos is null");
+  OP_TRY(check_addresses({{ids_dev, id_bytes, "ids"}, {perm_dev, 4, "perm"}, {pos_dev, 4, "pos"}, {offsets_dev, 4, "offsets"}}));
   OP_CHECK(ld_ids >= top_k, "row stride %lld of ids is below top_k %d", (long long)ld_ids, top_k);
   SortArgs a{};
   a.ids = ids_dev;
@@ -128,6 +143,8 @@ qmoe_status qmoe_dispatch(const void* x_dev, int64_t ld_x, const int32_t* pos_de
   OP_TRY(check_rows(hidden, ld_x, dtype));
   if (num_tokens == 0) return QMOE_OK;
   OP_CHECK(x_dev && pos_dev && offsets_dev && xs_dev, "x, pos, offsets or xs is null");
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{x_dev, size, "x"}, {pos_dev, 4, "pos"}, {offsets_dev, 4, "offsets"}, {xs_dev, size, "xs"}}));
   RowsArgs a{};
   a.src = x_dev;
   a.ld_src = ld_x;
@@ -148,6 +165,8 @@ qmoe_status qmoe_combine(const void* y_dev, int64_t ld_y, const float* weights_d
   OP_TRY(check_rows(hidden, ld_y, dtype));
   if (num_tokens == 0) return QMOE_OK;
   OP_CHECK(y_dev && pos_dev && out_dev, "y, pos or out is null");
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{y_dev, size, "y"}, {weights_dev, 4, "weights"}, {pos_dev, 4, "pos"}, {out_dev, size, "out"}}));
   RowsArgs a{};
   a.src = y_dev;
   a.ld_src = ld_y;
@@ -177,6 +196,9 @@ qmoe_status qmoe_combine_grad(const void* dout_dev, int64_t ld_dout, const void*
   OP_CHECK(dout_dev && pos_dev, "dout or pos is null");
   OP_CHECK(!dy_dev || offsets_dev, "dy needs offsets");
   OP_CHECK(!dweights_dev || y_dev, "dweights needs y");
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{dout_dev, size, "dout"}, {dweights_dev ? y_dev : nullptr, size, "y"}, {weights_dev, 4, "weights"},
+                          {pos_dev, 4, "pos"}, {offsets_dev, 4, "offsets"}, {dy_dev, size, "dy"}, {dweights_dev, 4, "dweights"}}));
   RowsArgs a{};
   a.src = dout_dev;
   a.ld_src = ld_dout;
@@ -216,8 +238,8 @@ qmoe_status qmoe_mx4_quantize(const void* x_dev, int64_t ld_x, int64_t rows, int
            (long long)panel_rows, (long long)out_rows);
   if (out_rows == 0) return QMOE_OK;
   OP_CHECK(x_dev && codes_dev && scales_dev, "x, codes or scales is null");
-  OP_CHECK(aligned16(codes_dev) && reinterpret_cast<uintptr_t>(scales_dev) % 4 == 0,
-           "codes must be 16-byte aligned and scales 4-byte aligned");
+  OP_TRY(check_addresses({{x_dev, dtype_size(dtype), "x"}, {pos_dev, 4, "pos"}, {offsets_dev, 4, "offsets"},
+                          {codes_dev, 16, "codes"}, {scales_dev, 4, "scales"}}));
   Mx4QuantArgs a{};
   a.x = x_dev;
   a.ld_x = ld_x;
@@ -243,7 +265,7 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_
            (long long)panel_rows, (long long)rows);
   if (rows == 0) return QMOE_OK;
   OP_CHECK(codes_dev && scales_dev && out_dev, "codes, scales or out is null");
-  OP_CHECK(reinterpret_cast<uintptr_t>(codes_dev) % 4 == 0, "codes must be 4-byte aligned");
+  OP_TRY(check_addresses({{codes_dev, 4, "codes"}, {out_dev, dtype_size(dtype), "out"}}));
   Mx4DequantArgs a{};
   a.codes = codes_dev;
   a.scales = scales_dev;
@@ -271,9 +293,8 @@ qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_
   OP_CHECK(n < (INT_MAX - reach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
   if (rows == 0) return QMOE_OK;
   OP_CHECK(a_codes_dev && a_scales_dev && w_codes_dev && w_scales_dev && out_dev, "an operand or out is null");
-  OP_CHECK(aligned16(a_codes_dev) && aligned16(w_codes_dev), "codes must be 16-byte aligned");
-  OP_CHECK(reinterpret_cast<uintptr_t>(a_scales_dev) % 4 == 0 && reinterpret_cast<uintptr_t>(w_scales_dev) % 4 == 0,
-           "scales must be 4-byte aligned");
+  OP_TRY(check_addresses({{a_codes_dev, 16, "a's codes"}, {a_scales_dev, 4, "a's scales"}, {w_codes_dev, 16, "w's codes"},
+                          {w_scales_dev, 4, "w's scales"}, {offsets_dev, 4, "offsets"}, {out_dev, dtype_size(out_dtype), "out"}}));
   Mx4MatmulArgs a{};
   a.a_codes = a_codes_dev;
   a.a_scales = a_scales_dev;
@@ -310,6 +331,8 @@ static qmoe_status norm_args(NormArgs& a, const void* x, int64_t ld_x, const voi
   OP_CHECK((gate != nullptr) == (gate_kind != QMOE_GATE_NONE), "gate and gate_kind disagree");
   OP_CHECK(gate_kind != QMOE_GATE_FULL || ld_gate >= H, "row stride %lld of gate is below the row length %lld",
            (long long)ld_gate, (long long)H);
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{x, size, "x"}, {o, size, "o"}, {gate, size, "gate"}, {w_post, size, "w_post"}, {w_pre, size, "w_pre"}}));
   a.x = x;
   a.ld_x = ld_x;
   a.o = o;
@@ -337,6 +360,8 @@ qmoe_status qmoe_block_norm(const void* x_dev, int64_t ld_x, const void* o_dev, 
   OP_CHECK((w_pre_dev != nullptr) == (h_dev != nullptr) || num_tokens == 0, "w_pre and h go together");
   OP_CHECK(r_dev || h_dev || num_tokens == 0, "neither r nor h is asked for");
   if (num_tokens == 0) return QMOE_OK;
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{r_dev, size, "r"}, {h_dev, size, "h"}, {rstd_post_dev, 4, "rstd_post"}, {rstd_pre_dev, 4, "rstd_pre"}}));
   a.r = r_dev;
   a.h = h_dev;
   a.rstd_post = w_post_dev ? rstd_post_dev : nullptr;
@@ -371,6 +396,10 @@ qmoe_status qmoe_block_norm_grad(const void* dr_dev, int64_t ld_dr, const void* 
   const size_t need = block_norm_grad_workspace(num_tokens, hidden, dtype);
   OP_CHECK(workspace_bytes >= need && (workspace_dev || need == 0), "workspace of %zu bytes is below the %zu needed",
            workspace_bytes, need);
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{dr_dev, size, "dr"}, {dh_dev, size, "dh"}, {rstd_post_dev, 4, "rstd_post"},
+                          {rstd_pre_dev, 4, "rstd_pre"}, {dx_dev, size, "dx"}, {do_dev, size, "do"}, {dgate_dev, size, "dgate"},
+                          {dw_post_dev, size, "dw_post"}, {dw_pre_dev, size, "dw_pre"}, {workspace_dev, 4, "workspace"}}));
   a.dr = dr_dev;
   a.ld_dr = ld_dr;
   a.dh = dh_dev;
