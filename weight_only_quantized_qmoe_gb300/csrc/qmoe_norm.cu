@@ -154,6 +154,10 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const NormArgs a) {
 // Threads of a row at most.
 constexpr int kNormThreads = 256;
 
+// The most shared memory the ring of a kernel takes: x, o and a gate for every
+// value, 512 threads.
+constexpr int norm_ring_most(int vpt) { return norm_ahead(vpt) * 3 * vpt * 512 * 16; }
+
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
   const bool vec = norm_vec(a);
   const int frag = norm_frag(a.dtype, vec);
@@ -165,10 +169,8 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
   const size_t ring = vec || a.dtype == QMOE_F32 ? (size_t)norm_ahead(vpt) * parts * vpt * threads * 16 : 0;
   return by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
     auto kern = all ? block_norm_kernel<dt, v, n, true> : block_norm_kernel<dt, v, n, false>;
-    if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
-      if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared(kern, ring, norm_ring_most(n));
+    if (e != cudaSuccess) return e;
     int64_t blocks = (a.T + g.rpb - 1) / g.rpb;
     if (blocks > kSms) {   // as many as are resident at once
       int per = 0;

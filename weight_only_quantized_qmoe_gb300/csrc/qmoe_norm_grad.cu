@@ -293,6 +293,12 @@ int64_t norm_grad_ctas(int64_t T, const RowShape& g) {
   return std::min<int64_t>((int64_t)kSms * std::max(1, 512 / (g.tpr * g.rpb)), (T + g.rpb - 1) / g.rpb);
 }
 
+// The most shared memory a kernel takes: rings of x, o, dr, dh and a gate for
+// every value, and columns, 512 threads.
+constexpr int norm_grad_shared_most(int vpt, bool vector) {
+  return (norm_grad_ahead(vpt) * 5 + (columns_shared(vpt, vector) ? 3 : 0)) * vpt * 512 * 16;
+}
+
 }  // namespace
 
 size_t block_norm_grad_workspace(int64_t T, int64_t H, int dtype) {
@@ -319,10 +325,8 @@ cudaError_t launch_block_norm_grad(const NormArgs& a, cudaStream_t s) {
   if (ctas > 0) {   // without rows the sums are zeros
     const cudaError_t e = by_norm(a.dtype, vec, vpt, [&](auto dt, auto v, auto n) {
       auto kern = all ? block_norm_grad_kernel<dt, v, n, true> : block_norm_grad_kernel<dt, v, n, false>;
-      if (ring > 40 * 1024) {   // beside the static sums: past the 48 KB a launch gets unasked
-        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
-        if (err != cudaSuccess) return err;
-      }
+      const cudaError_t err = allow_shared(kern, ring, norm_grad_shared_most(n, v));
+      if (err != cudaSuccess) return err;
       return launch_op(kern, dim3((unsigned)ctas), dim3(g.tpr, g.rpb), ring, s, a);
     });
     if (e != cudaSuccess) return e;

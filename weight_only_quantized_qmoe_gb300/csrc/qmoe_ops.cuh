@@ -163,6 +163,16 @@ cudaError_t launch_op(void (*kern)(Params...), dim3 grid, dim3 block, size_t sme
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+// Lets a kernel take more dynamic shared memory than a launch gets unasked (48 KB
+// with the static part, at most 8 KB here).  The limit belongs to the kernel in
+// the whole process: it is always set to the same value, the most that any call
+// of this kernel needs, so that calls from several threads do not lower it under
+// one another.
+template <typename... Params>
+cudaError_t allow_shared(void (*kern)(Params...), size_t bytes, int most) {
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
 // First thing in an operator's kernel: lets the next one start (once every CTA
 // of this one has), and waits for the ones before.  What follows sees their
 // memory, and as every operator waits, theirs before them too.  Tensors are read

@@ -156,6 +156,9 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(const SortArgs a) {
   if (C > 1) cluster.sync();   // no CTA leaves while another may still read its counts
 }
 
+// Shared memory of W warps: their counters, three values an expert and the end.
+static constexpr size_t sort_shared(int W, int E) { return ((size_t)W * (E | 1) + 3 * (size_t)E + 1) * sizeof(int); }
+
 cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
   // One CTA for a few routes, else a cluster of eight, whose two barriers cost
   // about a microsecond (us, one / eight CTAs: 256 routes 6.0 / 7.0, 512 6.2 /
@@ -163,7 +166,7 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
   const int C = a.R <= 256 ? 1 : kSortCluster;
   const int64_t passes = (a.R + 32 * C - 1) / (32 * C);
   const int W = (int)std::max<int64_t>(1, std::min<int64_t>(32, passes));
-  const size_t smem = ((size_t)W * (a.E | 1) + 3 * (size_t)a.E + 1) * sizeof(int);
+  const size_t smem = sort_shared(W, a.E);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -177,10 +180,8 @@ cudaError_t launch_expert_sort(const SortArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;   // a single CTA is its own cluster
   auto run = [&](auto kern) {
-    if (smem > 48 * 1024) {
-      const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (err != cudaSuccess) return err;
-    }
+    const cudaError_t err = allow_shared(kern, smem, (int)sort_shared(32, kSortMaxExperts));
+    if (err != cudaSuccess) return err;
     return cudaLaunchKernelEx(&cfg, kern, a);
   };
   return a.id_bytes == 8 ? run(expert_sort_kernel<long long>) : run(expert_sort_kernel<int>);
