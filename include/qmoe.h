@@ -467,8 +467,8 @@ qmoe_status qmoe_combine_grad(const void* dout_dev, int64_t ld_dout, const void*
  *          of its row, even d in the low half; zeros past cols
  *   scales uint8 [rows / panel_rows][ceil(nb / 4)][panel_rows][4]: in each
  *          panel the four scales of 128 values of consecutive rows side by
- *          side; zeros past nb.  A stack of E matrices [E, N, K] has
- *          panel_rows = N, a single matrix panel_rows = rows.
+ *          side; past nb they are written as zeros and not used.  A stack of E
+ *          matrices [E, N, K] has panel_rows = N, a single matrix panel_rows = rows.
  *
  * qmoe_mx4_quantize: s = clamp(floor(log2(largest magnitude)) - 2 + 127, 0,
  * 254); elements rounded to the nearest, ties to the even code, saturated at

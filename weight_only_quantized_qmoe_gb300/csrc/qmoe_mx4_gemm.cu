@@ -150,12 +150,12 @@ __device__ __forceinline__ void tma_2d_elect(void* dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
-// Four bytes global -> shared; or four zero bytes.
+// Four bytes global -> shared; or the first `real` of them, and zeros.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, int real) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -329,6 +329,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // ---------------- scale loaders: warp 2 + h takes the 128-value chunk h of each stage ----------------
     // Row 32 j + lane of a 128-row group goes to bytes lane * 16 + j * 4 of its
     // chunk.  Pointers are set up once a tile and step from panel to panel.
+    // Padding scales (past nb, in the last panel's words) are kept out: with an
+    // odd number of blocks the last MMA meets one, and NaN times a zero code is NaN.
     const int h = warp - 2;
     const uint32_t sfa0 = smem_u32(smem + RG::sfa_off) + h * 512 + lane * 16;
     const uint32_t sfb0 = smem_u32(smem + RG::sfb_off) + h * RG::groups * 512 + lane * 16;
@@ -348,22 +350,23 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t da = sfa0 + s * RG::sfa_bytes, db = sfb0 + s * RG::sfb_bytes;
-        if (inside && 2 * ks + h < nq) {   // every row exists: no tests between the copies
+        const int bytes = min(4, nb - 4 * (2 * ks + h));   // scales of this chunk, none if it is not above zero
+        if (inside && bytes > (nb & 1 ? 3 : 0)) {   // every row exists: no tests between the copies
 #pragma unroll
           for (int j = 0; j < kMxRows / 32; ++j) cp_async4(da + j * 4, pa + j * 128);
 #pragma unroll
           for (int j = 0; j < BN / 32; ++j) cp_async4(db + (j / 4) * 512 + (j & 3) * 4, pw + j * 128);
         } else {
-          const bool in = 2 * ks + h < nq;
+          const bool in = bytes > 0;
 #pragma unroll
           for (int j = 0; j < kMxRows / 32; ++j) {
             const bool real = in && 32 * j < na;
-            cp_async4_or_zero(da + j * 4, real ? pa + j * 128 : a.a_scales, real);
+            cp_async4_or_zero(da + j * 4, real ? pa + j * 128 : a.a_scales, real ? bytes : 0);
           }
 #pragma unroll
           for (int j = 0; j < BN / 32; ++j) {
             const bool real = in && 32 * j < nw;
-            cp_async4_or_zero(db + (j / 4) * 512 + (j & 3) * 4, real ? pw + j * 128 : a.w_scales, real);
+            cp_async4_or_zero(db + (j / 4) * 512 + (j & 3) * 4, real ? pw + j * 128 : a.w_scales, real ? bytes : 0);
           }
         }
         cp_async_arrive(&full[s]);

@@ -59,7 +59,8 @@ class ExpertPlan(NamedTuple):
 
 class MX4Tensor(NamedTuple):
     """Microscaled 4-bit rows [..., N, cols]: ``codes`` uint8 [..., N, 16 * nb]
-    and ``scales`` uint8 [..., ceil(nb / 4), N, 4], nb = ceil(cols / 32)."""
+    and ``scales`` uint8 [..., ceil(nb / 4), N, 4], nb = ceil(cols / 32).  Codes
+    past ``cols`` have to be zeros, scales past nb are not used."""
 
     codes: torch.Tensor
     scales: torch.Tensor
