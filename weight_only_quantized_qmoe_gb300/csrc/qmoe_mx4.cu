@@ -47,6 +47,8 @@ __device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
 // 16), takes the following ones from the next lane, which starts 8 elements on,
 // and shifts.  `size` is the number of elements of the tensor: aligned words
 // that are not wholly inside it are read element by element.
+// The loads of unaligned rows keep their place in the code (bf16, 2880 rows of
+// 4127: 12.3 us, left to the compiler 12.6; aligned rows, 4096 of 4096: 11.8 / 10.7).
 template <int DT, bool VEC>
 struct Load8 {
   using T = typename ElemT<DT>::t;
@@ -56,7 +58,7 @@ struct Load8 {
 
   __device__ static __forceinline__ void aligned(const T* x, int64_t from, int64_t size, uint32_t* out) {
     if (from >= 0 && from + per <= size) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + from);
+      const uint4 u = VEC ? *reinterpret_cast<const uint4*>(x + from) : ld_here_v4(x + from);
       out[0] = u.x;
       out[1] = u.y;
       out[2] = u.z;

@@ -183,6 +183,12 @@ __device__ __forceinline__ void op_begin() {
   pdl_launch_dependents();
   pdl_wait();
 }
+// 16 bytes, loaded where the code has it (after the wait, which is volatile too).
+__device__ __forceinline__ uint4 ld_here_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
 // 16 bytes of a row that is read once: past the L1.
 __device__ __forceinline__ uint4 ld_once_v4(const void* p) {
   uint4 r;
