@@ -33,3 +33,30 @@ def test_padding_scales_are_not_used(ops, R, N, K):
     assert torch.isfinite(want).all()
     assert torch.equal(ops.mx4_matmul(poisoned(a), poisoned(w), out_dtype=torch.float32), want)
     assert torch.equal(ops.mx4_dequantize(poisoned(a)), ops.mx4_dequantize(a))
+
+
+# --- empty arguments -------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+def test_no_rows_with_a_gate(ops, gate):
+    x = torch.empty((0, 32), device="cuda")
+    w = torch.ones(32, device="cuda")
+    g = {"token": x[:, :1], "channel": w, "full": x}[gate]
+    r, h, stats = ops.block_norm(x, x, w_post=w, w_pre=w, gate=g, return_stats=True)
+    assert r.shape == h.shape == (0, 32)
+    d = ops.block_norm_grad(x, x, x, x, stats, gate=g, w_post=w, w_pre=w)
+    assert d.gate.shape == g.shape and (d.gate == 0).all()
+    assert (d.w_post == 0).all() and (d.w_pre == 0).all() and d.x.shape == d.o.shape == (0, 32)
+
+
+def test_no_rows_at_the_entry_point():
+    from weight_only_quantized_qmoe_gb300 import binding as b, build
+    build.build()
+    P = 4096   # not used
+
+    def call(gate, kind, T=0):
+        return b.qmoe_block_norm(P, 32, P, 32, gate, kind, 32, P, P, 1.0, 1e-6, T, 32, b.QMOE_F32, P, P, 0, 0, None)
+    for gate in (0, P):
+        assert call(gate, b.QMOE_GATE_TOKEN) == call(gate, b.QMOE_GATE_FULL) == b.QMOE_OK
+    for gate, kind, T in ((0, b.QMOE_GATE_CHANNEL, 0), (P, b.QMOE_GATE_NONE, 0), (0, b.QMOE_GATE_TOKEN, 4), (0, b.QMOE_GATE_FULL, 4)):
+        assert call(gate, kind, T) == b.QMOE_ERR_INVALID_ARG

@@ -328,7 +328,9 @@ static qmoe_status norm_args(NormArgs& a, const void* x, int64_t ld_x, const voi
   OP_CHECK(x || T == 0, "x is null");
   OP_CHECK(o || T == 0 || (!w_post && gate_kind == QMOE_GATE_NONE), "w_post and gate need o");
   OP_CHECK(!o || ld_o >= H, "row stride %lld of o is below the row length %lld", (long long)ld_o, (long long)H);
-  OP_CHECK((gate != nullptr) == (gate_kind != QMOE_GATE_NONE), "gate and gate_kind disagree");
+  // without tokens a gate of one or more values a token is empty, and may be null
+  const bool empty = T == 0 && (gate_kind == QMOE_GATE_TOKEN || gate_kind == QMOE_GATE_FULL);
+  OP_CHECK((gate != nullptr) == (gate_kind != QMOE_GATE_NONE) || empty, "gate and gate_kind disagree");
   OP_CHECK(gate_kind != QMOE_GATE_FULL || ld_gate >= H, "row stride %lld of gate is below the row length %lld",
            (long long)ld_gate, (long long)H);
   const int size = dtype_size(dtype);
@@ -389,7 +391,7 @@ qmoe_status qmoe_block_norm_grad(const void* dr_dev, int64_t ld_dr, const void* 
   OP_CHECK(!dh_dev || (w_pre_dev && ld_dh >= hidden), "dh needs w_pre and a row stride of at least the row length");
   OP_CHECK(!dw_pre_dev || w_pre_dev, "dw_pre needs w_pre");
   OP_CHECK(!dw_post_dev || w_post_dev, "dw_post needs w_post");
-  OP_CHECK(!dgate_dev || gate_dev, "dgate needs gate");
+  OP_CHECK(!dgate_dev || gate_kind != QMOE_GATE_NONE, "dgate needs gate");
   OP_CHECK(!do_dev || o_dev || num_tokens == 0, "do needs o");
   OP_CHECK(num_tokens == 0 || (!w_post_dev || rstd_post_dev), "w_post needs rstd_post");
   OP_CHECK(num_tokens == 0 || (!w_pre_dev || rstd_pre_dev), "w_pre needs rstd_pre");
