@@ -60,3 +60,24 @@ def test_no_rows_at_the_entry_point():
         assert call(gate, b.QMOE_GATE_TOKEN) == call(gate, b.QMOE_GATE_FULL) == b.QMOE_OK
     for gate, kind, T in ((0, b.QMOE_GATE_CHANNEL, 0), (P, b.QMOE_GATE_NONE, 0), (0, b.QMOE_GATE_TOKEN, 4), (0, b.QMOE_GATE_FULL, 4)):
         assert call(gate, kind, T) == b.QMOE_ERR_INVALID_ARG
+
+
+# --- shapes ------------------------------------------------------------------------
+@pytest.mark.gpu
+def test_route_weights_of_another_shape_are_refused(ops):
+    from weight_only_quantized_qmoe_gb300 import QMoEError, binding
+    T, k, H = 6, 2, 16
+    plan = ops.expert_sort(torch.randint(0, 3, (T, k), device="cuda"), 3)
+    y, dout = torch.randn((T * k, H), device="cuda"), torch.randn((T, H), device="cuda")
+    w = torch.rand((T, k), device="cuda")
+    for bad in (w.t(), w.t().contiguous(), w.reshape(-1)[:6], w[None], w.reshape(4, 3)):
+        for call in (lambda: ops.combine(y, bad, plan), lambda: ops.combine_grad(dout, y, bad, plan)):
+            with pytest.raises(QMoEError) as e:
+                call()
+            assert e.value.status == binding.QMOE_ERR_INVALID_ARG
+    strided = torch.rand((T, 2 * k), device="cuda")[:, ::2]      # of the right shape: any strides, or flat
+    want = ops.combine(y, strided.contiguous(), plan)
+    assert torch.equal(ops.combine(y, strided, plan), want) and torch.equal(ops.combine(y, strided.reshape(-1), plan), want)
+    flat = w.reshape(-1).clone().requires_grad_()
+    (dw,) = torch.autograd.grad(ops.combine(y, flat, plan), [flat], [dout])
+    assert torch.equal(dw.reshape(T, k), ops.combine_grad(dout, y, w, plan)[1])

@@ -104,14 +104,12 @@ Rows rows_2d(const Tensor& t, const char* name) {
   return rows_of(t);
 }
 
-// A contiguous tensor of `numel` elements.
+// A tensor's elements in order.
 struct Flat {
   Tensor held;
   void* p = nullptr;
 };
-Flat flat(PyObject* o, const char* name, at::ScalarType type, int64_t numel, const Tensor& like) {
-  const Tensor& t = further(o, name, type, like);
-  if (t.numel() != numel) refuse(std::string(name) + " has " + std::to_string(t.numel()) + " elements, not " + std::to_string(numel));
+Flat flat(const Tensor& t) {
   Flat f;
   if (t.is_contiguous()) {
     f.p = const_cast<void*>(t.const_data_ptr());
@@ -120,6 +118,20 @@ Flat flat(PyObject* o, const char* name, at::ScalarType type, int64_t numel, con
     f.p = const_cast<void*>(f.held.const_data_ptr());
   }
   return f;
+}
+// A further tensor of `numel` elements.
+Flat flat(PyObject* o, const char* name, at::ScalarType type, int64_t numel, const Tensor& like) {
+  const Tensor& t = further(o, name, type, like);
+  if (t.numel() != numel) refuse(std::string(name) + " has " + std::to_string(t.numel()) + " elements, not " + std::to_string(numel));
+  return flat(t);
+}
+// A value a route: [tokens, k], or flat.
+Flat route_values(PyObject* o, const char* name, int64_t tokens, int64_t k, const Tensor& like) {
+  const Tensor& t = further(o, name, at::kFloat, like);
+  const auto s = t.sizes();
+  if (!(s.size() == 2 && s[0] == tokens && s[1] == k) && !(s.size() == 1 && s[0] == tokens * k))
+    refuse(std::string(name) + " is " + shape_of(s) + ", not " + shape_of({tokens, k}));
+  return flat(t);
 }
 
 Tensor make(at::IntArrayRef size, at::ScalarType type, const Tensor& like) {
@@ -248,7 +260,7 @@ const Plan p = plan_of(a[2], y);
 if (r.n != p.tokens * p.k)
   refuse("y has " + std::to_string(r.n) + " rows, the plan " + std::to_string(p.tokens * p.k));
 Flat w;
-if (a[1] != Py_None) w = flat(a[1], "weights", at::kFloat, r.n, y);
+if (a[1] != Py_None) w = route_values(a[1], "weights", p.tokens, p.k, y);
 Tensor out = make({p.tokens, r.width}, y.scalar_type(), y);
 check(qmoe_combine(r.p, r.ld, static_cast<float*>(w.p), static_cast<int32_t*>(p.pos.p), p.tokens, p.k, r.width, dt,
                    out.mutable_data_ptr(), stream()));
@@ -263,7 +275,7 @@ const Rows r = rows_2d(dout, "dout");
 const Plan p = plan_of(a[3], dout, r.n);
 const bool need_dy = PyObject_IsTrue(a[4]) == 1, need_dw = PyObject_IsTrue(a[5]) == 1;
 Flat w;
-if (a[2] != Py_None) w = flat(a[2], "weights", at::kFloat, r.n * p.k, dout);
+if (a[2] != Py_None) w = route_values(a[2], "weights", r.n, p.k, dout);
 Rows y;
 if (need_dw) {
   y = rows_2d(further(a[1], "y", dout.scalar_type(), dout), "y");
