@@ -81,3 +81,21 @@ def test_route_weights_of_another_shape_are_refused(ops):
     flat = w.reshape(-1).clone().requires_grad_()
     (dw,) = torch.autograd.grad(ops.combine(y, flat, plan), [flat], [dout])
     assert torch.equal(dw.reshape(T, k), ops.combine_grad(dout, y, w, plan)[1])
+
+
+@pytest.mark.gpu
+def test_norm_weights_of_another_shape_are_refused(ops):
+    from weight_only_quantized_qmoe_gb300 import QMoEError, binding
+    x, w = torch.randn((4, 16), device="cuda"), torch.ones(16, device="cuda")
+    for bad in (w.reshape(4, 4), w.reshape(16, 1), w[None, :, None], w[:8]):
+        for kw in (dict(w_post=bad), dict(w_pre=bad)):
+            with pytest.raises(QMoEError) as e:
+                ops.block_norm(x, x, **kw)
+            assert e.value.status == binding.QMOE_ERR_INVALID_ARG
+    # axes of one before it say nothing, and the gradient has them too
+    want = ops.block_norm(x, x, w_post=w, w_pre=w)
+    row = torch.ones((1, 16), device="cuda", requires_grad=True)
+    got = ops.block_norm(x, x, w_post=row, w_pre=row)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    (g,) = torch.autograd.grad(got[1].sum(), [row])
+    assert g.shape == (1, 16)

@@ -133,6 +133,13 @@ Flat route_values(PyObject* o, const char* name, int64_t tokens, int64_t k, cons
     refuse(std::string(name) + " is " + shape_of(s) + ", not " + shape_of({tokens, k}));
   return flat(t);
 }
+// A value a column: [width], or with leading axes of one.
+Flat column_values(PyObject* o, const char* name, int64_t width, const Tensor& like) {
+  const Tensor& t = further(o, name, like.scalar_type(), like);
+  if (t.dim() < 1 || t.size(-1) != width || t.numel() != width)
+    refuse(std::string(name) + " is " + shape_of(t.sizes()) + ", not " + shape_of({width}));
+  return flat(t);
+}
 
 Tensor make(at::IntArrayRef size, at::ScalarType type, const Tensor& like) {
   return at::detail::empty_cuda(size, type, like.device(), std::nullopt);
@@ -447,8 +454,8 @@ Norm norm_of(PyObject* const* a) {
       refuse("gate " + shape_of(gs) + " is not of the shape of x, of its last axis or of its rows");
     }
   }
-  if (a[3] != Py_None) m.wq = flat(a[3], "w_post", x.scalar_type(), m.rx.width, x);
-  if (a[4] != Py_None) m.wp = flat(a[4], "w_pre", x.scalar_type(), m.rx.width, x);
+  if (a[3] != Py_None) m.wq = column_values(a[3], "w_post", m.rx.width, x);
+  if (a[4] != Py_None) m.wp = column_values(a[4], "w_pre", m.rx.width, x);
   return m;
 }
 PyObject* make_stats(const Tensor& s1, const Tensor& s2) {
@@ -498,8 +505,8 @@ const float scale = (float)to_double(a[9]);
 Tensor dx = make(x.sizes(), type, x), d_o, dg, dwq, dwp;
 if (m.has_o) d_o = make(x.sizes(), type, x);
 if (m.gate || m.kind != QMOE_GATE_NONE) dg = make(THPVariable_Unpack(a[2]).sizes(), type, x);
-if (a[3] != Py_None) dwq = make({H}, type, x);
-if (a[4] != Py_None) dwp = make({H}, type, x);
+if (a[3] != Py_None) dwq = make(THPVariable_Unpack(a[3]).sizes(), type, x);
+if (a[4] != Py_None) dwp = make(THPVariable_Unpack(a[4]).sizes(), type, x);
 const size_t bytes = qmoe_block_norm_grad_workspace(T, H, m.dt);
 Tensor work = make({(int64_t)bytes}, at::kByte, x);
 check(qmoe_block_norm_grad(dr.p, dr.ld, dh.p, dh.ld, m.rx.p, m.rx.ld, m.ro.p, m.ro.ld, m.gate, m.kind, m.rg.ld, m.wq.p, m.wp.p,
