@@ -99,3 +99,33 @@ def test_norm_weights_of_another_shape_are_refused(ops):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     (g,) = torch.autograd.grad(got[1].sum(), [row])
     assert g.shape == (1, 16)
+
+
+# --- automatic differentiation ---------------------------------------------------------
+def test_forward_mode_derivatives_are_refused(ops):
+    # there is no tangent to give: an output without one would mean zero
+    from torch.autograd import forward_ad
+    from weight_only_quantized_qmoe_gb300 import QMoEError
+    plan = ops.ExpertPlan(*(torch.zeros(4, dtype=torch.int32) for _ in range(3)), 2, 3)
+    x, w = torch.randn(4, 8), torch.ones(8)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        dual_w = forward_ad.make_dual(w, torch.ones_like(w))
+        weights = forward_ad.make_dual(torch.ones(2, 2), torch.ones(2, 2))
+        for call in (lambda: ops.dispatch(dual, plan), lambda: ops.combine(dual, None, plan),
+                     lambda: ops.combine(x, weights, plan), lambda: ops.block_norm(dual), lambda: ops.block_norm(x, dual),
+                     lambda: ops.block_norm(x, x, w_post=dual_w), lambda: ops.block_norm(x, w_pre=dual_w),
+                     lambda: ops.block_norm(x, x, gate=dual_w)):
+            for enabled in (True, False):
+                with torch.set_grad_enabled(enabled), pytest.raises(QMoEError, match="forward-mode"):
+                    call()
+
+
+@pytest.mark.gpu
+def test_tensors_without_a_tangent_pass_inside_a_dual_level(ops):
+    from torch.autograd import forward_ad
+    x, w = torch.randn((4, 8), device="cuda"), torch.ones(8, device="cuda")
+    want = ops.block_norm(x, w_pre=w)
+    with forward_ad.dual_level():
+        got = ops.block_norm(x, w_pre=w)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

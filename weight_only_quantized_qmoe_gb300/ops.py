@@ -13,7 +13,8 @@ part), which define what each computes:
   block with the gate of its output and the residual scale.
 
 ``dispatch``, ``combine`` and ``block_norm`` take part in automatic
-differentiation where an input requires a gradient.  Refused arguments raise
+differentiation where an input requires a gradient; forward mode is refused.
+Refused arguments raise
 :class:`~weight_only_quantized_qmoe_gb300.QMoEError`.  Every call runs on the
 current stream, or on ``stream=``: its outputs then belong to that stream (a
 reader on another stream has to wait for it), and its inputs have to be ready
@@ -27,6 +28,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import QMoEError, binding
@@ -110,6 +112,10 @@ def _elsewhere(stream, call, *args):
 
 
 def _differentiable(*tensors):
+    if forward_ad._current_level >= 0:   # inside a dual level: a tangent is not to be lost without a word
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                _refuse("forward-mode differentiation is not supported")
     if torch.is_grad_enabled():
         for t in tensors:
             if getattr(t, "requires_grad", False):
