@@ -129,3 +129,38 @@ def test_tensors_without_a_tangent_pass_inside_a_dual_level(ops):
     with forward_ad.dual_level():
         got = ops.block_norm(x, w_pre=w)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_a_plan_changed_before_the_gradient_is_refused(ops):
+    # as for any tensor that a gradient needs
+    T, k, H = 5, 2, 16
+    ids = torch.randint(0, 3, (T, k), device="cuda")
+
+    def routed(what):
+        plan = ops.expert_sort(ids, 3)
+        if what == "dispatch":
+            x = torch.randn((T, H), device="cuda", requires_grad=True)
+            return plan, ops.dispatch(x, plan), x
+        y = torch.randn((T * k, H), device="cuda", requires_grad=True)
+        return plan, ops.combine(y, torch.rand((T, k), device="cuda"), plan), y
+
+    for what in ("dispatch", "combine"):
+        plan, out, leaf = routed(what)
+        plan.pos.copy_(plan.pos.flip(0))
+        with pytest.raises(RuntimeError, match="inplace"):
+            torch.autograd.grad(out.sum(), [leaf])
+        plan, out, leaf = routed(what)
+        (g,) = torch.autograd.grad(out.sum(), [leaf])
+        assert g.shape == leaf.shape
+
+
+@pytest.mark.gpu
+def test_a_plan_that_is_none_is_refused_where_a_gradient_is_needed_too(ops):
+    from weight_only_quantized_qmoe_gb300 import QMoEError
+    x = torch.randn((4, 16), device="cuda", requires_grad=True)
+    for plan in (None, torch.zeros(4, device="cuda")):
+        with pytest.raises(QMoEError):
+            ops.dispatch(x, plan)
+        with pytest.raises(QMoEError):
+            ops.combine(x, None, plan)

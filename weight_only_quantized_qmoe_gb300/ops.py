@@ -141,27 +141,31 @@ def expert_sort(ids, experts, stream=None) -> ExpertPlan:
 class _DispatchFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, plan):
-        ctx.plan = plan
-        return _c.dispatch(x, plan)
+        out = _c.dispatch(x, plan)
+        ctx.save_for_backward(plan.pos, plan.offsets)
+        ctx.sizes = plan.k, plan.experts
+        return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
-        return dispatch_grad(dxs, ctx.plan), None
+        return dispatch_grad(dxs, ExpertPlan(None, *ctx.saved_tensors, *ctx.sizes)), None
 
 
 class _CombineFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, plan):
-        ctx.save_for_backward(y, weights)
-        ctx.plan = plan
-        return _c.combine(y, weights, plan)
+        out = _c.combine(y, weights, plan)
+        ctx.save_for_backward(y, weights, plan.pos, plan.offsets)
+        ctx.sizes = plan.k, plan.experts
+        return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        y, weights = ctx.saved_tensors
-        dy, dw = combine_grad(dout, y, weights, ctx.plan, ctx.needs_input_grad[0],
+        y, weights, pos, offsets = ctx.saved_tensors
+        plan = ExpertPlan(None, pos, offsets, *ctx.sizes)
+        dy, dw = combine_grad(dout, y, weights, plan, ctx.needs_input_grad[0],
                               weights is not None and ctx.needs_input_grad[1])
         return dy, None if dw is None else dw.reshape(weights.shape), None
 
