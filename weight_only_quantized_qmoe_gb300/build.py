@@ -1,6 +1,7 @@
 """Build libqmoe.so (the C-ABI library) in-tree with nvcc for sm_103a, and
 _ops_torch.so (the operators on torch tensors, a CPython module that calls the
-library) with g++ against torch's headers.
+library) with g++ against torch's headers.  The library needs no torch; without
+one the module is left out.
 
 Every translation unit is compiled in parallel; the objects go to
 ``<repo>/_build`` and the libraries next to this file.  No cmake.
@@ -42,18 +43,27 @@ def nvcc_path() -> str:
     return found
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
-    files.append(os.path.join(INCLUDE, "qmoe.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _newer(target: str, suffixes) -> bool:
+    """The target is there and no older than the sources of these kinds."""
+    if not os.path.exists(target):
+        return False
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(suffixes)]
+    files += [os.path.join(INCLUDE, "qmoe.h"), os.path.abspath(__file__)]
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB_PATH, (".cu", ".cuh", ".h"))
+
+
+def module_up_to_date() -> bool:
+    """The module on torch tensors is current, or there is no torch to build it against."""
+    return find_spec("torch") is None or _newer(TORCH_MODULE, (".cpp",))
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(TORCH_MODULE)):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_MODULE))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return library_up_to_date() and module_up_to_date()
 
 
 def torch_module_commands(nvcc: str, obj: str):
@@ -80,7 +90,10 @@ def _run(cmd, what):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    """Compile what is not current; the module on torch tensors only where there is a torch."""
+    with_library = force or not library_up_to_date()
+    with_module = find_spec("torch") is not None and (force or not module_up_to_date())
+    if not with_library and not with_module:
         return LIB_PATH
     nvcc = nvcc_path()
     objdir = os.path.join(ROOT, "_build")
@@ -98,19 +111,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    compile_torch, link_torch = torch_module_commands(nvcc, os.path.join(objdir, TORCH_SOURCE.replace(".cpp", ".o")))
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        torch_obj = ex.submit(_run, compile_torch, "g++ for " + TORCH_SOURCE)
-        objs = list(ex.map(compile_one, SOURCES))
-        torch_obj.result()
-    tmp = LIB_PATH + ".tmp"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcuda"],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    _run(link_torch, "link of " + os.path.basename(TORCH_MODULE))
-    os.replace(TORCH_MODULE + ".tmp", TORCH_MODULE)
+        torch_obj = None
+        if with_module:
+            compile_torch, link_torch = torch_module_commands(nvcc, os.path.join(objdir, TORCH_SOURCE.replace(".cpp", ".o")))
+            torch_obj = ex.submit(_run, compile_torch, "g++ for " + TORCH_SOURCE)
+        if with_library:
+            objs = list(ex.map(compile_one, SOURCES))
+            tmp = LIB_PATH + ".tmp"
+            _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcuda"], "link of " + os.path.basename(LIB_PATH))
+            os.replace(tmp, LIB_PATH)
+        if with_module:
+            torch_obj.result()
+            _run(link_torch, "link of " + os.path.basename(TORCH_MODULE))
+            os.replace(TORCH_MODULE + ".tmp", TORCH_MODULE)
     return LIB_PATH
 
 
