@@ -44,3 +44,22 @@ def test_the_library_needs_no_torch(compilers, monkeypatch):
     assert "libqmoe.so" in got and "qmoe_api.o" in got and not any("torch" in n for n in got)
     B.build()                       # and is current without it
     assert compilers.take() == []
+
+
+def test_the_module_is_built_again_for_another_torch(compilers, monkeypatch):
+    monkeypatch.setattr(B, "torch_version", lambda: "2.9.1+cu130", raising=False)
+    B.build()
+    assert {"libqmoe.so", "_ops_torch.so"} <= set(compilers.take())
+    assert B.up_to_date()
+    B.build()
+    assert compilers.take() == []
+    monkeypatch.setattr(B, "torch_version", lambda: "2.11.0+cu130")
+    assert not B.up_to_date() and B.library_up_to_date()
+    B.build()
+    assert compilers.take() == ["qmoe_ops_torch.o", "_ops_torch.so"]
+    assert B.up_to_date()
+
+
+def test_the_version_is_that_of_the_torch_there_is():
+    torch = pytest.importorskip("torch")
+    assert torch.__version__ in B.torch_version()

@@ -10,8 +10,11 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import platform
+import re
 import shutil
 import subprocess
+import sys
 import sysconfig
 from importlib.util import find_spec
 
@@ -57,9 +60,25 @@ def library_up_to_date() -> bool:
     return _newer(LIB_PATH, (".cu", ".cuh", ".h"))
 
 
+def torch_version() -> str:
+    """The torch and the Python that the module belongs to (without importing torch)."""
+    with open(os.path.join(list(find_spec("torch").submodule_search_locations)[0], "version.py")) as f:
+        found = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)
+    return f"{found.group(1) if found else '?'} {sys.version.split()[0]} {platform.machine()}"
+
+
+def _built_for() -> str:
+    """What torch_version() was when the module was built."""
+    try:
+        with open(TORCH_MODULE + ".torch") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def module_up_to_date() -> bool:
     """The module on torch tensors is current, or there is no torch to build it against."""
-    return find_spec("torch") is None or _newer(TORCH_MODULE, (".cpp",))
+    return find_spec("torch") is None or (_newer(TORCH_MODULE, (".cpp",)) and _built_for() == torch_version())
 
 
 def up_to_date() -> bool:
@@ -125,6 +144,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             torch_obj.result()
             _run(link_torch, "link of " + os.path.basename(TORCH_MODULE))
             os.replace(TORCH_MODULE + ".tmp", TORCH_MODULE)
+            with open(TORCH_MODULE + ".torch", "w") as f:
+                f.write(torch_version())
     return LIB_PATH
 
 
