@@ -15,7 +15,7 @@
 // to its rows in expert order: read once, quantised once, written k times at
 // 17/32 byte a value, instead of k 16-bit copies read again.  (bf16, rows of
 // 4127 that start anywhere: 2880 of them in 12 us, read back in 10; 4096 rows of
-// 1536 to eight places each 12 us.)
+// 1536 to eight places each 11 us.)
 #include <algorithm>
 #include <cstring>
 
@@ -203,9 +203,9 @@ __global__ void __launch_bounds__(32 * kQuantWarps) mx4_quantize_kernel(const Mx
 // the next one's loads in flight while it works, which one that ends after a
 // step has not: up to `most` steps while every multiprocessor still gets 32
 // warps, more where a row's kQuantWarps warps need them.  (Quantise and back,
-// us, with 6 / as few as possible: 8192 x 2048 f16 11.8 + 11.2 / 17.7 + 13.2,
-// 20000 x 704 bf16 11.9 + 10.6 / 17.1 + 14.0, 2880 x 4127 bf16 12.3 + 9.6 /
-// 13.5 + 10.3; but 32-bit rows written, 2880 x 4128: 13.5 / 11.0 with 3.)
+// us, with 6 / with one: 8192 x 2048 f16 10.8 + 11.2 / 18.0 + 13.2, 20000 x 704
+// bf16 11.1 + 10.6 / 21.7 + 21.7, 2880 x 4127 bf16 12.3 + 9.6 / 13.5 + 10.3;
+// but 32-bit rows written, 2880 x 4128: 13.3 / 10.9 with 3.)
 static dim3 mx4_block(int64_t segs, int64_t rows, int64_t most) {
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(most, rows * segs / (kSms * 32)));
   const int64_t at_most = std::min<int64_t>(kQuantWarps, (segs + want - 1) / want);

@@ -25,12 +25,12 @@
 // weight tile) list, which every CTA derives from the device offsets.
 //
 // Bound: at few rows an expert the weight bytes (17/32 byte a weight; 256 rows
-// of 2048 to 1536 over 128 experts: 34 us, 6.3 TB/s); at many the way of a stage
-// round the ring, about 4000 cycles for four stages of 384 cycles of MMAs
-// (32768 rows of 1536 to 4096 over 64 experts: 125 us, 3.3 PFLOP/s, 4.1 TB/s of
-// its bytes; the same copies without MMAs, scales and stores take 107).  BN =
-// 192 is what two accumulators and the scales leave of TMEM; BN = 64 puts more
-// multiprocessors to work where there are few tiles.
+// of 2048 to 1536 over 128 experts, 99 of which have rows, 166 MB: 33 us, 5.0
+// TB/s); at many the way of a stage round the ring, about 4000 cycles for four
+// stages of 384 cycles of MMAs (32768 rows of 1536 to 4096 over 64 experts: 122
+// us, 3.4 PFLOP/s, 4.2 TB/s of its bytes; the same copies without MMAs, scales and
+// stores take 107).  BN = 192 is what two accumulators and the scales leave of
+// TMEM; BN = 64 puts more multiprocessors to work where there are few tiles.
 //
 // Every wait is bounded; a timeout aborts all roles, drains what is in
 // flight, frees TMEM and is reported by qmoe_op_poll_status.
