@@ -387,9 +387,10 @@ void qmoe_destroy(qmoe_layer* layer);
  * Operators around the expert layer
  *
  * What a block built from the layer's parts needs beside qmoe_forward: the
- * routes sorted by expert and the rows taken there and back (with their
- * gradients), microscaled 4-bit floating point rows and their product, and
- * the norms on either side of the block.  (No counterpart in the pages but
+ * router, the routes sorted by expert and the rows taken there and back (with
+ * their gradients), microscaled 4-bit floating point rows and their product,
+ * 8-bit floating point rows and their products, the gradient of the experts'
+ * weights, and the norms on either side of the block.  (No counterpart in the pages but
  * the grouping and the combine, whose definitions are those of qmoe_forward:
  * [qmoe.rs launch_grouping, qmoe_combine_impl].)
  *
@@ -409,16 +410,50 @@ void qmoe_destroy(qmoe_layer* layer);
 const char* qmoe_op_last_error(void);
 
 /* Read and clear the device status of these operators: QMOE_OK, or
- * QMOE_ERR_TIMEOUT if a bounded wait of a qmoe_mx4_matmul of this context ran
- * out since the last poll (its output is then meaningless).  Synchronises the
- * device. */
+ * QMOE_ERR_TIMEOUT if a bounded wait of a qmoe_mx4_matmul, qmoe_fp8_matmul or
+ * qmoe_weight_grad of this context ran out since the last poll (its output is
+ * then meaningless).  Synchronises the device. */
 qmoe_status qmoe_op_poll_status(void);
 
 /* The iteration limit of their bounded waits (0 = the default), and the test
- * hook that arms the first copy of every later qmoe_mx4_matmul without
+ * hook that arms the first copy of every later call of the three without
  * issuing it (see qmoe_debug_inject_stall).  Both hold for the process. */
 qmoe_status qmoe_op_set_wait_limit(int64_t iterations);
 qmoe_status qmoe_op_debug_inject_stall(int enable);
+
+/*
+ * The router: top_k experts of every token and their weights.
+ *   s_e = softmax(logits[t])_e (QMOE_SCORE_SOFTMAX) or sigmoid(logits[t, e]);
+ *   c_e = s_e + bias[e];  without a bias experts are ranked by their logits
+ *   (the total order of qmoe_forward), which is the order of their scores.
+ * With top_groups < groups the experts are `groups` runs of experts / groups; a
+ * group's score is the sum of its group_best (1 or 2) largest c (without a bias
+ * and with 2: largest s), and only the top_groups best groups take part.  The
+ * top_k largest c are chosen, best first; ties, of groups too, go to the lower
+ * index.  Choices are those of c in 64 bits.
+ *   weights[t, j] = scale * s_j, or with renormalize scale * s_j / (sum of the
+ *   chosen s); float32.
+ * An expert whose logit (or bias) is -infinity is never chosen; a slot without
+ * an expert gets id -1 (which qmoe_expert_sort drops) and weight 0.  An expert
+ * whose logit or bias is NaN is not chosen either, and the token's weights are
+ * all NaN.
+ *   logits_dev  dtype [num_tokens, experts], row stride ld_logits
+ *   bias_dev    float32 [experts], or NULL
+ *   ids_dev     int32, weights_dev float32 [num_tokens, top_k]
+ * experts <= 1024, top_k and groups <= 32 (UNSUPPORTED beyond); top_k <=
+ * top_groups * (experts / groups); group_best 2 needs groups of two.
+ */
+enum { QMOE_SCORE_SOFTMAX = 0, QMOE_SCORE_SIGMOID = 1 };
+qmoe_status qmoe_expert_route(const void* logits_dev, int64_t ld_logits, int dtype, const float* bias_dev, int64_t num_tokens,
+                              int experts, int top_k, int scoring, int groups, int top_groups, int group_best, int renormalize,
+                              float scale, int32_t* ids_dev, float* weights_dev, void* stream);
+
+/* The gradient of its weights: dlogits [num_tokens, experts] (dtype, contiguous)
+ * of dweights float32 [num_tokens, top_k], for the logits and the ids chosen (an
+ * id outside [0, experts) adds nothing).  The choice and the bias have none. */
+qmoe_status qmoe_expert_route_grad(const float* dweights_dev, const void* logits_dev, int64_t ld_logits, int dtype,
+                                   const int32_t* ids_dev, int64_t num_tokens, int experts, int top_k, int scoring,
+                                   int renormalize, float scale, void* dlogits_dev, void* stream);
 
 /*
  * Routes sorted by expert.  Route r = t * top_k + j goes to expert ids[t, j];
@@ -506,6 +541,68 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_
 qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
                             const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,
                             int experts, int64_t n, int64_t k, int out_dtype, void* out_dev, int64_t ld_out, void* stream);
+
+/*
+ * 8-bit rows: E4M3 values (1, 4 and 3 bits; the largest 448) whose blocks share
+ * a power-of-two scale 2^(s - 127), s = its byte (255: NaN).
+ *   codes  uint8 [rows, 16 * ceil(cols / 16)]; what lies past cols is written
+ *          as zeros and not used
+ *   scales of rows (square 0): a block is 128 values of a row; uint8
+ *          [rows / panel_rows][ceil(nb / 4)][panel_rows][4], nb = ceil(cols /
+ *          128), in the order of the 4-bit rows' scales; past nb written as zeros
+ *          and not used
+ *   scales of blocks (square 1): a block is 128 x 128 of a matrix of panel_rows
+ *          rows; uint8 [rows / panel_rows][ceil(panel_rows / 128)][nb]
+ *
+ * qmoe_fp8_quantize: s is the smallest for which the block's largest magnitude
+ * is at most 448 * 2^(s - 127) (at least 0); elements rounded to the nearest, ties
+ * to even; a block with a NaN or an infinity gets s = 255 and codes 0.  x_dev,
+ * activation, pos_dev, offsets_dev, top_k and experts as in qmoe_mx4_quantize;
+ * square 1 takes neither an activation nor pos.  codes_dev must be 16-byte,
+ * scales_dev (of rows) 4-byte aligned.
+ */
+qmoe_status qmoe_fp8_quantize(const void* x_dev, int64_t ld_x, int64_t rows, int64_t cols, int dtype, int activation,
+                              const int32_t* pos_dev, const int32_t* offsets_dev, int top_k, int experts,
+                              int64_t panel_rows, int square, uint8_t* codes_dev, uint8_t* scales_dev, void* stream);
+
+/* The values of 8-bit rows, rounded once to dtype (a magnitude of 2^128, which
+ * one rounded up from the last 3 % of float32's range has, is infinite). */
+qmoe_status qmoe_fp8_dequantize(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_t rows, int64_t cols,
+                                int64_t panel_rows, int square, int dtype, void* out_dev, int64_t ld_out, void* stream);
+
+/*
+ * Product of 8-bit rows with 8-bit weights, offsets[e] <= i < offsets[e + 1]:
+ *   transpose 0:  out[i, c] = sum_d a[i, d] * w[e, c, d];  a [rows, k], out [rows, n]
+ *   transpose 1:  out[i, d] = sum_c a[i, c] * w[e, c, d];  a [rows, n], out [rows, k]
+ * (fp32 accumulation, one rounding to out_dtype); rows from offsets[experts]
+ * on are zeros.  offsets_dev NULL: one expert, all rows.
+ *   a  scales of rows, one panel;  w  [experts, n, k], scales of blocks (square 1)
+ *   out_dev  out_dtype, row stride ld_out
+ * Both codes must be 16-byte, a's scales 4-byte aligned; experts <= 1024; rows
+ * and experts * n have to be below 2^31 - 512.
+ */
+qmoe_status qmoe_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
+                            const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,
+                            int experts, int64_t n, int64_t k, int transpose, int out_dtype, void* out_dev, int64_t ld_out,
+                            void* stream);
+
+/*
+ * Gradient of the experts' weights of a product out[i, :] = w[e] x[i, :]:
+ *   dw[e, c, d] = sum over offsets[e] <= i < offsets[e + 1] of dy[i, c] * x[i, d]
+ * (fp32 accumulation in an order that does not change from run to run, one
+ * rounding to out_dtype); an expert without rows gets zeros.  offsets_dev NULL:
+ * one expert, all rows.
+ *   dy_dev  dtype [rows, n], x_dev  dtype [rows, k]; QMOE_F16 or QMOE_BF16
+ *           (QMOE_F32: UNSUPPORTED)
+ *   dw_dev  out_dtype [experts, n, k]
+ * qmoe_weight_grad_workspace: bytes of workspace (16-byte aligned) for operands
+ * with these addresses and strides; 0 where rows start on 16-byte boundaries.
+ */
+size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int64_t n,
+                                  int64_t k);
+qmoe_status qmoe_weight_grad(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const int32_t* offsets_dev,
+                             int64_t rows, int experts, int64_t n, int64_t k, int dtype, int out_dtype, void* dw_dev,
+                             void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /*
  * The norms on either side of a block, with the gate of its output and the

@@ -29,6 +29,7 @@ QMOE_PATH_NONE, QMOE_PATH_SEPARATE, QMOE_PATH_FUSED = 0, 1, 2
 QMOE_FUSED_OFF, QMOE_FUSED_ON, QMOE_FUSED_AUTO = 0, 1, 2
 QMOE_COMBINE_REDUCE, QMOE_COMBINE_ORDERED, QMOE_COMBINE_AUTO = 0, 1, 2
 QMOE_ACT_NONE = -1
+QMOE_SCORE_SOFTMAX, QMOE_SCORE_SIGMOID = 0, 1
 QMOE_GATE_NONE, QMOE_GATE_TOKEN, QMOE_GATE_CHANNEL, QMOE_GATE_FULL = 0, 1, 2, 3
 
 _p = ctypes.c_void_p
@@ -67,6 +68,8 @@ _SIGS = {
     "qmoe_op_poll_status": (_i, []),
     "qmoe_op_set_wait_limit": (_i, [_i64]),
     "qmoe_op_debug_inject_stall": (_i, [_i]),
+    "qmoe_expert_route": (_i, [_p, _i64, _i, _p, _i64, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]),
+    "qmoe_expert_route_grad": (_i, [_p, _p, _i64, _i, _p, _i64, _i, _i, _i, _i, _f, _p, _p]),
     "qmoe_expert_sort": (_i, [_p, _i, _i64, _i64, _i, _i, _p, _p, _p, _p]),
     "qmoe_dispatch": (_i, [_p, _i64, _p, _p, _i64, _i, _i, _i64, _i, _p, _p]),
     "qmoe_dispatch_grad": (_i, [_p, _i64, _p, _i64, _i, _i64, _i, _p, _p]),
@@ -75,6 +78,11 @@ _SIGS = {
     "qmoe_mx4_quantize": (_i, [_p, _i64, _i64, _i64, _i, _i, _p, _p, _i, _i, _i64, _p, _p, _p]),
     "qmoe_mx4_dequantize": (_i, [_p, _p, _i64, _i64, _i64, _i, _p, _i64, _p]),
     "qmoe_mx4_matmul": (_i, [_p, _p, _i64, _p, _p, _p, _i, _i64, _i64, _i, _p, _i64, _p]),
+    "qmoe_fp8_quantize": (_i, [_p, _i64, _i64, _i64, _i, _i, _p, _p, _i, _i, _i64, _i, _p, _p, _p]),
+    "qmoe_fp8_dequantize": (_i, [_p, _p, _i64, _i64, _i64, _i, _i, _p, _i64, _p]),
+    "qmoe_fp8_matmul": (_i, [_p, _p, _i64, _p, _p, _p, _i, _i64, _i64, _i, _i, _p, _i64, _p]),
+    "qmoe_weight_grad_workspace": (_sz, [_p, _i64, _p, _i64, _i64, _i64, _i64]),
+    "qmoe_weight_grad": (_i, [_p, _i64, _p, _i64, _p, _i64, _i, _i64, _i64, _i, _i, _p, _p, _sz, _p]),
     "qmoe_block_norm": (_i, [_p, _i64, _p, _i64, _p, _i, _i64, _p, _p, _f, _f, _i64, _i64, _i, _p, _p, _p, _p, _p]),
     "qmoe_block_norm_grad_workspace": (_sz, [_i64, _i64, _i]),
     "qmoe_block_norm_grad": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i, _i64, _p, _p, _p, _p, _f, _i64, _i64,
@@ -232,8 +240,9 @@ def qmoe_destroy(layer):
 # are integers (0 or None = NULL), strides and sizes in elements, in the order
 # of include/qmoe.h.
 _OPERATORS = frozenset((
-    "qmoe_op_poll_status", "qmoe_op_set_wait_limit", "qmoe_op_debug_inject_stall", "qmoe_expert_sort", "qmoe_dispatch",
-    "qmoe_dispatch_grad", "qmoe_combine", "qmoe_combine_grad", "qmoe_mx4_quantize", "qmoe_mx4_dequantize",
+    "qmoe_op_poll_status", "qmoe_op_set_wait_limit", "qmoe_op_debug_inject_stall", "qmoe_expert_route",
+    "qmoe_expert_route_grad", "qmoe_fp8_quantize", "qmoe_fp8_dequantize", "qmoe_fp8_matmul", "qmoe_weight_grad_workspace",
+    "qmoe_weight_grad", "qmoe_expert_sort", "qmoe_dispatch", "qmoe_dispatch_grad", "qmoe_combine", "qmoe_combine_grad", "qmoe_mx4_quantize", "qmoe_mx4_dequantize",
     "qmoe_mx4_matmul", "qmoe_block_norm", "qmoe_block_norm_grad_workspace", "qmoe_block_norm_grad"))
 
 

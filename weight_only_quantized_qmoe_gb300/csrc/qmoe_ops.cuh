@@ -1,6 +1,7 @@
 // Operators around the expert layer: argument blocks and launchers shared by
-// their entry points (qmoe_ops_api.cu) and their kernels (qmoe_sort.cu,
-// qmoe_mx4.cu, qmoe_mx4_gemm.cu, qmoe_norm.cu).
+// their entry points (qmoe_ops_api.cu) and their kernels (qmoe_choice.cu,
+// qmoe_sort.cu, qmoe_mx4.cu, qmoe_mx4_gemm.cu, qmoe_fp8.cu, qmoe_fp8_gemm.cu,
+// qmoe_wgrad.cu, qmoe_norm.cu).
 #pragma once
 
 #include <utility>
@@ -94,6 +95,89 @@ struct Mx4MatmulArgs {
   WaitCfg wait;
 };
 cudaError_t launch_mx4_matmul(const Mx4MatmulArgs& a, int inject_stall, cudaStream_t s);
+
+// The router.
+struct ChoiceArgs {
+  const void* logits;       // [T, E], rows ld apart
+  int64_t ld;
+  int dtype;
+  const float* bias;        // [E] or null
+  int64_t T;
+  int E, k, scoring, groups, top_groups, best, renorm;
+  float scale;
+  int* ids;                 // [T, k]
+  float* w;                 // [T, k]
+  // gradient
+  const float* dw;          // [T, k]
+  void* dlogits;            // [T, E]
+};
+cudaError_t launch_choice(const ChoiceArgs& a, cudaStream_t s);
+cudaError_t launch_choice_grad(const ChoiceArgs& a, cudaStream_t s);
+constexpr int kChoiceMax = 32;   // slots, groups: a lane each
+
+// 8-bit rows.  Codes: rows of fp8_pitch(cols) bytes.  Scales of rows: one panel
+// [ceil(nb / 4), rows, 4] bytes a matrix, nb = ceil(cols / 128) (the layout of the
+// 4-bit rows); of blocks: [ceil(rows / 128), nb] a matrix.
+__host__ __device__ inline int64_t fp8_pitch(int64_t cols) { return (cols + 15) / 16 * 16; }
+
+struct Fp8QuantArgs {
+  const void* x;            // [rows, cols] (gated activation: [rows, 2 * cols], gate | up)
+  int64_t ld_x;
+  int64_t rows, cols;
+  int dtype;
+  ActParams act;            // act = -1: none
+  const int* pos;           // as in Mx4QuantArgs
+  const int* offsets;
+  int k, E;
+  int64_t panel;            // rows of a matrix
+  int square;               // a scale per 128 x 128 block
+  uint8_t* codes;
+  uint8_t* scales;
+};
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, cudaStream_t s);
+
+struct Fp8DequantArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows, cols, panel;
+  int square, dtype;
+  void* out;                // [rows, cols]
+  int64_t ld_out;
+};
+cudaError_t launch_fp8_dequantize(const Fp8DequantArgs& a, cudaStream_t s);
+
+struct Fp8MatmulArgs {
+  const uint8_t* a_codes;   // [R, inner]
+  const uint8_t* a_scales;  // one panel of R rows
+  const uint8_t* w_codes;   // [E, N, K]
+  const uint8_t* w_scales;  // blocks of each
+  const int* offsets;       // [E + 1], or null: one group of R rows
+  int64_t R;
+  int E, N, K;
+  int back;                 // 0: rows of K to rows of N; 1: rows of N to rows of K
+  int out_dtype;
+  void* out;                // [R, N or K]
+  int64_t ld_out;
+  WaitCfg wait;
+};
+cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStream_t s);
+
+// Gradient of the experts' weights.
+struct WgradArgs {
+  const void* dy;           // [R, N]
+  int64_t ld_dy;
+  const void* x;            // [R, K]
+  int64_t ld_x;
+  const int* offsets;       // as above
+  int64_t R;
+  int E, N, K;
+  int dtype, out_dtype;     // 16-bit; any
+  void* dw;                 // [E, N, K]
+  uint8_t* workspace;       // aligned copies of operands that TMA cannot read
+  WaitCfg wait;
+};
+cudaError_t launch_weight_grad(const WgradArgs& a, int inject_stall, cudaStream_t s);
+size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t R, int64_t N, int64_t K);
 
 // Norms around a block.
 

@@ -15,8 +15,8 @@ using namespace qmoe;
 
 namespace {
 
-// Set by a bounded wait that ran out (qmoe_mx4_matmul), read and cleared by
-// qmoe_op_poll_status.
+// Set by a bounded wait that ran out (the products and the weight gradient),
+// read and cleared by qmoe_op_poll_status.
 __device__ int g_op_status;
 
 thread_local char t_err[256] = "";
@@ -84,6 +84,44 @@ qmoe_status check_rows(int64_t H, int64_t ld, int dtype) {
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+// A tile's rows, of either operand of a product, may reach past the last one by
+// less than this.
+constexpr int kReach = 256;
+
+// Shapes of a product grouped by expert: rows, and experts of n rows of k.
+qmoe_status check_grouped(int64_t rows, const void* offsets, int experts, int64_t n, int64_t k) {
+  OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
+  OP_CHECK(rows < INT_MAX - kReach, "rows %lld do not fit 31 bits", (long long)rows);
+  OP_CHECK(experts >= 1, "experts %d is not positive", experts);
+  OP_SUPPORTED(experts <= kSortMaxExperts, "experts %d: at most %d", experts, kSortMaxExperts);
+  OP_CHECK(offsets || experts == 1, "%d experts need offsets", experts);
+  OP_CHECK(n >= 1 && k >= 1 && k < (1LL << 30), "a weight of %lld x %lld is out of range", (long long)n, (long long)k);
+  OP_CHECK(n < (INT_MAX - kReach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
+  return QMOE_OK;
+}
+// The bounded waits' status word and limit.
+qmoe_status wait_config(WaitCfg& w) {
+  void* status = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&status, g_op_status);
+  if (e != cudaSuccess) return done(e, "look up the status word");
+  const long long limit = g_wait_limit.load();
+  w = WaitCfg{static_cast<int*>(status), limit ? limit : kDefaultWaitLimit};
+  return QMOE_OK;
+}
+
+qmoe_status check_choice(int64_t ld, int dtype, int64_t T, int E, int k, int scoring, float scale) {
+  OP_TRY(check_rows(E, ld, dtype));
+  OP_CHECK(T >= 0, "num_tokens %lld is negative", (long long)T);
+  OP_CHECK(k >= 1, "top_k %d is not positive", k);
+  OP_CHECK(k <= E, "top_k %d is above the %d experts", k, E);
+  OP_SUPPORTED(E <= kSortMaxExperts, "experts %d: at most %d", E, kSortMaxExperts);
+  OP_SUPPORTED(k <= kChoiceMax, "top_k %d: at most %d", k, kChoiceMax);
+  OP_CHECK(T <= (INT_MAX - 1) / k, "num_tokens %lld x top_k %d does not fit 31 bits", (long long)T, k);
+  OP_CHECK(scoring == QMOE_SCORE_SOFTMAX || scoring == QMOE_SCORE_SIGMOID, "scoring %d is unknown", scoring);
+  OP_CHECK(std::isfinite(scale), "scale must be finite");
+  return QMOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -112,6 +150,64 @@ qmoe_status qmoe_op_poll_status(void) {
   e = cudaMemcpyToSymbol(g_op_status, &zero, sizeof zero);
   if (e != cudaSuccess) return done(e, "clear the status word");
   return fail(QMOE_ERR_TIMEOUT, "a bounded device-side wait ran out");
+}
+
+qmoe_status qmoe_expert_route(const void* logits_dev, int64_t ld_logits, int dtype, const float* bias_dev, int64_t num_tokens,
+                              int experts, int top_k, int scoring, int groups, int top_groups, int group_best, int renormalize,
+                              float scale, int32_t* ids_dev, float* weights_dev, void* stream) {
+  OP_TRY(check_choice(ld_logits, dtype, num_tokens, experts, top_k, scoring, scale));
+  OP_CHECK(groups >= 1 && experts % groups == 0, "groups %d does not divide the %d experts", groups, experts);
+  OP_SUPPORTED(groups <= kChoiceMax, "groups %d: at most %d", groups, kChoiceMax);
+  OP_CHECK(top_groups >= 1 && top_groups <= groups, "top_groups %d is not from 1 to %d", top_groups, groups);
+  OP_CHECK(group_best == 1 || group_best == 2, "group_best %d is not 1 or 2", group_best);
+  OP_CHECK(top_groups == groups || group_best <= experts / groups, "group_best %d: groups hold %d expert(s)", group_best,
+           experts / groups);
+  OP_CHECK(top_k <= (int64_t)top_groups * (experts / groups), "top_k %d: %d group(s) hold %d experts", top_k, top_groups,
+           top_groups * (experts / groups));
+  if (num_tokens == 0) return QMOE_OK;
+  OP_CHECK(logits_dev && ids_dev && weights_dev, "logits, ids or weights is null");
+  OP_TRY(check_addresses({{logits_dev, dtype_size(dtype), "logits"}, {bias_dev, 4, "bias"}, {ids_dev, 4, "ids"}, {weights_dev, 4, "weights"}}));
+  ChoiceArgs a{};
+  a.logits = logits_dev;
+  a.ld = ld_logits;
+  a.dtype = dtype;
+  a.bias = bias_dev;
+  a.T = num_tokens;
+  a.E = experts;
+  a.k = top_k;
+  a.scoring = scoring;
+  a.groups = groups;
+  a.top_groups = top_groups;
+  a.best = group_best;
+  a.renorm = renormalize ? 1 : 0;
+  a.scale = scale;
+  a.ids = ids_dev;
+  a.w = weights_dev;
+  return done(launch_choice(a, as_stream(stream)), "expert route");
+}
+
+qmoe_status qmoe_expert_route_grad(const float* dweights_dev, const void* logits_dev, int64_t ld_logits, int dtype,
+                                   const int32_t* ids_dev, int64_t num_tokens, int experts, int top_k, int scoring,
+                                   int renormalize, float scale, void* dlogits_dev, void* stream) {
+  OP_TRY(check_choice(ld_logits, dtype, num_tokens, experts, top_k, scoring, scale));
+  if (num_tokens == 0) return QMOE_OK;
+  OP_CHECK(dweights_dev && logits_dev && ids_dev && dlogits_dev, "dweights, logits, ids or dlogits is null");
+  const int size = dtype_size(dtype);
+  OP_TRY(check_addresses({{dweights_dev, 4, "dweights"}, {logits_dev, size, "logits"}, {ids_dev, 4, "ids"}, {dlogits_dev, size, "dlogits"}}));
+  ChoiceArgs a{};
+  a.logits = logits_dev;
+  a.ld = ld_logits;
+  a.dtype = dtype;
+  a.T = num_tokens;
+  a.E = experts;
+  a.k = top_k;
+  a.scoring = scoring;
+  a.renorm = renormalize ? 1 : 0;
+  a.scale = scale;
+  a.ids = const_cast<int*>(ids_dev);
+  a.dw = dweights_dev;
+  a.dlogits = dlogits_dev;
+  return done(launch_choice_grad(a, as_stream(stream)), "expert route gradient");
 }
 
 qmoe_status qmoe_expert_sort(const void* ids_dev, int id_bytes, int64_t ld_ids, int64_t num_tokens, int top_k, int experts,
@@ -281,16 +377,14 @@ qmoe_status qmoe_mx4_dequantize(const uint8_t* codes_dev, const uint8_t* scales_
 qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
                             const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,
                             int experts, int64_t n, int64_t k, int out_dtype, void* out_dev, int64_t ld_out, void* stream) {
-  // a tile's rows, of either operand, may reach past the last one by less than this
-  constexpr int reach = 256;
   OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
-  OP_CHECK(rows < INT_MAX - reach, "rows %lld do not fit 31 bits", (long long)rows);
+  OP_CHECK(rows < INT_MAX - kReach, "rows %lld do not fit 31 bits", (long long)rows);
   OP_CHECK(experts >= 1, "experts %d is not positive", experts);
   OP_SUPPORTED(experts <= kSortMaxExperts, "experts %d: at most %d", experts, kSortMaxExperts);
   OP_CHECK(offsets_dev || experts == 1, "%d experts need offsets", experts);
   OP_TRY(check_rows(n, ld_out, out_dtype));
   OP_CHECK(k >= 1 && k < (1LL << 30), "reduction length %lld is out of range", (long long)k);
-  OP_CHECK(n < (INT_MAX - reach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
+  OP_CHECK(n < (INT_MAX - kReach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
   if (rows == 0) return QMOE_OK;
   OP_CHECK(a_codes_dev && a_scales_dev && w_codes_dev && w_scales_dev && out_dev, "an operand or out is null");
   OP_TRY(check_addresses({{a_codes_dev, 16, "a's codes"}, {a_scales_dev, 4, "a's scales"}, {w_codes_dev, 16, "w's codes"},
@@ -308,12 +402,141 @@ qmoe_status qmoe_mx4_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_
   a.out_dtype = out_dtype;
   a.out = out_dev;
   a.ld_out = ld_out;
-  void* status = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&status, g_op_status);
-  if (e != cudaSuccess) return done(e, "look up the status word");
-  const long long limit = g_wait_limit.load();
-  a.wait = WaitCfg{static_cast<int*>(status), limit ? limit : kDefaultWaitLimit};
+  OP_TRY(wait_config(a.wait));
   return done(launch_mx4_matmul(a, g_inject_stall.load(), as_stream(stream)), "mx4 matmul");
+}
+
+qmoe_status qmoe_fp8_quantize(const void* x_dev, int64_t ld_x, int64_t rows, int64_t cols, int dtype, int activation,
+                              const int32_t* pos_dev, const int32_t* offsets_dev, int top_k, int experts,
+                              int64_t panel_rows, int square, uint8_t* codes_dev, uint8_t* scales_dev, void* stream) {
+  OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
+  OP_CHECK(activation == QMOE_ACT_NONE || activation == QMOE_ACT_SWIGLU || activation == QMOE_ACT_GEGLU_TANH,
+           "activation %d is not QMOE_ACT_NONE or a gated one", activation);
+  OP_CHECK(cols >= 1 && cols <= (1 << 29), "cols %lld is out of range", (long long)cols);
+  OP_TRY(check_rows(activation == QMOE_ACT_NONE ? cols : 2 * cols, ld_x, dtype));
+  OP_CHECK(!square || (activation == QMOE_ACT_NONE && !pos_dev), "square blocks take neither an activation nor pos");
+  int64_t out_rows = rows;
+  if (pos_dev) {
+    OP_TRY(check_routes(rows, top_k, experts));
+    OP_CHECK(offsets_dev, "offsets is null beside pos");
+    out_rows = rows * top_k;
+    OP_CHECK(panel_rows == out_rows, "panel_rows %lld: with pos the output is one panel of %lld rows", (long long)panel_rows,
+             (long long)out_rows);
+  }
+  OP_CHECK(panel_rows >= 1 || out_rows == 0, "panel_rows %lld is not positive", (long long)panel_rows);
+  OP_CHECK(out_rows == 0 || out_rows % panel_rows == 0, "panel_rows %lld does not divide the %lld rows",
+           (long long)panel_rows, (long long)out_rows);
+  if (out_rows == 0) return QMOE_OK;
+  OP_CHECK(x_dev && codes_dev && scales_dev, "x, codes or scales is null");
+  OP_TRY(check_addresses({{x_dev, dtype_size(dtype), "x"}, {pos_dev, 4, "pos"}, {offsets_dev, 4, "offsets"},
+                          {codes_dev, 16, "codes"}, {scales_dev, square ? 1 : 4, "scales"}}));
+  Fp8QuantArgs a{};
+  a.x = x_dev;
+  a.ld_x = ld_x;
+  a.rows = rows;
+  a.cols = cols;
+  a.dtype = dtype;
+  a.act = ActParams{activation, 1.f, 0.f, INFINITY};
+  a.pos = pos_dev;
+  a.offsets = offsets_dev;
+  a.k = top_k;
+  a.E = experts;
+  a.panel = panel_rows;
+  a.square = square ? 1 : 0;
+  a.codes = codes_dev;
+  a.scales = scales_dev;
+  return done(launch_fp8_quantize(a, as_stream(stream)), "fp8 quantize");
+}
+
+qmoe_status qmoe_fp8_dequantize(const uint8_t* codes_dev, const uint8_t* scales_dev, int64_t rows, int64_t cols,
+                                int64_t panel_rows, int square, int dtype, void* out_dev, int64_t ld_out, void* stream) {
+  OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
+  OP_CHECK(cols >= 1 && cols <= (1 << 29), "cols %lld is out of range", (long long)cols);
+  OP_TRY(check_rows(cols, ld_out, dtype));
+  OP_CHECK(rows == 0 || (panel_rows >= 1 && rows % panel_rows == 0), "panel_rows %lld does not divide the %lld rows",
+           (long long)panel_rows, (long long)rows);
+  if (rows == 0) return QMOE_OK;
+  OP_CHECK(codes_dev && scales_dev && out_dev, "codes, scales or out is null");
+  OP_TRY(check_addresses({{codes_dev, 16, "codes"}, {out_dev, dtype_size(dtype), "out"}}));
+  Fp8DequantArgs a{};
+  a.codes = codes_dev;
+  a.scales = scales_dev;
+  a.rows = rows;
+  a.cols = cols;
+  a.panel = panel_rows;
+  a.square = square ? 1 : 0;
+  a.dtype = dtype;
+  a.out = out_dev;
+  a.ld_out = ld_out;
+  return done(launch_fp8_dequantize(a, as_stream(stream)), "fp8 dequantize");
+}
+
+qmoe_status qmoe_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_dev, int64_t rows,
+                            const uint8_t* w_codes_dev, const uint8_t* w_scales_dev, const int32_t* offsets_dev,
+                            int experts, int64_t n, int64_t k, int transpose, int out_dtype, void* out_dev, int64_t ld_out,
+                            void* stream) {
+  OP_TRY(check_grouped(rows, offsets_dev, experts, n, k));
+  OP_TRY(check_rows(transpose ? k : n, ld_out, out_dtype));
+  if (rows == 0) return QMOE_OK;
+  OP_CHECK(a_codes_dev && a_scales_dev && w_codes_dev && w_scales_dev && out_dev, "an operand or out is null");
+  OP_TRY(check_addresses({{a_codes_dev, 16, "a's codes"}, {a_scales_dev, 4, "a's scales"}, {w_codes_dev, 16, "w's codes"},
+                          {offsets_dev, 4, "offsets"}, {out_dev, dtype_size(out_dtype), "out"}}));
+  Fp8MatmulArgs a{};
+  a.a_codes = a_codes_dev;
+  a.a_scales = a_scales_dev;
+  a.w_codes = w_codes_dev;
+  a.w_scales = w_scales_dev;
+  a.offsets = offsets_dev;
+  a.R = rows;
+  a.E = experts;
+  a.N = (int)n;
+  a.K = (int)k;
+  a.back = transpose ? 1 : 0;
+  a.out_dtype = out_dtype;
+  a.out = out_dev;
+  a.ld_out = ld_out;
+  OP_TRY(wait_config(a.wait));
+  return done(launch_fp8_matmul(a, g_inject_stall.load(), as_stream(stream)), "fp8 matmul");
+}
+
+size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int64_t n,
+                                  int64_t k) {
+  return rows < 1 || n < 1 || k < 1 ? 0 : weight_grad_workspace(dy_dev, ld_dy, x_dev, ld_x, rows, n, k);
+}
+
+qmoe_status qmoe_weight_grad(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const int32_t* offsets_dev,
+                             int64_t rows, int experts, int64_t n, int64_t k, int dtype, int out_dtype, void* dw_dev,
+                             void* workspace_dev, size_t workspace_bytes, void* stream) {
+  OP_TRY(check_grouped(rows, offsets_dev, experts, n, k));
+  OP_TRY(check_rows(n, ld_dy, dtype));
+  OP_TRY(check_rows(k, ld_x, dtype));
+  OP_SUPPORTED(dtype != QMOE_F32, "dtype QMOE_F32: 16-bit operands only");
+  OP_CHECK(dtype_ok(out_dtype), "out_dtype %d is not QMOE_F32, QMOE_F16 or QMOE_BF16", out_dtype);
+  OP_CHECK(dw_dev, "dw is null");
+  if (rows == 0)
+    return done(cudaMemsetAsync(dw_dev, 0, (size_t)experts * n * k * dtype_size(out_dtype), as_stream(stream)), "clear dw");
+  OP_CHECK(dy_dev && x_dev, "dy or x is null");
+  OP_TRY(check_addresses({{dy_dev, 2, "dy"}, {x_dev, 2, "x"}, {offsets_dev, 4, "offsets"}, {dw_dev, dtype_size(out_dtype), "dw"},
+                          {workspace_dev, 16, "workspace"}}));
+  const size_t need = weight_grad_workspace(dy_dev, ld_dy, x_dev, ld_x, rows, n, k);
+  OP_CHECK(workspace_bytes >= need && (workspace_dev || need == 0), "workspace of %zu bytes is below the %zu needed",
+           workspace_bytes, need);
+  WgradArgs a{};
+  a.dy = dy_dev;
+  a.ld_dy = ld_dy;
+  a.x = x_dev;
+  a.ld_x = ld_x;
+  a.offsets = offsets_dev;
+  a.R = rows;
+  a.E = experts;
+  a.N = (int)n;
+  a.K = (int)k;
+  a.dtype = dtype;
+  a.out_dtype = out_dtype;
+  a.dw = dw_dev;
+  a.workspace = static_cast<uint8_t*>(workspace_dev);
+  OP_TRY(wait_config(a.wait));
+  return done(launch_weight_grad(a, g_inject_stall.load(), as_stream(stream)), "weight gradient");
 }
 
 static qmoe_status norm_args(NormArgs& a, const void* x, int64_t ld_x, const void* o, int64_t ld_o, const void* gate,

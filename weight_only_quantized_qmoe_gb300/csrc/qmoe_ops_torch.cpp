@@ -23,7 +23,8 @@ namespace {
 using at::Tensor;
 
 // Python classes of ops.py, set once by setup().
-PyObject *g_error = nullptr, *g_plan = nullptr, *g_mx4 = nullptr, *g_stats = nullptr, *g_grads = nullptr;
+PyObject *g_error = nullptr, *g_plan = nullptr, *g_mx4 = nullptr, *g_stats = nullptr, *g_grads = nullptr,
+         *g_route = nullptr, *g_fp8 = nullptr;
 
 // A Python exception is set.
 struct Refused {};
@@ -211,15 +212,61 @@ void need_args(Py_ssize_t n, Py_ssize_t want) {
   });             \
   }
 
-// setup(QMoEError, ExpertPlan, MX4Tensor, NormStats, NormGrads)
-ENTRY(setup, 5)
-PyObject** to[] = {&g_error, &g_plan, &g_mx4, &g_stats, &g_grads};
-for (int i = 0; i < 5; ++i) {
+// setup(QMoEError, ExpertPlan, MX4Tensor, NormStats, NormGrads, Route, FP8Tensor)
+ENTRY(setup, 7)
+PyObject** to[] = {&g_error, &g_plan, &g_mx4, &g_stats, &g_grads, &g_route, &g_fp8};
+for (int i = 0; i < 7; ++i) {
   Py_INCREF(a[i]);
   Py_XDECREF(*to[i]);
   *to[i] = a[i];
 }
 Py_RETURN_NONE;
+END_ENTRY
+
+// ---- the router ----
+
+// (logits, k, bias or None, scoring, groups, top_groups, group_best, renormalize, scale) -> Route
+ENTRY(expert_route, 9)
+const Tensor& logits = first(a[0], "logits");
+const int dt = dtype_code(logits.scalar_type(), "logits");
+const Rows r = rows_2d(logits, "logits");
+const long k = to_long(a[1], "k"), groups = to_long(a[4], "groups"), top = to_long(a[5], "top_groups"), best = to_long(a[6], "group_best");
+for (const long v : {k, groups, top, best})
+  if (v < 1 || v > INT32_MAX) refuse("k, groups, top_groups and group_best must be positive");
+if (r.width < 1 || r.width > INT32_MAX) refuse("logits has no experts");
+if (k > r.width) refuse("k " + std::to_string(k) + " is above the " + std::to_string(r.width) + " experts");
+Flat bias;
+if (a[2] != Py_None) {
+  const Tensor& b = further(a[2], "bias", at::kFloat, logits);
+  if (b.dim() != 1 || b.size(0) != r.width) refuse("bias is " + shape_of(b.sizes()) + ", not " + shape_of({r.width}));
+  bias = flat(b);
+}
+Tensor ids = make({r.n, (int64_t)k}, at::kInt, logits), weights = make({r.n, (int64_t)k}, at::kFloat, logits);
+check(qmoe_expert_route(r.p, r.ld, dt, static_cast<float*>(bias.p), r.n, (int)r.width, (int)k, (int)to_long(a[3], "scoring"), (int)groups,
+                        (int)top, (int)best, PyObject_IsTrue(a[7]) == 1, (float)to_double(a[8]), ids.mutable_data_ptr<int32_t>(),
+                        weights.mutable_data_ptr<float>(), stream()));
+PyObject *o0 = wrap(ids), *o1 = wrap(weights);
+PyObject* out = o0 && o1 ? PyObject_CallFunctionObjArgs(g_route, o0, o1, nullptr) : nullptr;
+Py_XDECREF(o0);
+Py_XDECREF(o1);
+return out;
+END_ENTRY
+
+// (dweights, logits, ids, scoring, renormalize, scale) -> dlogits
+ENTRY(expert_route_grad, 6)
+const Tensor& logits = first(a[1], "logits");
+const int dt = dtype_code(logits.scalar_type(), "logits");
+const Rows r = rows_2d(logits, "logits");
+const Tensor& ids = further(a[2], "ids", at::kInt, logits);
+if (ids.dim() != 2 || ids.size(0) != r.n || ids.size(1) < 1 || r.width < 1 || r.width > INT32_MAX || ids.size(1) > INT32_MAX)
+  refuse("ids is " + shape_of(ids.sizes()) + ": a row of slots for each of " + std::to_string(r.n) + " tokens is wanted");
+const int64_t k = ids.size(1);
+const Flat i = flat(ids), dw = route_values(a[0], "dweights", r.n, k, logits);
+Tensor out = make({r.n, r.width}, logits.scalar_type(), logits);
+check(qmoe_expert_route_grad(static_cast<float*>(dw.p), r.p, r.ld, dt, static_cast<int32_t*>(i.p), r.n, (int)r.width, (int)k,
+                             (int)to_long(a[3], "scoring"), PyObject_IsTrue(a[4]) == 1, (float)to_double(a[5]), out.mutable_data_ptr(),
+                             stream()));
+return wrap(std::move(out));
 END_ENTRY
 
 // ---- tokens sorted by expert and back ----
@@ -409,6 +456,148 @@ check(qmoe_mx4_matmul(static_cast<uint8_t*>(x.codes.p), static_cast<uint8_t*>(x.
 return wrap(std::move(out));
 END_ENTRY
 
+// ---- 8-bit floating point ----
+
+PyObject* make_fp8(Tensor codes, Tensor scales, int64_t cols, bool square) {
+  PyObject *o0 = wrap(std::move(codes)), *o1 = wrap(std::move(scales)), *o2 = PyLong_FromLongLong(cols);
+  PyObject* out = o0 && o1 && o2 ? PyObject_CallFunctionObjArgs(g_fp8, o0, o1, o2, square ? Py_True : Py_False, nullptr) : nullptr;
+  Py_XDECREF(o0);
+  Py_XDECREF(o1);
+  Py_XDECREF(o2);
+  return out;
+}
+
+// (x, plan or None, QMOE_ACT_* or QMOE_ACT_NONE, square) -> FP8Tensor
+ENTRY(fp8_quantize, 4)
+const Tensor& x = first(a[0], "x");
+const int dt = dtype_code(x.scalar_type(), "x");
+const long act = to_long(a[2], "activation");
+const bool square = PyObject_IsTrue(a[3]) == 1;
+if (x.dim() < 2) refuse("x must have rows: two dimensions at least");
+if (square && (act != QMOE_ACT_NONE || a[1] != Py_None)) refuse("square blocks take neither an activation nor a plan");
+const Rows r = rows_of(x);
+int64_t cols = r.width;
+if (act != QMOE_ACT_NONE) {
+  if (cols % 2) refuse("gate | up needs an even row length, not " + std::to_string(cols));
+  cols /= 2;
+}
+if (cols < 1) refuse("x has rows without values");
+Plan p;
+p.k = p.experts = 1;
+int64_t n = x.size(-2);
+if (a[1] != Py_None) {
+  if (x.dim() != 2) refuse("with a plan x is [T, K]");
+  p = plan_of(a[1], x, r.n);
+  n = r.n * p.k;
+}
+const int64_t nb = (cols + 127) / 128;
+c10::SmallVector<int64_t, 6> cs(x.sizes().begin(), x.sizes().end() - 2), ss(cs);
+cs.append({n, (cols + 15) / 16 * 16});
+if (square) ss.append({(n + 127) / 128, nb});
+else ss.append({(nb + 3) / 4, n, 4});
+Tensor codes = make(cs, at::kByte, x), scales = make(ss, at::kByte, x);
+check(qmoe_fp8_quantize(r.p, r.ld, r.n, cols, dt, (int)act, static_cast<int32_t*>(p.pos.p), static_cast<int32_t*>(p.offsets.p), p.k,
+                        p.experts, n, square, codes.mutable_data_ptr<uint8_t>(), scales.mutable_data_ptr<uint8_t>(), stream()));
+return make_fp8(std::move(codes), std::move(scales), cols, square);
+END_ENTRY
+
+// An FP8Tensor.
+struct Fp8 {
+  const Tensor* codes_t = nullptr;
+  Flat codes, scales;
+  int64_t cols = 0, rows = 0;   // values a row, rows of a matrix
+  bool square = false;
+};
+Fp8 fp8_of(PyObject* o, const char* name, const Tensor* like) {
+  const std::string nm(name);
+  if (!g_fp8 || !PyObject_TypeCheck(o, reinterpret_cast<PyTypeObject*>(g_fp8)) || PyTuple_GET_SIZE(o) != 4)
+    refuse(nm + " must be an FP8Tensor");
+  Fp8 m;
+  m.cols = to_long(PyTuple_GET_ITEM(o, 2), "cols");
+  m.square = PyObject_IsTrue(PyTuple_GET_ITEM(o, 3)) == 1;
+  const std::string nc = nm + ".codes", ns = nm + ".scales";
+  const Tensor& c = like ? further(PyTuple_GET_ITEM(o, 0), nc.c_str(), at::kByte, *like) : first(PyTuple_GET_ITEM(o, 0), nc.c_str());
+  const int64_t nb = (m.cols + 127) / 128, d = c.dim();
+  if (m.cols < 1 || d < 2 || c.scalar_type() != at::kByte || c.size(-1) != (m.cols + 15) / 16 * 16)
+    refuse(nc + " " + shape_of(c.sizes()) + " does not hold rows of " + std::to_string(m.cols) + " values");
+  m.codes_t = &c;
+  m.rows = c.size(-2);
+  m.codes = flat(c);
+  const Tensor& sc = further(PyTuple_GET_ITEM(o, 1), ns.c_str(), at::kByte, c);
+  c10::SmallVector<int64_t, 6> want(c.sizes().begin(), c.sizes().end() - 2);
+  if (m.square) want.append({(m.rows + 127) / 128, nb});
+  else want.append({(nb + 3) / 4, m.rows, 4});
+  if (sc.sizes() != at::IntArrayRef(want)) refuse(ns + " " + shape_of(sc.sizes()) + " does not belong to codes " + shape_of(c.sizes()));
+  m.scales = flat(sc);
+  return m;
+}
+
+// (q, dtype code) -> values
+ENTRY(fp8_dequantize, 2)
+const Fp8 q = fp8_of(a[0], "q", nullptr);
+const long dt = to_long(a[1], "dtype");
+const at::ScalarType type = dt == QMOE_F32 ? at::kFloat : dt == QMOE_F16 ? at::kHalf : at::kBFloat16;
+c10::SmallVector<int64_t, 6> size(q.codes_t->sizes().begin(), q.codes_t->sizes().end());
+size.back() = q.cols;
+Tensor out = make(size, type, *q.codes_t);
+check(qmoe_fp8_dequantize(static_cast<uint8_t*>(q.codes.p), static_cast<uint8_t*>(q.scales.p), out.numel() / q.cols, q.cols, q.rows,
+                          q.square, (int)dt, out.mutable_data_ptr(), q.cols, stream()));
+return wrap(std::move(out));
+END_ENTRY
+
+// (a, w, plan or None, transpose, dtype code) -> product
+ENTRY(fp8_matmul, 5)
+const Fp8 x = fp8_of(a[0], "a", nullptr), w = fp8_of(a[1], "w", x.codes_t);
+const bool transpose = PyObject_IsTrue(a[3]) == 1;
+const long dt = to_long(a[4], "out_dtype");
+const at::ScalarType type = dt == QMOE_F32 ? at::kFloat : dt == QMOE_F16 ? at::kHalf : at::kBFloat16;
+if (x.codes_t->dim() != 2 || x.square) refuse("a must be [R, K] with scales of rows");
+if (!w.square) refuse("w must have scales of 128 x 128 blocks (fp8_quantize with square=True)");
+const int64_t inner = transpose ? w.rows : w.cols, width = transpose ? w.cols : w.rows;
+if (x.cols != inner) refuse("a has rows of " + std::to_string(x.cols) + " values, w of " + std::to_string(inner));
+Plan p;
+p.k = p.experts = 1;
+if (a[2] != Py_None) {
+  p = plan_of(a[2], *x.codes_t);
+  if (p.tokens * p.k != x.rows) refuse("a has " + std::to_string(x.rows) + " rows, the plan " + std::to_string(p.tokens * p.k));
+}
+const int64_t d = w.codes_t->dim();
+if (d > 3 || (d == 3 ? w.codes_t->size(0) : 1) != p.experts)
+  refuse("w.codes " + shape_of(w.codes_t->sizes()) + " does not hold " + std::to_string(p.experts) + " expert(s)");
+Tensor out = make({x.rows, width}, type, *x.codes_t);
+check(qmoe_fp8_matmul(static_cast<uint8_t*>(x.codes.p), static_cast<uint8_t*>(x.scales.p), x.rows, static_cast<uint8_t*>(w.codes.p),
+                      static_cast<uint8_t*>(w.scales.p), static_cast<int32_t*>(p.offsets.p), p.experts, w.rows, w.cols, transpose,
+                      (int)dt, out.mutable_data_ptr(), width, stream()));
+return wrap(std::move(out));
+END_ENTRY
+
+// (dy, x, plan or None, dtype code) -> dw
+ENTRY(weight_grad, 4)
+const Tensor& dy = first(a[0], "dy");
+const int dt = dtype_code(dy.scalar_type(), "dy");
+const Tensor& x = further(a[1], "x", dy.scalar_type(), dy);
+const Rows ry = rows_2d(dy, "dy"), rx = rows_2d(x, "x");
+const long odt = to_long(a[3], "out_dtype");
+const at::ScalarType type = odt == QMOE_F32 ? at::kFloat : odt == QMOE_F16 ? at::kHalf : at::kBFloat16;
+if (ry.n != rx.n) refuse("dy has " + std::to_string(ry.n) + " rows, x " + std::to_string(rx.n));
+if (ry.width < 1 || rx.width < 1) refuse("dy or x has rows without values");
+Plan p;
+p.k = p.experts = 1;
+if (a[2] != Py_None) {
+  p = plan_of(a[2], dy);
+  if (p.tokens * p.k != ry.n) refuse("dy has " + std::to_string(ry.n) + " rows, the plan " + std::to_string(p.tokens * p.k));
+}
+c10::SmallVector<int64_t, 3> size;
+if (a[2] != Py_None) size.push_back(p.experts);
+size.append({ry.width, rx.width});
+Tensor dw = make(size, type, dy), work;
+const size_t bytes = qmoe_weight_grad_workspace(ry.p, ry.ld, rx.p, rx.ld, ry.n, ry.width, rx.width);
+if (bytes) work = make({(int64_t)bytes}, at::kByte, dy);
+check(qmoe_weight_grad(ry.p, ry.ld, rx.p, rx.ld, static_cast<int32_t*>(p.offsets.p), ry.n, p.experts, ry.width, rx.width, dt, (int)odt,
+                       dw.mutable_data_ptr(), ptr(work), bytes, stream()));
+return wrap(std::move(dw));
+END_ENTRY
+
 // ---- norms around a block ----
 
 Rows norm_rows(PyObject* o, const char* name, const Tensor& x) {
@@ -521,9 +710,11 @@ return out;
 END_ENTRY
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {METHOD(setup),          METHOD(expert_sort),  METHOD(dispatch),   METHOD(combine),
-                           METHOD(combine_grad),   METHOD(mx4_quantize), METHOD(mx4_dequantize), METHOD(mx4_matmul),
-                           METHOD(block_norm),     METHOD(block_norm_grad), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {METHOD(setup),        METHOD(expert_route), METHOD(expert_route_grad), METHOD(expert_sort),
+                           METHOD(dispatch),     METHOD(combine),      METHOD(combine_grad),      METHOD(mx4_quantize),
+                           METHOD(mx4_dequantize), METHOD(mx4_matmul), METHOD(fp8_quantize),      METHOD(fp8_dequantize),
+                           METHOD(fp8_matmul),   METHOD(weight_grad),  METHOD(block_norm),        METHOD(block_norm_grad),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops_torch", "Operators around the expert layer on torch tensors", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,187 @@
+// What the 8-bit product and the weight gradient share: the list of row tiles
+// of experts' rows, a tile's way from TMEM to global memory, and the sum of a
+// cluster's partial tiles.
+//
+// Both put the long, regular axis (weight rows, or weight columns) on the MMA's
+// M side, 128 TMEM lanes, and the ragged one on its N side, whose width an
+// instruction chooses: a tile of few rows then costs few columns, and a warp
+// stores a TMEM column as one contiguous run of an output row, whatever the
+// row's alignment.
+#pragma once
+
+#include <algorithm>
+
+#include "qmoe_ops.cuh"
+#include "qmoe_tma.cuh"
+
+namespace qmoe {
+
+constexpr int kTileM = 128;
+
+__device__ __forceinline__ void tma_3d_elect(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Shared-memory matrix descriptor of an operand that lies along M or N (the
+// reduction down the rows): rows of 128 bytes in the 128-byte swizzle, eight rows
+// to the next 1024 bytes, panels of 128 bytes `panel` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFF) >> 4);
+  d |= (uint64_t)(panel >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// First row of group e (0 .. E; group E is the rows without a route).  Clamped
+// to the rows there are, so that no offsets make a role leave its operands.
+__device__ __forceinline__ int group_first_row(const int* offsets, int E, int64_t R, int e) {
+  if (e <= 0) return 0;
+  if (!offsets || e > E) return (int)R;
+  return min(max(offsets[e], 0), (int)R);
+}
+
+// First row tile (of `bn` rows) and first row of every group, by a whole warp:
+// tp[e], tp[E + 1] their number, row0[e].
+__device__ __forceinline__ void group_tiles(const int* offsets, int E, int64_t R, int bn, int* tp, int* row0) {
+  const int lane = threadIdx.x & 31;
+  int first = 0;
+  for (int e0 = 0; e0 <= E; e0 += 32) {
+    const int e = e0 + lane;
+    int n = 0;
+    if (e <= E) {
+      const int lo = group_first_row(offsets, E, R, e), hi = group_first_row(offsets, E, R, e + 1);
+      n = hi > lo ? (hi - lo + bn - 1) / bn : 0;
+      row0[e] = lo;
+    }
+    int run = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += up;
+    }
+    if (e <= E) tp[e] = first + run - n;
+    first += __shfl_sync(0xffffffffu, run, 31);
+  }
+  if (lane == 0) {
+    tp[E + 1] = first;
+    row0[E + 1] = (int)R;
+  }
+}
+struct RowTile {
+  int e, start, rows;   // e == E: rows without a route (zeros)
+};
+__device__ __forceinline__ RowTile row_tile(int E, const int* tp, const int* row0, int bn, int mt) {
+  int lo = 0, hi = E;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tp[mid] <= mt) lo = mid;
+    else hi = mid - 1;
+  }
+  RowTile t;
+  t.e = lo;
+  t.start = row0[lo] + (mt - tp[lo]) * bn;
+  t.rows = min(bn, row0[lo + 1] - t.start);
+  return t;
+}
+
+// Columns 0 .. n of a warp's quarter of a tile to rows 0 .. n of the output, a
+// lane an element of each (`in`: the lane has one).  `out`: the lane's element
+// of the first row.
+template <int OUT>
+__device__ __forceinline__ void store_tile(uint32_t taddr, typename ElemT<OUT>::t* out, int64_t ld, int n, bool in) {
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    uint32_t v[32];
+    TC_LD32(taddr + c0, v);
+    tc_wait_ld();
+    if (!in) continue;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c0 + c < n) store_d<OUT>(out + (size_t)(c0 + c) * ld, 0, __uint_as_float(v[c]));
+  }
+}
+template <int OUT>
+__device__ __forceinline__ void store_zeros(typename ElemT<OUT>::t* out, int64_t ld, int n, bool in) {
+  if (in)
+    for (int c = 0; c < n; ++c) store_d<OUT>(out + (size_t)c * ld, 0, 0.f);
+}
+
+// A tile whose reduction is split over the CTAs of a cluster: each CTA's
+// partial sums to its own shared memory, [column][128] ...
+__device__ __forceinline__ void put_partial(uint32_t taddr, float* part, int q, int n) {
+  const int lane = threadIdx.x & 31;
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    uint32_t v[32];
+    TC_LD32(taddr + c0, v);
+    tc_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c0 + c < n) part[(c0 + c) * kTileM + q * 32 + lane] = __uint_as_float(v[c]);
+  }
+}
+// ... and, after a barrier of the cluster, every CTA adds up its share of the
+// columns in the order of the ranks and stores them.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, int rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int OUT>
+__device__ __forceinline__ void store_sum(const float* part, int q, typename ElemT<OUT>::t* out, int64_t ld, int n, bool in,
+                                          int rank, int ranks) {
+  const int lane = threadIdx.x & 31;
+  for (int c = rank; c < n; c += ranks) {
+    const uint32_t at = smem_u32(part + c * kTileM + q * 32 + lane);
+    float v = 0.f;
+    for (int r = 0; r < ranks; ++r) v += ld_cluster_f32(at, r);
+    if (in) store_d<OUT>(out + (size_t)c * ld, 0, v);
+  }
+}
+
+// Rows [rows, inner] of `size`-byte elements, `matrices` of them, rows `pitch`
+// bytes apart: boxes of 128 bytes by box_rows rows, 128-byte swizzle, zeros outside.
+inline bool encode_tiles(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, int64_t inner, int64_t rows,
+                         int64_t matrices, int64_t pitch, int box_rows) {
+  const EncodeFn f = encoder();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)matrices};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)(pitch * rows)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return f(m, type, 3, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The launch of a tile kernel: clusters of `cluster` CTAs, dependent on the kernel before.
+template <typename... Params, typename... Args>
+cudaError_t launch_tiles(void (*kern)(Params...), int64_t ctas, int cluster, int threads, int smem, cudaStream_t s, const Args&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace qmoe

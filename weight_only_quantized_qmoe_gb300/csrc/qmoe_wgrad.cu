@@ -1,0 +1,350 @@
+// Gradient of the experts' weights:
+//
+//   dw[e, n, k] = sum over rows i in [offsets[e], offsets[e + 1]) of dy[i, n] x[i, k]
+//
+// 16-bit operands, fp32 accumulation, one rounding to the output type.
+//
+// GB300 form: tcgen05.mma kind::f16 with both operands read along M and N: the
+// reduction goes down the rows, so tiles of dy and x are used as they lie in
+// memory, nothing is transposed.  The MMA's M side is 128 columns of x, its N
+// side up to BN columns of dy, so that a TMEM column is a run of a row of dw; a
+// ring stage holds 64 rows of both, in panels of 64 columns (128-byte rows,
+// swizzled) copied by TMA.  An expert's rows start and end anywhere: the last
+// stage runs as many K = 16 MMAs as there are rows, and the rows past the last in
+// the last of them are overwritten with zeros in both operands (they belong to the
+// next expert, and may hold anything).
+//   warp 0    TMA producer (one elected lane)
+//   warp 1    MMA issuer, zeros past the last row
+//   warp 3    first rows of the experts
+//   warps 4-7 epilogue: TMEM columns to rows of dw
+// Two accumulators alternate.  CTAs are persistent over the (expert, tile) list.
+// Where there are few tiles, the CTAs of a cluster share a tile's rows and add up
+// their parts in a fixed order.  Operands that TMA cannot read (rows that do not
+// start on 16 bytes) are copied to rows that do first.
+//
+// Every wait is bounded, as in the products' kernels.
+#include "qmoe_tile.cuh"
+
+namespace qmoe {
+
+constexpr int kWgRows = 64;                     // rows a stage
+constexpr int kWgPanel = 64;                    // columns of a panel (128 bytes)
+constexpr int kWgPanelBytes = kWgRows * 128;
+constexpr int kWgThreads = 256;
+constexpr int kWgBN = 256;
+constexpr long long kWgDrainPolls = 4096;
+
+struct WgRing {
+  static constexpr int stages = 4;
+  static constexpr int x_panels = kTileM / kWgPanel, dy_panels = kWgBN / kWgPanel;
+  static constexpr int x_bytes = x_panels * kWgPanelBytes;
+  static constexpr int dy_bytes = dy_panels * kWgPanelBytes;
+  static constexpr int x_off = 0;
+  static constexpr int dy_off = x_off + stages * x_bytes;
+  static constexpr int bar_off = dy_off + stages * dy_bytes;
+  static constexpr int row_off = bar_off + 512;                 // first row of each expert
+  static constexpr int total = row_off + (kSortMaxExperts + 1) * 4;
+  static constexpr int tmem_cols = 2 * kWgBN;
+  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kWgBN * kTileM * 4 <= bar_off, "a partial tile fits the ring");
+};
+
+// Up to four K = 16 MMAs of a stage and the commit that frees it, by one elected
+// lane; 16 rows on is 2048 bytes in either operand.
+__device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty) {
+  asm volatile(
+      "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
+      "setp.gt.and.s32 q1, %5, 1, e;\n\tsetp.gt.and.s32 q2, %5, 2, e;\n\tsetp.gt.and.s32 q3, %5, 3, e;\n\t"
+      "add.u64 y1, %1, 128;\n\tadd.u64 y2, %1, 256;\n\tadd.u64 y3, %1, 384;\n\t"
+      "add.u64 z1, %2, 128;\n\tadd.u64 z2, %2, 256;\n\tadd.u64 z3, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+      "@q1 tcgen05.mma.cta_group::1.kind::f16 [%0], y1, z1, %3, p1;\n\t"
+      "@q2 tcgen05.mma.cta_group::1.kind::f16 [%0], y2, z2, %3, p1;\n\t"
+      "@q3 tcgen05.mma.cta_group::1.kind::f16 [%0], y3, z3, %3, p1;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}" ::"r"(d),
+      "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk), "r"(smem_u32(empty))
+      : "memory");
+}
+
+// Instruction descriptor, kind::f16: D f32, both operands f16 or both bf16,
+// both along M and N (bits 15 and 16), M = 128.
+__device__ __forceinline__ uint32_t idesc_wgrad(int bf16, int N) {
+  return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+}
+
+struct WgKernelArgs {
+  WgradArgs a;
+  int inject_stall;
+};
+struct WgTile {
+  int e, n0, k0, lo, hi;   // this CTA's rows of it
+};
+
+template <int OUT, bool SPLIT>
+__global__ void __launch_bounds__(kWgThreads, 1)
+    weight_grad_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const WgKernelArgs args) {
+  using RG = WgRing;
+  using T = typename ElemT<OUT>::t;
+  constexpr int S = RG::stages;
+  extern __shared__ __align__(1024) uint8_t wg_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(wg_smem_raw) + 1023) & ~uintptr_t(1023));
+  const WgradArgs& a = args.a;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RG::bar_off);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain_bar = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* row0 = reinterpret_cast<int*>(smem + RG::row_off);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, RG::tmem_cols);
+    tmem_relinquish();
+  }
+  op_begin();   // the operands and offsets may come from the kernel before
+  if (warp == 3)
+    for (int e = lane; e <= a.E; e += 32) row0[e] = a.offsets ? min(max(a.offsets[e], 0), (int)a.R) : (e ? (int)a.R : 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + kTileM - 1) / kTileM;
+  const int total = a.E * ntn * ntk;
+  int ranks = 1, rank = 0, first = blockIdx.x, stride = gridDim.x;
+  if constexpr (SPLIT) {
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    first = blockIdx.x / ranks;
+    stride = gridDim.x / ranks;
+  }
+  // whole stages to each rank; the first ranks have rows where there are few
+  auto tile_of = [&](int tile) {
+    WgTile t;
+    const int kt = tile % ntk, rest = tile / ntk, nt = rest % ntn;
+    t.e = rest / ntn;
+    t.n0 = nt * kWgBN;
+    t.k0 = kt * kTileM;
+    const int lo = row0[t.e], hi = max(row0[t.e + 1], lo);
+    const int steps = (hi - lo + kWgRows - 1) / kWgRows, each = (steps + ranks - 1) / ranks;
+    t.lo = min(lo + rank * each * kWgRows, hi);
+    t.hi = min(t.lo + each * kWgRows, hi);
+    return t;
+  };
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      const int panels = min(RG::dy_panels, (a.N - t.n0 + kWgPanel - 1) / kWgPanel);
+      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
+        const int s = it % S;
+        ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        mbar_arrive_expect_tx_elect(&full[s], (uint32_t)((RG::x_panels + panels) * kWgPanelBytes));
+        // Test hook: the first stage's barrier is armed, its copies are never issued.
+        if (args.inject_stall && it == 0) continue;
+#pragma unroll
+        for (int p = 0; p < RG::x_panels; ++p)
+          tma_3d_elect(smem + RG::x_off + s * RG::x_bytes + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, &full[s]);
+        for (int p = 0; p < panels; ++p)
+          tma_3d_elect(smem + RG::dy_off + s * RG::dy_bytes + p * kWgPanelBytes, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
+      }
+    }
+    if (!ok) {
+      // the copies in flight must land before the CTA leaves
+      const WaitCfg drain{a.wait.status, kWgDrainPolls};
+      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), kWgPanelBytes);
+    const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), kWgPanelBytes);
+    int it = 0, tc = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      if (t.lo >= t.hi) continue;
+      const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, (min(kWgBN, a.N - t.n0) + 15) & ~15);
+      const int ab = tc & 1;
+      ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
+        const int s = it % S;
+        if (!warp_test_wait(&full[s], (it / S) & 1)) {
+          ok = spin_or_abort(&full[s], (it / S) & 1, a.wait, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        const int rows = min(kWgRows, t.hi - r), nk = (rows + 15) / 16;
+        if (rows & 15) {
+          // rows of 128 bytes: zeros from the last one to the end of its 16
+          const int n = (nk * 16 - rows) * 8;   // 16-byte pieces a panel
+          const int panels = RG::x_panels + min(RG::dy_panels, (a.N - t.n0 + kWgPanel - 1) / kWgPanel);
+          for (int p = 0; p < panels; ++p) {
+            uint8_t* base = p < RG::x_panels ? smem + RG::x_off + s * RG::x_bytes + p * kWgPanelBytes
+                                             : smem + RG::dy_off + s * RG::dy_bytes + (p - RG::x_panels) * kWgPanelBytes;
+            for (int i = lane; i < n; i += 32) reinterpret_cast<uint4*>(base + rows * 128)[i] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        wg_stage_elect(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4), idesc,
+                       r != t.lo ? 1u : 0u, nk, &empty[s]);
+      }
+      if (ok) tc_commit_elect(&acc_full[ab]);
+      ++tc;
+    }
+    tc_commit_elect(drain_bar);
+    const WaitCfg drain{a.wait.status, kDrainWaitLimit};
+    mbar_wait_bounded(drain_bar, 0, drain);
+  } else if (warp >= 4) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3;
+    int tc = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      const int col = t.k0 + q * 32 + lane, n = min(kWgBN, a.N - t.n0);
+      const bool in = col < a.K;
+      T* out = static_cast<T*>(a.dw) + ((size_t)t.e * a.N + t.n0) * a.K + col;
+      if (t.lo >= t.hi) {
+        if constexpr (SPLIT) {
+          float* part = reinterpret_cast<float*>(smem);
+          for (int c = 0; c < n; ++c) part[c * kTileM + q * 32 + lane] = 0.f;
+        } else {
+          store_zeros<OUT>(out, a.K, n, in);
+        }
+        continue;
+      }
+      const int ab = tc & 1;
+      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
+      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem), q, n);   // the ring is empty
+      else store_tile<OUT>(acc, out, a.K, n, in);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      ++tc;
+    }
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= 4 && first < total) {
+      const WgTile t = tile_of(first);
+      const int q = warp & 3, col = t.k0 + q * 32 + lane;
+      store_sum<OUT>(reinterpret_cast<const float*>(smem), q, static_cast<T*>(a.dw) + ((size_t)t.e * a.N + t.n0) * a.K + col, a.K,
+                     min(kWgBN, a.N - t.n0), col < a.K, rank, ranks);
+    }
+    __syncwarp();
+    cluster_sync_all();   // no CTA leaves while another may still read its part
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, RG::tmem_cols);
+}
+
+// Rows that start on any element to rows that start on 16 bytes.
+constexpr int kAlignThreads = 256;
+__global__ void __launch_bounds__(kAlignThreads) align_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int width, uint16_t* dst, int64_t pitch) {
+  op_begin();
+  const int groups = (width + 7) / 8;
+  const int64_t n = rows * groups;
+  for (int64_t i = blockIdx.x * (int64_t)kAlignThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kAlignThreads) {
+    const int64_t r = i / groups;
+    const int c = (int)(i - r * groups) * 8;
+    const uint16_t* p = src + r * ld + c;
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < width ? p[j] : 0u;
+    *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Host side
+// ----------------------------------------------------------------------------
+namespace {
+
+// TMA reads rows that start on 16 bytes, 16-byte multiples apart.
+bool tma_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
+size_t align_bytes(const void* p, int64_t ld, int64_t R, int64_t width) {
+  return tma_rows(p, ld) ? 0 : (size_t)R * (size_t)((width + 7) / 8 * 8) * 2;
+}
+
+cudaError_t align_rows(const void*& p, int64_t& ld, int64_t R, int width, uint8_t*& work, cudaStream_t s) {
+  if (tma_rows(p, ld)) return cudaSuccess;
+  const int64_t pitch = (width + 7) / 8 * 8, n = R * (pitch / 8);
+  const unsigned blocks = (unsigned)std::min<int64_t>((n + kAlignThreads - 1) / kAlignThreads, kSms * 8);
+  const cudaError_t e = launch_op(align_rows_kernel, dim3(blocks), dim3(kAlignThreads), 0, s, static_cast<const uint16_t*>(p), ld, R, width,
+                                  reinterpret_cast<uint16_t*>(work), pitch);
+  p = work;
+  ld = pitch;
+  work += (size_t)R * pitch * 2;
+  return e;
+}
+
+template <int OUT>
+cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, cudaStream_t s) {
+  const WgradArgs& a = args.a;
+  CUtensorMap map_x, map_dy;
+  const auto type = a.dtype == QMOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!encode_tiles(&map_x, type, 2, a.x, a.K, a.R, 1, a.ld_x * 2, kWgRows) ||
+      !encode_tiles(&map_dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, kWgRows))
+    return cudaErrorInvalidValue;
+  constexpr int smem = WgRing::total + 1024;   // + alignment slack
+  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
+  return launch_tiles(weight_grad_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
+}
+
+}  // namespace
+
+size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t R, int64_t N, int64_t K) {
+  return align_bytes(dy, ld_dy, R, N) + align_bytes(x, ld_x, R, K);
+}
+
+cudaError_t launch_weight_grad(const WgradArgs& a, int inject_stall, cudaStream_t s) {
+  WgKernelArgs args{a, inject_stall};
+  uint8_t* work = a.workspace;
+  cudaError_t e = align_rows(args.a.dy, args.a.ld_dy, a.R, a.N, work, s);
+  if (e == cudaSuccess) e = align_rows(args.a.x, args.a.ld_x, a.R, a.K, work, s);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)a.E * ((a.N + kWgBN - 1) / kWgBN) * ((a.K + kTileM - 1) / kTileM);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  // a tile's rows over the CTAs of a cluster while there are CTAs without a tile
+  // and each gets a stage, if they are spread evenly
+  const int64_t steps = (a.R / a.E + kWgRows - 1) / kWgRows;
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= kSms && split * 2 <= steps) split *= 2;
+  if (a.out_dtype == QMOE_F32) return launch_wg<QMOE_F32>(args, tiles, split, s);
+  if (a.out_dtype == QMOE_F16) return launch_wg<QMOE_F16>(args, tiles, split, s);
+  return launch_wg<QMOE_BF16>(args, tiles, split, s);
+}
+
+}  // namespace qmoe
