@@ -13,6 +13,7 @@
 // Bound: latency.  A warp takes a token: lane l holds the logits of experts l,
 // l + 32, ..., a rank is one redux for the best key and one for the lowest index
 // at it.  The logits are read once, two 4-byte words a token and rank written.
+#include <algorithm>
 #include <climits>
 
 #include "qmoe_ops.cuh"
@@ -89,15 +90,17 @@ __device__ __noinline__ int choose64(const ChoiceArgs& a, const typename ElemT<D
     float m = -INFINITY;
     for (int e = lane; e < E; e += 32) m = fmaxf(m, load_d<DT>(row, e));
     mx = warp_max(m);
+#pragma unroll 4
     for (int e = lane; e < E; e += 32) {
       const double l = load_d<DT>(row, e);
-      if (l == l) sum += exp(l - mx);
+      sum += l == l ? exp(l - mx) : 0.0;
     }
-    sum = warp_sum(sum);
+    sum = warp_sum(sum);   // (unrolled loops: an exponential in 64 bits is some 3000 cycles of latency)
   }
   auto score = [&](double l) { return a.scoring == QMOE_SCORE_SOFTMAX ? exp(l - mx) / sum : 1.0 / (1.0 + exp(-l)); };
   const bool filter = a.top_groups < a.groups;
   // the keys of the groups: the scores themselves where there is no bias
+#pragma unroll 4
   for (int e = lane; e < E; e += 32) {
     const double l = load_d<DT>(row, e);
     const double v = l > low ? score(l) + (a.bias ? (double)a.bias[e] : 0.0) : low;
@@ -139,10 +142,42 @@ __device__ __noinline__ int choose64(const ChoiceArgs& a, const typename ElemT<D
   return mine;
 }
 
+// The same where only a few experts may be among the k best: lane i has one of n,
+// `e` (-1: none).  list: room for 32.
+template <int DT>
+__device__ __noinline__ int choose64_of(const ChoiceArgs& a, const typename ElemT<DT>::t* row, int e, float mx, int* list) {
+  const int lane = threadIdx.x & 31;
+  double v = -static_cast<double>(INFINITY);
+  if (a.scoring == QMOE_SCORE_SOFTMAX) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = lane; i < a.E; i += 32) {
+      const double l = load_d<DT>(row, i);
+      sum += l == l ? exp(l - mx) : 0.0;
+    }
+    sum = warp_sum(sum);
+    if (e >= 0) v = exp((double)load_d<DT>(row, e) - mx) / sum + (double)a.bias[e];
+  } else if (e >= 0) {
+    v = 1.0 / (1.0 + exp(-(double)load_d<DT>(row, e))) + (double)a.bias[e];
+  }
+  int rank = 0;
+  for (int i = 0; i < 32; ++i) {
+    const double w = __shfl_sync(kAll, v, i);
+    const int f = __shfl_sync(kAll, e, i);
+    rank += f >= 0 && (w > v || (w == v && f < e)) ? 1 : 0;
+  }
+  __syncwarp();
+  list[lane] = -1;
+  __syncwarp();
+  if (e >= 0 && rank < a.k) list[rank] = e;
+  __syncwarp();
+  return list[lane];
+}
+
 template <int DT, int NPL>
 __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceArgs a) {
   op_begin();
-  extern __shared__ double choice_smem[];   // E a warp, where the choice may need them
+  extern __shared__ double choice_smem[];   // a.room a warp, where the choice may need them
   using T = typename ElemT<DT>::t;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E, k = a.k;
   const int64_t t = blockIdx.x * (int64_t)kChoiceWarps + warp;
@@ -203,7 +238,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       for (int i = 0; i < NPL; ++i) c[i] = l[i];
     }
     if (filter) {
-      float* sm = reinterpret_cast<float*>(choice_smem + (size_t)warp * E);
+      float* sm = reinterpret_cast<float*>(choice_smem + (size_t)warp * a.room);
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
         if (lane + 32 * i < E) sm[lane + 32 * i] = c[i];
@@ -220,7 +255,8 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       key[i] = may ? topk_order_key(v) : INT_MIN;
     }
   }
-  int mine = -1, before = INT_MAX;
+  const bool groups_unsure = __any_sync(kAll, unsure);
+  int mine = -1, before = INT_MAX, kth = 0;
   for (int slot = 0; slot <= k; ++slot) {   // one more than asked for: the border of the last
     int best = key[0], at = lane;
 #pragma unroll
@@ -237,13 +273,34 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     }
     before = m;
     if (slot == k) break;
+    kth = m;
     const int sel = topk_redux_min(best == m ? at : INT_MAX);
     if (lane == slot) mine = sel;
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (sel == lane + 32 * i) key[i] = INT_MIN;
   }
-  if (by_score && __any_sync(kAll, unsure)) mine = choose64<DT>(a, row, choice_smem + (size_t)warp * E);
+  if (groups_unsure) {
+    mine = choose64<DT>(a, row, choice_smem + (size_t)warp * a.room);
+  } else if (unsure) {
+    // those chosen, and those left that are as near to the last of them
+    const float last = __int_as_float(kth ^ ((kth >> 31) & INT_MAX)), least = last - (tau + 0x1p-21f * fabsf(last));
+    int* list = reinterpret_cast<int*>(choice_smem + (size_t)warp * a.room);
+    int n = __popc(__ballot_sync(kAll, mine >= 0));
+    __syncwarp();
+    if (mine >= 0) list[lane] = mine;   // the lanes from 0 on
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const bool near = key[i] != INT_MIN && !(__int_as_float(key[i] ^ ((key[i] >> 31) & INT_MAX)) < least);
+      const unsigned who = __ballot_sync(kAll, near);
+      const int at = n + __popc(who & ((1u << lane) - 1u));
+      if (near && at < 32) list[at] = lane + 32 * i;
+      n += __popc(who);
+    }
+    __syncwarp();
+    if (n <= 32) mine = choose64_of<DT>(a, row, lane < n ? list[lane] : -1, mx, list);
+    else mine = choose64<DT>(a, row, choice_smem + (size_t)warp * a.room);
+  }
 
   const float chosen = mine >= 0 ? load_d<DT>(row, mine) : -INFINITY;
   float w = 0.f;
@@ -367,10 +424,11 @@ cudaError_t with_types(const ChoiceArgs& a, F&& f) {
 
 cudaError_t launch_choice(const ChoiceArgs& a, cudaStream_t s) {
   const unsigned blocks = (unsigned)((a.T + kChoiceWarps - 1) / kChoiceWarps);
-  const bool room = a.bias || a.top_groups < a.groups;
-  const size_t smem = room ? sizeof(double) * kChoiceWarps * a.E : 0;   // at most 32 KB
+  ChoiceArgs args = a;
+  args.room = a.bias || a.top_groups < a.groups ? std::max(a.E, 32) : 0;
+  const size_t smem = sizeof(double) * kChoiceWarps * args.room;   // at most 32 KB
   return with_types(a, [&](auto dt, auto npl) {
-    return launch_op(choice_kernel<decltype(dt)::value, decltype(npl)::value>, dim3(blocks), dim3(32 * kChoiceWarps), smem, s, a);
+    return launch_op(choice_kernel<decltype(dt)::value, decltype(npl)::value>, dim3(blocks), dim3(32 * kChoiceWarps), smem, s, args);
   });
 }
 

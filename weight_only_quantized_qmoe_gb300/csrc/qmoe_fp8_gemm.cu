@@ -62,7 +62,7 @@ struct F8Ring {
 
 // One stage, issued by one elected lane: the scales of W and of A's row groups
 // to TMEM, up to four K = 32 MMAs, the commit that frees the stage.
-template <int GROUPS>
+template <int GROUPS, int MC>
 __device__ __forceinline__ void f8_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sf,
                                                uint64_t sw, uint64_t sa, uint32_t acc, int nk, uint64_t* empty) {
   static_assert(GROUPS == 1 || GROUPS == 2, "row groups of A");
@@ -72,7 +72,7 @@ __device__ __forceinline__ void f8_stage_elect(uint32_t d, uint64_t w, uint64_t 
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p0, %8, 0;\n\tsetp.eq.b32 p1, %8, %8;\n\t"
       "setp.gt.and.s32 q1, %9, 1, e;\n\tsetp.gt.and.s32 q2, %9, 2, e;\n\tsetp.gt.and.s32 q3, %9, 3, e;\n\t"
-      "setp.gt.and.s32 g2, %11, 1, e;\n\t"
+      "setp.gt.and.s32 g2, %10, 1, e;\n\t"
       "add.u32 t1, %5, 4;\n\tadd.u32 t2, %5, 8;\n\tadd.u64 x1, %7, 32;\n\t"
       "add.u64 y1, %1, %2;\n\tadd.u64 y2, y1, %2;\n\tadd.u64 y3, y2, %2;\n\t"
       "add.u64 z1, %3, 2;\n\tadd.u64 z2, %3, 4;\n\tadd.u64 z3, %3, 6;\n\t"
@@ -82,10 +82,11 @@ __device__ __forceinline__ void f8_stage_elect(uint32_t d, uint64_t w, uint64_t 
       "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %3, %4, [%5], [t1], p0;\n\t"
       "@q1 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y1, z1, %4, [%5], [t1], p1;\n\t"
       "@q2 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y2, z2, %4, [%5], [t1], p1;\n\t"
-      "@q3 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [t1], p1;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t}" ::"r"(d),
-      "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sf), "l"(sw), "l"(sa), "r"(acc), "r"(nk), "r"(smem_u32(empty)), "n"(GROUPS)
+      "@q3 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [t1], p1;\n\t}" ::"r"(d),
+      "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sf), "l"(sw), "l"(sa), "r"(acc), "r"(nk), "n"(GROUPS)
       : "memory");
+  if constexpr (MC > 1) tc_commit_pair_elect(empty);
+  else tc_commit_elect(empty);
 }
 
 // Instruction descriptor, kind::mxf8f6f4: both operands E4M3, scales E8M0, M =
@@ -100,8 +101,10 @@ struct F8KernelArgs {
   int inject_stall;
 };
 
-// SPLIT: a cluster shares each tile's reduction, and there is one tile a cluster at most.
-template <int BN, int OUT, bool SPLIT>
+// SPLIT: a cluster shares each tile's reduction, and there is one tile a cluster
+// at most.  MC = 2: the CTAs of a pair take neighbouring weight rows with the
+// same rows of A; each loads half of the latter and sends it to both.
+template <int BN, int OUT, bool SPLIT, int MC>
 __global__ void __launch_bounds__(kF8Threads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a32,
                       const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1 + 32 + 1);   // the announced bytes, the lanes of A's scales, the weight's scale
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], MC);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -143,10 +146,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (warp == 3) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
   tc_fence_before();
   __syncthreads();
+  if constexpr (MC > 1) cluster_sync_all();   // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int inner = a.back ? a.N : a.K, width = a.back ? a.K : a.N;   // of A's rows, of the output's
-  const int ntw = (width + kTileM - 1) / kTileM;
+  const int ntw = (width + MC * kTileM - 1) / (MC * kTileM);   // of the CTAs that go together
   const int total = tp[a.E + 1] * ntw;
   const int nbn = (a.N + kF8StageK - 1) / kF8StageK, nbk = (a.K + kF8StageK - 1) / kF8StageK;
   const int ksteps = a.back ? nbn : nbk;
@@ -157,10 +161,15 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     first = blockIdx.x / ranks;
     stride = gridDim.x / ranks;
   }
+  const int mc = MC > 1 ? blockIdx.x % MC : 0;   // this CTA in its pair
+  if constexpr (MC > 1) {
+    first = blockIdx.x / MC;
+    stride = gridDim.x / MC;
+  }
   const int ks0 = (int)((int64_t)ksteps * rank / ranks), ks1 = (int)((int64_t)ksteps * (rank + 1) / ranks);
   auto tile_of = [&](int tile, int& n0) {
     const int mt = tile / ntw;
-    n0 = (tile - mt * ntw) * kTileM;
+    n0 = ((tile - mt * ntw) * MC + mc) * kTileM;
     return row_tile(a.E, tp, row0, BN, mt);
   };
 
@@ -183,11 +192,18 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         // Test hook: the first stage's barrier is armed, its copies are never issued.
         if (args.inject_stall && it == 0) continue;
         uint8_t* da = smem + RG::a_off + s * RG::a_bytes;
-        if (boxes == BN / kF8BoxRows)
+        if constexpr (MC > 1) {
+          if (boxes == BN / kF8BoxRows)
+            tma_3d_pair_elect(da + mc * (BN / MC) * kF8StageK, &map_a, ks * kF8StageK, t.start + mc * (BN / MC), 0, &full[s]);
+          else
+            for (int b = mc; b < boxes; b += MC)
+              tma_3d_pair_elect(da + b * kF8BoxRows * kF8StageK, &map_a32, ks * kF8StageK, t.start + b * kF8BoxRows, 0, &full[s]);
+        } else if (boxes == BN / kF8BoxRows) {
           tma_3d_elect(da, &map_a, ks * kF8StageK, t.start, 0, &full[s]);
-        else
+        } else {
           for (int b = 0; b < boxes; ++b)
             tma_3d_elect(da + b * kF8BoxRows * kF8StageK, &map_a32, ks * kF8StageK, t.start + b * kF8BoxRows, 0, &full[s]);
+        }
         uint8_t* dw = smem + RG::w_off + s * RG::w_bytes;
         if (a.back) tma_3d_elect(dw, &map_w, n0, ks * kF8StageK, t.e, &full[s]);
         else tma_3d_elect(dw, &map_w, ks * kF8StageK, n0, t.e, &full[s]);
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       int n0;
       const RowTile t = tile_of(tile, n0);
       if (t.e == a.E) continue;
-      const int ob = n0 / kTileM;
+      const int ob = min(n0, width - 1) / kTileM;
       const uint8_t* src = a.w_scales + (size_t)t.e * nbn * nbk + (a.back ? ob : (size_t)ob * nbk);
       const size_t step = a.back ? nbk : 1;
       uint32_t next = src[ks0 * step];
@@ -288,7 +304,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             if (ok) {
               tc_fence_after();
               fence_proxy_async_smem();   // the scales were written through the generic proxy
-              f8_stage_elect<RG::groups>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
+              f8_stage_elect<RG::groups, MC>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
                                          adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
                                          idesc0 | (uint32_t)(ks & 3) << 29 | (uint32_t)(ks & 3) << 4, tmem + RG::sf_col0 + u * RG::sf_cols,
                                          swdesc0 + (uint64_t)((u * RG::sfw_bytes) >> 4), sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
@@ -350,6 +366,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while another may still read its part
   }
+  if constexpr (MC > 1) {
+    __syncwarp();
+    cluster_sync_all();   // no CTA leaves while the other may still send to it
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -362,19 +382,21 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 namespace {
 
 template <int BN, int OUT>
-cudaError_t launch_f8(const F8KernelArgs& args, int64_t tiles, int split, cudaStream_t s) {
+cudaError_t launch_f8(const F8KernelArgs& args, int64_t tiles, int split, bool pairs, cudaStream_t s) {
   const Fp8MatmulArgs& a = args.a;
   const int64_t inner = a.back ? a.N : a.K;
   CUtensorMap map_a, map_a32, map_w;
   constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, fp8_pitch(inner), BN) ||
+  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, fp8_pitch(inner), pairs ? BN / 2 : BN) ||
       !encode_tiles(&map_a32, u8, 1, a.a_codes, inner, a.R, 1, fp8_pitch(inner), kF8BoxRows) ||
       !encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM))
     return cudaErrorInvalidValue;
   constexpr int smem = F8Ring<BN>::total + 1024;   // + alignment slack
   if constexpr (BN == 32)
-    if (split > 1) return launch_tiles(fp8_matmul_kernel<BN, OUT, true>, tiles * split, split, kF8Threads, smem, s, map_a, map_a32, map_w, args);
-  return launch_tiles(fp8_matmul_kernel<BN, OUT, false>, std::min<int64_t>(tiles, kSms), 1, kF8Threads, smem, s, map_a, map_a32, map_w, args);
+    if (split > 1) return launch_tiles(fp8_matmul_kernel<BN, OUT, true, 1>, tiles * split, split, kF8Threads, smem, s, map_a, map_a32, map_w, args);
+  if constexpr (BN == 192)
+    if (pairs) return launch_tiles(fp8_matmul_kernel<BN, OUT, false, 2>, kSms, 2, kF8Threads, smem, s, map_a, map_a32, map_w, args);
+  return launch_tiles(fp8_matmul_kernel<BN, OUT, false, 1>, std::min<int64_t>(tiles, kSms), 1, kF8Threads, smem, s, map_a, map_a32, map_w, args);
 }
 
 // Output tiles there can be at most (the device offsets decide how many there are).
@@ -390,9 +412,10 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStre
   const int64_t ksteps = ((a.back ? a.N : a.K) + kF8StageK - 1) / kF8StageK, narrow = most_tiles(a, 32);
   auto run = [&](auto bn, int64_t tiles, int split) {
     constexpr int BN = decltype(bn)::value;
-    if (a.out_dtype == QMOE_F32) return launch_f8<BN, QMOE_F32>(args, tiles, split, s);
-    if (a.out_dtype == QMOE_F16) return launch_f8<BN, QMOE_F16>(args, tiles, split, s);
-    return launch_f8<BN, QMOE_BF16>(args, tiles, split, s);
+    const bool pairs = BN == 192 && tiles > kSms && (a.back ? a.K : a.N) > kTileM;
+    if (a.out_dtype == QMOE_F32) return launch_f8<BN, QMOE_F32>(args, tiles, split, pairs, s);
+    if (a.out_dtype == QMOE_F16) return launch_f8<BN, QMOE_F16>(args, tiles, split, pairs, s);
+    return launch_f8<BN, QMOE_BF16>(args, tiles, split, pairs, s);
   };
   const int64_t rows = a.offsets ? a.R / std::min<int64_t>(a.E, a.R) : a.R;   // of an expert, if they are spread evenly
   if (narrow > kSms && rows > 32) return run(std::integral_constant<int, 192>{}, most_tiles(a, 192), 1);

@@ -105,6 +105,7 @@ struct ChoiceArgs {
   int64_t T;
   int E, k, scoring, groups, top_groups, best, renorm;
   float scale;
+  int room;                 // values of a warp in shared memory (set by the launch)
   int* ids;                 // [T, k]
   float* w;                 // [T, k]
   // gradient

@@ -51,6 +51,7 @@ struct WgRing {
 
 // Up to four K = 16 MMAs of a stage and the commit that frees it, by one elected
 // lane; 16 rows on is 2048 bytes in either operand.
+template <int MC>
 __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty) {
   asm volatile(
       "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
@@ -63,9 +64,11 @@ __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t 
       "@q1 tcgen05.mma.cta_group::1.kind::f16 [%0], y1, z1, %3, p1;\n\t"
       "@q2 tcgen05.mma.cta_group::1.kind::f16 [%0], y2, z2, %3, p1;\n\t"
       "@q3 tcgen05.mma.cta_group::1.kind::f16 [%0], y3, z3, %3, p1;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}" ::"r"(d),
-      "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk), "r"(smem_u32(empty))
+      "}" ::"r"(d),
+      "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
       : "memory");
+  if constexpr (MC > 1) tc_commit_pair_elect(empty);
+  else tc_commit_elect(empty);
 }
 
 // Instruction descriptor, kind::f16: D f32, both operands f16 or both bf16,
@@ -82,7 +85,10 @@ struct WgTile {
   int e, n0, k0, lo, hi;   // this CTA's rows of it
 };
 
-template <int OUT, bool SPLIT>
+// SPLIT: a cluster shares each tile's rows, and there is one tile a cluster at
+// most.  MC = 2: the CTAs of a pair take neighbouring columns of x with the same
+// columns of dy; each loads half of the latter and sends it to both.
+template <int OUT, bool SPLIT, int MC>
 __global__ void __launch_bounds__(kWgThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const WgKernelArgs args) {
   using RG = WgRing;
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], MC);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -123,9 +129,10 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     for (int e = lane; e <= a.E; e += 32) row0[e] = a.offsets ? min(max(a.offsets[e], 0), (int)a.R) : (e ? (int)a.R : 0);
   tc_fence_before();
   __syncthreads();
+  if constexpr (MC > 1) cluster_sync_all();   // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + kTileM - 1) / kTileM;
+  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + MC * kTileM - 1) / (MC * kTileM);
   const int total = a.E * ntn * ntk;
   int ranks = 1, rank = 0, first = blockIdx.x, stride = gridDim.x;
   if constexpr (SPLIT) {
@@ -134,13 +141,18 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     first = blockIdx.x / ranks;
     stride = gridDim.x / ranks;
   }
+  const int mc = MC > 1 ? blockIdx.x % MC : 0;   // this CTA in its pair
+  if constexpr (MC > 1) {
+    first = blockIdx.x / MC;
+    stride = gridDim.x / MC;
+  }
   // whole stages to each rank; the first ranks have rows where there are few
   auto tile_of = [&](int tile) {
     WgTile t;
     const int kt = tile % ntk, rest = tile / ntk, nt = rest % ntn;
     t.e = rest / ntn;
     t.n0 = nt * kWgBN;
-    t.k0 = kt * kTileM;
+    t.k0 = (kt * MC + mc) * kTileM;
     const int lo = row0[t.e], hi = max(row0[t.e + 1], lo);
     const int steps = (hi - lo + kWgRows - 1) / kWgRows, each = (steps + ranks - 1) / ranks;
     t.lo = min(lo + rank * each * kWgRows, hi);
@@ -166,8 +178,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
         for (int p = 0; p < RG::x_panels; ++p)
           tma_3d_elect(smem + RG::x_off + s * RG::x_bytes + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, &full[s]);
-        for (int p = 0; p < panels; ++p)
-          tma_3d_elect(smem + RG::dy_off + s * RG::dy_bytes + p * kWgPanelBytes, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
+        for (int p = mc; p < panels; p += MC) {
+          uint8_t* dst = smem + RG::dy_off + s * RG::dy_bytes + p * kWgPanelBytes;
+          if constexpr (MC > 1) tma_3d_pair_elect(dst, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
+          else tma_3d_elect(dst, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
+        }
       }
     }
     if (!ok) {
@@ -210,7 +225,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           __syncwarp();
         }
         tc_fence_after();
-        wg_stage_elect(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4), idesc,
+        wg_stage_elect<MC>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4), idesc,
                        r != t.lo ? 1u : 0u, nk, &empty[s]);
       }
       if (ok) tc_commit_elect(&acc_full[ab]);
@@ -264,26 +279,56 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while another may still read its part
   }
+  if constexpr (MC > 1) {
+    __syncwarp();
+    cluster_sync_all();   // no CTA leaves while the other may still send to it
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, RG::tmem_cols);
 }
 
-// Rows that start on any element to rows that start on 16 bytes.
+// Rows that start on any element to rows that start on 16 bytes, of both
+// operands in one launch.  A thread writes 16 bytes: it loads the aligned 16
+// bytes that hold its first element and the following ones (words that are not
+// wholly inside the tensor element by element) and shifts.
+struct AlignArgs {
+  const uint16_t* src[2];
+  int64_t ld[2], pitch[2];
+  uint16_t* dst[2];
+  int width[2], groups[2];   // of 8 elements a row; 0: nothing to copy
+  int64_t rows;
+};
 constexpr int kAlignThreads = 256;
-__global__ void __launch_bounds__(kAlignThreads) align_rows_kernel(const uint16_t* src, int64_t ld, int64_t rows, int width, uint16_t* dst, int64_t pitch) {
-  op_begin();
-  const int groups = (width + 7) / 8;
-  const int64_t n = rows * groups;
-  for (int64_t i = blockIdx.x * (int64_t)kAlignThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kAlignThreads) {
-    const int64_t r = i / groups;
-    const int c = (int)(i - r * groups) * 8;
-    const uint16_t* p = src + r * ld + c;
-    uint32_t v[8];
+__device__ __forceinline__ uint4 load_inside(const uint16_t* x, int64_t from, int64_t size) {
+  if (from >= 0 && from + 8 <= size) return ld_once_v4(x + from);
+  uint32_t v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < width ? p[j] : 0u;
-    *reinterpret_cast<uint4*>(dst + r * pitch + c) = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  for (int j = 0; j < 8; ++j) v[j] = from + j >= 0 && from + j < size ? x[from + j] : 0u;
+  return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+__global__ void __launch_bounds__(kAlignThreads) align_rows_kernel(const AlignArgs a) {
+  op_begin();
+  const int per_row = a.groups[0] + a.groups[1];
+  const int64_t n = a.rows * per_row;
+  for (int64_t i = blockIdx.x * (int64_t)kAlignThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kAlignThreads) {
+    const int64_t r = i / per_row;
+    int g = (int)(i - r * per_row);
+    const int which = g >= a.groups[0] ? 1 : 0;
+    g -= which ? a.groups[0] : 0;
+    const uint16_t* x = which ? a.src[1] : a.src[0];
+    const int64_t ld = which ? a.ld[1] : a.ld[0], row0 = r * ld, size = (a.rows - 1) * ld + (which ? a.width[1] : a.width[0]);
+    const int m = (int)((reinterpret_cast<uintptr_t>(x + row0) & 15) >> 1), c = g * 8;
+    const uint4 lo = load_inside(x, row0 + c - m, size), hi = m ? load_inside(x, row0 + c - m + 8, size) : lo;
+    uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int j = 0; j < 6; ++j) u[j] = (m & 4) ? u[j + 2] : u[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) u[j] = (m & 2) ? u[j + 1] : u[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = (m & 1) ? __funnelshift_r(u[j], u[j + 1], 16) : u[j];
+    *reinterpret_cast<uint4*>((which ? a.dst[1] : a.dst[0]) + r * (which ? a.pitch[1] : a.pitch[0]) + c) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -298,20 +343,33 @@ size_t align_bytes(const void* p, int64_t ld, int64_t R, int64_t width) {
   return tma_rows(p, ld) ? 0 : (size_t)R * (size_t)((width + 7) / 8 * 8) * 2;
 }
 
-cudaError_t align_rows(const void*& p, int64_t& ld, int64_t R, int width, uint8_t*& work, cudaStream_t s) {
-  if (tma_rows(p, ld)) return cudaSuccess;
-  const int64_t pitch = (width + 7) / 8 * 8, n = R * (pitch / 8);
+// Copies what TMA cannot read into the workspace, and points the arguments there.
+cudaError_t align_operands(WgradArgs& a, cudaStream_t s) {
+  AlignArgs c{};
+  c.rows = a.R;
+  uint8_t* work = a.workspace;
+  auto take = [&](int i, const void*& p, int64_t& ld, int width) {
+    if (tma_rows(p, ld)) return;
+    c.src[i] = static_cast<const uint16_t*>(p);
+    c.ld[i] = ld;
+    c.width[i] = width;
+    c.groups[i] = (width + 7) / 8;
+    c.pitch[i] = (int64_t)c.groups[i] * 8;
+    c.dst[i] = reinterpret_cast<uint16_t*>(work);
+    work += (size_t)a.R * c.pitch[i] * 2;
+    p = c.dst[i];
+    ld = c.pitch[i];
+  };
+  take(0, a.dy, a.ld_dy, a.N);
+  take(1, a.x, a.ld_x, a.K);
+  const int64_t n = a.R * (c.groups[0] + c.groups[1]);
+  if (n == 0) return cudaSuccess;
   const unsigned blocks = (unsigned)std::min<int64_t>((n + kAlignThreads - 1) / kAlignThreads, kSms * 8);
-  const cudaError_t e = launch_op(align_rows_kernel, dim3(blocks), dim3(kAlignThreads), 0, s, static_cast<const uint16_t*>(p), ld, R, width,
-                                  reinterpret_cast<uint16_t*>(work), pitch);
-  p = work;
-  ld = pitch;
-  work += (size_t)R * pitch * 2;
-  return e;
+  return launch_op(align_rows_kernel, dim3(blocks), dim3(kAlignThreads), 0, s, c);
 }
 
 template <int OUT>
-cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, cudaStream_t s) {
+cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, bool pairs, cudaStream_t s) {
   const WgradArgs& a = args.a;
   CUtensorMap map_x, map_dy;
   const auto type = a.dtype == QMOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -319,8 +377,9 @@ cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, cudaSt
       !encode_tiles(&map_dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, kWgRows))
     return cudaErrorInvalidValue;
   constexpr int smem = WgRing::total + 1024;   // + alignment slack
-  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
-  return launch_tiles(weight_grad_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
+  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true, 1>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
+  if (pairs) return launch_tiles(weight_grad_kernel<OUT, false, 2>, kSms, 2, kWgThreads, smem, s, map_x, map_dy, args);
+  return launch_tiles(weight_grad_kernel<OUT, false, 1>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
 }
 
 }  // namespace
@@ -331,9 +390,7 @@ size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64
 
 cudaError_t launch_weight_grad(const WgradArgs& a, int inject_stall, cudaStream_t s) {
   WgKernelArgs args{a, inject_stall};
-  uint8_t* work = a.workspace;
-  cudaError_t e = align_rows(args.a.dy, args.a.ld_dy, a.R, a.N, work, s);
-  if (e == cudaSuccess) e = align_rows(args.a.x, args.a.ld_x, a.R, a.K, work, s);
+  const cudaError_t e = align_operands(args.a, s);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)a.E * ((a.N + kWgBN - 1) / kWgBN) * ((a.K + kTileM - 1) / kTileM);
   if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
@@ -342,9 +399,10 @@ cudaError_t launch_weight_grad(const WgradArgs& a, int inject_stall, cudaStream_
   const int64_t steps = (a.R / a.E + kWgRows - 1) / kWgRows;
   int split = 1;
   while (split < 8 && tiles * split * 2 <= kSms && split * 2 <= steps) split *= 2;
-  if (a.out_dtype == QMOE_F32) return launch_wg<QMOE_F32>(args, tiles, split, s);
-  if (a.out_dtype == QMOE_F16) return launch_wg<QMOE_F16>(args, tiles, split, s);
-  return launch_wg<QMOE_BF16>(args, tiles, split, s);
+  const bool pairs = tiles > kSms && a.K > kTileM;
+  if (a.out_dtype == QMOE_F32) return launch_wg<QMOE_F32>(args, tiles, split, pairs, s);
+  if (a.out_dtype == QMOE_F16) return launch_wg<QMOE_F16>(args, tiles, split, pairs, s);
+  return launch_wg<QMOE_BF16>(args, tiles, split, pairs, s);
 }
 
 }  // namespace qmoe
