@@ -17,7 +17,7 @@
 //   warp 1    MMA issuer: scales to TMEM, then four K = 32 MMAs a stage
 //   warp 2    scales of A's rows: four bytes a row by cp.async (512 values' worth)
 //   warp 3    scale of the weight block: one byte, spread over 512
-//   warps 4-7 epilogue: TMEM columns to rows of the output
+//   warps 4-11 epilogue: TMEM columns to rows of the output
 // Two accumulators of BN columns alternate, so the epilogue of one tile runs
 // under the MMAs of the next.  CTAs are persistent over the (expert, row tile,
 // weight tile) list, which every CTA derives from the device offsets.  Where
@@ -32,7 +32,7 @@ namespace qmoe {
 
 constexpr int kF8StageK = 128;                 // values along the reduction a stage: one swizzle atom
 constexpr int kF8BoxRows = 32;                 // rows of A a copy where a tile is not full
-constexpr int kF8Threads = 256;
+constexpr int kF8Threads = 128 + 32 * kEpiWarps;
 constexpr long long kF8DrainPolls = 4096;      // parked polls (about 4 ms) a copy in flight is given to land
 
 template <int BN>
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], kEpiWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     mbar_wait_bounded(drain_bar, 0, drain);
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp >> 2) - 1;
     int tc = 0;
     bool ok = true;
     for (int tile = first; tile < total && ok; tile += stride) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const bool in = col < width;
       T* out = static_cast<T*>(a.out) + (size_t)t.start * a.ld_out + col;
       if (t.e == a.E) {
-        if (rank == 0) store_zeros<OUT>(out, a.ld_out, t.rows, in);
+        if (rank == 0) store_zeros<OUT>(out, a.ld_out, t.rows, in, half);
         continue;
       }
       const int ab = tc & 1;
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * BN;
-      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem + RG::w_off), q, t.rows);   // the ring is empty
-      else store_tile<OUT>(acc, out, a.ld_out, t.rows, in);
+      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem + RG::w_off), q, t.rows, half);   // the ring is empty
+      else store_tile<OUT>(acc, out, a.ld_out, t.rows, in, half);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const int q = warp & 3, col = n0 + q * 32 + lane;
       if (t.e != a.E)
         store_sum<OUT>(reinterpret_cast<const float*>(smem + RG::w_off), q, static_cast<T*>(a.out) + (size_t)t.start * a.ld_out + col,
-                       a.ld_out, t.rows, col < width, rank, ranks);
+                       a.ld_out, t.rows, col < width, rank, ranks, (warp >> 2) - 1);
     }
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while another may still read its part

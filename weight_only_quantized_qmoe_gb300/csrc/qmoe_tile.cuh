@@ -110,32 +110,46 @@ __device__ __forceinline__ RowTile row_tile(int E, const int* tp, const int* row
   return t;
 }
 
-// Columns 0 .. n of a warp's quarter of a tile to rows 0 .. n of the output, a
-// lane an element of each (`in`: the lane has one).  `out`: the lane's element
-// of the first row.
+// Two warps take a quarter of a tile's lanes, every other 32 columns each.  With
+// one, and an address and a test for every store, the epilogue was what bounded
+// both kernels (16 instructions a column; a tile of the weight gradient over 512
+// rows took 7000 cycles, its MMAs 4350).
+constexpr int kEpiWarps = 8;
+
+// Columns of a warp's quarter of a tile to rows 0 .. n of the output, a lane an
+// element of each (`in`: the lane has one).  `out`: the lane's element of the
+// first row; half: which of the two warps.
 template <int OUT>
-__device__ __forceinline__ void store_tile(uint32_t taddr, typename ElemT<OUT>::t* out, int64_t ld, int n, bool in) {
-  for (int c0 = 0; c0 < n; c0 += 32) {
+__device__ __forceinline__ void store_tile(uint32_t taddr, typename ElemT<OUT>::t* out, int64_t ld, int n, bool in, int half) {
+  using T = typename ElemT<OUT>::t;
+  out += (size_t)(half * 32) * ld;
+  for (int c0 = half * 32; c0 < n; c0 += 64, out += (size_t)64 * ld) {
     uint32_t v[32];
     TC_LD32(taddr + c0, v);
     tc_wait_ld();
     if (!in) continue;
+    T* p = out;
+    if (c0 + 32 <= n) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (c0 + c < n) store_d<OUT>(out + (size_t)(c0 + c) * ld, 0, __uint_as_float(v[c]));
+      for (int c = 0; c < 32; ++c, p += ld) store_d<OUT>(p, 0, __uint_as_float(v[c]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c, p += ld)
+        if (c0 + c < n) store_d<OUT>(p, 0, __uint_as_float(v[c]));
+    }
   }
 }
 template <int OUT>
-__device__ __forceinline__ void store_zeros(typename ElemT<OUT>::t* out, int64_t ld, int n, bool in) {
+__device__ __forceinline__ void store_zeros(typename ElemT<OUT>::t* out, int64_t ld, int n, bool in, int half) {
   if (in)
-    for (int c = 0; c < n; ++c) store_d<OUT>(out + (size_t)c * ld, 0, 0.f);
+    for (int c = half; c < n; c += 2) store_d<OUT>(out + (size_t)c * ld, 0, 0.f);
 }
 
 // A tile whose reduction is split over the CTAs of a cluster: each CTA's
 // partial sums to its own shared memory, [column][128] ...
-__device__ __forceinline__ void put_partial(uint32_t taddr, float* part, int q, int n) {
+__device__ __forceinline__ void put_partial(uint32_t taddr, float* part, int q, int n, int half) {
   const int lane = threadIdx.x & 31;
-  for (int c0 = 0; c0 < n; c0 += 32) {
+  for (int c0 = half * 32; c0 < n; c0 += 64) {
     uint32_t v[32];
     TC_LD32(taddr + c0, v);
     tc_wait_ld();
@@ -161,10 +175,10 @@ __device__ __forceinline__ void cluster_sync_all() {
 // of 1001 x 513: 27.7 us, now SUM_US).
 template <int OUT>
 __device__ __forceinline__ void store_sum(const float* part, int q, typename ElemT<OUT>::t* out, int64_t ld, int n, bool in,
-                                          int rank, int ranks) {
+                                          int rank, int ranks, int half) {
   constexpr int most = 8, cols = 4;
   const int lane = threadIdx.x & 31;
-  for (int c0 = rank; c0 < n; c0 += ranks * cols) {
+  for (int c0 = rank + half * ranks * cols; c0 < n; c0 += 2 * ranks * cols) {
     float v[cols][most];
 #pragma unroll
     for (int u = 0; u < cols; ++u) {

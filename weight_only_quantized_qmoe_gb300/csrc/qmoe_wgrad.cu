@@ -16,7 +16,7 @@
 //   warp 0    TMA producer (one elected lane)
 //   warp 1    MMA issuer, zeros past the last row
 //   warp 3    first rows of the experts
-//   warps 4-7 epilogue: TMEM columns to rows of dw
+//   warps 4-11 epilogue: TMEM columns to rows of dw
 // Two accumulators alternate.  CTAs are persistent over the (expert, tile) list.
 // Where there are few tiles, the CTAs of a cluster share a tile's rows and add up
 // their parts in a fixed order.  Operands that TMA cannot read (rows that do not
@@ -30,7 +30,7 @@ namespace qmoe {
 constexpr int kWgRows = 64;                     // rows a stage
 constexpr int kWgPanel = 64;                    // columns of a panel (128 bytes)
 constexpr int kWgPanelBytes = kWgRows * 128;
-constexpr int kWgThreads = 256;
+constexpr int kWgThreads = 128 + 32 * kEpiWarps;
 constexpr int kWgBN = 256;
 constexpr long long kWgDrainPolls = 4096;
 
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], kEpiWarps);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     mbar_wait_bounded(drain_bar, 0, drain);
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp >> 2) - 1;
     int tc = 0;
     bool ok = true;
     for (int tile = first; tile < total && ok; tile += stride) {
@@ -247,9 +247,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       if (t.lo >= t.hi) {
         if constexpr (SPLIT) {
           float* part = reinterpret_cast<float*>(smem);
-          for (int c = 0; c < n; ++c) part[c * kTileM + q * 32 + lane] = 0.f;
+          for (int c = half; c < n; c += 2) part[c * kTileM + q * 32 + lane] = 0.f;
         } else {
-          store_zeros<OUT>(out, a.K, n, in);
+          store_zeros<OUT>(out, a.K, n, in, half);
         }
         continue;
       }
@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
-      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem), q, n);   // the ring is empty
-      else store_tile<OUT>(acc, out, a.K, n, in);
+      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem), q, n, half);   // the ring is empty
+      else store_tile<OUT>(acc, out, a.K, n, in, half);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[ab]);
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const WgTile t = tile_of(first);
       const int q = warp & 3, col = t.k0 + q * 32 + lane;
       store_sum<OUT>(reinterpret_cast<const float*>(smem), q, static_cast<T*>(a.dw) + ((size_t)t.e * a.N + t.n0) * a.K + col, a.K,
-                     min(kWgBN, a.N - t.n0), col < a.K, rank, ranks);
+                     min(kWgBN, a.N - t.n0), col < a.K, rank, ranks, (warp >> 2) - 1);
     }
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while another may still read its part
