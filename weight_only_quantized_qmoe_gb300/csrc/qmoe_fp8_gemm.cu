@@ -37,7 +37,7 @@ constexpr long long kF8DrainPolls = 4096;      // parked polls (about 4 ms) a co
 
 template <int BN>
 struct F8Ring {
-  static constexpr int stages = BN == 192 ? 5 : 10;
+  static constexpr int stages = 10;
   static constexpr int groups = (BN + 127) / 128;                 // 128-row scale groups of A
   static constexpr int w_bytes = kTileM * kF8StageK;
   static constexpr int a_bytes = BN * kF8StageK;
@@ -57,12 +57,12 @@ struct F8Ring {
   static_assert(sf_col0 + stages * sf_cols <= tmem_cols, "TMEM columns");
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
-  static_assert(BN * kTileM * 4 <= stages * w_bytes || BN == 192, "a partial tile fits the ring");
+  static_assert(BN * kTileM * 4 <= stages * w_bytes, "a partial tile fits the ring");
 };
 
 // One stage, issued by one elected lane: the scales of W and of A's row groups
 // to TMEM, up to four K = 32 MMAs, the commit that frees the stage.
-template <int GROUPS, int MC>
+template <int GROUPS>
 __device__ __forceinline__ void f8_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sf,
                                                uint64_t sw, uint64_t sa, uint32_t acc, int nk, uint64_t* empty) {
   static_assert(GROUPS == 1 || GROUPS == 2, "row groups of A");
@@ -85,15 +85,14 @@ __device__ __forceinline__ void f8_stage_elect(uint32_t d, uint64_t w, uint64_t 
       "@q3 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [t1], p1;\n\t}" ::"r"(d),
       "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sf), "l"(sw), "l"(sa), "r"(acc), "r"(nk), "n"(GROUPS)
       : "memory");
-  if constexpr (MC > 1) tc_commit_pair_elect(empty);
-  else tc_commit_elect(empty);
+  tc_commit_elect(empty);
 }
 
-// Instruction descriptor, kind::mxf8f6f4: both operands E4M3, scales E8M0, M =
-// 128; W along K, or along M (bit 15).  The scale ids (bits 29-30 and 4-5) name
+// Instruction descriptor, kind::mxf8f6f4: both operands E4M3, scales E8M0; W
+// along K, or along M (bit 15).  The scale ids (bits 29-30 and 4-5) name
 // the byte of a 32-bit scale word.
-__device__ __forceinline__ uint32_t idesc_mxf8(int N, int back) {
-  return ((uint32_t)back << 15) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(kTileM >> 7) << 27);
+__device__ __forceinline__ uint32_t idesc_mxf8(int M, int N, int back) {
+  return ((uint32_t)back << 15) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
 struct F8KernelArgs {
@@ -102,9 +101,8 @@ struct F8KernelArgs {
 };
 
 // SPLIT: a cluster shares each tile's reduction, and there is one tile a cluster
-// at most.  MC = 2: the CTAs of a pair take neighbouring weight rows with the
-// same rows of A; each loads half of the latter and sends it to both.
-template <int BN, int OUT, bool SPLIT, int MC>
+// at most.
+template <int BN, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kF8Threads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a32,
                       const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
@@ -128,7 +126,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1 + 32 + 1);   // the announced bytes, the lanes of A's scales, the weight's scale
-      mbar_init(&empty[i], MC);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -146,11 +144,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (warp == 3) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
   tc_fence_before();
   __syncthreads();
-  if constexpr (MC > 1) cluster_sync_all();   // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int inner = a.back ? a.N : a.K, width = a.back ? a.K : a.N;   // of A's rows, of the output's
-  const int ntw = (width + MC * kTileM - 1) / (MC * kTileM);   // of the CTAs that go together
+  const int ntw = (width + kTileM - 1) / kTileM;
   const int total = tp[a.E + 1] * ntw;
   const int nbn = (a.N + kF8StageK - 1) / kF8StageK, nbk = (a.K + kF8StageK - 1) / kF8StageK;
   const int ksteps = a.back ? nbn : nbk;
@@ -161,15 +158,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     first = blockIdx.x / ranks;
     stride = gridDim.x / ranks;
   }
-  const int mc = MC > 1 ? blockIdx.x % MC : 0;   // this CTA in its pair
-  if constexpr (MC > 1) {
-    first = blockIdx.x / MC;
-    stride = gridDim.x / MC;
-  }
   const int ks0 = (int)((int64_t)ksteps * rank / ranks), ks1 = (int)((int64_t)ksteps * (rank + 1) / ranks);
   auto tile_of = [&](int tile, int& n0) {
     const int mt = tile / ntw;
-    n0 = ((tile - mt * ntw) * MC + mc) * kTileM;
+    n0 = (tile - mt * ntw) * kTileM;
     return row_tile(a.E, tp, row0, BN, mt);
   };
 
@@ -192,13 +184,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         // Test hook: the first stage's barrier is armed, its copies are never issued.
         if (args.inject_stall && it == 0) continue;
         uint8_t* da = smem + RG::a_off + s * RG::a_bytes;
-        if constexpr (MC > 1) {
-          if (boxes == BN / kF8BoxRows)
-            tma_3d_pair_elect(da + mc * (BN / MC) * kF8StageK, &map_a, ks * kF8StageK, t.start + mc * (BN / MC), 0, &full[s]);
-          else
-            for (int b = mc; b < boxes; b += MC)
-              tma_3d_pair_elect(da + b * kF8BoxRows * kF8StageK, &map_a32, ks * kF8StageK, t.start + b * kF8BoxRows, 0, &full[s]);
-        } else if (boxes == BN / kF8BoxRows) {
+        if (boxes == BN / kF8BoxRows) {
           tma_3d_elect(da, &map_a, ks * kF8StageK, t.start, 0, &full[s]);
         } else {
           for (int b = 0; b < boxes; ++b)
@@ -253,7 +239,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       int n0;
       const RowTile t = tile_of(tile, n0);
       if (t.e == a.E) continue;
-      const int ob = min(n0, width - 1) / kTileM;
+      const int ob = n0 / kTileM;
       const uint8_t* src = a.w_scales + (size_t)t.e * nbn * nbk + (a.back ? ob : (size_t)ob * nbk);
       const size_t step = a.back ? nbk : 1;
       uint32_t next = src[ks0 * step];
@@ -286,7 +272,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     for (int tile = first; tile < real && ok; tile += stride, ++tc) {
       int n0;
       const RowTile t = tile_of(tile, n0);
-      const uint32_t idesc0 = idesc_mxf8((t.rows + 15) & ~15, a.back);
+      const uint32_t idesc0 = idesc_mxf8(kTileM, (t.rows + 15) & ~15, a.back);
       const int ab = tc & 1;
       ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -304,7 +290,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             if (ok) {
               tc_fence_after();
               fence_proxy_async_smem();   // the scales were written through the generic proxy
-              f8_stage_elect<RG::groups, MC>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
+              f8_stage_elect<RG::groups>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
                                          adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
                                          idesc0 | (uint32_t)(ks & 3) << 29 | (uint32_t)(ks & 3) << 4, tmem + RG::sf_col0 + u * RG::sf_cols,
                                          swdesc0 + (uint64_t)((u * RG::sfw_bytes) >> 4), sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
@@ -366,10 +352,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while another may still read its part
   }
-  if constexpr (MC > 1) {
-    __syncwarp();
-    cluster_sync_all();   // no CTA leaves while the other may still send to it
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -377,26 +359,305 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 }
 
 // ----------------------------------------------------------------------------
+// Pairs of CTAs, for many rows: tiles of 256 weight rows (back: columns) by up to
+// 224 rows of A, of which each CTA loads half.  Scales do not pass through shared
+// memory: four warps a CTA, one for each quarter of the TMEM lanes, load the
+// words of 512 reduction values (all rows of A, this CTA's weight block) and
+// write them to TMEM, every quarter the same, and arrive on the first CTA's
+// barrier once in four stages: a remote arrival a stage had cost a microsecond.
+// ----------------------------------------------------------------------------
+struct F8PairRing {
+  static constexpr int bn = 224;
+  static constexpr int stages = 7;
+  static constexpr int sf_groups = 5;                             // scales of four stages each
+  static constexpr int w_bytes = kTileM * kF8StageK;
+  static constexpr int a_bytes = bn / 2 * kF8StageK;
+  static constexpr int w_off = 0;
+  static constexpr int a_off = w_off + stages * w_bytes;
+  static constexpr int bar_off = a_off + stages * a_bytes;
+  static constexpr int tp_off = bar_off + 512;
+  static constexpr int total = tp_off + 2 * (kSortMaxExperts + 2) * 4;
+  static constexpr int sf_col0 = 2 * bn;
+  static constexpr int sf_cols = 12;                              // W's four columns, then A's eight
+  static_assert(sf_col0 + sf_groups * sf_cols <= 512, "TMEM columns");
+  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(a_bytes % 1024 == 0, "swizzle atoms");
+};
+constexpr int kF8PairBox = 16;                                    // rows of A a copy where a tile is not full
+constexpr int kF8PairThreads = 256 + 32 * kEpiWarps;
+
+// One stage: up to four K = 32 MMAs of the pair and the commit that frees it.
+__device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sfw,
+                                                    uint32_t sfa, uint32_t acc, int nk, uint64_t* empty) {
+  asm volatile(
+      "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p0, %7, 0;\n\tsetp.eq.b32 p1, %7, %7;\n\t"
+      "setp.gt.and.s32 q1, %8, 1, e;\n\tsetp.gt.and.s32 q2, %8, 2, e;\n\tsetp.gt.and.s32 q3, %8, 3, e;\n\t"
+      "add.u64 y1, %1, %2;\n\tadd.u64 y2, y1, %2;\n\tadd.u64 y3, y2, %2;\n\t"
+      "add.u64 z1, %3, 2;\n\tadd.u64 z2, %3, 4;\n\tadd.u64 z3, %3, 6;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %3, %4, [%5], [%6], p0;\n\t"
+      "@q1 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y1, z1, %4, [%5], [%6], p1;\n\t"
+      "@q2 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y2, z2, %4, [%5], [%6], p1;\n\t"
+      "@q3 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [%6], p1;\n\t}" ::"r"(d),
+      "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sfw), "r"(sfa), "r"(acc), "r"(nk)
+      : "memory");
+  tc_commit_pair_elect(empty);
+}
+__device__ __forceinline__ void tmem_store_x4(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(taddr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void tmem_store_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kF8PairThreads, 1)
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a16,
+                           const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
+  using RG = F8PairRing;
+  using T = typename ElemT<OUT>::t;
+  constexpr int S = RG::stages, G = RG::sf_groups, BN = RG::bn;
+  extern __shared__ __align__(1024) uint8_t f8_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f8_smem_raw) + 1023) & ~uintptr_t(1023));
+  const Fp8MatmulArgs& a = args.a;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RG::bar_off);   // the first CTA's count for both
+  uint64_t* empty = full + S;
+  uint64_t* sf_full = empty + S;                                      // the first CTA's count for both
+  uint64_t* sf_empty = sf_full + G;
+  uint64_t* acc_full = sf_empty + G;
+  uint64_t* acc_empty = acc_full + 2;                                 // the first CTA's count for both
+  uint64_t* drain_bar = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* tp = reinterpret_cast<int*>(smem + RG::tp_off);
+  int* row0 = tp + kSortMaxExperts + 2;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < G; ++i) {
+      mbar_init(&sf_full[i], 8);    // four warps of each CTA
+      mbar_init(&sf_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
+  op_begin();   // the operands and offsets may come from the kernel before
+  if (warp == 2) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the other CTA's barriers and TMEM are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int inner = a.back ? a.N : a.K, width = a.back ? a.K : a.N;   // of A's rows, of the output's
+  const int ntw = (width + 2 * kTileM - 1) / (2 * kTileM);
+  const int total = tp[a.E + 1] * ntw, real = tp[a.E] * ntw;          // with and without the rows that have no route
+  const int nbn = (a.N + kF8StageK - 1) / kF8StageK, nbk = (a.K + kF8StageK - 1) / kF8StageK;
+  const int ksteps = a.back ? nbn : nbk, first = blockIdx.x / 2, stride = gridDim.x / 2;
+  auto tile_of = [&](int tile, int& n0) {
+    const int mt = tile / ntw;
+    n0 = ((tile - mt * ntw) * 2 + rank) * kTileM;
+    return row_tile(a.E, tp, row0, BN, mt);
+  };
+  // rows of A of each CTA: half of the tile's, in whole sixteens
+  auto half_of = [&](const RowTile& t) { return ((t.rows + 31) & ~31) / 2; };
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < real && ok; tile += stride) {
+      int n0;
+      const RowTile t = tile_of(tile, n0);
+      const int half = half_of(t), start = t.start + rank * half;
+      for (int ks = 0; ks < ksteps; ++ks, ++it) {
+        const int s = it % S;
+        ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t bar = rank == 0 ? smem_u32(&full[s]) : first_cta_bar(&full[s]);
+        if (rank == 0) mbar_arrive_expect_tx_elect(&full[s], (uint32_t)(2 * (half * kF8StageK + RG::w_bytes)));
+        // Test hook: the first stage's barrier is armed, its copies are never issued.
+        if (args.inject_stall && it == 0) continue;
+        uint8_t *da = smem + RG::a_off + s * RG::a_bytes, *dw = smem + RG::w_off + s * RG::w_bytes;
+        if (half == BN / 2)
+          tma_3d_pair_elect(da, &map_a, ks * kF8StageK, start, 0, bar);
+        else
+          for (int b = 0; b < half; b += kF8PairBox)
+            tma_3d_pair_elect(da + b * kF8StageK, &map_a16, ks * kF8StageK, start + b, 0, bar);
+        if (a.back) tma_3d_pair_elect(dw, &map_w, n0, ks * kF8StageK, t.e, bar);
+        else tma_3d_pair_elect(dw, &map_w, ks * kF8StageK, n0, t.e, bar);
+      }
+    }
+    if (!ok) {
+      // The copies in flight must land before the pair leaves: those of both CTAs
+      // count on the first one's barriers; the second one's own never complete, so
+      // it waits for as long as the limit says.
+      const WaitCfg drain{a.wait.status, kF8DrainPolls};
+      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer ----------------
+    const uint64_t wdesc0 = a.back ? smem_desc_mn128(smem_u32(smem + RG::w_off), RG::w_bytes) : smem_desc_sw128(smem_u32(smem + RG::w_off));
+    const uint64_t wstep = a.back ? (32 * 128) >> 4 : 32 >> 4;   // 32 reduction values on: 32 rows, or 32 bytes
+    const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + RG::a_off));
+    const int tail = (inner - (ksteps - 1) * kF8StageK + 31) / 32;   // MMAs of the last stage
+    int st = 0, tc = 0, g = 0;
+    uint32_t ph = 0, gph = 0;
+    bool ok = true;
+    for (int tile = first; tile < real && ok; tile += stride, ++tc) {
+      int n0;
+      const RowTile t = tile_of(tile, n0);
+      const uint32_t idesc0 = idesc_mxf8(2 * kTileM, 2 * half_of(t), a.back);
+      const int ab = tc & 1;
+      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      for (int ks = 0; ks < ksteps && ok; ++ks) {
+        if ((ks & 3) == 0) {
+          ok = warp_spin_cluster(&sf_full[g], gph, a.wait, abort_flag);
+          if (!ok) break;
+        }
+        ok = warp_spin_cluster(&full[st], ph, a.wait, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t id = (uint32_t)(ks & 3), sf = tmem + RG::sf_col0 + g * RG::sf_cols;
+        f8_pair_stage_elect(tmem + ab * BN, wdesc0 + (uint64_t)((st * RG::w_bytes) >> 4), wstep, adesc0 + (uint64_t)((st * RG::a_bytes) >> 4),
+                            idesc0 | id << 29 | id << 4, sf, sf + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[st]);
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if ((ks & 3) == 3 || ks + 1 == ksteps) {
+          tc_commit_pair_elect(&sf_empty[g]);
+          if (++g == G) {
+            g = 0;
+            gph ^= 1u;
+          }
+        }
+      }
+      if (ok) tc_commit_pair_elect(&acc_full[ab]);
+    }
+    tc_commit_pair_here_elect(drain_bar);
+    const WaitCfg drain{a.wait.status, kDrainWaitLimit};
+    mbar_wait_bounded(drain_bar, 0, drain);
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------- scales ----------------
+    // Row 32 j + lane's word of A goes to column 4 + j of this quarter's lane; the
+    // weight block's word, the same for every row, to columns 0 to 3.
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int g = 0;
+    uint32_t gph = 0;
+    bool ok = true;
+    for (int tile = first; tile < real && ok; tile += stride) {
+      int n0;
+      const RowTile t = tile_of(tile, n0);
+      const int left = min((int)a.R - t.start, BN) - lane;   // row 32 j exists: 32 j < left
+      const int ob = min(n0, width - 1) / kTileM;
+      const uint8_t* w0 = a.w_scales + (size_t)t.e * nbn * nbk + (a.back ? ob : (size_t)ob * nbk);
+      const size_t wstep = a.back ? nbk : 1;
+      uint32_t word[8], w = 0;
+      auto fetch = [&](int ks) {
+        const uint8_t* src = a.a_scales + ((size_t)(ks >> 2) * a.R + t.start + lane) * 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) word[j] = 32 * j < left ? *reinterpret_cast<const uint32_t*>(src + j * 128) : 0u;
+        w = lane < 4 && ks + lane < ksteps ? (uint32_t)w0[(ks + lane) * wstep] << (8 * lane) : 0u;
+      };
+      fetch(0);
+      for (int ks = 0; ks < ksteps; ks += 4) {
+        w |= __shfl_xor_sync(0xffffffffu, w, 1);
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        const uint32_t every = __shfl_sync(0xffffffffu, w, 0);
+        ok = wait_or_abort(&sf_empty[g], gph ^ 1u, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tmem + lanes + RG::sf_col0 + g * RG::sf_cols;
+        tmem_store_x4(at, every);
+        tmem_store_x8(at + 4, word);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_bar_arrive(first_cta_bar(&sf_full[g]));
+        if (ks + 4 < ksteps) fetch(ks + 4);
+        if (++g == G) {
+          g = 0;
+          gph ^= 1u;
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, half = (warp >> 2) - 2;
+    int tc = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      int n0;
+      const RowTile t = tile_of(tile, n0);
+      const int col = n0 + q * 32 + lane;
+      const bool in = col < width;
+      T* out = static_cast<T*>(a.out) + (size_t)t.start * a.ld_out + col;
+      if (t.e == a.E) {
+        store_zeros<OUT>(out, a.ld_out, t.rows, in, half);
+        continue;
+      }
+      const int ab = tc & 1;
+      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * BN, out, a.ld_out, t.rows, in, half);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      ++tc;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ----------------------------------------------------------------------------
 // Host side
 // ----------------------------------------------------------------------------
 namespace {
 
-template <int BN, int OUT>
-cudaError_t launch_f8(const F8KernelArgs& args, int64_t tiles, int split, bool pairs, cudaStream_t s) {
+template <int OUT>
+cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split, cudaStream_t s) {
   const Fp8MatmulArgs& a = args.a;
-  const int64_t inner = a.back ? a.N : a.K;
-  CUtensorMap map_a, map_a32, map_w;
+  const int64_t inner = a.back ? a.N : a.K, pitch = fp8_pitch(inner);
+  const bool pairs = bn == F8PairRing::bn;
+  CUtensorMap map_a, map_part, map_w;
   constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, fp8_pitch(inner), pairs ? BN / 2 : BN) ||
-      !encode_tiles(&map_a32, u8, 1, a.a_codes, inner, a.R, 1, fp8_pitch(inner), kF8BoxRows) ||
+  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? bn / 2 : bn) ||
+      !encode_tiles(&map_part, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? kF8PairBox : kF8BoxRows) ||
       !encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM))
     return cudaErrorInvalidValue;
-  constexpr int smem = F8Ring<BN>::total + 1024;   // + alignment slack
-  if constexpr (BN == 32)
-    if (split > 1) return launch_tiles(fp8_matmul_kernel<BN, OUT, true, 1>, tiles * split, split, kF8Threads, smem, s, map_a, map_a32, map_w, args);
-  if constexpr (BN == 192)
-    if (pairs) return launch_tiles(fp8_matmul_kernel<BN, OUT, false, 2>, kSms, 2, kF8Threads, smem, s, map_a, map_a32, map_w, args);
-  return launch_tiles(fp8_matmul_kernel<BN, OUT, false, 1>, std::min<int64_t>(tiles, kSms), 1, kF8Threads, smem, s, map_a, map_a32, map_w, args);
+  constexpr int slack = 1024;   // of the alignment
+  if (pairs)
+    return launch_tiles(fp8_matmul_pair_kernel<OUT>, std::min<int64_t>((tiles + 1) / 2 * 2, kSms), 2, kF8PairThreads, F8PairRing::total + slack,
+                        s, map_a, map_part, map_w, args);
+  if (split > 1)
+    return launch_tiles(fp8_matmul_kernel<32, OUT, true>, tiles * split, split, kF8Threads, F8Ring<32>::total + slack, s, map_a, map_part,
+                        map_w, args);
+  return launch_tiles(fp8_matmul_kernel<32, OUT, false>, std::min<int64_t>(tiles, kSms), 1, kF8Threads, F8Ring<32>::total + slack, s, map_a,
+                      map_part, map_w, args);
 }
 
 // Output tiles there can be at most (the device offsets decide how many there are).
@@ -410,20 +671,18 @@ int64_t most_tiles(const Fp8MatmulArgs& a, int bn) {
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStream_t s) {
   const F8KernelArgs args{a, inject_stall};
   const int64_t ksteps = ((a.back ? a.N : a.K) + kF8StageK - 1) / kF8StageK, narrow = most_tiles(a, 32);
-  auto run = [&](auto bn, int64_t tiles, int split) {
-    constexpr int BN = decltype(bn)::value;
-    const bool pairs = BN == 192 && tiles > kSms && (a.back ? a.K : a.N) > kTileM;
-    if (a.out_dtype == QMOE_F32) return launch_f8<BN, QMOE_F32>(args, tiles, split, pairs, s);
-    if (a.out_dtype == QMOE_F16) return launch_f8<BN, QMOE_F16>(args, tiles, split, pairs, s);
-    return launch_f8<BN, QMOE_BF16>(args, tiles, split, pairs, s);
+  auto run = [&](int bn, int64_t tiles, int split) {
+    if (a.out_dtype == QMOE_F32) return launch_f8<QMOE_F32>(args, bn, tiles, split, s);
+    if (a.out_dtype == QMOE_F16) return launch_f8<QMOE_F16>(args, bn, tiles, split, s);
+    return launch_f8<QMOE_BF16>(args, bn, tiles, split, s);
   };
   const int64_t rows = a.offsets ? a.R / std::min<int64_t>(a.E, a.R) : a.R;   // of an expert, if they are spread evenly
-  if (narrow > kSms && rows > 32) return run(std::integral_constant<int, 192>{}, most_tiles(a, 192), 1);
+  if (narrow > kSms && rows > 32) return run(F8PairRing::bn, most_tiles(a, F8PairRing::bn), 1);
   // a tile's reduction over the CTAs of a cluster while there are CTAs without a
   // tile, at least two stages each
   int split = 1;
   while (split < 8 && narrow * split * 2 <= kSms && split * 4 <= ksteps) split *= 2;
-  return run(std::integral_constant<int, 32>{}, narrow, split);
+  return run(32, narrow, split);
 }
 
 }  // namespace qmoe

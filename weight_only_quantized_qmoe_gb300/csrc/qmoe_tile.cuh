@@ -27,22 +27,78 @@ __device__ __forceinline__ void tma_3d_elect(void* dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// The same copy to the same place of both CTAs of a pair, completing on the same
-// barrier of each; and a commit that arrives on the same barrier of each.
-__device__ __forceinline__ void tma_3d_pair_elect(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-      "[%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
+// ----------------------------------------------------------------------------
+// Pairs of CTAs (cta_group::2): one MMA of M = 256, each CTA with its half of M,
+// half of the rows of N in its shared memory and an accumulator of all N columns
+// in its TMEM.  An SM takes in 64 bytes a cycle, and a tile of 128 x 192 needs 107
+// to keep its tensor core busy, of a pair's 256 x 224 an SM 67.  Rank 0 issues the
+// MMAs; both CTAs' copies complete on its barriers.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives, when the MMAs issued so far are done, on the barrier of both CTAs; on
+// that of this one.
 __device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_here_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// A barrier's address in rank 0 of the cluster.
+__device__ __forceinline__ uint32_t first_cta_bar(uint64_t* bar) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
+  return at;
+}
+__device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A copy to this CTA's shared memory that completes on a barrier of either.
+__device__ __forceinline__ void tma_3d_pair_elect(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// spin_or_abort for a phase that the other CTA's threads arrive on too: one
+// answer for the whole warp.
+__device__ __forceinline__ bool warp_spin_cluster(uint64_t* bar, uint32_t parity, const WaitCfg& w, volatile int* abort_flag) {
+  const long long limit = w.limit * 64;
+  bool ok = false;
+  for (long long i = 0; i < limit; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (__shfl_sync(0xffffffffu, done, 0)) {
+      ok = true;
+      break;
+    }
+    if ((i & 255) == 255 && __shfl_sync(0xffffffffu, *abort_flag, 0)) return false;
+  }
+  if (!ok) {
+    atomicExch(w.status, DEV_TIMEOUT);
+    *abort_flag = 1;
+  }
+  return ok;
 }
 
 // Shared-memory matrix descriptor of an operand that lies along M or N (the
@@ -167,6 +223,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, int rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
 }
+// All threads of all CTAs of the cluster; converged warps.
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

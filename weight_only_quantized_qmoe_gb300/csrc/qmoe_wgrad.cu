@@ -49,32 +49,57 @@ struct WgRing {
   static_assert(kWgBN * kTileM * 4 <= bar_off, "a partial tile fits the ring");
 };
 
+// Zeros from row `rows` of a stage to the end of its 16, in `panels` panels, by a
+// whole warp.
+__device__ __forceinline__ void zero_rows(uint8_t* base, int panels, int rows) {
+  const int n = (((rows + 15) & ~15) - rows) * 8;   // 16-byte pieces a panel
+  for (int p = 0; p < panels; ++p)
+    for (int i = threadIdx.x & 31; i < n; i += 32)
+      reinterpret_cast<uint4*>(base + p * kWgPanelBytes + rows * 128)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Up to four K = 16 MMAs of a stage and the commit that frees it, by one elected
-// lane; 16 rows on is 2048 bytes in either operand.
-template <int MC>
+// lane of a CTA or of the first CTA of a pair; 16 rows on is 2048 bytes in either
+// operand.
+template <int CTAS>
 __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty) {
-  asm volatile(
-      "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
-      "setp.gt.and.s32 q1, %5, 1, e;\n\tsetp.gt.and.s32 q2, %5, 2, e;\n\tsetp.gt.and.s32 q3, %5, 3, e;\n\t"
-      "add.u64 y1, %1, 128;\n\tadd.u64 y2, %1, 256;\n\tadd.u64 y3, %1, 384;\n\t"
-      "add.u64 z1, %2, 128;\n\tadd.u64 z2, %2, 256;\n\tadd.u64 z3, %2, 384;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
-      "@q1 tcgen05.mma.cta_group::1.kind::f16 [%0], y1, z1, %3, p1;\n\t"
-      "@q2 tcgen05.mma.cta_group::1.kind::f16 [%0], y2, z2, %3, p1;\n\t"
-      "@q3 tcgen05.mma.cta_group::1.kind::f16 [%0], y3, z3, %3, p1;\n\t"
-      "}" ::"r"(d),
-      "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
-      : "memory");
-  if constexpr (MC > 1) tc_commit_pair_elect(empty);
-  else tc_commit_elect(empty);
+  if constexpr (CTAS == 1) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
+        "setp.gt.and.s32 q1, %5, 1, e;\n\tsetp.gt.and.s32 q2, %5, 2, e;\n\tsetp.gt.and.s32 q3, %5, 3, e;\n\t"
+        "add.u64 y1, %1, 128;\n\tadd.u64 y2, %1, 256;\n\tadd.u64 y3, %1, 384;\n\t"
+        "add.u64 z1, %2, 128;\n\tadd.u64 z2, %2, 256;\n\tadd.u64 z3, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+        "@q1 tcgen05.mma.cta_group::1.kind::f16 [%0], y1, z1, %3, p1;\n\t"
+        "@q2 tcgen05.mma.cta_group::1.kind::f16 [%0], y2, z2, %3, p1;\n\t"
+        "@q3 tcgen05.mma.cta_group::1.kind::f16 [%0], y3, z3, %3, p1;\n\t}" ::"r"(d),
+        "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
+        : "memory");
+    tc_commit_elect(empty);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\tsetp.eq.b32 p1, %4, %4;\n\t"
+        "setp.gt.and.s32 q1, %5, 1, e;\n\tsetp.gt.and.s32 q2, %5, 2, e;\n\tsetp.gt.and.s32 q3, %5, 3, e;\n\t"
+        "add.u64 y1, %1, 128;\n\tadd.u64 y2, %1, 256;\n\tadd.u64 y3, %1, 384;\n\t"
+        "add.u64 z1, %2, 128;\n\tadd.u64 z2, %2, 256;\n\tadd.u64 z3, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+        "@q1 tcgen05.mma.cta_group::2.kind::f16 [%0], y1, z1, %3, p1;\n\t"
+        "@q2 tcgen05.mma.cta_group::2.kind::f16 [%0], y2, z2, %3, p1;\n\t"
+        "@q3 tcgen05.mma.cta_group::2.kind::f16 [%0], y3, z3, %3, p1;\n\t}" ::"r"(d),
+        "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
+        : "memory");
+    tc_commit_pair_elect(empty);
+  }
 }
 
 // Instruction descriptor, kind::f16: D f32, both operands f16 or both bf16,
-// both along M and N (bits 15 and 16), M = 128.
-__device__ __forceinline__ uint32_t idesc_wgrad(int bf16, int N) {
-  return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+// both along M and N (bits 15 and 16).
+__device__ __forceinline__ uint32_t idesc_wgrad(int bf16, int M, int N) {
+  return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | 1u << 15 | 1u << 16 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
 struct WgKernelArgs {
@@ -86,9 +111,8 @@ struct WgTile {
 };
 
 // SPLIT: a cluster shares each tile's rows, and there is one tile a cluster at
-// most.  MC = 2: the CTAs of a pair take neighbouring columns of x with the same
-// columns of dy; each loads half of the latter and sends it to both.
-template <int OUT, bool SPLIT, int MC>
+// most.
+template <int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kWgThreads, 1)
     weight_grad_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const WgKernelArgs args) {
   using RG = WgRing;
@@ -110,7 +134,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], MC);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -129,10 +153,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     for (int e = lane; e <= a.E; e += 32) row0[e] = a.offsets ? min(max(a.offsets[e], 0), (int)a.R) : (e ? (int)a.R : 0);
   tc_fence_before();
   __syncthreads();
-  if constexpr (MC > 1) cluster_sync_all();   // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + MC * kTileM - 1) / (MC * kTileM);
+  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + kTileM - 1) / kTileM;
   const int total = a.E * ntn * ntk;
   int ranks = 1, rank = 0, first = blockIdx.x, stride = gridDim.x;
   if constexpr (SPLIT) {
@@ -141,18 +164,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     first = blockIdx.x / ranks;
     stride = gridDim.x / ranks;
   }
-  const int mc = MC > 1 ? blockIdx.x % MC : 0;   // this CTA in its pair
-  if constexpr (MC > 1) {
-    first = blockIdx.x / MC;
-    stride = gridDim.x / MC;
-  }
   // whole stages to each rank; the first ranks have rows where there are few
   auto tile_of = [&](int tile) {
     WgTile t;
     const int kt = tile % ntk, rest = tile / ntk, nt = rest % ntn;
     t.e = rest / ntn;
     t.n0 = nt * kWgBN;
-    t.k0 = (kt * MC + mc) * kTileM;
+    t.k0 = kt * kTileM;
     const int lo = row0[t.e], hi = max(row0[t.e + 1], lo);
     const int steps = (hi - lo + kWgRows - 1) / kWgRows, each = (steps + ranks - 1) / ranks;
     t.lo = min(lo + rank * each * kWgRows, hi);
@@ -178,11 +196,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
         for (int p = 0; p < RG::x_panels; ++p)
           tma_3d_elect(smem + RG::x_off + s * RG::x_bytes + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, &full[s]);
-        for (int p = mc; p < panels; p += MC) {
-          uint8_t* dst = smem + RG::dy_off + s * RG::dy_bytes + p * kWgPanelBytes;
-          if constexpr (MC > 1) tma_3d_pair_elect(dst, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
-          else tma_3d_elect(dst, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
-        }
+        for (int p = 0; p < panels; ++p)
+          tma_3d_elect(smem + RG::dy_off + s * RG::dy_bytes + p * kWgPanelBytes, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
       }
     }
     if (!ok) {
@@ -199,7 +214,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     for (int tile = first; tile < total && ok; tile += stride) {
       const WgTile t = tile_of(tile);
       if (t.lo >= t.hi) continue;
-      const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, (min(kWgBN, a.N - t.n0) + 15) & ~15);
+      const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, kTileM, (min(kWgBN, a.N - t.n0) + 15) & ~15);
       const int ab = tc & 1;
       ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -213,19 +228,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         }
         const int rows = min(kWgRows, t.hi - r), nk = (rows + 15) / 16;
         if (rows & 15) {
-          // rows of 128 bytes: zeros from the last one to the end of its 16
-          const int n = (nk * 16 - rows) * 8;   // 16-byte pieces a panel
-          const int panels = RG::x_panels + min(RG::dy_panels, (a.N - t.n0 + kWgPanel - 1) / kWgPanel);
-          for (int p = 0; p < panels; ++p) {
-            uint8_t* base = p < RG::x_panels ? smem + RG::x_off + s * RG::x_bytes + p * kWgPanelBytes
-                                             : smem + RG::dy_off + s * RG::dy_bytes + (p - RG::x_panels) * kWgPanelBytes;
-            for (int i = lane; i < n; i += 32) reinterpret_cast<uint4*>(base + rows * 128)[i] = make_uint4(0, 0, 0, 0);
-          }
+          zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::x_panels, rows);
+          zero_rows(smem + RG::dy_off + s * RG::dy_bytes, min(RG::dy_panels, (a.N - t.n0 + kWgPanel - 1) / kWgPanel), rows);
           fence_proxy_async_smem();
           __syncwarp();
         }
         tc_fence_after();
-        wg_stage_elect<MC>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4), idesc,
+        wg_stage_elect<1>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4), idesc,
                        r != t.lo ? 1u : 0u, nk, &empty[s]);
       }
       if (ok) tc_commit_elect(&acc_full[ab]);
@@ -279,14 +288,217 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     __syncwarp();
     cluster_sync_all();   // no CTA leaves while another may still read its part
   }
-  if constexpr (MC > 1) {
-    __syncwarp();
-    cluster_sync_all();   // no CTA leaves while the other may still send to it
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, RG::tmem_cols);
+}
+
+// The same with pairs of CTAs: tiles of 256 columns of x by up to 256 of dy, of
+// which each CTA loads half.  A tail stage's zeros are each CTA's own: the other
+// CTA's copies of that stage complete on a barrier of its own, and a warp there
+// that has written the zeros arrives for them.
+struct WgPairRing {
+  static constexpr int stages = 6;
+  static constexpr int panels = 2;                              // of x, and of a half of dy's columns
+  static constexpr int x_bytes = panels * kWgPanelBytes;
+  static constexpr int dy_bytes = panels * kWgPanelBytes;
+  static constexpr int x_off = 0;
+  static constexpr int dy_off = x_off + stages * x_bytes;
+  static constexpr int bar_off = dy_off + stages * dy_bytes;
+  static constexpr int row_off = bar_off + 512;
+  static constexpr int total = row_off + (kSortMaxExperts + 1) * 4;
+  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+};
+
+template <int OUT>
+__global__ void __launch_bounds__(kWgThreads, 1)
+    weight_grad_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const WgKernelArgs args) {
+  using RG = WgPairRing;
+  using T = typename ElemT<OUT>::t;
+  constexpr int S = RG::stages;
+  extern __shared__ __align__(1024) uint8_t wg_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(wg_smem_raw) + 1023) & ~uintptr_t(1023));
+  const WgradArgs& a = args.a;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RG::bar_off);   // the first CTA's count for both
+  uint64_t* empty = full + S;
+  uint64_t* tail = empty + S;                                         // the second CTA's
+  uint64_t* acc_full = tail + S;
+  uint64_t* acc_empty = acc_full + 2;                                 // the first CTA's count for both
+  uint64_t* drain_bar = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* row0 = reinterpret_cast<int*>(smem + RG::row_off);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 2);   // the announced bytes; the other CTA's zeros, or nothing to wait for
+      mbar_init(&empty[i], 1);
+      mbar_init(&tail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 2 * kWgBN);
+  op_begin();   // the operands and offsets may come from the kernel before
+  if (warp == 3)
+    for (int e = lane; e <= a.E; e += 32) row0[e] = a.offsets ? min(max(a.offsets[e], 0), (int)a.R) : (e ? (int)a.R : 0);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the other CTA's barriers and TMEM are there
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + 2 * kTileM - 1) / (2 * kTileM);
+  const int total = a.E * ntn * ntk, first = blockIdx.x / 2, stride = gridDim.x / 2;
+  auto tile_of = [&](int tile) {
+    WgTile t;
+    const int kt = tile % ntk, rest = tile / ntk;
+    t.e = rest / ntn;
+    t.n0 = (rest % ntn) * kWgBN;
+    t.k0 = (2 * kt + rank) * kTileM;
+    t.lo = row0[t.e];
+    t.hi = max(row0[t.e + 1], t.lo);
+    return t;
+  };
+  // columns of dy of each CTA: half of the tile's, in whole sixteens
+  auto half_of = [&](const WgTile& t) { return ((min(kWgBN, a.N - t.n0) + 31) & ~31) / 2; };
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    int it = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      const int half = half_of(t), panels = (half + kWgPanel - 1) / kWgPanel, col0 = t.n0 + rank * half;
+      const uint32_t bytes = (uint32_t)((RG::panels + panels) * kWgPanelBytes);
+      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
+        const int s = it % S;
+        ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool zeros = t.hi - r < kWgRows && ((t.hi - r) & 15);
+        uint32_t bar = rank == 0 ? smem_u32(&full[s]) : first_cta_bar(&full[s]);
+        if (rank == 0) {
+          mbar_arrive_expect_tx_elect(&full[s], zeros ? bytes : 2 * bytes);
+          if (!zeros && lane == 0) mbar_arrive(&full[s]);
+          __syncwarp();
+        } else if (zeros) {
+          mbar_arrive_expect_tx_elect(&tail[s], bytes);
+          bar = smem_u32(&tail[s]);
+        }
+        // Test hook: the first stage's barrier is armed, its copies are never issued.
+        if (args.inject_stall && it == 0) continue;
+        uint8_t *dx = smem + RG::x_off + s * RG::x_bytes, *ddy = smem + RG::dy_off + s * RG::dy_bytes;
+#pragma unroll
+        for (int p = 0; p < RG::panels; ++p) {
+          tma_3d_pair_elect(dx + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, bar);
+          if (p < panels) tma_3d_pair_elect(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar);
+        }
+      }
+    }
+    if (!ok) {
+      // The copies in flight must land before the pair leaves: those of both CTAs
+      // count on the first one's barriers; the second one's own never complete, so
+      // it waits for as long as the limit says.
+      const WaitCfg drain{a.wait.status, kWgDrainPolls};
+      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer ----------------
+    const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), kWgPanelBytes);
+    const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), kWgPanelBytes);
+    int it = 0, tc = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      if (t.lo >= t.hi) continue;
+      const int half = half_of(t);
+      const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, 2 * kTileM, 2 * half);
+      const int ab = tc & 1;
+      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      if (!ok) break;
+      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
+        const int s = it % S;
+        ok = warp_spin_cluster(&full[s], (it / S) & 1, a.wait, abort_flag);
+        if (!ok) break;
+        const int rows = min(kWgRows, t.hi - r);
+        if (rows & 15) {
+          zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::panels, rows);
+          zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half + kWgPanel - 1) / kWgPanel, rows);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4),
+                          idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
+      }
+      if (ok) tc_commit_pair_elect(&acc_full[ab]);
+      ++tc;
+    }
+    tc_commit_pair_here_elect(drain_bar);
+    const WaitCfg drain{a.wait.status, kDrainWaitLimit};
+    mbar_wait_bounded(drain_bar, 0, drain);
+  } else if (warp == 1) {
+    // ---------------- the second CTA's zeros ----------------
+    int it = 0;
+    uint32_t phases = 0;   // of `tail`, a bit each
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      if (t.lo >= t.hi) continue;
+      it += (t.hi - t.lo + kWgRows - 1) / kWgRows;
+      const int rows = (t.hi - t.lo - 1) % kWgRows + 1, s = (it - 1) % S;
+      if (!(rows & 15)) continue;
+      ok = wait_or_abort(&tail[s], (phases >> s) & 1u, a.wait, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      phases ^= 1u << s;
+      zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::panels, rows);
+      zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half_of(t) + kWgPanel - 1) / kWgPanel, rows);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) cluster_bar_arrive(first_cta_bar(&full[s]));
+    }
+  } else if (warp >= 4) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3, half = (warp >> 2) - 1;
+    int tc = 0;
+    bool ok = true;
+    for (int tile = first; tile < total && ok; tile += stride) {
+      const WgTile t = tile_of(tile);
+      const int col = t.k0 + q * 32 + lane, n = min(kWgBN, a.N - t.n0);
+      const bool in = col < a.K;
+      T* out = static_cast<T*>(a.dw) + ((size_t)t.e * a.N + t.n0) * a.K + col;
+      if (t.lo >= t.hi) {
+        store_zeros<OUT>(out, a.K, n, in, half);
+        continue;
+      }
+      const int ab = tc & 1;
+      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN, out, a.K, n, in, half);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      ++tc;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 2 * kWgBN);
 }
 
 // Rows that start on any element to rows that start on 16 bytes, of both
@@ -377,9 +589,11 @@ cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, bool p
       !encode_tiles(&map_dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, kWgRows))
     return cudaErrorInvalidValue;
   constexpr int smem = WgRing::total + 1024;   // + alignment slack
-  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true, 1>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
-  if (pairs) return launch_tiles(weight_grad_kernel<OUT, false, 2>, kSms, 2, kWgThreads, smem, s, map_x, map_dy, args);
-  return launch_tiles(weight_grad_kernel<OUT, false, 1>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
+  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
+  if (pairs)
+    return launch_tiles(weight_grad_pair_kernel<OUT>, std::min<int64_t>((tiles + 1) / 2 * 2, kSms), 2, kWgThreads, WgPairRing::total + 1024, s,
+                        map_x, map_dy, args);
+  return launch_tiles(weight_grad_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
 }
 
 }  // namespace
