@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
 // ----------------------------------------------------------------------------
 // Pairs of CTAs, for many rows: tiles of 256 weight rows (back: columns) by up to
-// 224 rows of A, of which each CTA loads half.  Scales do not pass through shared
+// 224 rows of A, of which each CTA loads half; two pairs take neighbouring weight rows and share A's.
+// Scales do not pass through shared
 // memory: four warps a CTA, one for each quarter of the TMEM lanes, load the
 // words of 512 reduction values (all rows of A, this CTA's weight block) and
 // write them to TMEM, every quarter the same, and arrive on the first CTA's
@@ -383,12 +384,12 @@ struct F8PairRing {
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
 };
-constexpr int kF8PairBox = 16;                                    // rows of A a copy where a tile is not full
+constexpr int kF8PairBox = 8;                                     // rows of A a copy where a tile is not full
 constexpr int kF8PairThreads = 256 + 32 * kEpiWarps;
 
 // One stage: up to four K = 32 MMAs of the pair and the commit that frees it.
 __device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sfw,
-                                                    uint32_t sfa, uint32_t acc, int nk, uint64_t* empty) {
+                                                    uint32_t sfa, uint32_t acc, int nk, uint64_t* empty, uint16_t mask) {
   asm volatile(
       "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -402,7 +403,7 @@ __device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint
       "@q3 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [%6], p1;\n\t}" ::"r"(d),
       "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sfw), "r"(sfa), "r"(acc), "r"(nk)
       : "memory");
-  tc_commit_pair_elect(empty);
+  tc_commit_pair_elect(empty, mask);
 }
 __device__ __forceinline__ void tmem_store_x4(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(taddr), "r"(v) : "memory");
@@ -413,9 +414,9 @@ __device__ __forceinline__ void tmem_store_x8(uint32_t taddr, const uint32_t (&v
                : "memory");
 }
 
-template <int OUT>
+template <int OUT, int PAIRS>
 __global__ void __launch_bounds__(kF8PairThreads, 1)
-    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a16,
+    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_part,
                            const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
   using RG = F8PairRing;
   using T = typename ElemT<OUT>::t;
@@ -436,11 +437,12 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   int* row0 = tp + kSortMaxExperts + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x & 1;
+  const PairPlace cta = pair_place<PAIRS>();
+  const int rank = cta.h;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], PAIRS);
     }
     for (int i = 0; i < G; ++i) {
       mbar_init(&sf_full[i], 8);    // four warps of each CTA
@@ -460,17 +462,17 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   if (warp == 2) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // the other CTA's barriers and TMEM are there
+  cluster_sync_all();   // the other CTAs' barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int inner = a.back ? a.N : a.K, width = a.back ? a.K : a.N;   // of A's rows, of the output's
-  const int ntw = (width + 2 * kTileM - 1) / (2 * kTileM);
+  const int ntw = (width + 2 * PAIRS * kTileM - 1) / (2 * PAIRS * kTileM);
   const int total = tp[a.E + 1] * ntw, real = tp[a.E] * ntw;          // with and without the rows that have no route
   const int nbn = (a.N + kF8StageK - 1) / kF8StageK, nbk = (a.K + kF8StageK - 1) / kF8StageK;
-  const int ksteps = a.back ? nbn : nbk, first = blockIdx.x / 2, stride = gridDim.x / 2;
+  const int ksteps = a.back ? nbn : nbk, first = blockIdx.x / (2 * PAIRS), stride = gridDim.x / (2 * PAIRS);
   auto tile_of = [&](int tile, int& n0) {
     const int mt = tile / ntw;
-    n0 = ((tile - mt * ntw) * 2 + rank) * kTileM;
+    n0 = (((tile - mt * ntw) * PAIRS + cta.p) * 2 + rank) * kTileM;
     return row_tile(a.E, tp, row0, BN, mt);
   };
   // rows of A of each CTA: half of the tile's, in whole sixteens
@@ -483,22 +485,25 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     for (int tile = first; tile < real && ok; tile += stride) {
       int n0;
       const RowTile t = tile_of(tile, n0);
-      const int half = half_of(t), start = t.start + rank * half;
+      // this CTA's share of its half, and where it goes
+      const int half = half_of(t), part = half / PAIRS, at = cta.p * part, start = t.start + rank * half + at;
       for (int ks = 0; ks < ksteps; ++ks, ++it) {
         const int s = it % S;
         ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t bar = rank == 0 ? smem_u32(&full[s]) : first_cta_bar(&full[s]);
+        const uint32_t bar = bar_of(&full[s], cta.lead);
         if (rank == 0) mbar_arrive_expect_tx_elect(&full[s], (uint32_t)(2 * (half * kF8StageK + RG::w_bytes)));
         // Test hook: the first stage's barrier is armed, its copies are never issued.
         if (args.inject_stall && it == 0) continue;
-        uint8_t *da = smem + RG::a_off + s * RG::a_bytes, *dw = smem + RG::w_off + s * RG::w_bytes;
-        if (half == BN / 2)
-          tma_3d_pair_elect(da, &map_a, ks * kF8StageK, start, 0, bar);
+        uint8_t *da = smem + RG::a_off + s * RG::a_bytes + at * kF8StageK, *dw = smem + RG::w_off + s * RG::w_bytes;
+        auto copy = [&](int row, const CUtensorMap* map) {
+          if constexpr (PAIRS == 1) tma_3d_pair_elect(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar);
+          else tma_3d_pairs_elect(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar, cta.shared);
+        };
+        if (half == BN / 2) copy(0, &map_a);
         else
-          for (int b = 0; b < half; b += kF8PairBox)
-            tma_3d_pair_elect(da + b * kF8StageK, &map_a16, ks * kF8StageK, start + b, 0, bar);
+          for (int b = 0; b < part; b += kF8PairBox) copy(b, &map_part);
         if (a.back) tma_3d_pair_elect(dw, &map_w, n0, ks * kF8StageK, t.e, bar);
         else tma_3d_pair_elect(dw, &map_w, ks * kF8StageK, n0, t.e, bar);
       }
@@ -535,20 +540,21 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         tc_fence_after();
         const uint32_t id = (uint32_t)(ks & 3), sf = tmem + RG::sf_col0 + g * RG::sf_cols;
         f8_pair_stage_elect(tmem + ab * BN, wdesc0 + (uint64_t)((st * RG::w_bytes) >> 4), wstep, adesc0 + (uint64_t)((st * RG::a_bytes) >> 4),
-                            idesc0 | id << 29 | id << 4, sf, sf + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[st]);
+                            idesc0 | id << 29 | id << 4, sf, sf + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[st],
+                            (uint16_t)((1 << 2 * PAIRS) - 1));
         if (++st == S) {
           st = 0;
           ph ^= 1u;
         }
         if ((ks & 3) == 3 || ks + 1 == ksteps) {
-          tc_commit_pair_elect(&sf_empty[g]);
+          tc_commit_pair_elect(&sf_empty[g], cta.here);
           if (++g == G) {
             g = 0;
             gph ^= 1u;
           }
         }
       }
-      if (ok) tc_commit_pair_elect(&acc_full[ab]);
+      if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
     }
     tc_commit_pair_here_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cluster_bar_arrive(first_cta_bar(&sf_full[g]));
+        if (lane == 0) cluster_bar_arrive(bar_of(&sf_full[g], cta.lead));
         if (ks + 4 < ksteps) fetch(ks + 4);
         if (++g == G) {
           g = 0;
@@ -621,14 +627,14 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * BN, out, a.ld_out, t.rows, in, half);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      if (lane == 0) cluster_bar_arrive(bar_of(&acc_empty[ab], cta.lead));
       ++tc;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
+  cluster_sync_all();   // no CTA leaves, or frees TMEM, while another may still use it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
@@ -643,16 +649,24 @@ cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split
   const Fp8MatmulArgs& a = args.a;
   const int64_t inner = a.back ? a.N : a.K, pitch = fp8_pitch(inner);
   const bool pairs = bn == F8PairRing::bn;
+  const int cluster = (a.back ? a.K : a.N) > 2 * kTileM ? 4 : 2;   // two pairs, if both have weight rows
   CUtensorMap map_a, map_part, map_w;
   constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? bn / 2 : bn) ||
+  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? bn / cluster : bn) ||
       !encode_tiles(&map_part, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? kF8PairBox : kF8BoxRows) ||
       !encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM))
     return cudaErrorInvalidValue;
   constexpr int slack = 1024;   // of the alignment
-  if (pairs)
-    return launch_tiles(fp8_matmul_pair_kernel<OUT>, std::min<int64_t>((tiles + 1) / 2 * 2, kSms), 2, kF8PairThreads, F8PairRing::total + slack,
-                        s, map_a, map_part, map_w, args);
+  if (pairs) {
+    auto run = [&](auto kern) {
+      int64_t ctas;
+      constexpr int smem = F8PairRing::total + slack;
+      const cudaError_t e = cluster_ctas(kern, tiles, cluster, kF8PairThreads, smem, ctas);
+      if (e != cudaSuccess) return e;
+      return launch_tiles(kern, ctas, cluster, kF8PairThreads, smem, s, map_a, map_part, map_w, args);
+    };
+    return cluster == 4 ? run(fp8_matmul_pair_kernel<OUT, 2>) : run(fp8_matmul_pair_kernel<OUT, 1>);
+  }
   if (split > 1)
     return launch_tiles(fp8_matmul_kernel<32, OUT, true>, tiles * split, split, kF8Threads, F8Ring<32>::total + slack, s, map_a, map_part,
                         map_w, args);

@@ -62,7 +62,8 @@ __device__ __forceinline__ void zero_rows(uint8_t* base, int panels, int rows) {
 // lane of a CTA or of the first CTA of a pair; 16 rows on is 2048 bytes in either
 // operand.
 template <int CTAS>
-__device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty) {
+__device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty,
+                                               uint16_t mask = 0) {
   if constexpr (CTAS == 1) {
     asm volatile(
         "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
@@ -92,7 +93,7 @@ __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t 
         "@q3 tcgen05.mma.cta_group::2.kind::f16 [%0], y3, z3, %3, p1;\n\t}" ::"r"(d),
         "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
         : "memory");
-    tc_commit_pair_elect(empty);
+    tc_commit_pair_elect(empty, mask);
   }
 }
 
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 }
 
 // The same with pairs of CTAs: tiles of 256 columns of x by up to 256 of dy, of
-// which each CTA loads half.  A tail stage's zeros are each CTA's own: the other
+// which each CTA loads half; two pairs take neighbouring columns of x and share dy's.  A tail stage's zeros are each CTA's own: the other
 // CTA's copies of that stage complete on a barrier of its own, and a warp there
 // that has written the zeros arrives for them.
 struct WgPairRing {
@@ -311,7 +312,7 @@ struct WgPairRing {
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
 };
 
-template <int OUT>
+template <int OUT, int PAIRS>
 __global__ void __launch_bounds__(kWgThreads, 1)
     weight_grad_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const WgKernelArgs args) {
   using RG = WgPairRing;
@@ -331,11 +332,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   int* row0 = reinterpret_cast<int*>(smem + RG::row_off);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x & 1;
+  const PairPlace cta = pair_place<PAIRS>();
+  const int rank = cta.h;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 2);   // the announced bytes; the other CTA's zeros, or nothing to wait for
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], PAIRS);
       mbar_init(&tail[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -353,17 +355,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     for (int e = lane; e <= a.E; e += 32) row0[e] = a.offsets ? min(max(a.offsets[e], 0), (int)a.R) : (e ? (int)a.R : 0);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // the other CTA's barriers and TMEM are there
+  cluster_sync_all();   // the other CTAs' barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + 2 * kTileM - 1) / (2 * kTileM);
-  const int total = a.E * ntn * ntk, first = blockIdx.x / 2, stride = gridDim.x / 2;
+  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + 2 * PAIRS * kTileM - 1) / (2 * PAIRS * kTileM);
+  const int total = a.E * ntn * ntk, first = blockIdx.x / (2 * PAIRS), stride = gridDim.x / (2 * PAIRS);
   auto tile_of = [&](int tile) {
     WgTile t;
     const int kt = tile % ntk, rest = tile / ntk;
     t.e = rest / ntn;
     t.n0 = (rest % ntn) * kWgBN;
-    t.k0 = (2 * kt + rank) * kTileM;
+    t.k0 = ((kt * PAIRS + cta.p) * 2 + rank) * kTileM;
     t.lo = row0[t.e];
     t.hi = max(row0[t.e + 1], t.lo);
     return t;
@@ -385,14 +387,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const bool zeros = t.hi - r < kWgRows && ((t.hi - r) & 15);
-        uint32_t bar = rank == 0 ? smem_u32(&full[s]) : first_cta_bar(&full[s]);
+        uint32_t bar = bar_of(&full[s], cta.lead);
         if (rank == 0) {
           mbar_arrive_expect_tx_elect(&full[s], zeros ? bytes : 2 * bytes);
           if (!zeros && lane == 0) mbar_arrive(&full[s]);
           __syncwarp();
         } else if (zeros) {
           mbar_arrive_expect_tx_elect(&tail[s], bytes);
-          bar = smem_u32(&tail[s]);
+          bar = bar_of(&tail[s], cta.lead + 1);
         }
         // Test hook: the first stage's barrier is armed, its copies are never issued.
         if (args.inject_stall && it == 0) continue;
@@ -400,7 +402,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
         for (int p = 0; p < RG::panels; ++p) {
           tma_3d_pair_elect(dx + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, bar);
-          if (p < panels) tma_3d_pair_elect(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar);
+          if (p >= panels) continue;
+          if constexpr (PAIRS == 1) tma_3d_pair_elect(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar);
+          else if (p == cta.p) tma_3d_pairs_elect(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar, cta.shared);
         }
       }
     }
@@ -438,9 +442,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         }
         tc_fence_after();
         wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4),
-                          idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
+                          idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s], (uint16_t)((1 << 2 * PAIRS) - 1));
       }
-      if (ok) tc_commit_pair_elect(&acc_full[ab]);
+      if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
       ++tc;
     }
     tc_commit_pair_here_elect(drain_bar);
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half_of(t) + kWgPanel - 1) / kWgPanel, rows);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive(first_cta_bar(&full[s]));
+      if (lane == 0) cluster_bar_arrive(bar_of(&full[s], cta.lead));
     }
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
@@ -489,14 +493,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN, out, a.K, n, in, half);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      if (lane == 0) cluster_bar_arrive(bar_of(&acc_empty[ab], cta.lead));
       ++tc;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
+  cluster_sync_all();   // no CTA leaves, or frees TMEM, while another may still use it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * kWgBN);
 }
@@ -590,9 +594,16 @@ cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, bool p
     return cudaErrorInvalidValue;
   constexpr int smem = WgRing::total + 1024;   // + alignment slack
   if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
-  if (pairs)
-    return launch_tiles(weight_grad_pair_kernel<OUT>, std::min<int64_t>((tiles + 1) / 2 * 2, kSms), 2, kWgThreads, WgPairRing::total + 1024, s,
-                        map_x, map_dy, args);
+  if (pairs) {
+    auto run = [&](auto kern, int cluster) {
+      int64_t ctas;
+      constexpr int pair_smem = WgPairRing::total + 1024;
+      const cudaError_t e = cluster_ctas(kern, tiles, cluster, kWgThreads, pair_smem, ctas);
+      if (e != cudaSuccess) return e;
+      return launch_tiles(kern, ctas, cluster, kWgThreads, pair_smem, s, map_x, map_dy, args);
+    };
+    return a.K > 2 * kTileM ? run(weight_grad_pair_kernel<OUT, 2>, 4) : run(weight_grad_pair_kernel<OUT, 1>, 2);
+  }
   return launch_tiles(weight_grad_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
 }
 
