@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   __syncwarp();
   if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
   op_begin();   // the operands and offsets may come from the kernel before
-  if (warp == 2) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
+  if (warp == 3) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // the other CTAs' barriers and TMEM are there
@@ -478,42 +478,46 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   // rows of A of each CTA: half of the tile's, in whole sixteens
   auto half_of = [&](const RowTile& t) { return ((t.rows + 31) & ~31) / 2; };
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
-    int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < real && ok; tile += stride) {
-      int n0;
-      const RowTile t = tile_of(tile, n0);
-      // this CTA's share of its half, and where it goes
-      const int half = half_of(t), part = half / PAIRS, at = cta.p * part, start = t.start + rank * half + at;
-      for (int ks = 0; ks < ksteps; ++ks, ++it) {
-        const int s = it % S;
-        ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t bar = bar_of(&full[s], cta.lead);
-        if (rank == 0) mbar_arrive_expect_tx_elect(&full[s], (uint32_t)(2 * (half * kF8StageK + RG::w_bytes)));
-        // Test hook: the first stage's barrier is armed, its copies are never issued.
-        if (args.inject_stall && it == 0) continue;
-        uint8_t *da = smem + RG::a_off + s * RG::a_bytes + at * kF8StageK, *dw = smem + RG::w_off + s * RG::w_bytes;
-        auto copy = [&](int row, const CUtensorMap* map) {
-          if constexpr (PAIRS == 1) tma_3d_pair_elect(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar);
-          else tma_3d_pairs_elect(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar, cta.shared);
-        };
-        if (half == BN / 2) copy(0, &map_a);
-        else
-          for (int b = 0; b < part; b += kF8PairBox) copy(b, &map_part);
-        if (a.back) tma_3d_pair_elect(dw, &map_w, n0, ks * kF8StageK, t.e, bar);
-        else tma_3d_pair_elect(dw, &map_w, ks * kF8StageK, n0, t.e, bar);
+  if (warp == 0 || warp == 2) {
+    // ---------------- producers: W, and A's rows ----------------
+    // One thread each: a stage's wait, announcement and two copies by one warp
+    // took 740 cycles, its MMAs 448.
+    if (lane == 0) {
+      RingAt<S> at;
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < real && ok; tile += stride) {
+        int n0;
+        const RowTile t = tile_of(tile, n0);
+        // this CTA's share of its half, and where it goes
+        const int half = half_of(t), part = half / PAIRS, skip = cta.p * part, start = t.start + rank * half + skip;
+        for (int ks = 0; ks < ksteps; ++ks, ++it, at.step()) {
+          const int s = at.s;
+          ok = poll_or_wait(&empty[s], at.ph ^ 1u, a.wait, abort_flag);
+          if (!ok) break;
+          const uint32_t bar = bar_of(&full[s], cta.lead);
+          if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * (half * kF8StageK + RG::w_bytes)));
+          // Test hook: the first stage's barrier is armed, its copies are never issued.
+          if (args.inject_stall && it == 0) continue;
+          if (warp == 0) {
+            uint8_t* dw = smem + RG::w_off + s * RG::w_bytes;
+            if (a.back) tma_3d_pair(dw, &map_w, n0, ks * kF8StageK, t.e, bar);
+            else tma_3d_pair(dw, &map_w, ks * kF8StageK, n0, t.e, bar);
+            continue;
+          }
+          uint8_t* da = smem + RG::a_off + s * RG::a_bytes + skip * kF8StageK;
+          auto copy = [&](int row, const CUtensorMap* map) {
+            if constexpr (PAIRS == 1) tma_3d_pair(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar);
+            else tma_3d_pairs(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar, cta.shared);
+          };
+          if (half == BN / 2) copy(0, &map_a);
+          else
+            for (int b = 0; b < part; b += kF8PairBox) copy(b, &map_part);
+        }
       }
-    }
-    if (!ok) {
-      // The copies in flight must land before the pair leaves: those of both CTAs
-      // count on the first one's barriers; the second one's own never complete, so
-      // it waits for as long as the limit says.
-      const WaitCfg drain{a.wait.status, kF8DrainPolls};
-      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
+      // (both CTAs' copies count on the first one's barriers; the second one's own
+      // never complete, so it waits for as long as the limit says)
+      if (!ok) drain_ring<S>(full, it, a.wait.status, kF8DrainPolls);
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
@@ -521,9 +525,13 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     const uint64_t wstep = a.back ? (32 * 128) >> 4 : 32 >> 4;   // 32 reduction values on: 32 rows, or 32 bytes
     const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem + RG::a_off));
     const int tail = (inner - (ksteps - 1) * kF8StageK + 31) / 32;   // MMAs of the last stage
-    int st = 0, tc = 0, g = 0;
-    uint32_t ph = 0, gph = 0;
+    RingAt<S> at;
+    RingAt<G> sf;
+    int tc = 0;
     bool ok = true;
+    // whether the next stage is there, asked before the MMAs of the one before
+    // are issued
+    bool there = mbar_test_wait(&full[0], 0);
     for (int tile = first; tile < real && ok; tile += stride, ++tc) {
       int n0;
       const RowTile t = tile_of(tile, n0);
@@ -531,27 +539,26 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       const int ab = tc & 1;
       ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       for (int ks = 0; ks < ksteps && ok; ++ks) {
-        if ((ks & 3) == 0) {
-          ok = warp_spin_cluster(&sf_full[g], gph, a.wait, abort_flag);
+        const int id = ks & 3, s = at.s;
+        if (id == 0) {
+          ok = warp_spin_cluster(&sf_full[sf.s], sf.ph, a.wait, abort_flag);
           if (!ok) break;
         }
-        ok = warp_spin_cluster(&full[st], ph, a.wait, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t id = (uint32_t)(ks & 3), sf = tmem + RG::sf_col0 + g * RG::sf_cols;
-        f8_pair_stage_elect(tmem + ab * BN, wdesc0 + (uint64_t)((st * RG::w_bytes) >> 4), wstep, adesc0 + (uint64_t)((st * RG::a_bytes) >> 4),
-                            idesc0 | id << 29 | id << 4, sf, sf + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[st],
-                            (uint16_t)((1 << 2 * PAIRS) - 1));
-        if (++st == S) {
-          st = 0;
-          ph ^= 1u;
+        if (!__shfl_sync(0xffffffffu, there, 0)) {
+          ok = spin_or_abort(&full[s], at.ph, a.wait, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
-        if ((ks & 3) == 3 || ks + 1 == ksteps) {
-          tc_commit_pair_elect(&sf_empty[g], cta.here);
-          if (++g == G) {
-            g = 0;
-            gph ^= 1u;
-          }
+        at.step();
+        there = mbar_test_wait(&full[at.s], at.ph);
+        tc_fence_after();
+        const uint32_t sft = tmem + RG::sf_col0 + sf.s * RG::sf_cols;
+        f8_pair_stage_elect(tmem + ab * BN, wdesc0 + (uint32_t)((s * RG::w_bytes) >> 4), wstep, adesc0 + (uint32_t)((s * RG::a_bytes) >> 4),
+                            idesc0 | (uint32_t)id << 29 | (uint32_t)id << 4, sft, sft + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail,
+                            &empty[s], (uint16_t)((1 << 2 * PAIRS) - 1));
+        if (id == 3 || ks + 1 == ksteps) {
+          tc_commit_pair_elect(&sf_empty[sf.s], cta.here);
+          sf.step();
         }
       }
       if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
@@ -564,8 +571,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     // Row 32 j + lane's word of A goes to column 4 + j of this quarter's lane; the
     // weight block's word, the same for every row, to columns 0 to 3.
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    int g = 0;
-    uint32_t gph = 0;
+    RingAt<G> sf;
     bool ok = true;
     for (int tile = first; tile < real && ok; tile += stride) {
       int n0;
@@ -574,34 +580,33 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       const int ob = min(n0, width - 1) / kTileM;
       const uint8_t* w0 = a.w_scales + (size_t)t.e * nbn * nbk + (a.back ? ob : (size_t)ob * nbk);
       const size_t wstep = a.back ? nbk : 1;
-      uint32_t word[8], w = 0;
+      uint32_t next[8], next_w = 0;   // on their way while the ones before are written
       auto fetch = [&](int ks) {
         const uint8_t* src = a.a_scales + ((size_t)(ks >> 2) * a.R + t.start + lane) * 4;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) word[j] = 32 * j < left ? *reinterpret_cast<const uint32_t*>(src + j * 128) : 0u;
-        w = lane < 4 && ks + lane < ksteps ? (uint32_t)w0[(ks + lane) * wstep] << (8 * lane) : 0u;
+        for (int j = 0; j < 8; ++j) next[j] = 32 * j < left ? *reinterpret_cast<const uint32_t*>(src + j * 128) : 0u;
+        next_w = lane < 4 && ks + lane < ksteps ? (uint32_t)w0[(ks + lane) * wstep] << (8 * lane) : 0u;
       };
       fetch(0);
-      for (int ks = 0; ks < ksteps; ks += 4) {
+      for (int ks = 0; ks < ksteps; ks += 4, sf.step()) {
+        uint32_t word[8], w = next_w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) word[j] = next[j];
+        if (ks + 4 < ksteps) fetch(ks + 4);
         w |= __shfl_xor_sync(0xffffffffu, w, 1);
         w |= __shfl_xor_sync(0xffffffffu, w, 2);
         const uint32_t every = __shfl_sync(0xffffffffu, w, 0);
-        ok = wait_or_abort(&sf_empty[g], gph ^ 1u, a.wait, abort_flag);
+        ok = wait_or_abort(&sf_empty[sf.s], sf.ph ^ 1u, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = tmem + lanes + RG::sf_col0 + g * RG::sf_cols;
+        const uint32_t at = tmem + lanes + RG::sf_col0 + sf.s * RG::sf_cols;
         tmem_store_x4(at, every);
         tmem_store_x8(at + 4, word);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cluster_bar_arrive(bar_of(&sf_full[g], cta.lead));
-        if (ks + 4 < ksteps) fetch(ks + 4);
-        if (++g == G) {
-          g = 0;
-          gph ^= 1u;
-        }
+        if (lane == 0) cluster_bar_arrive(bar_of(&sf_full[sf.s], cta.lead));
       }
     }
   } else if (warp >= 8) {

@@ -90,22 +90,44 @@ __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
 }
 // A copy to this CTA's shared memory that completes on a barrier of its pair; to
 // the same place of every CTA of a mask, each completing on the barrier of the CTA
-// of its pair that is in the place of the barrier's own.
-__device__ __forceinline__ void tma_3d_pair_elect(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+// of its pair that is in the place of the barrier's own.  By one thread.
+__device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_3d_pairs_elect(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint16_t mask) {
+__device__ __forceinline__ void tma_3d_pairs(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint16_t mask) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(smem_u32(dst)),
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
       : "memory");
+}
+// A producer's wait, by one thread: a poll that does not park first (a parked one
+// takes some 230 cycles where the phase is complete already).
+__device__ __forceinline__ bool poll_or_wait(uint64_t* bar, uint32_t parity, const WaitCfg& w, volatile int* abort_flag) {
+  return mbar_test_wait(bar, parity) || wait_or_abort(bar, parity, w, abort_flag);
+}
+// A slot of a ring of S and the parity of its phase.
+template <int S>
+struct RingAt {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == S) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+// After a wait that ran out: the copies in flight must land before the CTA leaves.
+// Waits for the barriers of the last S of `it` stages, with a limit.
+template <int S>
+__device__ __forceinline__ void drain_ring(uint64_t* full, int it, int* status, long long polls) {
+  const WaitCfg drain{status, polls};
+  for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
 }
 // spin_or_abort for a phase that the other CTA's threads arrive on too: one
 // answer for the whole warp.

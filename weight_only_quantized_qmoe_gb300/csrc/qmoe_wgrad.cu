@@ -373,54 +373,52 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   // columns of dy of each CTA: half of the tile's, in whole sixteens
   auto half_of = [&](const WgTile& t) { return ((min(kWgBN, a.N - t.n0) + 31) & ~31) / 2; };
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
-    int it = 0;
-    bool ok = true;
-    for (int tile = first; tile < total && ok; tile += stride) {
-      const WgTile t = tile_of(tile);
-      const int half = half_of(t), panels = (half + kWgPanel - 1) / kWgPanel, col0 = t.n0 + rank * half;
-      const uint32_t bytes = (uint32_t)((RG::panels + panels) * kWgPanelBytes);
-      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
-        const int s = it % S;
-        ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const bool zeros = t.hi - r < kWgRows && ((t.hi - r) & 15);
-        uint32_t bar = bar_of(&full[s], cta.lead);
-        if (rank == 0) {
-          mbar_arrive_expect_tx_elect(&full[s], zeros ? bytes : 2 * bytes);
-          if (!zeros && lane == 0) mbar_arrive(&full[s]);
-          __syncwarp();
-        } else if (zeros) {
-          mbar_arrive_expect_tx_elect(&tail[s], bytes);
-          bar = bar_of(&tail[s], cta.lead + 1);
-        }
-        // Test hook: the first stage's barrier is armed, its copies are never issued.
-        if (args.inject_stall && it == 0) continue;
-        uint8_t *dx = smem + RG::x_off + s * RG::x_bytes, *ddy = smem + RG::dy_off + s * RG::dy_bytes;
+  if (warp == 0 || warp == 2) {
+    // ---------------- producers: x, and dy ----------------
+    if (lane == 0) {   // one thread each, as in the products' kernel
+      RingAt<S> at;
+      int it = 0;
+      bool ok = true;
+      for (int tile = first; tile < total && ok; tile += stride) {
+        const WgTile t = tile_of(tile);
+        const int half = half_of(t), panels = (half + kWgPanel - 1) / kWgPanel, col0 = t.n0 + rank * half;
+        const uint32_t bytes = (uint32_t)((RG::panels + panels) * kWgPanelBytes);
+        for (int r = t.lo; r < t.hi; r += kWgRows, ++it, at.step()) {
+          const int s = at.s;
+          ok = poll_or_wait(&empty[s], at.ph ^ 1u, a.wait, abort_flag);
+          if (!ok) break;
+          const bool zeros = t.hi - r < kWgRows && ((t.hi - r) & 15), own = rank == 1 && zeros;
+          const uint32_t bar = own ? bar_of(&tail[s], cta.lead + 1) : bar_of(&full[s], cta.lead);
+          if (warp == 0 && rank == 0) {
+            mbar_arrive_expect_tx(&full[s], zeros ? bytes : 2 * bytes);
+            if (!zeros) mbar_arrive(&full[s]);
+          } else if (warp == 0 && own) {
+            mbar_arrive_expect_tx(&tail[s], bytes);
+          }
+          // Test hook: the first stage's barrier is armed, its copies are never issued.
+          if (args.inject_stall && it == 0) continue;
+          uint8_t *dx = smem + RG::x_off + s * RG::x_bytes, *ddy = smem + RG::dy_off + s * RG::dy_bytes;
 #pragma unroll
-        for (int p = 0; p < RG::panels; ++p) {
-          tma_3d_pair_elect(dx + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, bar);
-          if (p >= panels) continue;
-          if constexpr (PAIRS == 1) tma_3d_pair_elect(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar);
-          else if (p == cta.p) tma_3d_pairs_elect(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar, cta.shared);
+          for (int p = 0; p < RG::panels; ++p) {
+            if (warp == 0) tma_3d_pair(dx + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, bar);
+            else if (p >= panels) continue;
+            else if constexpr (PAIRS == 1) tma_3d_pair(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar);
+            else if (p == cta.p) tma_3d_pairs(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar, cta.shared);
+          }
         }
       }
-    }
-    if (!ok) {
-      // The copies in flight must land before the pair leaves: those of both CTAs
-      // count on the first one's barriers; the second one's own never complete, so
-      // it waits for as long as the limit says.
-      const WaitCfg drain{a.wait.status, kWgDrainPolls};
-      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
+      // (both CTAs' copies count on the first one's barriers; the second one's own
+      // never complete, so it waits for as long as the limit says)
+      if (!ok) drain_ring<S>(full, it, a.wait.status, kWgDrainPolls);
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
     const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), kWgPanelBytes);
     const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), kWgPanelBytes);
-    int it = 0, tc = 0;
+    RingAt<S> at;
+    int tc = 0;
     bool ok = true;
+    bool there = mbar_test_wait(&full[0], 0);   // the next stage, asked ahead as in the products' kernel
     for (int tile = first; tile < total && ok; tile += stride) {
       const WgTile t = tile_of(tile);
       if (t.lo >= t.hi) continue;
@@ -429,19 +427,24 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const int ab = tc & 1;
       ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       if (!ok) break;
-      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
-        const int s = it % S;
-        ok = warp_spin_cluster(&full[s], (it / S) & 1, a.wait, abort_flag);
-        if (!ok) break;
-        const int rows = min(kWgRows, t.hi - r);
+      for (int r = t.lo; r < t.hi; r += kWgRows) {
+        const int s = at.s, rows = min(kWgRows, t.hi - r);
         if (rows & 15) {
+          ok = warp_spin_cluster(&full[s], at.ph, a.wait, abort_flag);   // the other CTA's zeros too
+          if (!ok) break;
           zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::panels, rows);
           zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half + kWgPanel - 1) / kWgPanel, rows);
           fence_proxy_async_smem();
           __syncwarp();
+        } else if (!__shfl_sync(0xffffffffu, there, 0)) {
+          ok = spin_or_abort(&full[s], at.ph, a.wait, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
+        at.step();
+        there = mbar_test_wait(&full[at.s], at.ph);
         tc_fence_after();
-        wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4),
+        wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint32_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint32_t)((s * RG::dy_bytes) >> 4),
                           idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s], (uint16_t)((1 << 2 * PAIRS) - 1));
       }
       if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
