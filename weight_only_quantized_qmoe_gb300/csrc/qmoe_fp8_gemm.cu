@@ -384,7 +384,11 @@ struct F8PairRing {
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
 };
-constexpr int kF8PairBox = 8;                                     // rows of A a copy where a tile is not full
+// Copies of A's rows of every size that a tile has, so that a stage is one copy: a
+// part of 16 i rows of a pair's half, or of 8 i of two pairs' quarter, i = 1 .. 7.
+struct F8RowMaps {
+  CUtensorMap of[F8PairRing::bn / 32];
+};
 constexpr int kF8PairThreads = 256 + 32 * kEpiWarps;
 
 // One stage: up to four K = 32 MMAs of the pair and the commit that frees it.
@@ -416,8 +420,7 @@ __device__ __forceinline__ void tmem_store_x8(uint32_t taddr, const uint32_t (&v
 
 template <int OUT, int PAIRS>
 __global__ void __launch_bounds__(kF8PairThreads, 1)
-    fp8_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_part,
-                           const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
+    fp8_matmul_pair_kernel(const __grid_constant__ F8RowMaps map_a, const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
   using RG = F8PairRing;
   using T = typename ElemT<OUT>::t;
   constexpr int S = RG::stages, G = RG::sf_groups, BN = RG::bn;
@@ -506,13 +509,9 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
             continue;
           }
           uint8_t* da = smem + RG::a_off + s * RG::a_bytes + skip * kF8StageK;
-          auto copy = [&](int row, const CUtensorMap* map) {
-            if constexpr (PAIRS == 1) tma_3d_pair(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar);
-            else tma_3d_pairs(da + row * kF8StageK, map, ks * kF8StageK, start + row, 0, bar, cta.shared);
-          };
-          if (half == BN / 2) copy(0, &map_a);
-          else
-            for (int b = 0; b < part; b += kF8PairBox) copy(b, &map_part);
+          const CUtensorMap* map = &map_a.of[half / 16 - 1];
+          if constexpr (PAIRS == 1) tma_3d_pair(da, map, ks * kF8StageK, start, 0, bar);
+          else tma_3d_pairs(da, map, ks * kF8StageK, start, 0, bar, cta.shared);
         }
       }
       // (both CTAs' copies count on the first one's barriers; the second one's own
@@ -531,17 +530,18 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     bool ok = true;
     // whether the next stage is there, asked before the MMAs of the one before
     // are issued
-    bool there = mbar_test_wait(&full[0], 0);
+    bool there = mbar_test_wait(&full[0], 0), sf_there = false;
     for (int tile = first; tile < real && ok; tile += stride, ++tc) {
       int n0;
       const RowTile t = tile_of(tile, n0);
       const uint32_t idesc0 = idesc_mxf8(2 * kTileM, 2 * half_of(t), a.back);
       const int ab = tc & 1;
-      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      ok = warp_spin_cluster<false>(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       for (int ks = 0; ks < ksteps && ok; ++ks) {
         const int id = ks & 3, s = at.s;
         if (id == 0) {
-          ok = warp_spin_cluster(&sf_full[sf.s], sf.ph, a.wait, abort_flag);
+          // (asked for ahead as well)
+          ok = __shfl_sync(0xffffffffu, sf_there, 0) || warp_spin_cluster<false>(&sf_full[sf.s], sf.ph, a.wait, abort_flag);
           if (!ok) break;
         }
         if (!__shfl_sync(0xffffffffu, there, 0)) {
@@ -559,6 +559,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         if (id == 3 || ks + 1 == ksteps) {
           tc_commit_pair_elect(&sf_empty[sf.s], cta.here);
           sf.step();
+          sf_there = cluster_test_wait<false>(&sf_full[sf.s], sf.ph);
         }
       }
       if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cluster_bar_arrive(bar_of(&sf_full[sf.s], cta.lead));
+        if (lane == 0) cluster_bar_arrive<false>(bar_of(&sf_full[sf.s], cta.lead));
       }
     }
   } else if (warp >= 8) {
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * BN, out, a.ld_out, t.rows, in, half);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive(bar_of(&acc_empty[ab], cta.lead));
+      if (lane == 0) cluster_bar_arrive<false>(bar_of(&acc_empty[ab], cta.lead));
       ++tc;
     }
   }
@@ -655,23 +656,27 @@ cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split
   const int64_t inner = a.back ? a.N : a.K, pitch = fp8_pitch(inner);
   const bool pairs = bn == F8PairRing::bn;
   const int cluster = (a.back ? a.K : a.N) > 2 * kTileM ? 4 : 2;   // two pairs, if both have weight rows
-  CUtensorMap map_a, map_part, map_w;
+  CUtensorMap map_w;
   constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? bn / cluster : bn) ||
-      !encode_tiles(&map_part, u8, 1, a.a_codes, inner, a.R, 1, pitch, pairs ? kF8PairBox : kF8BoxRows) ||
-      !encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM))
-    return cudaErrorInvalidValue;
+  if (!encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM)) return cudaErrorInvalidValue;
   constexpr int slack = 1024;   // of the alignment
   if (pairs) {
+    F8RowMaps map_a;
+    for (int i = 0; i < F8PairRing::bn / 32; ++i)
+      if (!encode_tiles(&map_a.of[i], u8, 1, a.a_codes, inner, a.R, 1, pitch, 32 / cluster * (i + 1))) return cudaErrorInvalidValue;
     auto run = [&](auto kern) {
       int64_t ctas;
       constexpr int smem = F8PairRing::total + slack;
       const cudaError_t e = cluster_ctas(kern, tiles, cluster, kF8PairThreads, smem, ctas);
       if (e != cudaSuccess) return e;
-      return launch_tiles(kern, ctas, cluster, kF8PairThreads, smem, s, map_a, map_part, map_w, args);
+      return launch_tiles(kern, ctas, cluster, kF8PairThreads, smem, s, map_a, map_w, args);
     };
     return cluster == 4 ? run(fp8_matmul_pair_kernel<OUT, 2>) : run(fp8_matmul_pair_kernel<OUT, 1>);
   }
+  CUtensorMap map_a, map_part;
+  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, bn) ||
+      !encode_tiles(&map_part, u8, 1, a.a_codes, inner, a.R, 1, pitch, kF8BoxRows))
+    return cudaErrorInvalidValue;
   if (split > 1)
     return launch_tiles(fp8_matmul_kernel<32, OUT, true>, tiles * split, split, kF8Threads, F8Ring<32>::total + slack, s, map_a, map_part,
                         map_w, args);

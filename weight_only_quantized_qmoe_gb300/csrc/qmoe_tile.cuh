@@ -85,8 +85,35 @@ __device__ __forceinline__ uint32_t bar_of(uint64_t* bar, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(rank));
   return at;
 }
+// Arrivals from other CTAs of the cluster.  Where what they stand for is tensor
+// memory read or written, the tcgen05 fences on either side order it and the
+// arrival and the wait are relaxed; shared memory written by other threads needs
+// release and acquire, which cost some 700 cycles each at this scope.
+template <bool MEMORY>
 __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  if constexpr (MEMORY) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  else asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <bool MEMORY>
+__device__ __forceinline__ bool cluster_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  if constexpr (MEMORY)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  return done != 0;
 }
 // A copy to this CTA's shared memory that completes on a barrier of its pair; to
 // the same place of every CTA of a mask, each completing on the barrier of the CTA
@@ -129,31 +156,17 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int it, int* status, 
   const WaitCfg drain{status, polls};
   for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
 }
-// spin_or_abort for a phase that the other CTA's threads arrive on too: one
-// answer for the whole warp.
+// spin_or_abort for such a phase: one answer for the whole warp.
+template <bool MEMORY>
 __device__ __forceinline__ bool warp_spin_cluster(uint64_t* bar, uint32_t parity, const WaitCfg& w, volatile int* abort_flag) {
   const long long limit = w.limit * 64;
-  bool ok = false;
   for (long long i = 0; i < limit; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (__shfl_sync(0xffffffffu, done, 0)) {
-      ok = true;
-      break;
-    }
+    if (__shfl_sync(0xffffffffu, cluster_test_wait<MEMORY>(bar, parity), 0)) return true;
     if ((i & 255) == 255 && __shfl_sync(0xffffffffu, *abort_flag, 0)) return false;
   }
-  if (!ok) {
-    atomicExch(w.status, DEV_TIMEOUT);
-    *abort_flag = 1;
-  }
-  return ok;
+  atomicExch(w.status, DEV_TIMEOUT);
+  *abort_flag = 1;
+  return false;
 }
 
 // Shared-memory matrix descriptor of an operand that lies along M or N (the

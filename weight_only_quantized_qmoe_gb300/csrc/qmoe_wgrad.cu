@@ -425,12 +425,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const int half = half_of(t);
       const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, 2 * kTileM, 2 * half);
       const int ab = tc & 1;
-      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      ok = warp_spin_cluster<false>(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       if (!ok) break;
       for (int r = t.lo; r < t.hi; r += kWgRows) {
         const int s = at.s, rows = min(kWgRows, t.hi - r);
         if (rows & 15) {
-          ok = warp_spin_cluster(&full[s], at.ph, a.wait, abort_flag);   // the other CTA's zeros too
+          ok = warp_spin_cluster<true>(&full[s], at.ph, a.wait, abort_flag);   // the other CTA's zeros too
           if (!ok) break;
           zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::panels, rows);
           zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half + kWgPanel - 1) / kWgPanel, rows);
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half_of(t) + kWgPanel - 1) / kWgPanel, rows);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive(bar_of(&full[s], cta.lead));
+      if (lane == 0) cluster_bar_arrive<true>(bar_of(&full[s], cta.lead));
     }
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN, out, a.K, n, in, half);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive(bar_of(&acc_empty[ab], cta.lead));
+      if (lane == 0) cluster_bar_arrive<false>(bar_of(&acc_empty[ab], cta.lead));
       ++tc;
     }
   }
