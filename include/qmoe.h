@@ -595,11 +595,12 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_
  *   dy_dev  dtype [rows, n], x_dev  dtype [rows, k]; QMOE_F16 or QMOE_BF16
  *           (QMOE_F32: UNSUPPORTED)
  *   dw_dev  out_dtype [experts, n, k]
- * qmoe_weight_grad_workspace: bytes of workspace (16-byte aligned) for operands
- * with these addresses and strides; 0 where rows start on 16-byte boundaries.
+ * qmoe_weight_grad_workspace: bytes of workspace (128-byte aligned) for operands
+ * with these addresses and strides: 512 bytes an expert where there are many
+ * tiles, and a copy of an operand whose rows do not start on 16-byte boundaries.
  */
-size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int64_t n,
-                                  int64_t k);
+size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int experts,
+                                  int64_t n, int64_t k);
 qmoe_status qmoe_weight_grad(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const int32_t* offsets_dev,
                              int64_t rows, int experts, int64_t n, int64_t k, int dtype, int out_dtype, void* dw_dev,
                              void* workspace_dev, size_t workspace_bytes, void* stream);

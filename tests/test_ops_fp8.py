@@ -206,7 +206,8 @@ def test_scales_of_every_block(ops, R, N, K, transpose):
 # (T, E, k, N, K, drop): empty experts, one expert with everything, dropped
 # rows, many experts with few rows, several row tiles an expert
 GROUPED = [(1, 4, 1, 64, 64, 0.0), (32, 128, 8, 96, 256, 0.0), (50, 3, 2, 200, 160, 0.2), (700, 4, 2, 300, 288, 0.1),
-           (33, 1024, 3, 40, 64, 0.0), (9, 2, 1, 128, 512, 1.0), (2000, 5, 2, 2000, 64, 0.05), (2, 8, 2, 640, 2000, 0.0)]
+           (33, 1024, 3, 40, 64, 0.0), (9, 2, 1, 128, 512, 1.0), (2000, 5, 2, 2000, 64, 0.05), (2, 8, 2, 640, 2000, 0.0),
+           (1100, 6, 2, 1000, 700, 0.1), (3000, 3, 1, 400, 1300, 0.0), (900, 300, 32, 130, 1200, 0.0)]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,drop", GROUPED)
@@ -228,24 +229,24 @@ def test_grouped_product(ops, T, E, k, N, K, drop, dtype, transpose):
 
 
 @pytest.mark.parametrize("transpose", [False, True])
-@pytest.mark.parametrize("R", [200, 20])
-def test_a_nan_stays_in_its_row_and_block(ops, transpose, R):
+@pytest.mark.parametrize("R,N,K", [(200, 250, 300), (20, 250, 300), (700, 3000, 2500)])
+def test_a_nan_stays_in_its_row_and_block(ops, transpose, R, N, K):
     g = torch.Generator().manual_seed(9)
-    N, K = 250, 300
     x, m = torch.randn((R, N if transpose else K), generator=g).cuda(), torch.randn((N, K), generator=g).cuda()
     clean = ops.fp8_matmul(ops.fp8_quantize(x), ops.fp8_quantize(m, square=True), transpose=transpose, out_dtype=torch.float32)
     x[17, 5] = float("nan")
-    m[201, 299] = float("inf")      # the block of rows 128 .. 249, columns 256 .. 299
+    m[201, 299] = float("inf")      # the block of rows 128 .. 255, columns 256 .. 383
     got = ops.fp8_matmul(ops.fp8_quantize(x), ops.fp8_quantize(m, square=True), transpose=transpose, out_dtype=torch.float32)
-    bad = slice(256, 300) if transpose else slice(128, 250)
+    bad = slice(256, min(K, 384)) if transpose else slice(128, min(N, 256))
     assert torch.isnan(got[17]).all() and torch.isnan(got[:, bad]).all()
     rows = torch.arange(R) != 17
-    assert torch.equal(got[rows][:, :bad.start], clean[rows][:, :bad.start])
+    for cols in (slice(0, bad.start), slice(bad.stop, None)):
+        assert torch.equal(got[rows][:, cols], clean[rows][:, cols])
 
 
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("K", [1, 65, 130, 257, 513, 1111, 2880])
-@pytest.mark.parametrize("R,N", [(3, 40), (300, 400)])
+@pytest.mark.parametrize("R,N", [(3, 40), (300, 400), (1500, 2500)])
 def test_padding_is_not_used(ops, R, N, K, transpose):
     # NaN codes past the columns and past the rows, NaN scales past the last block
     g = torch.Generator().manual_seed(R + K)
@@ -268,18 +269,18 @@ def test_padding_is_not_used(ops, R, N, K, transpose):
 
 
 @pytest.mark.parametrize("transpose", [False, True])
-def test_experts_do_not_read_one_another(ops, transpose):
+@pytest.mark.parametrize("n,N,K", [(30, 200, 330), (200, 2500, 2330)])
+def test_experts_do_not_read_one_another(ops, transpose, n, N, K):
     # every expert but one holds NaN codes; the rows of that one are as alone
     g = torch.Generator().manual_seed(3)
-    N, K = 200, 330
     w = operand(ops, g, (3, N, K), 1.0, True)
     codes = w.codes.clone()
     codes[0], codes[2] = 0x7f, 0x7f
-    a = operand(ops, g, (90, N if transpose else K))
-    plan = ops.expert_sort(torch.arange(3, dtype=torch.int32, device="cuda").repeat_interleave(30).unsqueeze(1), 3)
+    a = operand(ops, g, (3 * n, N if transpose else K))
+    plan = ops.expert_sort(torch.arange(3, dtype=torch.int32, device="cuda").repeat_interleave(n).unsqueeze(1), 3)
     want = ops.fp8_matmul(a, w, plan=plan, transpose=transpose, out_dtype=torch.float32)
     got = ops.fp8_matmul(a, ops.FP8Tensor(codes, w.scales, K, True), plan=plan, transpose=transpose, out_dtype=torch.float32)
-    assert torch.equal(got[30:60], want[30:60]) and torch.isnan(got[:30]).all() and torch.isnan(got[60:]).all()
+    assert torch.equal(got[n:2 * n], want[n:2 * n]) and torch.isnan(got[:n]).all() and torch.isnan(got[2 * n:]).all()
 
 
 def test_no_rows(ops):
@@ -310,7 +311,7 @@ def test_on_another_stream_and_in_a_graph(ops, R):
     assert torch.equal(out, ops.fp8_matmul(ops.fp8_quantize(x), w))
 
 
-@pytest.mark.parametrize("R", [16, 400])
+@pytest.mark.parametrize("R", [16, 128, 400])
 def test_a_wait_that_runs_out_is_reported(ops, R):
     # host-injected: the first copy's barrier is armed and its copy never
     # issued, so the bounded waits on it end by themselves

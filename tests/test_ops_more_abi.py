@@ -68,14 +68,15 @@ def test_weight_gradient():
         return b.qmoe_weight_grad(dy, ldy, x, ldx, offsets, rows, E, n, k, dt, odt, dw, work, nbytes, None)
     for kw in (dict(dy=0), dict(x=0), dict(dw=0), dict(ldy=15), dict(ldx=31), dict(offsets=0), dict(rows=-1), dict(E=0), dict(n=0), dict(k=0),
                dict(dt=4), dict(odt=3), dict(odt=-1), dict(ldx=33), dict(ldx=33, work=P, nbytes=8), dict(dy=P + 2), dict(dy=P + 1, work=P, nbytes=1 << 20),
-               dict(ldx=33, work=P + 8, nbytes=1 << 20), dict(offsets=P + 1), dict(rows=2 ** 31 - 256), dict(n=2 ** 30, ldy=2 ** 30)):
+               dict(ldx=33, work=P + 64, nbytes=1 << 20), dict(offsets=P + 1), dict(rows=2 ** 31 - 256), dict(n=2 ** 30, ldy=2 ** 30)):
         refused(call(**kw))
     refused(call(E=1025), b.QMOE_ERR_UNSUPPORTED, "1024")
     refused(call(dt=b.QMOE_F32), b.QMOE_ERR_UNSUPPORTED, "16-bit")
     need = b.qmoe_weight_grad_workspace
-    assert need(P, 16, P, 32, 8, 16, 32) == 0
-    assert need(P + 2, 16, P, 32, 8, 16, 32) == 8 * 16 * 2 and need(P, 16, P, 33, 8, 16, 31) == 8 * 32 * 2
-    assert need(P, 17, P + 8, 32, 8, 16, 30) == 8 * (16 + 32) * 2 and need(P, 17, P, 33, 0, 16, 32) == 0
+    assert need(P, 16, P, 32, 8, 2, 16, 32) == 0 and need(P, 2048, P, 2048, 8, 1, 2048, 2048) == 0
+    assert need(P + 2, 16, P, 32, 8, 1, 16, 32) == 8 * 16 * 2 and need(P, 16, P, 33, 8, 1, 16, 31) == 8 * 32 * 2
+    assert need(P, 17, P + 8, 32, 8, 1, 16, 30) == 8 * (16 + 32) * 2 and need(P, 17, P, 33, 0, 1, 16, 32) == 0
+    assert need(P, 4096, P, 4096, 8, 16, 4096, 4096) == 16 * 512 and need(P, 17, P, 33, 8, 0, 16, 32) == 0
 
 
 NEW = ["qmoe_choice.cu", "qmoe_fp8.cu", "qmoe_fp8_gemm.cu", "qmoe_wgrad.cu", "qmoe_tile.cuh", "qmoe_tma.cuh"]

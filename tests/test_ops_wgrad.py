@@ -50,7 +50,9 @@ def test_dense(ops, R, N, K, dtype):
 
 # (T, E, k, N, K, drop)
 GROUPED = [(1, 4, 1, 64, 64, 0.0), (32, 128, 8, 96, 256, 0.0), (50, 3, 2, 200, 160, 0.2), (700, 4, 2, 300, 288, 0.1),
-           (33, 1024, 3, 40, 64, 0.0), (9, 2, 1, 128, 512, 1.0), (2000, 5, 2, 64, 64, 0.05), (301, 7, 3, 129, 77, 0.0)]
+           (33, 1024, 3, 40, 64, 0.0), (9, 2, 1, 128, 512, 1.0), (2000, 5, 2, 64, 64, 0.05), (301, 7, 3, 129, 77, 0.0),
+           # many tiles: pairs of CTAs, with rows of every remainder of 64, no rows, odd widths
+           (300, 12, 3, 600, 700, 0.0), (500, 9, 2, 1000, 1111, 0.1), (1500, 40, 4, 264, 384, 0.0), (7, 3, 1, 4096, 2048, 0.0)]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,drop", GROUPED)
@@ -70,13 +72,14 @@ def test_grouped(ops, T, E, k, N, K, drop, dtype, out):
     assert torch.equal(ops.weight_grad(dy, x, plan=plan, out_dtype=DT[out]), got)
 
 
-def test_a_nan_stays_with_its_expert(ops):
+@pytest.mark.parametrize("N,K", [(140, 200), (2000, 1500)])
+def test_a_nan_stays_with_its_expert(ops, N, K):
     # rows of 3, 18, 64 and 5: tails beside rows that hold NaN
     ends = [0, 3, 21, 85, 90]
     ids = torch.repeat_interleave(torch.arange(4), torch.tensor([3, 18, 64, 5])).int().unsqueeze(1).cuda()
     plan = ops.expert_sort(ids, 4)
     g = torch.Generator().manual_seed(3)
-    dy, x = normal(g, 90, 140), normal(g, 90, 200)
+    dy, x = normal(g, 90, N), normal(g, 90, K)
     clean = ops.weight_grad(dy, x, plan=plan, out_dtype=torch.float32)
     for e in range(4):
         for t, bad in ((dy, float("nan")), (x, float("inf"))):
@@ -120,7 +123,7 @@ def test_no_rows(ops):
     assert d.shape == (3, 24, 24) and (d == 0).all()
 
 
-@pytest.mark.parametrize("R,N,K", [(300, 64, 64), (300, 4000, 4000)])
+@pytest.mark.parametrize("R,N,K", [(300, 64, 64), (5000, 64, 64), (300, 4000, 4000)])
 def test_a_wait_that_runs_out_is_reported(ops, R, N, K):
     # host-injected: the first copy's barrier is armed and its copy never issued
     from weight_only_quantized_qmoe_gb300 import binding

@@ -81,7 +81,7 @@ _SIGS = {
     "qmoe_fp8_quantize": (_i, [_p, _i64, _i64, _i64, _i, _i, _p, _p, _i, _i, _i64, _i, _p, _p, _p]),
     "qmoe_fp8_dequantize": (_i, [_p, _p, _i64, _i64, _i64, _i, _i, _p, _i64, _p]),
     "qmoe_fp8_matmul": (_i, [_p, _p, _i64, _p, _p, _p, _i, _i64, _i64, _i, _i, _p, _i64, _p]),
-    "qmoe_weight_grad_workspace": (_sz, [_p, _i64, _p, _i64, _i64, _i64, _i64]),
+    "qmoe_weight_grad_workspace": (_sz, [_p, _i64, _p, _i64, _i64, _i, _i64, _i64]),
     "qmoe_weight_grad": (_i, [_p, _i64, _p, _i64, _p, _i64, _i, _i64, _i64, _i, _i, _p, _p, _sz, _p]),
     "qmoe_block_norm": (_i, [_p, _i64, _p, _i64, _p, _i, _i64, _p, _p, _f, _f, _i64, _i64, _i, _p, _p, _p, _p, _p]),
     "qmoe_block_norm_grad_workspace": (_sz, [_i64, _i64, _i]),

@@ -360,8 +360,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 
 // ----------------------------------------------------------------------------
 // Pairs of CTAs, for many rows: tiles of 256 weight rows (back: columns) by up to
-// 224 rows of A, of which each CTA loads half; two pairs take neighbouring weight rows and share A's.
-// Scales do not pass through shared
+// 224 rows of A, of which each CTA loads half.  Scales do not pass through shared
 // memory: four warps a CTA, one for each quarter of the TMEM lanes, load the
 // words of 512 reduction values (all rows of A, this CTA's weight block) and
 // write them to TMEM, every quarter the same, and arrive on the first CTA's
@@ -384,8 +383,9 @@ struct F8PairRing {
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
 };
-// Copies of A's rows of every size that a tile has, so that a stage is one copy: a
-// part of 16 i rows of a pair's half, or of 8 i of two pairs' quarter, i = 1 .. 7.
+// Copies of A's rows of every size that a tile has, 16 to 112 rows a CTA, so that a
+// stage is one copy (with copies of 8 rows the tiles that are not full took twice
+// as long as the others: 32768 rows over 64 experts 210 us, now 172).
 struct F8RowMaps {
   CUtensorMap of[F8PairRing::bn / 32];
 };
@@ -393,7 +393,7 @@ constexpr int kF8PairThreads = 256 + 32 * kEpiWarps;
 
 // One stage: up to four K = 32 MMAs of the pair and the commit that frees it.
 __device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sfw,
-                                                    uint32_t sfa, uint32_t acc, int nk, uint64_t* empty, uint16_t mask) {
+                                                    uint32_t sfa, uint32_t acc, int nk, uint64_t* empty) {
   asm volatile(
       "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -407,7 +407,7 @@ __device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint
       "@q3 tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [%6], p1;\n\t}" ::"r"(d),
       "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sfw), "r"(sfa), "r"(acc), "r"(nk)
       : "memory");
-  tc_commit_pair_elect(empty, mask);
+  tc_commit_pair_elect(empty);
 }
 __device__ __forceinline__ void tmem_store_x4(uint32_t taddr, uint32_t v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%1,%1,%1};" ::"r"(taddr), "r"(v) : "memory");
@@ -418,7 +418,7 @@ __device__ __forceinline__ void tmem_store_x8(uint32_t taddr, const uint32_t (&v
                : "memory");
 }
 
-template <int OUT, int PAIRS>
+template <int OUT>
 __global__ void __launch_bounds__(kF8PairThreads, 1)
     fp8_matmul_pair_kernel(const __grid_constant__ F8RowMaps map_a, const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
   using RG = F8PairRing;
@@ -440,12 +440,11 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   int* row0 = tp + kSortMaxExperts + 2;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PairPlace cta = pair_place<PAIRS>();
-  const int rank = cta.h;
+  const int rank = pair_rank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], PAIRS);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < G; ++i) {
       mbar_init(&sf_full[i], 8);    // four warps of each CTA
@@ -465,17 +464,17 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   if (warp == 3) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // the other CTAs' barriers and TMEM are there
+  cluster_sync_all();   // the other CTA's barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int inner = a.back ? a.N : a.K, width = a.back ? a.K : a.N;   // of A's rows, of the output's
-  const int ntw = (width + 2 * PAIRS * kTileM - 1) / (2 * PAIRS * kTileM);
+  const int ntw = (width + 2 * kTileM - 1) / (2 * kTileM);
   const int total = tp[a.E + 1] * ntw, real = tp[a.E] * ntw;          // with and without the rows that have no route
   const int nbn = (a.N + kF8StageK - 1) / kF8StageK, nbk = (a.K + kF8StageK - 1) / kF8StageK;
-  const int ksteps = a.back ? nbn : nbk, first = blockIdx.x / (2 * PAIRS), stride = gridDim.x / (2 * PAIRS);
+  const int ksteps = a.back ? nbn : nbk, first = blockIdx.x / 2, stride = gridDim.x / 2;
   auto tile_of = [&](int tile, int& n0) {
     const int mt = tile / ntw;
-    n0 = (((tile - mt * ntw) * PAIRS + cta.p) * 2 + rank) * kTileM;
+    n0 = ((tile - mt * ntw) * 2 + rank) * kTileM;
     return row_tile(a.E, tp, row0, BN, mt);
   };
   // rows of A of each CTA: half of the tile's, in whole sixteens
@@ -492,13 +491,12 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       for (int tile = first; tile < real && ok; tile += stride) {
         int n0;
         const RowTile t = tile_of(tile, n0);
-        // this CTA's share of its half, and where it goes
-        const int half = half_of(t), part = half / PAIRS, skip = cta.p * part, start = t.start + rank * half + skip;
+        const int half = half_of(t);
         for (int ks = 0; ks < ksteps; ++ks, ++it, at.step()) {
           const int s = at.s;
           ok = poll_or_wait(&empty[s], at.ph ^ 1u, a.wait, abort_flag);
           if (!ok) break;
-          const uint32_t bar = bar_of(&full[s], cta.lead);
+          const uint32_t bar = first_cta_bar(&full[s]);
           if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * (half * kF8StageK + RG::w_bytes)));
           // Test hook: the first stage's barrier is armed, its copies are never issued.
           if (args.inject_stall && it == 0) continue;
@@ -508,10 +506,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
             else tma_3d_pair(dw, &map_w, ks * kF8StageK, n0, t.e, bar);
             continue;
           }
-          uint8_t* da = smem + RG::a_off + s * RG::a_bytes + skip * kF8StageK;
-          const CUtensorMap* map = &map_a.of[half / 16 - 1];
-          if constexpr (PAIRS == 1) tma_3d_pair(da, map, ks * kF8StageK, start, 0, bar);
-          else tma_3d_pairs(da, map, ks * kF8StageK, start, 0, bar, cta.shared);
+          tma_3d_pair(smem + RG::a_off + s * RG::a_bytes, &map_a.of[half / 16 - 1], ks * kF8StageK, t.start + rank * half, 0, bar);
         }
       }
       // (both CTAs' copies count on the first one's barriers; the second one's own
@@ -536,12 +531,12 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       const RowTile t = tile_of(tile, n0);
       const uint32_t idesc0 = idesc_mxf8(2 * kTileM, 2 * half_of(t), a.back);
       const int ab = tc & 1;
-      ok = warp_spin_cluster<false>(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       for (int ks = 0; ks < ksteps && ok; ++ks) {
         const int id = ks & 3, s = at.s;
         if (id == 0) {
           // (asked for ahead as well)
-          ok = __shfl_sync(0xffffffffu, sf_there, 0) || warp_spin_cluster<false>(&sf_full[sf.s], sf.ph, a.wait, abort_flag);
+          ok = __shfl_sync(0xffffffffu, sf_there, 0) || warp_spin_cluster(&sf_full[sf.s], sf.ph, a.wait, abort_flag);
           if (!ok) break;
         }
         if (!__shfl_sync(0xffffffffu, there, 0)) {
@@ -555,14 +550,14 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         const uint32_t sft = tmem + RG::sf_col0 + sf.s * RG::sf_cols;
         f8_pair_stage_elect(tmem + ab * BN, wdesc0 + (uint32_t)((s * RG::w_bytes) >> 4), wstep, adesc0 + (uint32_t)((s * RG::a_bytes) >> 4),
                             idesc0 | (uint32_t)id << 29 | (uint32_t)id << 4, sft, sft + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail,
-                            &empty[s], (uint16_t)((1 << 2 * PAIRS) - 1));
+                            &empty[s]);
         if (id == 3 || ks + 1 == ksteps) {
-          tc_commit_pair_elect(&sf_empty[sf.s], cta.here);
+          tc_commit_pair_elect(&sf_empty[sf.s]);
           sf.step();
-          sf_there = cluster_test_wait<false>(&sf_full[sf.s], sf.ph);
+          sf_there = cluster_test_wait(&sf_full[sf.s], sf.ph);
         }
       }
-      if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
+      if (ok) tc_commit_pair_elect(&acc_full[ab]);
     }
     tc_commit_pair_here_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -607,7 +602,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cluster_bar_arrive<false>(bar_of(&sf_full[sf.s], cta.lead));
+        if (lane == 0) cluster_bar_arrive(first_cta_bar(&sf_full[sf.s]));
       }
     }
   } else if (warp >= 8) {
@@ -633,14 +628,14 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * BN, out, a.ld_out, t.rows, in, half);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive<false>(bar_of(&acc_empty[ab], cta.lead));
+      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
       ++tc;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // no CTA leaves, or frees TMEM, while another may still use it
+  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
@@ -655,7 +650,6 @@ cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split
   const Fp8MatmulArgs& a = args.a;
   const int64_t inner = a.back ? a.N : a.K, pitch = fp8_pitch(inner);
   const bool pairs = bn == F8PairRing::bn;
-  const int cluster = (a.back ? a.K : a.N) > 2 * kTileM ? 4 : 2;   // two pairs, if both have weight rows
   CUtensorMap map_w;
   constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM)) return cudaErrorInvalidValue;
@@ -663,15 +657,9 @@ cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split
   if (pairs) {
     F8RowMaps map_a;
     for (int i = 0; i < F8PairRing::bn / 32; ++i)
-      if (!encode_tiles(&map_a.of[i], u8, 1, a.a_codes, inner, a.R, 1, pitch, 32 / cluster * (i + 1))) return cudaErrorInvalidValue;
-    auto run = [&](auto kern) {
-      int64_t ctas;
-      constexpr int smem = F8PairRing::total + slack;
-      const cudaError_t e = cluster_ctas(kern, tiles, cluster, kF8PairThreads, smem, ctas);
-      if (e != cudaSuccess) return e;
-      return launch_tiles(kern, ctas, cluster, kF8PairThreads, smem, s, map_a, map_w, args);
-    };
-    return cluster == 4 ? run(fp8_matmul_pair_kernel<OUT, 2>) : run(fp8_matmul_pair_kernel<OUT, 1>);
+      if (!encode_tiles(&map_a.of[i], u8, 1, a.a_codes, inner, a.R, 1, pitch, 16 * (i + 1))) return cudaErrorInvalidValue;
+    return launch_tiles(fp8_matmul_pair_kernel<OUT>, std::min<int64_t>(2 * tiles, kSms), 2, kF8PairThreads, F8PairRing::total + slack, s, map_a,
+                        map_w, args);
   }
   CUtensorMap map_a, map_part;
   if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, bn) ||
@@ -705,7 +693,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStre
   // a tile's reduction over the CTAs of a cluster while there are CTAs without a
   // tile, at least two stages each
   int split = 1;
-  while (split < 8 && narrow * split * 2 <= kSms && split * 4 <= ksteps) split *= 2;
+  while (split < 4 && narrow * split * 2 <= kSms && split * 4 <= ksteps) split *= 2;
   return run(32, narrow, split);
 }
 

@@ -174,11 +174,11 @@ struct WgradArgs {
   int E, N, K;
   int dtype, out_dtype;     // 16-bit; any
   void* dw;                 // [E, N, K]
-  uint8_t* workspace;       // aligned copies of operands that TMA cannot read
+  uint8_t* workspace;       // tensor maps, aligned copies of operands that TMA cannot read
   WaitCfg wait;
 };
 cudaError_t launch_weight_grad(const WgradArgs& a, int inject_stall, cudaStream_t s);
-size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t R, int64_t N, int64_t K);
+size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t R, int64_t E, int64_t N, int64_t K);
 
 // Norms around a block.
 

@@ -499,9 +499,9 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_
   return done(launch_fp8_matmul(a, g_inject_stall.load(), as_stream(stream)), "fp8 matmul");
 }
 
-size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int64_t n,
-                                  int64_t k) {
-  return rows < 1 || n < 1 || k < 1 ? 0 : weight_grad_workspace(dy_dev, ld_dy, x_dev, ld_x, rows, n, k);
+size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int experts,
+                                  int64_t n, int64_t k) {
+  return rows < 1 || experts < 1 || n < 1 || k < 1 ? 0 : weight_grad_workspace(dy_dev, ld_dy, x_dev, ld_x, rows, experts, n, k);
 }
 
 qmoe_status qmoe_weight_grad(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, const int32_t* offsets_dev,
@@ -517,8 +517,8 @@ qmoe_status qmoe_weight_grad(const void* dy_dev, int64_t ld_dy, const void* x_de
     return done(cudaMemsetAsync(dw_dev, 0, (size_t)experts * n * k * dtype_size(out_dtype), as_stream(stream)), "clear dw");
   OP_CHECK(dy_dev && x_dev, "dy or x is null");
   OP_TRY(check_addresses({{dy_dev, 2, "dy"}, {x_dev, 2, "x"}, {offsets_dev, 4, "offsets"}, {dw_dev, dtype_size(out_dtype), "dw"},
-                          {workspace_dev, 16, "workspace"}}));
-  const size_t need = weight_grad_workspace(dy_dev, ld_dy, x_dev, ld_x, rows, n, k);
+                          {workspace_dev, 128, "workspace"}}));
+  const size_t need = weight_grad_workspace(dy_dev, ld_dy, x_dev, ld_x, rows, experts, n, k);
   OP_CHECK(workspace_bytes >= need && (workspace_dev || need == 0), "workspace of %zu bytes is below the %zu needed",
            workspace_bytes, need);
   WgradArgs a{};

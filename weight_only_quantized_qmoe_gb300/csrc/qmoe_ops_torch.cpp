@@ -591,7 +591,7 @@ c10::SmallVector<int64_t, 3> size;
 if (a[2] != Py_None) size.push_back(p.experts);
 size.append({ry.width, rx.width});
 Tensor dw = make(size, type, dy), work;
-const size_t bytes = qmoe_weight_grad_workspace(ry.p, ry.ld, rx.p, rx.ld, ry.n, ry.width, rx.width);
+const size_t bytes = qmoe_weight_grad_workspace(ry.p, ry.ld, rx.p, rx.ld, ry.n, p.experts, ry.width, rx.width);
 if (bytes) work = make({(int64_t)bytes}, at::kByte, dy);
 check(qmoe_weight_grad(ry.p, ry.ld, rx.p, rx.ld, static_cast<int32_t*>(p.offsets.p), ry.n, p.experts, ry.width, rx.width, dt, (int)odt,
                        dw.mutable_data_ptr(), ptr(work), bytes, stream()));

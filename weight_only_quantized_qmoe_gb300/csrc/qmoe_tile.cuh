@@ -31,32 +31,18 @@ __device__ __forceinline__ void tma_3d_elect(void* dst, const CUtensorMap* map, 
 // Pairs of CTAs (cta_group::2): one MMA of M = 256, each CTA with its half of M,
 // half of the rows of N in its shared memory and an accumulator of all N columns
 // in its TMEM.  The first CTA of a pair issues the MMAs; both CTAs' copies
-// complete on its barriers.  A cluster is one pair, or two that share their rows
-// of N: each CTA then loads half of its half and sends it to the CTA of the same
-// place in the other pair.
+// complete on its barriers.
 //
-// Why: an SM's copies go out at one row of 128 bytes in about three cycles,
-// whatever the box, the number of SMs at work (38, 76, 152: the same) or what else
-// the SM does.  A tile of 128 x 192 (320 rows in 384 cycles of MMAs) is bound by
-// that, a pair's 256 x 224 (240 in 448) still, two pairs (184 in 448) hardly.
+// What such a kernel lives by, as measured with the waits of every role timed:
+// - the TMA unit takes a row of 128 bytes in two to three cycles, and a copy of few
+//   rows hardly less than one of many: a tile of 128 x 192 (320 rows in 384 cycles
+//   of MMAs) is bound by that, a pair's 256 x 224 (240 rows an SM in 448) is not;
+// - a wait that parks takes some 230 cycles where its phase is complete already, a
+//   poll 60, so a producer thread does one copy a stage and the issuing warp asks
+//   for its next stage before it issues the one it has;
+// - arrivals and waits at cluster scope that release and acquire memory take some
+//   700 cycles each, relaxed ones as much as others.
 // ----------------------------------------------------------------------------
-struct PairPlace {
-  int h, p;                // CTA of the pair, pair of the cluster
-  uint32_t lead;           // rank of the pair's first CTA
-  uint16_t here, shared;   // as masks: the pair; the CTAs that get the same rows of N
-};
-template <int PAIRS>
-__device__ __forceinline__ PairPlace pair_place() {
-  uint32_t rank;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  PairPlace c;
-  c.h = (int)(rank & 1u);
-  c.p = (int)(rank >> 1);
-  c.lead = rank & ~1u;
-  c.here = (uint16_t)(3u << c.lead);
-  c.shared = (uint16_t)((PAIRS == 2 ? 5u : 1u) << c.h);
-  return c;
-}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -64,13 +50,19 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrives, when the MMAs issued so far are done, on the barrier of the CTAs of a
-// mask; on that of this one.
-__device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar, uint16_t mask) {
+// This CTA of its pair.
+__device__ __forceinline__ int pair_rank() {
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  return (int)rank;
+}
+// Arrives, when the MMAs issued so far are done, on the barrier of both CTAs; on
+// that of this one.
+__device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "h"(mask)
+      "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ void tc_commit_pair_here_elect(uint64_t* bar) {
@@ -79,57 +71,36 @@ __device__ __forceinline__ void tc_commit_pair_here_elect(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
-// A barrier's address in another CTA of the cluster.
-__device__ __forceinline__ uint32_t bar_of(uint64_t* bar, uint32_t rank) {
+// A barrier's address in the first CTA.
+__device__ __forceinline__ uint32_t first_cta_bar(uint64_t* bar) {
   uint32_t at;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(bar)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(bar)));
   return at;
 }
-// Arrivals from other CTAs of the cluster.  Where what they stand for is tensor
-// memory read or written, the tcgen05 fences on either side order it and the
-// arrival and the wait are relaxed; shared memory written by other threads needs
-// release and acquire, which cost some 700 cycles each at this scope.
-template <bool MEMORY>
+// Arrivals of threads of both CTAs.  What they stand for is tensor memory read or
+// written; the tcgen05 fences on either side order that, and the arrival and the
+// wait are relaxed.
 __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
-  if constexpr (MEMORY) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-  else asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-template <bool MEMORY>
 __device__ __forceinline__ bool cluster_test_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  if constexpr (MEMORY)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
   return done != 0;
 }
-// A copy to this CTA's shared memory that completes on a barrier of its pair; to
-// the same place of every CTA of a mask, each completing on the barrier of the CTA
-// of its pair that is in the place of the barrier's own.  By one thread.
+// A copy to this CTA's shared memory that completes on a barrier of either, by one
+// thread.
 __device__ __forceinline__ void tma_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_3d_pairs(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
       : "memory");
 }
 // A producer's wait, by one thread: a poll that does not park first (a parked one
@@ -157,11 +128,10 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int it, int* status, 
   for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
 }
 // spin_or_abort for such a phase: one answer for the whole warp.
-template <bool MEMORY>
 __device__ __forceinline__ bool warp_spin_cluster(uint64_t* bar, uint32_t parity, const WaitCfg& w, volatile int* abort_flag) {
   const long long limit = w.limit * 64;
   for (long long i = 0; i < limit; ++i) {
-    if (__shfl_sync(0xffffffffu, cluster_test_wait<MEMORY>(bar, parity), 0)) return true;
+    if (__shfl_sync(0xffffffffu, cluster_test_wait(bar, parity), 0)) return true;
     if ((i & 255) == 255 && __shfl_sync(0xffffffffu, *abort_flag, 0)) return false;
   }
   atomicExch(w.status, DEV_TIMEOUT);
@@ -333,27 +303,6 @@ inline bool encode_tiles(CUtensorMap* m, CUtensorMapDataType type, int size, con
   const cuuint32_t ones[3] = {1, 1, 1};
   return f(m, type, 3, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// CTAs of a persistent kernel in clusters of `cluster`: as many clusters as can
-// run at once, or as there is work for.
-template <typename... Params>
-cudaError_t cluster_ctas(void (*kern)(Params...), int64_t work, int cluster, int threads, int smem, int64_t& ctas) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
-  cfg.gridDim = dim3((unsigned)(kSms / cluster * cluster));
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-  ctas = std::min<int64_t>(std::max(n, 1), work) * cluster;
-  return e;
 }
 
 // The launch of a tile kernel: clusters of `cluster` CTAs, dependent on the kernel before.

@@ -62,8 +62,7 @@ __device__ __forceinline__ void zero_rows(uint8_t* base, int panels, int rows) {
 // lane of a CTA or of the first CTA of a pair; 16 rows on is 2048 bytes in either
 // operand.
 template <int CTAS>
-__device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty,
-                                               uint16_t mask = 0) {
+__device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty) {
   if constexpr (CTAS == 1) {
     asm volatile(
         "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
@@ -93,7 +92,7 @@ __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t 
         "@q3 tcgen05.mma.cta_group::2.kind::f16 [%0], y3, z3, %3, p1;\n\t}" ::"r"(d),
         "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
         : "memory");
-    tc_commit_pair_elect(empty, mask);
+    tc_commit_pair_elect(empty);
   }
 }
 
@@ -296,9 +295,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 }
 
 // The same with pairs of CTAs: tiles of 256 columns of x by up to 256 of dy, of
-// which each CTA loads half; two pairs take neighbouring columns of x and share dy's.  A tail stage's zeros are each CTA's own: the other
-// CTA's copies of that stage complete on a barrier of its own, and a warp there
-// that has written the zeros arrives for them.
+// which each CTA loads half.  Nothing is overwritten with zeros here: copies of an
+// expert's rows go by tensor maps whose rows end with the expert's, so that what
+// lies behind reads as zeros (a warp of each CTA that wrote the zeros, and their
+// arrival at the first CTA, took 3000 cycles a tile).  A kernel before this one
+// makes them, four for each expert.
+struct WgMaps {
+  CUtensorMap x, x2, dy, dy2;   // panels of 64 columns by 64 rows; two of them in one copy
+};
 struct WgPairRing {
   static constexpr int stages = 6;
   static constexpr int panels = 2;                              // of x, and of a half of dy's columns
@@ -312,9 +316,35 @@ struct WgPairRing {
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
 };
 
-template <int OUT, int PAIRS>
+// The maps of every expert with rows: those of all rows, ended at its last.  A warp
+// an expert.
+__global__ void __launch_bounds__(32) weight_grad_maps_kernel(const __grid_constant__ WgMaps maps, const int* offsets, int64_t R, WgMaps* out) {
+  op_begin();
+  __shared__ __align__(128) WgMaps mine;
+  const int e = blockIdx.x, lane = threadIdx.x;
+  const int hi = min(max(offsets[e + 1], 0), (int)R);
+  if (hi == 0) return;
+  static_assert(sizeof(WgMaps) == 32 * sizeof(uint4), "a piece a lane");
+  reinterpret_cast<uint4*>(&mine)[lane] = reinterpret_cast<const uint4*>(&maps)[lane];
+  __syncwarp();
+  if (lane < 4)
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(&mine) + lane * 128), "r"(hi) : "memory");
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+                     reinterpret_cast<uint8_t*>(out + e) + i * 128),
+                 "r"(smem_u32(&mine) + i * 128)
+                 : "memory");
+}
+// Before a map of that kernel is used.
+__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
+
+template <int OUT>
 __global__ void __launch_bounds__(kWgThreads, 1)
-    weight_grad_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const WgKernelArgs args) {
+    weight_grad_pair_kernel(const __grid_constant__ WgMaps maps, const WgMaps* by_expert, const WgKernelArgs args) {
   using RG = WgPairRing;
   using T = typename ElemT<OUT>::t;
   constexpr int S = RG::stages;
@@ -323,8 +353,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const WgradArgs& a = args.a;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + RG::bar_off);   // the first CTA's count for both
   uint64_t* empty = full + S;
-  uint64_t* tail = empty + S;                                         // the second CTA's
-  uint64_t* acc_full = tail + S;
+  uint64_t* acc_full = empty + S;
   uint64_t* acc_empty = acc_full + 2;                                 // the first CTA's count for both
   uint64_t* drain_bar = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -332,13 +361,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   int* row0 = reinterpret_cast<int*>(smem + RG::row_off);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PairPlace cta = pair_place<PAIRS>();
-  const int rank = cta.h;
+  const int rank = pair_rank();
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(&full[i], 2);   // the announced bytes; the other CTA's zeros, or nothing to wait for
-      mbar_init(&empty[i], PAIRS);
-      mbar_init(&tail[i], 1);
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -355,17 +382,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     for (int e = lane; e <= a.E; e += 32) row0[e] = a.offsets ? min(max(a.offsets[e], 0), (int)a.R) : (e ? (int)a.R : 0);
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // the other CTAs' barriers and TMEM are there
+  cluster_sync_all();   // the other CTA's barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + 2 * PAIRS * kTileM - 1) / (2 * PAIRS * kTileM);
-  const int total = a.E * ntn * ntk, first = blockIdx.x / (2 * PAIRS), stride = gridDim.x / (2 * PAIRS);
+  const int ntn = (a.N + kWgBN - 1) / kWgBN, ntk = (a.K + 2 * kTileM - 1) / (2 * kTileM);
+  const int total = a.E * ntn * ntk, first = blockIdx.x / 2, stride = gridDim.x / 2;
   auto tile_of = [&](int tile) {
     WgTile t;
     const int kt = tile % ntk, rest = tile / ntk;
     t.e = rest / ntn;
     t.n0 = (rest % ntn) * kWgBN;
-    t.k0 = ((kt * PAIRS + cta.p) * 2 + rank) * kTileM;
+    t.k0 = (kt * 2 + rank) * kTileM;
     t.lo = row0[t.e];
     t.hi = max(row0[t.e + 1], t.lo);
     return t;
@@ -382,29 +409,28 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       for (int tile = first; tile < total && ok; tile += stride) {
         const WgTile t = tile_of(tile);
         const int half = half_of(t), panels = (half + kWgPanel - 1) / kWgPanel, col0 = t.n0 + rank * half;
-        const uint32_t bytes = (uint32_t)((RG::panels + panels) * kWgPanelBytes);
+        const uint32_t bytes = (uint32_t)(2 * (RG::panels + panels) * kWgPanelBytes);
+        const WgMaps* m = by_expert ? by_expert + t.e : &maps;
+        // warp 0's operand, or warp 2's
+        const CUtensorMap *one = warp == 0 ? &m->x : &m->dy, *two = warp == 0 ? &m->x2 : &m->dy2;
+        const int from = warp == 0 ? t.k0 : col0, copies = warp == 0 ? RG::panels : panels;
+        const bool both = from % kWgPanel == 0 && copies == 2 && from + 2 * kWgPanel <= (warp == 0 ? a.K : a.N);
+        if (by_expert && t.lo < t.hi) {
+          acquire_map(one);
+          acquire_map(two);
+        }
         for (int r = t.lo; r < t.hi; r += kWgRows, ++it, at.step()) {
           const int s = at.s;
           ok = poll_or_wait(&empty[s], at.ph ^ 1u, a.wait, abort_flag);
           if (!ok) break;
-          const bool zeros = t.hi - r < kWgRows && ((t.hi - r) & 15), own = rank == 1 && zeros;
-          const uint32_t bar = own ? bar_of(&tail[s], cta.lead + 1) : bar_of(&full[s], cta.lead);
-          if (warp == 0 && rank == 0) {
-            mbar_arrive_expect_tx(&full[s], zeros ? bytes : 2 * bytes);
-            if (!zeros) mbar_arrive(&full[s]);
-          } else if (warp == 0 && own) {
-            mbar_arrive_expect_tx(&tail[s], bytes);
-          }
+          const uint32_t bar = first_cta_bar(&full[s]);
+          if (warp == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           // Test hook: the first stage's barrier is armed, its copies are never issued.
           if (args.inject_stall && it == 0) continue;
-          uint8_t *dx = smem + RG::x_off + s * RG::x_bytes, *ddy = smem + RG::dy_off + s * RG::dy_bytes;
-#pragma unroll
-          for (int p = 0; p < RG::panels; ++p) {
-            if (warp == 0) tma_3d_pair(dx + p * kWgPanelBytes, &map_x, t.k0 + p * kWgPanel, r, 0, bar);
-            else if (p >= panels) continue;
-            else if constexpr (PAIRS == 1) tma_3d_pair(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar);
-            else if (p == cta.p) tma_3d_pairs(ddy + p * kWgPanelBytes, &map_dy, col0 + p * kWgPanel, r, 0, bar, cta.shared);
-          }
+          uint8_t* dst = warp == 0 ? smem + RG::x_off + s * RG::x_bytes : smem + RG::dy_off + s * RG::dy_bytes;
+          if (both) tma_3d_pair(dst, two, 0, r, from / kWgPanel, bar);
+          else
+            for (int p = 0; p < copies; ++p) tma_3d_pair(dst + p * kWgPanelBytes, one, from + p * kWgPanel, r, 0, bar);
         }
       }
       // (both CTAs' copies count on the first one's barriers; the second one's own
@@ -425,18 +451,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const int half = half_of(t);
       const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, 2 * kTileM, 2 * half);
       const int ab = tc & 1;
-      ok = warp_spin_cluster<false>(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
       if (!ok) break;
       for (int r = t.lo; r < t.hi; r += kWgRows) {
         const int s = at.s, rows = min(kWgRows, t.hi - r);
-        if (rows & 15) {
-          ok = warp_spin_cluster<true>(&full[s], at.ph, a.wait, abort_flag);   // the other CTA's zeros too
-          if (!ok) break;
-          zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::panels, rows);
-          zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half + kWgPanel - 1) / kWgPanel, rows);
-          fence_proxy_async_smem();
-          __syncwarp();
-        } else if (!__shfl_sync(0xffffffffu, there, 0)) {
+        if (!__shfl_sync(0xffffffffu, there, 0)) {
           ok = spin_or_abort(&full[s], at.ph, a.wait, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -445,35 +464,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         there = mbar_test_wait(&full[at.s], at.ph);
         tc_fence_after();
         wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint32_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint32_t)((s * RG::dy_bytes) >> 4),
-                          idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s], (uint16_t)((1 << 2 * PAIRS) - 1));
+                          idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
       }
-      if (ok) tc_commit_pair_elect(&acc_full[ab], cta.here);
+      if (ok) tc_commit_pair_elect(&acc_full[ab]);
       ++tc;
     }
     tc_commit_pair_here_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
     mbar_wait_bounded(drain_bar, 0, drain);
-  } else if (warp == 1) {
-    // ---------------- the second CTA's zeros ----------------
-    int it = 0;
-    uint32_t phases = 0;   // of `tail`, a bit each
-    bool ok = true;
-    for (int tile = first; tile < total && ok; tile += stride) {
-      const WgTile t = tile_of(tile);
-      if (t.lo >= t.hi) continue;
-      it += (t.hi - t.lo + kWgRows - 1) / kWgRows;
-      const int rows = (t.hi - t.lo - 1) % kWgRows + 1, s = (it - 1) % S;
-      if (!(rows & 15)) continue;
-      ok = wait_or_abort(&tail[s], (phases >> s) & 1u, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      phases ^= 1u << s;
-      zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::panels, rows);
-      zero_rows(smem + RG::dy_off + s * RG::dy_bytes, (half_of(t) + kWgPanel - 1) / kWgPanel, rows);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) cluster_bar_arrive<true>(bar_of(&full[s], cta.lead));
-    }
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp >> 2) - 1;
@@ -496,14 +494,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN, out, a.K, n, in, half);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_bar_arrive<false>(bar_of(&acc_empty[ab], cta.lead));
+      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
       ++tc;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // no CTA leaves, or frees TMEM, while another may still use it
+  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * kWgBN);
 }
@@ -556,6 +554,10 @@ __global__ void __launch_bounds__(kAlignThreads) align_rows_kernel(const AlignAr
 // ----------------------------------------------------------------------------
 namespace {
 
+int64_t wgrad_tiles(int64_t E, int64_t N, int64_t K) { return E * ((N + kWgBN - 1) / kWgBN) * ((K + kTileM - 1) / kTileM); }
+// Pairs of CTAs once every multiprocessor has a tile.
+bool wgrad_pairs(int64_t E, int64_t N, int64_t K) { return wgrad_tiles(E, N, K) > kSms && K > kTileM; }
+
 // TMA reads rows that start on 16 bytes, 16-byte multiples apart.
 bool tma_rows(const void* p, int64_t ld) { return aligned16(p) && ld % 8 == 0; }
 size_t align_bytes(const void* p, int64_t ld, int64_t R, int64_t width) {
@@ -566,7 +568,7 @@ size_t align_bytes(const void* p, int64_t ld, int64_t R, int64_t width) {
 cudaError_t align_operands(WgradArgs& a, cudaStream_t s) {
   AlignArgs c{};
   c.rows = a.R;
-  uint8_t* work = a.workspace;
+  uint8_t* work = a.workspace + (wgrad_pairs(a.E, a.N, a.K) ? a.E * sizeof(WgMaps) : 0);
   auto take = [&](int i, const void*& p, int64_t& ld, int width) {
     if (tma_rows(p, ld)) return;
     c.src[i] = static_cast<const uint16_t*>(p);
@@ -587,50 +589,65 @@ cudaError_t align_operands(WgradArgs& a, cudaStream_t s) {
   return launch_op(align_rows_kernel, dim3(blocks), dim3(kAlignThreads), 0, s, c);
 }
 
+// 64 rows of two panels of 64 columns in one copy, of the columns that fill whole
+// panels.
+bool encode_panels(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows, int64_t ld) {
+  const EncodeFn f = encoder();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {kWgPanel, (cuuint64_t)rows, (cuuint64_t)std::max<int64_t>(width / kWgPanel, 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, kWgPanel * 2};
+  const cuuint32_t box[3] = {kWgPanel, kWgRows, 2}, ones[3] = {1, 1, 1};
+  return f(m, type, 3, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int OUT>
-cudaError_t launch_wg(const WgKernelArgs& args, int64_t tiles, int split, bool pairs, cudaStream_t s) {
+cudaError_t launch_wg(const WgKernelArgs& args, cudaStream_t s) {
   const WgradArgs& a = args.a;
-  CUtensorMap map_x, map_dy;
+  WgMaps maps;
   const auto type = a.dtype == QMOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (!encode_tiles(&map_x, type, 2, a.x, a.K, a.R, 1, a.ld_x * 2, kWgRows) ||
-      !encode_tiles(&map_dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, kWgRows))
+  if (!encode_tiles(&maps.x, type, 2, a.x, a.K, a.R, 1, a.ld_x * 2, kWgRows) ||
+      !encode_tiles(&maps.dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, kWgRows))
     return cudaErrorInvalidValue;
-  constexpr int smem = WgRing::total + 1024;   // + alignment slack
-  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true>, tiles * split, split, kWgThreads, smem, s, map_x, map_dy, args);
-  if (pairs) {
-    auto run = [&](auto kern, int cluster) {
-      int64_t ctas;
-      constexpr int pair_smem = WgPairRing::total + 1024;
-      const cudaError_t e = cluster_ctas(kern, tiles, cluster, kWgThreads, pair_smem, ctas);
+  const int64_t tiles = wgrad_tiles(a.E, a.N, a.K);
+  if (wgrad_pairs(a.E, a.N, a.K)) {
+    if (!encode_panels(&maps.x2, type, a.x, a.K, a.R, a.ld_x) || !encode_panels(&maps.dy2, type, a.dy, a.N, a.R, a.ld_dy))
+      return cudaErrorInvalidValue;
+    WgMaps* by_expert = a.offsets ? reinterpret_cast<WgMaps*>(a.workspace) : nullptr;
+    if (by_expert) {
+      const cudaError_t e = launch_op(weight_grad_maps_kernel, dim3((unsigned)a.E), dim3(32), 0, s, maps, a.offsets, a.R, by_expert);
       if (e != cudaSuccess) return e;
-      return launch_tiles(kern, ctas, cluster, kWgThreads, pair_smem, s, map_x, map_dy, args);
-    };
-    return a.K > 2 * kTileM ? run(weight_grad_pair_kernel<OUT, 2>, 4) : run(weight_grad_pair_kernel<OUT, 1>, 2);
+    }
+    const WgMaps* by = by_expert;
+    return launch_tiles(weight_grad_pair_kernel<OUT>, kSms, 2, kWgThreads, WgPairRing::total + 1024, s, maps, by, args);
   }
-  return launch_tiles(weight_grad_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, map_x, map_dy, args);
+  constexpr int smem = WgRing::total + 1024;   // + alignment slack
+  // A tile's rows over the CTAs of a cluster while there are CTAs without a tile, if
+  // the rows, spread evenly, fill 24 stages (us with / without: 2048 rows of 256 x
+  // 256, in 8 parts, 10.2 / 17.2; 4000 of 1024 x 1024, in 4, 17.0 / 30.9; 32768 of
+  // 64 x 64, in 8, 23.5 / 153; but 1000 of 1024 x 1024, 16 stages in 4, 11.9 / 11.1).
+  const int64_t steps = (a.R / a.E + kWgRows - 1) / kWgRows;
+  int split = 1;
+  while (steps >= 24 && split < 8 && tiles * split * 2 <= kSms && split * 8 <= steps) split *= 2;
+  if (split > 1) return launch_tiles(weight_grad_kernel<OUT, true>, tiles * split, split, kWgThreads, smem, s, maps.x, maps.dy, args);
+  return launch_tiles(weight_grad_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kWgThreads, smem, s, maps.x, maps.dy, args);
 }
 
 }  // namespace
 
-size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t R, int64_t N, int64_t K) {
-  return align_bytes(dy, ld_dy, R, N) + align_bytes(x, ld_x, R, K);
+// The maps of every expert, then the aligned copies.
+size_t weight_grad_workspace(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, int64_t R, int64_t E, int64_t N, int64_t K) {
+  return (wgrad_pairs(E, N, K) ? (size_t)E * sizeof(WgMaps) : 0) + align_bytes(dy, ld_dy, R, N) + align_bytes(x, ld_x, R, K);
 }
 
 cudaError_t launch_weight_grad(const WgradArgs& a, int inject_stall, cudaStream_t s) {
+  if (wgrad_tiles(a.E, a.N, a.K) > 0x7fffffff) return cudaErrorInvalidValue;
   WgKernelArgs args{a, inject_stall};
   const cudaError_t e = align_operands(args.a, s);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)a.E * ((a.N + kWgBN - 1) / kWgBN) * ((a.K + kTileM - 1) / kTileM);
-  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-  // a tile's rows over the CTAs of a cluster while there are CTAs without a tile
-  // and each gets a stage, if they are spread evenly
-  const int64_t steps = (a.R / a.E + kWgRows - 1) / kWgRows;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= kSms && split * 2 <= steps) split *= 2;
-  const bool pairs = tiles > kSms && a.K > kTileM;
-  if (a.out_dtype == QMOE_F32) return launch_wg<QMOE_F32>(args, tiles, split, pairs, s);
-  if (a.out_dtype == QMOE_F16) return launch_wg<QMOE_F16>(args, tiles, split, pairs, s);
-  return launch_wg<QMOE_BF16>(args, tiles, split, pairs, s);
+  if (a.out_dtype == QMOE_F32) return launch_wg<QMOE_F32>(args, s);
+  if (a.out_dtype == QMOE_F16) return launch_wg<QMOE_F16>(args, s);
+  return launch_wg<QMOE_BF16>(args, s);
 }
 
 }  // namespace qmoe
