@@ -36,84 +36,123 @@ __device__ __forceinline__ F warp_sum(F v) {
   return v;
 }
 
-// Whether group g of `groups` is among the `top` best, as a bit per group.  c:
-// the values of the experts, -infinity where one may not be chosen; a group's
-// score is its best, or the sum of its two best (one where it has one).  32 lanes
-// are shared among the groups.  unsure: set if the border between the last
-// group kept and the first left out is nearer than tau + rel * their magnitude.
+// A score in 64 bits; mx and sum: of a softmax.
+__device__ __forceinline__ double score64(int scoring, double l, double mx, double sum) {
+  return scoring == QMOE_SCORE_SOFTMAX ? exp(l - mx) / sum : 1.0 / (1.0 + exp(-l));
+}
+// Sum of a softmax in 64 bits.  (Unrolled, here and below: an exponential in 64
+// bits is some 3000 cycles of latency.)
+template <int DT>
+__device__ double softmax_sum64(const typename ElemT<DT>::t* row, int E, double mx) {
+  double sum = 0.0;
+#pragma unroll 4
+  for (int e = threadIdx.x & 31; e < E; e += 32) {
+    const double l = load_d<DT>(row, e);
+    sum += l == l ? exp(l - mx) : 0.0;
+  }
+  return warp_sum(sum);
+}
+
+// The two largest of a warp's values, in every lane (`lanes` of them that go together).
 template <typename F>
-__device__ __forceinline__ unsigned best_groups(const F* c, int E, int groups, int top, int best, F tau, F rel, bool* unsure) {
-  const int lane = threadIdx.x & 31, n = E / groups;
-  int per = 32;   // lanes of a group
-  while (per * groups > 32) per >>= 1;
-  const int g = lane / per, sub = lane % per;
-  const F low = -static_cast<F>(INFINITY);
-  F a1 = low, a2 = low;
-  if (g < groups)
-    for (int j = sub; j < n; j += per) {
-      const F v = c[g * n + j];
-      a2 = fmax(a2, fmin(a1, v));
-      a1 = fmax(a1, v);
-    }
-  for (int o = per >> 1; o > 0; o >>= 1) {
+__device__ __forceinline__ void two_best(F& a1, F& a2, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
     const F b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
     a2 = fmax(fmax(a2, b2), fmin(a1, b1));
     a1 = fmax(a1, b1);
   }
-  const F score = best == 2 && a2 != low ? a1 + a2 : a1;
+}
+// How many groups come before this lane's own: larger, or equal with a lower index.
+template <typename F>
+__device__ __forceinline__ int group_rank(F score, unsigned among) {
+  const int lane = threadIdx.x & 31;
   int rank = 0;
-  for (int h = 0; h < groups; ++h) {
-    const F other = __shfl_sync(kAll, score, h * per);
-    rank += other > score || (other == score && h < g) ? 1 : 0;
+  for (unsigned m = among; m; m &= m - 1) {
+    const int h = __ffs(m) - 1;
+    const F other = __shfl_sync(kAll, score, h);
+    rank += other > score || (other == score && h < lane) ? 1 : 0;
   }
-  const bool one = sub == 0 && g < groups, kept = one && rank < top;
-  const unsigned mask = __ballot_sync(kAll, kept);
-  if (unsure) {
-    // the last group kept and the first left out
-    const unsigned last = __ballot_sync(kAll, one && rank == top - 1), next = __ballot_sync(kAll, one && rank == top);
-    const F x = __shfl_sync(kAll, score, __ffs(last) - 1), y = __shfl_sync(kAll, score, __ffs(next) - 1);
-    if (y != low && !(x - y > tau + rel * (fabs(x) + fabs(y)))) *unsure = true;
-  }
-  unsigned bits = 0;
-  for (int h = 0; h < groups; ++h) bits |= (mask >> (h * per) & 1u) << h;
-  return bits;
+  return rank;
 }
 
-// The choice of a token in 64 bits, by a whole warp; c: room for E values.
-// Lane j gets the expert of rank j, or -1.
+// The r best of a few groups (bits of `among`) by scores in 64 bits.  c: the
+// experts' values in 32, -infinity where one may not be chosen.
 template <int DT>
-__device__ __noinline__ int choose64(const ChoiceArgs& a, const typename ElemT<DT>::t* row, double* c) {
-  const int lane = threadIdx.x & 31, E = a.E;
+__device__ __noinline__ unsigned best_groups64(const ChoiceArgs& a, const typename ElemT<DT>::t* row, const float* c, float mx,
+                                               unsigned among, int r) {
+  const int lane = threadIdx.x & 31, n = a.E / a.groups;
   const double low = -static_cast<double>(INFINITY);
-  double mx = low, sum = 0.0;
-  if (a.scoring == QMOE_SCORE_SOFTMAX) {
-    float m = -INFINITY;
-    for (int e = lane; e < E; e += 32) m = fmaxf(m, load_d<DT>(row, e));
-    mx = warp_max(m);
+  const double sum = a.scoring == QMOE_SCORE_SOFTMAX ? softmax_sum64<DT>(row, a.E, mx) : 1.0;
+  double mine = low;
+  for (unsigned m = among; m; m &= m - 1) {
+    const int g = __ffs(m) - 1;
+    double a1 = low, a2 = low;
 #pragma unroll 4
-    for (int e = lane; e < E; e += 32) {
-      const double l = load_d<DT>(row, e);
-      sum += l == l ? exp(l - mx) : 0.0;
+    for (int j = lane; j < n; j += 32) {
+      const int e = g * n + j;
+      if (c[e] > -INFINITY) {
+        const double v = score64(a.scoring, load_d<DT>(row, e), mx, sum) + (a.bias ? (double)a.bias[e] : 0.0);
+        a2 = fmax(a2, fmin(a1, v));
+        a1 = fmax(a1, v);
+      }
     }
-    sum = warp_sum(sum);   // (unrolled loops: an exponential in 64 bits is some 3000 cycles of latency)
+    two_best(a1, a2, 32);
+    if (lane == g) mine = a.best == 2 && a2 != low ? a1 + a2 : a1;
   }
-  auto score = [&](double l) { return a.scoring == QMOE_SCORE_SOFTMAX ? exp(l - mx) / sum : 1.0 / (1.0 + exp(-l)); };
-  const bool filter = a.top_groups < a.groups;
-  // the keys of the groups: the scores themselves where there is no bias
+  const int rank = group_rank(mine, among);   // by every lane: it shuffles
+  return __ballot_sync(kAll, (among >> lane & 1u) && rank < r);
+}
+
+// The top_groups best groups, a bit each.  c: as above, in shared memory.  A
+// group's score is its best, or the sum of its two best (one where it has one); the
+// lanes are shared among the groups.  by_score: c is rounded, by tau of each value
+// and its own rounding; groups that are too near to the border to be told apart go
+// by their scores in 64 bits.
+template <int DT>
+__device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typename ElemT<DT>::t* row, const float* c, float mx,
+                                                bool by_score, float tau) {
+  const int lane = threadIdx.x & 31, n = a.E / a.groups;
+  int per = 32;   // lanes of a group
+  while (per * a.groups > 32) per >>= 1;
+  const int g = lane / per;
+  float a1 = -INFINITY, a2 = -INFINITY;
+  if (g < a.groups)
+    for (int j = lane % per; j < n; j += per) {
+      const float v = c[g * n + j];
+      a2 = fmaxf(a2, fminf(a1, v));
+      a1 = fmaxf(a1, v);
+    }
+  two_best(a1, a2, per);
+  // group g's in lane g
+  const float score = __shfl_sync(kAll, a.best == 2 && a2 != -INFINITY ? a1 + a2 : a1, (lane * per) & 31);
+  const unsigned all = a.groups == 32 ? kAll : (1u << a.groups) - 1u;
+  const bool one = lane < a.groups;
+  const int rank = group_rank(score, all);
+  const unsigned open = __ballot_sync(kAll, one && rank < a.top_groups);
+  if (!by_score) return open;
+  // the last group kept and the first left out
+  const float x = __shfl_sync(kAll, score, __ffs(__ballot_sync(kAll, one && rank == a.top_groups - 1)) - 1);
+  const float y = __shfl_sync(kAll, score, __ffs(__ballot_sync(kAll, one && rank == a.top_groups)) - 1);
+  const float near = tau + tau + 0x1p-21f * (fabsf(x) + fabsf(y));
+  if (y == -INFINITY || x - y > near) return open;
+  const unsigned sure = __ballot_sync(kAll, one && score > y + near);
+  const unsigned among = __ballot_sync(kAll, one && score > -INFINITY && !(score > y + near) && !(score < x - near));
+  return sure | best_groups64<DT>(a, row, c, mx, among, a.top_groups - __popc(sure));
+}
+
+// The choice of a token in 64 bits from the open groups, by a whole warp; c: room
+// for E values.  Lane j gets the expert of rank j, or -1.
+template <int DT>
+__device__ __noinline__ int choose64(const ChoiceArgs& a, const typename ElemT<DT>::t* row, float mx, unsigned open, double* c) {
+  const int lane = threadIdx.x & 31, E = a.E, n = E / a.groups;
+  const double low = -static_cast<double>(INFINITY);
+  const double sum = a.scoring == QMOE_SCORE_SOFTMAX ? softmax_sum64<DT>(row, E, mx) : 1.0;
+  __syncwarp();
 #pragma unroll 4
   for (int e = lane; e < E; e += 32) {
     const double l = load_d<DT>(row, e);
-    const double v = l > low ? score(l) + (a.bias ? (double)a.bias[e] : 0.0) : low;
+    const double v = l > low && (open >> (e / n) & 1u) ? score64(a.scoring, l, mx, sum) + (double)a.bias[e] : low;
     c[e] = v > low ? v : low;   // NaN too
-  }
-  __syncwarp();
-  unsigned bits = kAll;
-  if (filter) bits = best_groups<double>(c, E, a.groups, a.top_groups, a.best, 0.0, 0.0, nullptr);
-  __syncwarp();
-  const int n = E / a.groups;
-  for (int e = lane; e < E; e += 32) {
-    if (filter && !(bits >> (e / n) & 1u)) c[e] = low;
-    else if (!a.bias && c[e] > low) c[e] = load_d<DT>(row, e);
   }
   __syncwarp();
   int mine = -1;
@@ -147,19 +186,8 @@ __device__ __noinline__ int choose64(const ChoiceArgs& a, const typename ElemT<D
 template <int DT>
 __device__ __noinline__ int choose64_of(const ChoiceArgs& a, const typename ElemT<DT>::t* row, int e, float mx, int* list) {
   const int lane = threadIdx.x & 31;
-  double v = -static_cast<double>(INFINITY);
-  if (a.scoring == QMOE_SCORE_SOFTMAX) {
-    double sum = 0.0;
-#pragma unroll 4
-    for (int i = lane; i < a.E; i += 32) {
-      const double l = load_d<DT>(row, i);
-      sum += l == l ? exp(l - mx) : 0.0;
-    }
-    sum = warp_sum(sum);
-    if (e >= 0) v = exp((double)load_d<DT>(row, e) - mx) / sum + (double)a.bias[e];
-  } else if (e >= 0) {
-    v = 1.0 / (1.0 + exp(-(double)load_d<DT>(row, e))) + (double)a.bias[e];
-  }
+  const double sum = a.scoring == QMOE_SCORE_SOFTMAX ? softmax_sum64<DT>(row, a.E, mx) : 1.0;
+  const double v = e >= 0 ? score64(a.scoring, load_d<DT>(row, e), mx, sum) + (double)a.bias[e] : -static_cast<double>(INFINITY);
   int rank = 0;
   for (int i = 0; i < 32; ++i) {
     const double w = __shfl_sync(kAll, v, i);
@@ -173,6 +201,65 @@ __device__ __noinline__ int choose64_of(const ChoiceArgs& a, const typename Elem
   __syncwarp();
   return list[lane];
 }
+
+// A lane's keys (INT_MIN: none) of experts lane, lane + 32, ...  Up to eight are
+// sorted once, best first, and the head drops out as it is chosen; more are looked
+// through for every rank.
+template <int NPL>
+struct LaneKeys {
+  static constexpr bool sorted = NPL <= 8;
+  int key[NPL], idx[sorted ? NPL : 1];
+  __device__ __forceinline__ void sort() {
+    if constexpr (sorted) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) idx[i] = (threadIdx.x & 31) + 32 * i;
+      // neighbours change places only where the second is larger: equal keys keep their order
+#pragma unroll
+      for (int round = 0; round < NPL; ++round) {
+#pragma unroll
+        for (int i = round & 1; i + 1 < NPL; i += 2) {
+          const bool swap = key[i + 1] > key[i];
+          const int k = key[i], x = idx[i];
+          key[i] = swap ? key[i + 1] : k;
+          idx[i] = swap ? idx[i + 1] : x;
+          key[i + 1] = swap ? k : key[i + 1];
+          idx[i + 1] = swap ? x : idx[i + 1];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ int index(int i) const {
+    if constexpr (sorted) return idx[i];
+    else return (threadIdx.x & 31) + 32 * i;
+  }
+  __device__ __forceinline__ void best(int& k, int& at) const {
+    k = key[0];
+    at = index(0);
+    if constexpr (!sorted) {
+#pragma unroll
+      for (int i = 1; i < NPL; ++i)
+        if (key[i] > k) {
+          k = key[i];
+          at = index(i);
+        }
+    }
+  }
+  __device__ __forceinline__ void drop(int sel) {
+    if constexpr (sorted) {
+      const bool pop = idx[0] == sel;
+#pragma unroll
+      for (int i = 0; i + 1 < NPL; ++i) {
+        key[i] = pop ? key[i + 1] : key[i];
+        idx[i] = pop ? idx[i + 1] : idx[i];
+      }
+      if (pop) key[NPL - 1] = INT_MIN;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (sel == index(i)) key[i] = INT_MIN;
+    }
+  }
+};
 
 template <int DT, int NPL>
 __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceArgs a) {
@@ -212,13 +299,13 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     sum = warp_sum(sum);
   }
 
-  int key[NPL];
+  LaneKeys<NPL> keys;
   unsigned open = kAll;   // groups
-  bool unsure = false;
   // how far two rounded keys may be off their difference: each by 2^-24 of its
-  // score times 4 (sigmoid: an exponential, a sum, a division) or 42 (softmax:
-  // with the sum of E terms, up to 32 of them one after the other in a lane),
-  // taken as 8 and 64, and by its own rounding
+  // score times 4 (sigmoid: the error of the exponential, 2 + 1.2 |l| steps, counts
+  // s (1 - s) times; a sum and a division) or 42 (softmax: with the sum of E terms,
+  // up to 32 of them one after the other in a lane), taken as 8 and 64, and by its
+  // own rounding
   float tau = 0.f;
   {
     float c[NPL];
@@ -228,7 +315,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const int e = lane + 32 * i;
-        float v = softmax ? expf(l[i] - mx) * inv : 1.f / (1.f + expf(-l[i]));
+        float v = softmax ? __expf(l[i] - mx) * inv : __fdividef(1.f, 1.f + __expf(-l[i]));
         if (a.bias && e < E) v += a.bias[e];
         if (isnan(v) && l[i] > -INFINITY) nan = true;
         c[i] = l[i] > -INFINITY && v > -INFINITY ? v : -INFINITY;
@@ -243,28 +330,22 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       for (int i = 0; i < NPL; ++i)
         if (lane + 32 * i < E) sm[lane + 32 * i] = c[i];
       __syncwarp();
-      open = best_groups<float>(sm, E, a.groups, a.top_groups, a.best, tau + tau, 0x1p-21f, by_score ? &unsure : nullptr);
-      __syncwarp();
+      open = best_groups<DT>(a, row, sm, mx, by_score, tau);
     }
-    const int n = E / a.groups;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int e = lane + 32 * i;
       const float v = a.bias ? c[i] : l[i];
-      const bool may = c[i] > -INFINITY && (!filter || (open >> (e / n) & 1u));
-      key[i] = may ? topk_order_key(v) : INT_MIN;
+      const bool may = c[i] > -INFINITY && (!filter || (open >> ((uint32_t)e * a.group_magic >> 20) & 1u));
+      keys.key[i] = may ? topk_order_key(v) : INT_MIN;
     }
   }
-  const bool groups_unsure = __any_sync(kAll, unsure);
+  keys.sort();
+  bool unsure = false;
   int mine = -1, before = INT_MAX, kth = 0;
   for (int slot = 0; slot <= k; ++slot) {   // one more than asked for: the border of the last
-    int best = key[0], at = lane;
-#pragma unroll
-    for (int i = 1; i < NPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = lane + 32 * i;
-      }
+    int best, at;
+    keys.best(best, at);
     const int m = topk_redux_max(best);
     if (m == INT_MIN || (slot == k && !a.bias)) break;
     if (a.bias && slot > 0) {
@@ -276,30 +357,28 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     kth = m;
     const int sel = topk_redux_min(best == m ? at : INT_MAX);
     if (lane == slot) mine = sel;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (sel == lane + 32 * i) key[i] = INT_MIN;
+    keys.drop(sel);
   }
-  if (groups_unsure) {
-    mine = choose64<DT>(a, row, choice_smem + (size_t)warp * a.room);
-  } else if (unsure) {
+  if (unsure) {   // (the same for the whole warp)
     // those chosen, and those left that are as near to the last of them
     const float last = __int_as_float(kth ^ ((kth >> 31) & INT_MAX)), least = last - (tau + 0x1p-21f * fabsf(last));
-    int* list = reinterpret_cast<int*>(choice_smem + (size_t)warp * a.room);
+    double* room = choice_smem + (size_t)warp * a.room;
+    int* list = reinterpret_cast<int*>(room);
     int n = __popc(__ballot_sync(kAll, mine >= 0));
     __syncwarp();
     if (mine >= 0) list[lane] = mine;   // the lanes from 0 on
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      const bool near = key[i] != INT_MIN && !(__int_as_float(key[i] ^ ((key[i] >> 31) & INT_MAX)) < least);
+      const int kv = keys.key[i];
+      const bool near = kv != INT_MIN && !(__int_as_float(kv ^ ((kv >> 31) & INT_MAX)) < least);
       const unsigned who = __ballot_sync(kAll, near);
       const int at = n + __popc(who & ((1u << lane) - 1u));
-      if (near && at < 32) list[at] = lane + 32 * i;
+      if (near && at < 32) list[at] = keys.index(i);
       n += __popc(who);
     }
     __syncwarp();
     if (n <= 32) mine = choose64_of<DT>(a, row, lane < n ? list[lane] : -1, mx, list);
-    else mine = choose64<DT>(a, row, choice_smem + (size_t)warp * a.room);
+    else mine = choose64<DT>(a, row, mx, open, room);
   }
 
   const float chosen = mine >= 0 ? load_d<DT>(row, mine) : -INFINITY;
@@ -426,6 +505,8 @@ cudaError_t launch_choice(const ChoiceArgs& a, cudaStream_t s) {
   const unsigned blocks = (unsigned)((a.T + kChoiceWarps - 1) / kChoiceWarps);
   ChoiceArgs args = a;
   args.room = a.bias || a.top_groups < a.groups ? std::max(a.E, 32) : 0;
+  const int n = a.E / a.groups;   // e / n = (e * magic) >> 20, exactly, for e and n up to 1024
+  args.group_magic = (uint32_t)(((1 << 20) + n - 1) / n);
   const size_t smem = sizeof(double) * kChoiceWarps * args.room;   // at most 32 KB
   return with_types(a, [&](auto dt, auto npl) {
     return launch_op(choice_kernel<decltype(dt)::value, decltype(npl)::value>, dim3(blocks), dim3(32 * kChoiceWarps), smem, s, args);

@@ -105,7 +105,8 @@ struct ChoiceArgs {
   int64_t T;
   int E, k, scoring, groups, top_groups, best, renorm;
   float scale;
-  int room;                 // values of a warp in shared memory (set by the launch)
+  int room;                 // values of a warp in shared memory (set by the launch,
+  uint32_t group_magic;     // and so is this)
   int* ids;                 // [T, k]
   float* w;                 // [T, k]
   // gradient
