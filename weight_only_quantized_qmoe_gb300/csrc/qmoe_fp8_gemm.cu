@@ -98,6 +98,7 @@ __device__ __forceinline__ uint32_t idesc_mxf8(int M, int N, int back) {
 struct F8KernelArgs {
   Fp8MatmulArgs a;
   int inject_stall;
+  int bn;                   // rows of A a tile, of pairs: 32 i
 };
 
 // SPLIT: a cluster shares each tile's reduction, and there is one tile a cluster
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   __syncwarp();
   if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
   op_begin();   // the operands and offsets may come from the kernel before
-  if (warp == 3) group_tiles(a.offsets, a.E, a.R, BN, tp, row0);
+  if (warp == 3) group_tiles(a.offsets, a.E, a.R, args.bn, tp, row0);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // the other CTA's barriers and TMEM are there
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   auto tile_of = [&](int tile, int& n0) {
     const int mt = tile / ntw;
     n0 = ((tile - mt * ntw) * 2 + rank) * kTileM;
-    return row_tile(a.E, tp, row0, BN, mt);
+    return row_tile(a.E, tp, row0, args.bn, mt);
   };
   // rows of A of each CTA: half of the tile's, in whole sixteens
   auto half_of = [&](const RowTile& t) { return ((t.rows + 31) & ~31) / 2; };
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     for (int tile = first; tile < real && ok; tile += stride) {
       int n0;
       const RowTile t = tile_of(tile, n0);
-      const int left = min((int)a.R - t.start, BN) - lane;   // row 32 j exists: 32 j < left
+      const int left = min((int)a.R - t.start, args.bn) - lane;   // row 32 j exists: 32 j < left
       const int ob = min(n0, width - 1) / kTileM;
       const uint8_t* w0 = a.w_scales + (size_t)t.e * nbn * nbk + (a.back ? ob : (size_t)ob * nbk);
       const size_t wstep = a.back ? nbk : 1;
@@ -646,10 +647,9 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
 namespace {
 
 template <int OUT>
-cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split, cudaStream_t s) {
+cudaError_t launch_f8(const F8KernelArgs& args, bool pairs, int64_t tiles, int split, cudaStream_t s) {
   const Fp8MatmulArgs& a = args.a;
   const int64_t inner = a.back ? a.N : a.K, pitch = fp8_pitch(inner);
-  const bool pairs = bn == F8PairRing::bn;
   CUtensorMap map_w;
   constexpr auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if (!encode_tiles(&map_w, u8, 1, a.w_codes, a.K, a.N, a.E, fp8_pitch(a.K), kTileM)) return cudaErrorInvalidValue;
@@ -662,7 +662,7 @@ cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split
                         map_w, args);
   }
   CUtensorMap map_a, map_part;
-  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, bn) ||
+  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, 32) ||
       !encode_tiles(&map_part, u8, 1, a.a_codes, inner, a.R, 1, pitch, kF8BoxRows))
     return cudaErrorInvalidValue;
   if (split > 1)
@@ -672,29 +672,59 @@ cudaError_t launch_f8(const F8KernelArgs& args, int bn, int64_t tiles, int split
                       map_part, map_w, args);
 }
 
-// Output tiles there can be at most (the device offsets decide how many there are).
-int64_t most_tiles(const Fp8MatmulArgs& a, int bn) {
-  const int64_t groups = a.offsets ? std::min<int64_t>((int64_t)a.E + 1, a.R) : 1;
-  return (a.R / bn + groups) * (((a.back ? a.K : a.N) + kTileM - 1) / kTileM);
+// Output tiles there can be at most (the device offsets decide how many there
+// are): of bn rows of A by `wide` weight rows.
+int64_t most_tiles(const Fp8MatmulArgs& a, int bn, int wide) {
+  const int64_t rows = a.offsets ? a.R / bn + std::min<int64_t>((int64_t)a.E + 1, a.R) : (a.R + bn - 1) / bn;
+  return rows * (((a.back ? a.K : a.N) + wide - 1) / wide);
+}
+
+// Rows of A a tile of pairs.  Dense: those that take the least rounds of 76 pairs
+// times a stage's time, which is that of the weight rows' copy (about 400 cycles) up
+// to 160 rows and that of the MMAs from there on (us with / with 224: 512 x 4096 x
+// 4096 12.6 / 13.1, 2001 x 2880 x 5761 34.9 / 37.3).  Grouped: as many as there can
+// be, as experts' rows are uneven and a remainder costs a tile of its own (32768
+// rows over 64 experts 175 us, by the rule for an even spread 186).
+int pair_rows(const Fp8MatmulArgs& a) {
+  int best = F8PairRing::bn;
+  if (a.offsets) return best;
+  const int64_t wide = ((a.back ? a.K : a.N) + 2 * kTileM - 1) / (2 * kTileM);
+  int64_t least = INT64_MAX;
+  for (int bn = F8PairRing::bn; bn >= 64; bn -= 32) {
+    const int64_t tiles = (a.R + bn - 1) / bn * wide, time = (tiles + kSms / 2 - 1) / (kSms / 2) * std::max(400, 5 * bn / 2);
+    if (time < least) {
+      least = time;
+      best = bn;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStream_t s) {
-  const F8KernelArgs args{a, inject_stall};
-  const int64_t ksteps = ((a.back ? a.N : a.K) + kF8StageK - 1) / kF8StageK, narrow = most_tiles(a, 32);
-  auto run = [&](int bn, int64_t tiles, int split) {
-    if (a.out_dtype == QMOE_F32) return launch_f8<QMOE_F32>(args, bn, tiles, split, s);
-    if (a.out_dtype == QMOE_F16) return launch_f8<QMOE_F16>(args, bn, tiles, split, s);
-    return launch_f8<QMOE_BF16>(args, bn, tiles, split, s);
+  F8KernelArgs args{a, inject_stall, 32};
+  const int64_t ksteps = ((a.back ? a.N : a.K) + kF8StageK - 1) / kF8StageK, narrow = most_tiles(a, 32, kTileM);
+  auto run = [&](bool pairs, int64_t tiles, int split) {
+    if (a.out_dtype == QMOE_F32) return launch_f8<QMOE_F32>(args, pairs, tiles, split, s);
+    if (a.out_dtype == QMOE_F16) return launch_f8<QMOE_F16>(args, pairs, tiles, split, s);
+    return launch_f8<QMOE_BF16>(args, pairs, tiles, split, s);
   };
   const int64_t rows = a.offsets ? a.R / std::min<int64_t>(a.E, a.R) : a.R;   // of an expert, if they are spread evenly
-  if (narrow > kSms && rows > 32) return run(F8PairRing::bn, most_tiles(a, F8PairRing::bn), 1);
-  // a tile's reduction over the CTAs of a cluster while there are CTAs without a
-  // tile, at least two stages each
+  // tiles of 32 rows while they are all under way at once, or an expert has few rows
+  // (us, narrow / pairs: 64 x 2048 x 2048 over all 7.7 / 7.4, 300 rows 13.5 / 8.0;
+  // experts of 1536 x 2048, 2 rows each of 128 50.8 / 52.0, 16 of 64 38.9 / 39.1, 32
+  // of 64 48.9 / 40.3)
+  if (narrow > kSms && rows >= 24) {
+    args.bn = pair_rows(a);
+    return run(true, most_tiles(a, args.bn, 2 * kTileM), 1);
+  }
+  // A tile's reduction over the CTAs of a cluster while there are CTAs without a
+  // tile, at least two stages each, up to four: eight CTAs' parts take longer to add
+  // up than four's to make (1 x 2048 x 2048 in 1, 2, 4, 8 parts: 7.8, 6.5, 5.9, 9.9 us).
   int split = 1;
   while (split < 4 && narrow * split * 2 <= kSms && split * 4 <= ksteps) split *= 2;
-  return run(32, narrow, split);
+  return run(false, narrow, split);
 }
 
 }  // namespace qmoe
