@@ -680,9 +680,9 @@ int64_t most_tiles(const Fp8MatmulArgs& a, int bn, int wide) {
 }
 
 // Rows of A a tile of pairs.  Dense: those that take the least rounds of 76 pairs
-// times a stage's time, which is that of the weight rows' copy (about 400 cycles) up
-// to 160 rows and that of the MMAs from there on (us with / with 224: 512 x 4096 x
-// 4096 12.6 / 13.1, 2001 x 2880 x 5761 34.9 / 37.3).  Grouped: as many as there can
+// times a stage's time, some 265 cycles and one more a row (8192 x 8192 x 8192, us:
+// 224 rows 321, 160 rows 384; those of the rule / 224: 512 x 4096 x 4096 12.6 /
+// 13.1, 2001 x 2880 x 5761 34.9 / 37.3).  Grouped: as many as there can
 // be, as experts' rows are uneven and a remainder costs a tile of its own (32768
 // rows over 64 experts 175 us, by the rule for an even spread 186).
 int pair_rows(const Fp8MatmulArgs& a) {
@@ -691,7 +691,7 @@ int pair_rows(const Fp8MatmulArgs& a) {
   const int64_t wide = ((a.back ? a.K : a.N) + 2 * kTileM - 1) / (2 * kTileM);
   int64_t least = INT64_MAX;
   for (int bn = F8PairRing::bn; bn >= 64; bn -= 32) {
-    const int64_t tiles = (a.R + bn - 1) / bn * wide, time = (tiles + kSms / 2 - 1) / (kSms / 2) * std::max(400, 5 * bn / 2);
+    const int64_t tiles = (a.R + bn - 1) / bn * wide, time = (tiles + kSms / 2 - 1) / (kSms / 2) * (265 + bn);
     if (time < least) {
       least = time;
       best = bn;
