@@ -48,6 +48,27 @@ def test_dense(ops, R, N, K, dtype):
     assert ops.weight_grad(dy, x).dtype == DT[dtype]
 
 
+# A sum in the tensor core is cut off towards zero: in one piece of 12800 rows it
+# would be some 1.5e-5 off.  32-bit results are summed in pieces of 640 rows: off
+# by some 8e-7 each, and the rounded sum of 20 pieces (20 2^-24) less than that.
+@pytest.mark.parametrize("N,K", [(96, 130), (1100, 1500), (300, 264)])
+@pytest.mark.parametrize("R", [640, 641, 1290, 12800])
+@pytest.mark.parametrize("dtype", HALF)
+def test_long_sums_keep_their_precision(ops, N, K, R, dtype):
+    g = torch.Generator(device="cuda").manual_seed(R + N)
+    dy, x = (torch.randn((R, n), generator=g, device="cuda").to(DT[dtype]) for n in (N, K))
+    want = dy.double().T @ x.double()
+    got = ops.weight_grad(dy, x, out_dtype=torch.float32)
+    assert float((got.double() - want).norm()) <= 2e-6 * float(want.norm())
+    # with experts: a short one before, a long one, one without rows
+    if R > 700:
+        plan = ops.expert_sort(torch.where(torch.arange(R, device="cuda") < 37, 0, 1).int().unsqueeze(1), 3)
+        grouped = ops.weight_grad(dy, x, plan=plan, out_dtype=torch.float32)
+        for e, rows in enumerate((slice(0, 37), slice(37, R), slice(0, 0))):
+            want = dy[rows].double().T @ x[rows].double()
+            assert float((grouped[e].double() - want).norm()) <= 2e-6 * float(want.norm())
+
+
 # (T, E, k, N, K, drop)
 GROUPED = [(1, 4, 1, 64, 64, 0.0), (32, 128, 8, 96, 256, 0.0), (50, 3, 2, 200, 160, 0.2), (700, 4, 2, 300, 288, 0.1),
            (33, 1024, 3, 40, 64, 0.0), (9, 2, 1, 128, 512, 1.0), (2000, 5, 2, 64, 64, 0.05), (301, 7, 3, 129, 77, 0.0),

@@ -391,6 +391,7 @@ struct F8RowMaps {
   CUtensorMap of[F8PairRing::bn / 32];
 };
 constexpr int kF8PairThreads = 256 + 32 * kEpiWarps;
+constexpr int kF8Piece = 48;   // stages, for 32-bit results (relative error of 16384 values in one piece 1.2e-6, in three 4e-7)
 
 // One stage: up to four K = 32 MMAs of the pair and the commit that frees it.
 __device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sfw,
@@ -478,6 +479,8 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     n0 = ((tile - mt * ntw) * 2 + rank) * kTileM;
     return row_tile(a.E, tp, row0, args.bn, mt);
   };
+  // stages summed in the tensor core at a time: whole groups of scales (see add_tile)
+  const int piece = OUT == QMOE_F32 ? kF8Piece : ksteps;
   // rows of A of each CTA: half of the tile's, in whole sixteens
   auto half_of = [&](const RowTile& t) { return ((t.rows + 31) & ~31) / 2; };
 
@@ -531,10 +534,18 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       int n0;
       const RowTile t = tile_of(tile, n0);
       const uint32_t idesc0 = idesc_mxf8(2 * kTileM, 2 * half_of(t), a.back);
-      const int ab = tc & 1;
-      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
-      for (int ks = 0; ks < ksteps && ok; ++ks) {
+      int left = 0;   // stages of this piece
+      for (int ks = 0; ks < ksteps && ok; ++ks, --left) {
         const int id = ks & 3, s = at.s;
+        if (left == 0) {
+          if (ks) {
+            tc_commit_pair_elect(&acc_full[tc & 1]);
+            ++tc;
+          }
+          left = piece;
+          ok = warp_spin_cluster(&acc_empty[tc & 1], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+          if (!ok) break;
+        }
         if (id == 0) {
           // (asked for ahead as well)
           ok = __shfl_sync(0xffffffffu, sf_there, 0) || warp_spin_cluster(&sf_full[sf.s], sf.ph, a.wait, abort_flag);
@@ -549,8 +560,8 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         there = mbar_test_wait(&full[at.s], at.ph);
         tc_fence_after();
         const uint32_t sft = tmem + RG::sf_col0 + sf.s * RG::sf_cols;
-        f8_pair_stage_elect(tmem + ab * BN, wdesc0 + (uint32_t)((s * RG::w_bytes) >> 4), wstep, adesc0 + (uint32_t)((s * RG::a_bytes) >> 4),
-                            idesc0 | (uint32_t)id << 29 | (uint32_t)id << 4, sft, sft + 4, ks != 0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail,
+        f8_pair_stage_elect(tmem + (tc & 1) * BN, wdesc0 + (uint32_t)((s * RG::w_bytes) >> 4), wstep, adesc0 + (uint32_t)((s * RG::a_bytes) >> 4),
+                            idesc0 | (uint32_t)id << 29 | (uint32_t)id << 4, sft, sft + 4, left != piece ? 1u : 0u, ks + 1 < ksteps ? 4 : tail,
                             &empty[s]);
         if (id == 3 || ks + 1 == ksteps) {
           tc_commit_pair_elect(&sf_empty[sf.s]);
@@ -558,7 +569,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
           sf_there = cluster_test_wait(&sf_full[sf.s], sf.ph);
         }
       }
-      if (ok) tc_commit_pair_elect(&acc_full[ab]);
+      if (ok) tc_commit_pair_elect(&acc_full[tc & 1]);
     }
     tc_commit_pair_here_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -621,16 +632,19 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         store_zeros<OUT>(out, a.ld_out, t.rows, in, half);
         continue;
       }
-      const int ab = tc & 1;
-      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * BN, out, a.ld_out, t.rows, in, half);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
-      ++tc;
+      for (int ks = 0; ks < ksteps; ks += piece, ++tc) {
+        const int ab = tc & 1;
+        ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * BN;
+        if (OUT == QMOE_F32 && ks) add_tile(acc, reinterpret_cast<float*>(out), a.ld_out, t.rows, in, half);
+        else store_tile<OUT>(acc, out, a.ld_out, t.rows, in, half);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      }
     }
   }
   __syncwarp();

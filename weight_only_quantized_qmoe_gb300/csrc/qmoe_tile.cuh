@@ -233,6 +233,31 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, typename ElemT<OUT>::
     }
   }
 }
+// The same added to what is there (32-bit results).  The tensor core cuts off what
+// an addition to its accumulator leaves over, always towards zero, so that a long
+// sum falls short by a share that grows with its length (2^-25.6 of it an MMA):
+// 32-bit results of long reductions are summed in pieces, and the pieces here, to
+// nearest, by the thread that stored the first one.
+__device__ __forceinline__ void add_tile(uint32_t taddr, float* out, int64_t ld, int n, bool in, int half) {
+  out += (size_t)(half * 32) * ld;
+  for (int c0 = half * 32; c0 < n; c0 += 64, out += (size_t)64 * ld) {
+    uint32_t v[32];
+    TC_LD32(taddr + c0, v);
+    tc_wait_ld();
+    if (!in) continue;
+    float* p = out;
+#pragma unroll
+    for (int b = 0; b < 32; b += 16) {   // sixteen loads under way
+      float was[16];
+      float* q = p;
+#pragma unroll
+      for (int c = 0; c < 16; ++c, q += ld) was[c] = c0 + b + c < n ? *q : 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c, p += ld)
+        if (c0 + b + c < n) *p = was[c] + __uint_as_float(v[b + c]);
+    }
+  }
+}
 template <int OUT>
 __device__ __forceinline__ void store_zeros(typename ElemT<OUT>::t* out, int64_t ld, int n, bool in, int half) {
   if (in)

@@ -33,6 +33,13 @@ constexpr int kWgPanelBytes = kWgRows * 128;
 constexpr int kWgThreads = 128 + 32 * kEpiWarps;
 constexpr int kWgBN = 256;
 constexpr long long kWgDrainPolls = 4096;
+// Rows summed in the tensor core at a time for 32-bit results (see add_tile; of
+// normal values, relative error of 1024 rows in one piece 1.2e-6, of 32768 3.8e-5).
+constexpr int kWgPiece = 10 * kWgRows;
+template <int OUT>
+__device__ __forceinline__ int piece_end(int from, int hi) {
+  return OUT == QMOE_F32 && hi - from > kWgPiece ? from + kWgPiece : hi;
+}
 
 struct WgRing {
   static constexpr int stages = 4;
@@ -110,6 +117,25 @@ struct WgTile {
   int e, n0, k0, lo, hi;   // this CTA's rows of it
 };
 
+// sum = piece, or sum + piece, of a warp's share of a tile's columns, in TMEM.
+__device__ __forceinline__ void add_pieces(uint32_t sum, uint32_t piece, int n, int half, bool first) {
+  for (int c0 = half * 32; c0 < n; c0 += 64) {
+    uint32_t v[32];
+    TC_LD32(piece + c0, v);
+    if (!first) {
+      uint32_t w[32];
+      TC_LD32(sum + c0, w);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(w[c]) + __uint_as_float(v[c]));
+    } else {
+      tc_wait_ld();
+    }
+    TC_ST32(sum + c0, v);
+  }
+  tc_wait_st();
+}
+
 // SPLIT: a cluster shares each tile's rows, and there is one tile a cluster at
 // most.
 template <int OUT, bool SPLIT>
@@ -118,6 +144,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   using RG = WgRing;
   using T = typename ElemT<OUT>::t;
   constexpr int S = RG::stages;
+  constexpr bool kInPieces = OUT == QMOE_F32;   // one accumulator for a piece, the other for their sum
   extern __shared__ __align__(1024) uint8_t wg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(wg_smem_raw) + 1023) & ~uintptr_t(1023));
   const WgradArgs& a = args.a;
@@ -215,30 +242,31 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const WgTile t = tile_of(tile);
       if (t.lo >= t.hi) continue;
       const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, kTileM, (min(kWgBN, a.N - t.n0) + 15) & ~15);
-      const int ab = tc & 1;
-      ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      for (int r = t.lo; r < t.hi; r += kWgRows, ++it) {
-        const int s = it % S;
-        if (!warp_test_wait(&full[s], (it / S) & 1)) {
-          ok = spin_or_abort(&full[s], (it / S) & 1, a.wait, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+      for (int lo = t.lo, end; lo < t.hi && ok; lo = end, ++tc) {
+        end = piece_end<OUT>(lo, t.hi);
+        const int ab = kInPieces ? 0 : tc & 1, use = kInPieces ? tc : tc >> 1;
+        ok = spin_or_abort(&acc_empty[ab], (use & 1) ^ 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        for (int r = lo; r < end && ok; r += kWgRows, ++it) {
+          const int s = it % S;
+          if (!warp_test_wait(&full[s], (it / S) & 1)) {
+            ok = spin_or_abort(&full[s], (it / S) & 1, a.wait, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          const int rows = min(kWgRows, end - r);
+          if (rows & 15) {
+            zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::x_panels, rows);
+            zero_rows(smem + RG::dy_off + s * RG::dy_bytes, min(RG::dy_panels, (a.N - t.n0 + kWgPanel - 1) / kWgPanel), rows);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          tc_fence_after();
+          wg_stage_elect<1>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4),
+                            idesc, r != lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
         }
-        const int rows = min(kWgRows, t.hi - r), nk = (rows + 15) / 16;
-        if (rows & 15) {
-          zero_rows(smem + RG::x_off + s * RG::x_bytes, RG::x_panels, rows);
-          zero_rows(smem + RG::dy_off + s * RG::dy_bytes, min(RG::dy_panels, (a.N - t.n0 + kWgPanel - 1) / kWgPanel), rows);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        wg_stage_elect<1>(tmem + ab * kWgBN, xdesc0 + (uint64_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint64_t)((s * RG::dy_bytes) >> 4), idesc,
-                       r != t.lo ? 1u : 0u, nk, &empty[s]);
+        if (ok) tc_commit_elect(&acc_full[ab]);
       }
-      if (ok) tc_commit_elect(&acc_full[ab]);
-      ++tc;
     }
     tc_commit_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -262,18 +290,27 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         }
         continue;
       }
-      const int ab = tc & 1;
-      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
-      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem), q, n, half);   // the ring is empty
-      else store_tile<OUT>(acc, out, a.K, n, in, half);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[ab]);
-      ++tc;
+      for (int lo = t.lo, end; lo < t.hi; lo = end, ++tc) {
+        end = piece_end<OUT>(lo, t.hi);
+        const int ab = kInPieces ? 0 : tc & 1, use = kInPieces ? tc : tc >> 1;
+        ok = wait_or_abort(&acc_full[ab], use & 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
+        if constexpr (kInPieces) {
+          // the sum of the pieces, in the second accumulator
+          if (lo != t.lo || end < t.hi) add_pieces(acc + kWgBN, acc, n, half, lo == t.lo);
+          if (lo != t.lo) acc += kWgBN;
+        }
+        if (end == t.hi) {
+          if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem), q, n, half);   // the ring is empty
+          else store_tile<OUT>(acc, out, a.K, n, in, half);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      }
     }
   }
   if constexpr (SPLIT) {
@@ -450,24 +487,25 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       if (t.lo >= t.hi) continue;
       const int half = half_of(t);
       const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, 2 * kTileM, 2 * half);
-      const int ab = tc & 1;
-      ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
-      if (!ok) break;
-      for (int r = t.lo; r < t.hi; r += kWgRows) {
-        const int s = at.s, rows = min(kWgRows, t.hi - r);
-        if (!__shfl_sync(0xffffffffu, there, 0)) {
-          ok = spin_or_abort(&full[s], at.ph, a.wait, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+      for (int lo = t.lo, end; lo < t.hi && ok; lo = end, ++tc) {
+        end = piece_end<OUT>(lo, t.hi);
+        const int ab = tc & 1;
+        ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+        for (int r = lo; r < end && ok; r += kWgRows) {
+          const int s = at.s, rows = min(kWgRows, end - r);
+          if (!__shfl_sync(0xffffffffu, there, 0)) {
+            ok = spin_or_abort(&full[s], at.ph, a.wait, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          at.step();
+          there = mbar_test_wait(&full[at.s], at.ph);
+          tc_fence_after();
+          wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint32_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint32_t)((s * RG::dy_bytes) >> 4),
+                            idesc, r != lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
         }
-        at.step();
-        there = mbar_test_wait(&full[at.s], at.ph);
-        tc_fence_after();
-        wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint32_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint32_t)((s * RG::dy_bytes) >> 4),
-                          idesc, r != t.lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
+        if (ok) tc_commit_pair_elect(&acc_full[ab]);
       }
-      if (ok) tc_commit_pair_elect(&acc_full[ab]);
-      ++tc;
     }
     tc_commit_pair_here_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -486,16 +524,19 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         store_zeros<OUT>(out, a.K, n, in, half);
         continue;
       }
-      const int ab = tc & 1;
-      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      store_tile<OUT>(tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN, out, a.K, n, in, half);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
-      ++tc;
+      for (int lo = t.lo; lo < t.hi; lo = piece_end<OUT>(lo, t.hi), ++tc) {
+        const int ab = tc & 1;
+        ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
+        if (OUT == QMOE_F32 && lo != t.lo) add_tile(acc, reinterpret_cast<float*>(out), a.K, n, in, half);
+        else store_tile<OUT>(acc, out, a.K, n, in, half);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      }
     }
   }
   __syncwarp();
