@@ -596,7 +596,7 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_
  *           (QMOE_F32: UNSUPPORTED)
  *   dw_dev  out_dtype [experts, n, k]
  * qmoe_weight_grad_workspace: bytes of workspace (128-byte aligned) for operands
- * with these addresses and strides: 512 bytes an expert where there are many
+ * with these addresses and strides: 256 bytes an expert where there are many
  * tiles, and a copy of an operand whose rows do not start on 16-byte boundaries.
  */
 size_t qmoe_weight_grad_workspace(const void* dy_dev, int64_t ld_dy, const void* x_dev, int64_t ld_x, int64_t rows, int experts,

@@ -76,7 +76,7 @@ def test_weight_gradient():
     assert need(P, 16, P, 32, 8, 2, 16, 32) == 0 and need(P, 2048, P, 2048, 8, 1, 2048, 2048) == 0
     assert need(P + 2, 16, P, 32, 8, 1, 16, 32) == 8 * 16 * 2 and need(P, 16, P, 33, 8, 1, 16, 31) == 8 * 32 * 2
     assert need(P, 17, P + 8, 32, 8, 1, 16, 30) == 8 * (16 + 32) * 2 and need(P, 17, P, 33, 0, 1, 16, 32) == 0
-    assert need(P, 4096, P, 4096, 8, 16, 4096, 4096) == 16 * 512 and need(P, 17, P, 33, 8, 0, 16, 32) == 0
+    assert need(P, 4096, P, 4096, 8, 16, 4096, 4096) == 16 * 256 and need(P, 17, P, 33, 8, 0, 16, 32) == 0
 
 
 NEW = ["qmoe_choice.cu", "qmoe_fp8.cu", "qmoe_fp8_gemm.cu", "qmoe_wgrad.cu", "qmoe_tile.cuh", "qmoe_tma.cuh"]

@@ -35,7 +35,7 @@ constexpr int kWgBN = 256;
 constexpr long long kWgDrainPolls = 4096;
 // Rows summed in the tensor core at a time for 32-bit results (see add_tile; of
 // normal values, relative error of 1024 rows in one piece 1.2e-6, of 32768 3.8e-5).
-constexpr int kWgPiece = 10 * kWgRows;
+constexpr int kWgPiece = 5 * 128;
 template <int OUT>
 __device__ __forceinline__ int piece_end(int from, int hi) {
   return OUT == QMOE_F32 && hi - from > kWgPiece ? from + kWgPiece : hi;
@@ -65,9 +65,9 @@ __device__ __forceinline__ void zero_rows(uint8_t* base, int panels, int rows) {
       reinterpret_cast<uint4*>(base + p * kWgPanelBytes + rows * 128)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Up to four K = 16 MMAs of a stage and the commit that frees it, by one elected
-// lane of a CTA or of the first CTA of a pair; 16 rows on is 2048 bytes in either
-// operand.
+// Up to four K = 16 MMAs of 64 rows, and the commit that frees their stage if they
+// are its last, by one elected lane of a CTA or of the first CTA of a pair; 16 rows
+// on is 2048 bytes in either operand.
 template <int CTAS>
 __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t dy, uint32_t idesc, uint32_t acc, int nk, uint64_t* empty) {
   if constexpr (CTAS == 1) {
@@ -84,7 +84,7 @@ __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t 
         "@q3 tcgen05.mma.cta_group::1.kind::f16 [%0], y3, z3, %3, p1;\n\t}" ::"r"(d),
         "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
         : "memory");
-    tc_commit_elect(empty);
+    if (empty) tc_commit_elect(empty);
   } else {
     asm volatile(
         "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
@@ -99,7 +99,7 @@ __device__ __forceinline__ void wg_stage_elect(uint32_t d, uint64_t x, uint64_t 
         "@q3 tcgen05.mma.cta_group::2.kind::f16 [%0], y3, z3, %3, p1;\n\t}" ::"r"(d),
         "l"(x), "l"(dy), "r"(idesc), "r"(acc), "r"(nk)
         : "memory");
-    tc_commit_pair_elect(empty);
+    if (empty) tc_commit_pair_elect(empty);
   }
 }
 
@@ -332,19 +332,22 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 }
 
 // The same with pairs of CTAs: tiles of 256 columns of x by up to 256 of dy, of
-// which each CTA loads half.  Nothing is overwritten with zeros here: copies of an
+// which each CTA loads half, 128 rows a stage: a copy of 64 rows hardly takes the
+// TMA unit less time than one of 128.  Nothing is overwritten with zeros here: copies of an
 // expert's rows go by tensor maps whose rows end with the expert's, so that what
 // lies behind reads as zeros (a warp of each CTA that wrote the zeros, and their
 // arrival at the first CTA, took 3000 cycles a tile).  A kernel before this one
-// makes them, four for each expert.
+// makes them, two for each expert.
+constexpr int kWgPairRows = 128;
 struct WgMaps {
-  CUtensorMap x, x2, dy, dy2;   // panels of 64 columns by 64 rows; two of them in one copy
+  CUtensorMap x, dy;   // copies of 64 columns by 128 rows
 };
 struct WgPairRing {
-  static constexpr int stages = 6;
+  static constexpr int stages = 3;
   static constexpr int panels = 2;                              // of x, and of a half of dy's columns
-  static constexpr int x_bytes = panels * kWgPanelBytes;
-  static constexpr int dy_bytes = panels * kWgPanelBytes;
+  static constexpr int panel_bytes = kWgPairRows * 128;
+  static constexpr int x_bytes = panels * panel_bytes;
+  static constexpr int dy_bytes = panels * panel_bytes;
   static constexpr int x_off = 0;
   static constexpr int dy_off = x_off + stages * x_bytes;
   static constexpr int bar_off = dy_off + stages * dy_bytes;
@@ -361,14 +364,14 @@ __global__ void __launch_bounds__(32) weight_grad_maps_kernel(const __grid_const
   const int e = blockIdx.x, lane = threadIdx.x;
   const int hi = min(max(offsets[e + 1], 0), (int)R);
   if (hi == 0) return;
-  static_assert(sizeof(WgMaps) == 32 * sizeof(uint4), "a piece a lane");
-  reinterpret_cast<uint4*>(&mine)[lane] = reinterpret_cast<const uint4*>(&maps)[lane];
+  static_assert(sizeof(WgMaps) == 32 * sizeof(uint2), "a piece a lane");
+  reinterpret_cast<uint2*>(&mine)[lane] = reinterpret_cast<const uint2*>(&maps)[lane];
   __syncwarp();
-  if (lane < 4)
+  if (lane < 2)
     asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(&mine) + lane * 128), "r"(hi) : "memory");
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
                      reinterpret_cast<uint8_t*>(out + e) + i * 128),
                  "r"(smem_u32(&mine) + i * 128)
@@ -446,17 +449,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       for (int tile = first; tile < total && ok; tile += stride) {
         const WgTile t = tile_of(tile);
         const int half = half_of(t), panels = (half + kWgPanel - 1) / kWgPanel, col0 = t.n0 + rank * half;
-        const uint32_t bytes = (uint32_t)(2 * (RG::panels + panels) * kWgPanelBytes);
+        const uint32_t bytes = (uint32_t)(2 * (RG::panels + panels) * RG::panel_bytes);
         const WgMaps* m = by_expert ? by_expert + t.e : &maps;
         // warp 0's operand, or warp 2's
-        const CUtensorMap *one = warp == 0 ? &m->x : &m->dy, *two = warp == 0 ? &m->x2 : &m->dy2;
+        const CUtensorMap* map = warp == 0 ? &m->x : &m->dy;
         const int from = warp == 0 ? t.k0 : col0, copies = warp == 0 ? RG::panels : panels;
-        const bool both = from % kWgPanel == 0 && copies == 2 && from + 2 * kWgPanel <= (warp == 0 ? a.K : a.N);
-        if (by_expert && t.lo < t.hi) {
-          acquire_map(one);
-          acquire_map(two);
-        }
-        for (int r = t.lo; r < t.hi; r += kWgRows, ++it, at.step()) {
+        if (by_expert && t.lo < t.hi) acquire_map(map);
+        for (int r = t.lo; r < t.hi; r += kWgPairRows, ++it, at.step()) {
           const int s = at.s;
           ok = poll_or_wait(&empty[s], at.ph ^ 1u, a.wait, abort_flag);
           if (!ok) break;
@@ -465,9 +464,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           // Test hook: the first stage's barrier is armed, its copies are never issued.
           if (args.inject_stall && it == 0) continue;
           uint8_t* dst = warp == 0 ? smem + RG::x_off + s * RG::x_bytes : smem + RG::dy_off + s * RG::dy_bytes;
-          if (both) tma_3d_pair(dst, two, 0, r, from / kWgPanel, bar);
-          else
-            for (int p = 0; p < copies; ++p) tma_3d_pair(dst + p * kWgPanelBytes, one, from + p * kWgPanel, r, 0, bar);
+          for (int p = 0; p < copies; ++p) tma_3d_pair(dst + p * RG::panel_bytes, map, from + p * kWgPanel, r, 0, bar);
         }
       }
       // (both CTAs' copies count on the first one's barriers; the second one's own
@@ -476,8 +473,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
-    const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), kWgPanelBytes);
-    const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), kWgPanelBytes);
+    const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), RG::panel_bytes);
+    const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), RG::panel_bytes);
     RingAt<S> at;
     int tc = 0;
     bool ok = true;
@@ -491,8 +488,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         end = piece_end<OUT>(lo, t.hi);
         const int ab = tc & 1;
         ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
-        for (int r = lo; r < end && ok; r += kWgRows) {
-          const int s = at.s, rows = min(kWgRows, end - r);
+        for (int r = lo; r < end && ok; r += kWgPairRows) {
+          const int s = at.s, rows = min(kWgPairRows, end - r);
           if (!__shfl_sync(0xffffffffu, there, 0)) {
             ok = spin_or_abort(&full[s], at.ph, a.wait, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -501,8 +498,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           at.step();
           there = mbar_test_wait(&full[at.s], at.ph);
           tc_fence_after();
-          wg_stage_elect<2>(tmem + ab * kWgBN, xdesc0 + (uint32_t)((s * RG::x_bytes) >> 4), dydesc0 + (uint32_t)((s * RG::dy_bytes) >> 4),
-                            idesc, r != lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
+          const uint64_t xd = xdesc0 + (uint32_t)((s * RG::x_bytes) >> 4), dyd = dydesc0 + (uint32_t)((s * RG::dy_bytes) >> 4);
+          constexpr uint32_t on = (kWgRows * 128) >> 4;   // 64 rows
+          wg_stage_elect<2>(tmem + ab * kWgBN, xd, dyd, idesc, r != lo ? 1u : 0u, (min(rows, kWgRows) + 15) / 16,
+                            rows > kWgRows ? nullptr : &empty[s]);
+          if (rows > kWgRows) wg_stage_elect<2>(tmem + ab * kWgBN, xd + on, dyd + on, idesc, 1u, (rows - kWgRows + 15) / 16, &empty[s]);
         }
         if (ok) tc_commit_pair_elect(&acc_full[ab]);
       }
@@ -630,30 +630,18 @@ cudaError_t align_operands(WgradArgs& a, cudaStream_t s) {
   return launch_op(align_rows_kernel, dim3(blocks), dim3(kAlignThreads), 0, s, c);
 }
 
-// 64 rows of two panels of 64 columns in one copy, of the columns that fill whole
-// panels.
-bool encode_panels(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t width, int64_t rows, int64_t ld) {
-  const EncodeFn f = encoder();
-  if (!f) return false;
-  const cuuint64_t dims[3] = {kWgPanel, (cuuint64_t)rows, (cuuint64_t)std::max<int64_t>(width / kWgPanel, 1)};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, kWgPanel * 2};
-  const cuuint32_t box[3] = {kWgPanel, kWgRows, 2}, ones[3] = {1, 1, 1};
-  return f(m, type, 3, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int OUT>
 cudaError_t launch_wg(const WgKernelArgs& args, cudaStream_t s) {
   const WgradArgs& a = args.a;
   WgMaps maps;
   const auto type = a.dtype == QMOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (!encode_tiles(&maps.x, type, 2, a.x, a.K, a.R, 1, a.ld_x * 2, kWgRows) ||
-      !encode_tiles(&maps.dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, kWgRows))
+  const bool pairs = wgrad_pairs(a.E, a.N, a.K);
+  const int box = pairs ? kWgPairRows : kWgRows;
+  if (!encode_tiles(&maps.x, type, 2, a.x, a.K, a.R, 1, a.ld_x * 2, box) ||
+      !encode_tiles(&maps.dy, type, 2, a.dy, a.N, a.R, 1, a.ld_dy * 2, box))
     return cudaErrorInvalidValue;
   const int64_t tiles = wgrad_tiles(a.E, a.N, a.K);
-  if (wgrad_pairs(a.E, a.N, a.K)) {
-    if (!encode_panels(&maps.x2, type, a.x, a.K, a.R, a.ld_x) || !encode_panels(&maps.dy2, type, a.dy, a.N, a.R, a.ld_dy))
-      return cudaErrorInvalidValue;
+  if (pairs) {
     WgMaps* by_expert = a.offsets ? reinterpret_cast<WgMaps*>(a.workspace) : nullptr;
     if (by_expert) {
       const cudaError_t e = launch_op(weight_grad_maps_kernel, dim3((unsigned)a.E), dim3(32), 0, s, maps, a.offsets, a.R, by_expert);
