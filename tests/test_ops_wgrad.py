@@ -200,6 +200,16 @@ def test_linear_and_its_gradients(ops, T, E, k, N, K, drop, dtype, wdtype):
     assert torch.equal(ops.fp8_linear(x.detach(), q, plan=plan), y.detach()) and torch.equal(ops.fp8_linear(x.detach(), w.detach(), plan=plan), y.detach())
 
 
+@pytest.mark.parametrize("grouped", [False, True])
+def test_linear_without_rows(ops, grouped):
+    x = torch.empty((0, 48), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    w = torch.randn((3, 20, 48) if grouped else (20, 48), device="cuda", requires_grad=True)
+    plan = ops.expert_sort(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 3) if grouped else None
+    y = ops.fp8_linear(x, w, plan=plan)
+    dx, dw = torch.autograd.grad(y, (x, w), torch.empty_like(y))
+    assert y.shape == (0, 20) and dx.shape == x.shape and dw.shape == w.shape and (dw == 0).all()
+
+
 def test_gradients_by_differences(ops):
     # operands that quantise to themselves, and a dy that does: the layer is then
     # linear in both, and differences with steps on the grid are exact

@@ -10,9 +10,15 @@
 // bits can tell, the warp repeats the token's choice in 64.  With keys that are
 // the logits themselves nothing is rounded and nothing repeated.
 //
-// Bound: latency.  A warp takes a token: lane l holds the logits of experts l,
-// l + 32, ..., a rank is one redux for the best key and one for the lowest index
-// at it.  The logits are read once, two 4-byte words a token and rank written.
+// Bound: instructions and latency.  A warp takes a token: lane l holds the logits of
+// experts l, l + 32, ..., sorted; a rank is one redux for the best key and one for
+// the lowest index at it.  The logits are read once, two 4-byte words a token and
+// rank written.  (8192 tokens, eight of 256 experts in f32, 8.4 MB: softmax 10.5 us,
+// sigmoid with a bias 14.5, with the four best of eight groups 17 to 20, softmax
+// with a bias 23; the gradient 4.3.  Half of the issue slots are used.  Few tokens
+// are repeated in 64 bits, some ten of these, but one that is takes as long as a
+// third of the others together; more CTAs, fewer registers or a warp that loads its
+// next token's logits early changed nothing.)
 #include <algorithm>
 #include <climits>
 

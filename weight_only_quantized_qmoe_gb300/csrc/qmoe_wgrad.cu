@@ -22,6 +22,10 @@
 // their parts in a fixed order.  Operands that TMA cannot read (rows that do not
 // start on 16 bytes) are copied to rows that do first.
 //
+// That is the form for few tiles (rows of 7 experts, 429 each, 1001 x 513: 9.5 us, and
+// 4.6 for the aligned copies; the launch, one round of the ring and the stores bound
+// it); more take pairs of CTAs, further down.
+//
 // Every wait is bounded, as in the products' kernels.
 #include "qmoe_tile.cuh"
 
@@ -337,7 +341,11 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 // expert's rows go by tensor maps whose rows end with the expert's, so that what
 // lies behind reads as zeros (a warp of each CTA that wrote the zeros, and their
 // arrival at the first CTA, took 3000 cycles a tile).  A kernel before this one
-// makes them, two for each expert.
+// makes them, two for each expert (4 us alone).
+// Bound: the MMAs, the copies at 2.4 cycles a row of 128 bytes and, with few rows an
+// expert, the stores (8192 rows of 8192 x 8192: 652 us, 1.69 PFLOP/s, 89 % of the
+// measured bf16 rate; 32768 rows of 64 experts, 4096 x 1536: 290 us, 1.42 PFLOP/s and
+// 4.0 TB/s of what has to move).
 constexpr int kWgPairRows = 128;
 struct WgMaps {
   CUtensorMap x, dy;   // copies of 64 columns by 128 rows

@@ -194,7 +194,8 @@ def expert_route(logits, k, scoring="softmax", bias=None, groups=1, top_groups=N
     experts are chosen from, the groups with the largest sum of their
     ``group_best`` (1 or 2) best.  Ties go to the lower index.  Weights are scale *
     score, with ``renormalize`` divided by the sum of the chosen scores.  Experts
-    with a logit of -inf are not chosen (id -1, weight 0 where none is left)."""
+    with a logit of -inf are not chosen (id -1, weight 0 where none is left).  The
+    weights have a gradient to the logits; the choice, and so the bias, has none."""
     if stream is not None:
         return _elsewhere(stream, expert_route, logits, k, scoring, bias, groups, top_groups, group_best, renormalize, scale)
     args = logits, k, bias, _scoring(scoring), groups, groups if top_groups is None else top_groups, group_best, renormalize, scale
