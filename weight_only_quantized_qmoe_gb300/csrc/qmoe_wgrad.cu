@@ -337,11 +337,12 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 
 // The same with pairs of CTAs: tiles of 256 columns of x by up to 256 of dy, of
 // which each CTA loads half, 128 rows a stage: a copy of 64 rows hardly takes the
-// TMA unit less time than one of 128.  Nothing is overwritten with zeros here: copies of an
-// expert's rows go by tensor maps whose rows end with the expert's, so that what
-// lies behind reads as zeros (a warp of each CTA that wrote the zeros, and their
-// arrival at the first CTA, took 3000 cycles a tile).  A kernel before this one
-// makes them, two for each expert (4 us alone).
+// TMA unit less time than one of 128.  Nothing is overwritten with zeros here:
+// copies of an expert's rows go by tensor maps whose rows end with the expert's, so
+// that what lies behind reads as zeros (a warp of each CTA that wrote the zeros, and
+// their arrival at the first CTA, took 3000 cycles a tile).  A kernel before this
+// one makes them, two for each expert (4 us alone).
+//
 // Bound: the MMAs, the copies at 2.4 cycles a row of 128 bytes and, with few rows an
 // expert, the stores (8192 rows of 8192 x 8192: 652 us, 1.69 PFLOP/s, 89 % of the
 // measured bf16 rate; 32768 rows of 64 experts, 4096 x 1536: 290 us, 1.42 PFLOP/s and
