@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  __syncwarp();   // the lanes of warp 1 leave its last wait one by one
   if (warp == 1) tmem_dealloc(tmem, RG::tmem_cols);
 }
 
@@ -585,7 +586,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       }
       if (ok) tc_commit_pair_elect(&acc_full[tc & 1]);
     }
-    tc_commit_pair_here_elect(drain_bar);
+    tc_commit_pair_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
     mbar_wait_bounded(drain_bar, 0, drain);
   } else if (warp >= 4 && warp < 8) {
@@ -664,8 +665,9 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
+  pair_end(drain_bar, rank, a.wait.status);   // neither CTA leaves, or frees TMEM, while the other may still use it
   tc_fence_after();
+  __syncwarp();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 

@@ -56,8 +56,7 @@ __device__ __forceinline__ int pair_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   return (int)rank;
 }
-// Arrives, when the MMAs issued so far are done, on the barrier of both CTAs; on
-// that of this one.
+// Arrives, when the MMAs issued so far are done, on the barrier of both CTAs.
 __device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -65,11 +64,19 @@ __device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void tc_commit_pair_here_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
+// All threads of all CTAs of the cluster.
+__device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();   // the barrier is the whole warp's, and lanes leave a wait one by one
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Last of a pair, behind a barrier of the CTA: the second CTA waits for the first
+// one's last commit (its multicast arrivals must not come to a CTA that has left;
+// by then they are all but there), then neither leaves before the other.
+__device__ __forceinline__ void pair_end(uint64_t* drain_bar, int rank, int* status) {
+  const WaitCfg drain{status, kDrainWaitLimit};
+  if (rank == 1 && threadIdx.x < 32) mbar_wait_bounded(drain_bar, 0, drain);
+  __syncthreads();
+  cluster_sync_all();
 }
 // A barrier's address in the first CTA.
 __device__ __forceinline__ uint32_t first_cta_bar(uint64_t* bar) {
@@ -219,6 +226,7 @@ __device__ __forceinline__ void store_tile(uint32_t taddr, typename ElemT<OUT>::
   out += (size_t)(half * 32) * ld;
   for (int c0 = half * 32; c0 < n; c0 += 64, out += (size_t)64 * ld) {
     uint32_t v[32];
+    __syncwarp();   // lanes outside left the last round early; the load is the whole warp's
     TC_LD32(taddr + c0, v);
     tc_wait_ld();
     if (!in) continue;
@@ -242,6 +250,7 @@ __device__ __forceinline__ void add_tile(uint32_t taddr, float* out, int64_t ld,
   out += (size_t)(half * 32) * ld;
   for (int c0 = half * 32; c0 < n; c0 += 64, out += (size_t)64 * ld) {
     uint32_t v[32];
+    __syncwarp();   // lanes outside left the last round early; the load is the whole warp's
     TC_LD32(taddr + c0, v);
     tc_wait_ld();
     if (!in) continue;
@@ -285,10 +294,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
-}
-// All threads of all CTAs of the cluster; converged warps.
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Four columns' loads from every rank are under way at once: each takes some 250
 // cycles, and added up one by one they were most of a small call's time (weight

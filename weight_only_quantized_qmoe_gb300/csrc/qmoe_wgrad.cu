@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  __syncwarp();   // the lanes of warp 1 leave its last wait one by one
   if (warp == 1) tmem_dealloc(tmem, RG::tmem_cols);
 }
 
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         if (ok) tc_commit_pair_elect(&acc_full[ab]);
       }
     }
-    tc_commit_pair_here_elect(drain_bar);
+    tc_commit_pair_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
     mbar_wait_bounded(drain_bar, 0, drain);
   } else if (warp >= 4) {
@@ -551,8 +552,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // neither CTA leaves, or frees TMEM, while the other may still use it
+  pair_end(drain_bar, rank, a.wait.status);   // neither CTA leaves, or frees TMEM, while the other may still use it
   tc_fence_after();
+  __syncwarp();
   if (warp == 1) tmem_dealloc_pair(tmem, 2 * kWgBN);
 }
 
