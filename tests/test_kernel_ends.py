@@ -1,0 +1,32 @@
+"""How the tensor-core kernels end, as their sources say it (no GPU needed: what goes
+wrong without it is a race, which nothing shows on purpose)."""
+import re
+
+import pytest
+
+from test_ops_sources import code
+
+
+def kernels(name):
+    """{kernel: its text}."""
+    found = re.findall(r"__global__\s+void[\s\S]*?\n}\n", code(name))
+    return {re.search(r"(\w+_kernel)\(", k).group(1): k for k in found}
+
+
+@pytest.mark.parametrize("name,kernel", [("qmoe_fp8_gemm.cu", "fp8_matmul_pair_kernel"), ("qmoe_wgrad.cu", "weight_grad_pair_kernel")])
+def test_every_commit_to_both_ctas_is_waited_for(name, kernel):
+    # a commit's arrival comes on its own: none may come to a CTA that has left, in
+    # the first CTA of the pair or the second
+    text = kernels(name)[kernel]
+    barriers = set(re.findall(r"(?:tc_commit_pair_elect\(|&)(\w*empty|acc_full|drain_bar)\b", text)) - {"acc_empty"}
+    assert barriers >= {"empty", "acc_full", "drain_bar"}
+    for bar in barriers:
+        if bar == "drain_bar":       # the issuer, and the other CTA
+            assert "mbar_wait_bounded(drain_bar, 0" in text and "pair_end(drain_bar, rank" in text
+        elif bar == "acc_full":      # the epilogue of either CTA
+            assert re.search(r"warp >= \d\) \{[\s\S]*wait_or_abort\(&acc_full\[ab\]", text)
+        else:                        # by a role that both CTAs have, whatever its waits gave
+            wait = re.search(r"\n *if \(warp == \d\) drain_ring<\w>\(%s, " % bar, text)
+            assert wait, bar
+            role = re.findall(r"\n  (?:} else )?if \((warp[^\n]*)\) {", text[:wait.start()])[-1]
+            assert "rank" not in role, (bar, role)

@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       // (both CTAs' copies count on the first one's barriers; the second one's own
       // never complete, so it waits for as long as the limit says)
       if (!ok) drain_ring<S>(full, it, a.wait.status, kF8DrainPolls);
+      if (warp == 0) drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kF8DrainPolls);   // see pair_end
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
     // weight block's word, the same for every row, to columns 0 to 3.
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     RingAt<G> sf;
+    int groups = 0;
     bool ok = true;
     for (int tile = first; tile < real && ok; tile += stride) {
       int n0;
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         next_w = lane < 4 && ks + lane < ksteps ? (uint32_t)w0[(ks + lane) * wstep] << (8 * lane) : 0u;
       };
       fetch(0);
-      for (int ks = 0; ks < ksteps; ks += 4, sf.step()) {
+      for (int ks = 0; ks < ksteps; ks += 4, ++groups, sf.step()) {
         uint32_t word[8], w = next_w;
 #pragma unroll
         for (int j = 0; j < 8; ++j) word[j] = next[j];
@@ -632,6 +634,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         if (lane == 0) cluster_bar_arrive(first_cta_bar(&sf_full[sf.s]));
       }
     }
+    if (warp == 4) drain_ring<G>(sf_empty, groups, a.wait.status, ok ? kDrainWaitLimit : kF8DrainPolls);   // see pair_end
   } else if (warp >= 8) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp >> 2) - 2;

@@ -69,9 +69,16 @@ __device__ __forceinline__ void cluster_sync_all() {
   __syncwarp();   // the barrier is the whole warp's, and lanes leave a wait one by one
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Last of a pair, behind a barrier of the CTA: the second CTA waits for the first
-// one's last commit (its multicast arrivals must not come to a CTA that has left;
-// by then they are all but there), then neither leaves before the other.
+// Last of a pair, behind a barrier of the CTA.  A commit arrives on its own, some
+// time after its MMAs, and nothing orders the arrivals of two commits: none may come
+// to a CTA that has left, where it would change another CTA's shared memory.  So both
+// CTAs wait for every one of them: a producer for the last phase of each stage's
+// barrier and a scale warp for that of each group's (drain_ring), the epilogue for
+// every accumulator, and here the second CTA for the issuer's last commit, as the
+// issuer did.  (After a wait that ran out the phases to come are not known: what the
+// issuer did commit arrives within the limits of these waits, thousands of MMAs long.)
+// Arrivals by threads come before their own arrival at the cluster's barrier, behind
+// which neither CTA leaves before the other.
 __device__ __forceinline__ void pair_end(uint64_t* drain_bar, int rank, int* status) {
   const WaitCfg drain{status, kDrainWaitLimit};
   if (rank == 1 && threadIdx.x < 32) mbar_wait_bounded(drain_bar, 0, drain);
@@ -85,8 +92,12 @@ __device__ __forceinline__ uint32_t first_cta_bar(uint64_t* bar) {
   return at;
 }
 // Arrivals of threads of both CTAs.  What they stand for is tensor memory read or
-// written; the tcgen05 fences on either side order that, and the arrival and the
-// wait are relaxed.
+// written (an accumulator that is free, scales that are there) and nothing in shared
+// or global memory, so the arrival and the wait are relaxed: the fences
+// tcgen05.fence::before_thread_sync and ::after_thread_sync order tensor memory
+// accesses against the instructions that order execution, of which an arrival and the
+// wait that observes it are one pair, relaxed or not; release and acquire would add
+// the order of ordinary memory (some 700 cycles each).
 __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -127,12 +138,13 @@ struct RingAt {
     }
   }
 };
-// After a wait that ran out: the copies in flight must land before the CTA leaves.
-// Waits for the barriers of the last S of `it` stages, with a limit.
+// Waits for the barriers of the last S of `it` stages, with a limit: for copies in
+// flight (after a wait that ran out they must land before the CTA leaves), or for the
+// commits that free the stages.
 template <int S>
-__device__ __forceinline__ void drain_ring(uint64_t* full, int it, int* status, long long polls) {
+__device__ __forceinline__ void drain_ring(uint64_t* bars, int it, int* status, long long polls) {
   const WaitCfg drain{status, polls};
-  for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
+  for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&bars[i % S], (i / S) & 1, drain);
 }
 // spin_or_abort for such a phase: one answer for the whole warp.
 __device__ __forceinline__ bool warp_spin_cluster(uint64_t* bar, uint32_t parity, const WaitCfg& w, volatile int* abort_flag) {

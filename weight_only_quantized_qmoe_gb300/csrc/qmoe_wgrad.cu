@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       // (both CTAs' copies count on the first one's barriers; the second one's own
       // never complete, so it waits for as long as the limit says)
       if (!ok) drain_ring<S>(full, it, a.wait.status, kWgDrainPolls);
+      if (warp == 0) drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kWgDrainPolls);   // see pair_end
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
