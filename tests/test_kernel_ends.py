@@ -30,3 +30,22 @@ def test_every_commit_to_both_ctas_is_waited_for(name, kernel):
             assert wait, bar
             role = re.findall(r"\n  (?:} else )?if \((warp[^\n]*)\) {", text[:wait.start()])[-1]
             assert "rank" not in role, (bar, role)
+
+
+WITH_TMEM = ["qmoe_prefill.cu", "qmoe_mx4_gemm.cu", "qmoe_fp8_gemm.cu", "qmoe_wgrad.cu"]
+
+
+@pytest.mark.parametrize("name", WITH_TMEM)
+def test_a_whole_warp_releases_tensor_memory(name):
+    # the lanes of the issuing warp leave its last wait one by one, and a barrier of
+    # the CTA does not bring them together again for an instruction of a whole warp
+    releases = re.findall(r"([^\n]*)\n[ \t]*if \(warp == 1\) tmem_dealloc\w*\(", re.sub(r"[ \t]+\n", "\n", code(name)))
+    assert releases and all(line.strip() == "__syncwarp();" for line in releases), releases
+
+
+def test_no_other_kernel_has_tensor_memory():
+    import os
+
+    from test_ops_sources import CSRC
+    users = [n for n in sorted(os.listdir(CSRC)) if n.endswith((".cu", ".cuh")) and re.search(r"\btmem_dealloc\w*\(tmem", code(n))]
+    assert users == sorted(WITH_TMEM)

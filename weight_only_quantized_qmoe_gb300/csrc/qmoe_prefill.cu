@@ -945,6 +945,7 @@ __global__ void __launch_bounds__((Ring<DEC, BITS>::threads), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  __syncwarp();   // the lanes of warp 1 leave its last wait one by one
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
