@@ -59,6 +59,9 @@ __device__ double softmax_sum64(const typename ElemT<DT>::t* row, int E, double 
   return warp_sum(sum);
 }
 
+// The value of an order key (topk_order_key).
+__device__ __forceinline__ float ordered_float(int key) { return __int_as_float(key ^ ((key >> 31) & INT_MAX)); }
+
 // The two largest of a warp's values, in every lane (`lanes` of them that go together).
 template <typename F>
 __device__ __forceinline__ void two_best(F& a1, F& a2, int lanes) {
@@ -110,10 +113,11 @@ __device__ __noinline__ unsigned best_groups64(const ChoiceArgs& a, const typena
 }
 
 // The top_groups best groups, a bit each.  c: as above, in shared memory.  A
-// group's score is its best, or the sum of its two best (one where it has one); the
-// lanes are shared among the groups.  by_score: c is rounded, by tau of each value
-// and its own rounding; groups that are too near to the border to be told apart go
-// by their scores in 64 bits.
+// group's score is its best, or the sum of its two best (one where it has one; half of
+// it here, which cannot overflow); the lanes are shared among the groups.  by_score: c
+// is rounded, by tau / 2 of each value and 2^-24 of its own size, and of the terms of a
+// sum that nearly cancel both show.  Groups whose bounds reach over the border go by
+// their scores in 64 bits.
 template <int DT>
 __device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typename ElemT<DT>::t* row, const float* c, float mx,
                                                 bool by_score, float tau) {
@@ -129,20 +133,29 @@ __device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typen
       a1 = fmaxf(a1, v);
     }
   two_best(a1, a2, per);
+  float size = fabsf(a1);   // of its terms
+  if (a.best == 2) {
+    const float second = a2 == -INFINITY ? 0.f : 0.5f * a2;
+    a1 = 0.5f * a1 + second;
+    size = 0.5f * size + fabsf(second);
+  }
   // group g's in lane g
-  const float score = __shfl_sync(kAll, a.best == 2 && a2 != -INFINITY ? a1 + a2 : a1, (lane * per) & 31);
+  const float score = __shfl_sync(kAll, a1, (lane * per) & 31);
   const unsigned all = a.groups == 32 ? kAll : (1u << a.groups) - 1u;
   const bool one = lane < a.groups;
   const int rank = group_rank(score, all);
-  const unsigned open = __ballot_sync(kAll, one && rank < a.top_groups);
+  const bool kept = rank < a.top_groups;
+  const unsigned open = __ballot_sync(kAll, one && kept);
   if (!by_score) return open;
-  // the last group kept and the first left out
-  const float x = __shfl_sync(kAll, score, __ffs(__ballot_sync(kAll, one && rank == a.top_groups - 1)) - 1);
-  const float y = __shfl_sync(kAll, score, __ffs(__ballot_sync(kAll, one && rank == a.top_groups)) - 1);
-  const float near = tau + tau + 0x1p-21f * (fabsf(x) + fabsf(y));
-  if (y == -INFINITY || x - y > near) return open;
-  const unsigned sure = __ballot_sync(kAll, one && score > y + near);
-  const unsigned among = __ballot_sync(kAll, one && score > -INFINITY && !(score > y + near) && !(score < x - near));
+  // Bounds of the score, twice what the above comes to.  Infinite ones are exact.
+  const float off = tau + 0x1p-22f * __shfl_sync(kAll, size, (lane * per) & 31);
+  const float low = isinf(score) ? score : score - off, high = isinf(score) ? score : score + off;
+  // the least bound of a group kept, the greatest of one left out
+  const float in = ordered_float(topk_redux_min(one && kept ? topk_order_key(low) : INT_MAX));
+  const float out = ordered_float(topk_redux_max(one && !kept ? topk_order_key(high) : INT_MIN));
+  if (out == -INFINITY || in > out) return open;
+  const unsigned sure = __ballot_sync(kAll, one && kept && low > out);
+  const unsigned among = __ballot_sync(kAll, one && score > -INFINITY && (kept ? low <= out : high >= in));
   return sure | best_groups64<DT>(a, row, c, mx, among, a.top_groups - __popc(sure));
 }
 
@@ -355,7 +368,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     const int m = topk_redux_max(best);
     if (m == INT_MIN || (slot == k && !a.bias)) break;
     if (a.bias && slot > 0) {
-      const float x = __int_as_float(before ^ ((before >> 31) & INT_MAX)), y = __int_as_float(m ^ ((m >> 31) & INT_MAX));
+      const float x = ordered_float(before), y = ordered_float(m);
       if (!(x - y > tau + 0x1p-22f * (fabsf(x) + fabsf(y)))) unsure = true;
     }
     before = m;
@@ -367,7 +380,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
   }
   if (unsure) {   // (the same for the whole warp)
     // those chosen, and those left that are as near to the last of them
-    const float last = __int_as_float(kth ^ ((kth >> 31) & INT_MAX)), least = last - (tau + 0x1p-21f * fabsf(last));
+    const float last = ordered_float(kth), least = last - (tau + 0x1p-21f * fabsf(last));
     double* room = choice_smem + (size_t)warp * a.room;
     int* list = reinterpret_cast<int*>(room);
     int n = __popc(__ballot_sync(kAll, mine >= 0));
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int kv = keys.key[i];
-      const bool near = kv != INT_MIN && !(__int_as_float(kv ^ ((kv >> 31) & INT_MAX)) < least);
+      const bool near = kv != INT_MIN && !(ordered_float(kv) < least);
       const unsigned who = __ballot_sync(kAll, near);
       const int at = n + __popc(who & ((1u << lane) - 1u));
       if (near && at < 32) list[at] = keys.index(i);
