@@ -436,7 +436,9 @@ qmoe_status qmoe_op_debug_inject_stall(int enable);
  * An expert whose logit (or bias) is -infinity is never chosen; a slot without
  * an expert gets id -1 (which qmoe_expert_sort drops) and weight 0.  An expert
  * whose logit or bias is NaN is not chosen either, and the token's weights are
- * all NaN (as those of a softmax over +infinity are).
+ * all NaN.  A softmax over +infinity has no scores: that token's weights are NaN
+ * too, and its experts, which keep their routes, those of the largest logits (of
+ * the groups with the largest, and but for what a bias of -infinity or NaN closes).
  *   logits_dev  dtype [num_tokens, experts], row stride ld_logits
  *   bias_dev    float32 [experts], or NULL
  *   ids_dev     int32, weights_dev float32 [num_tokens, top_k]

@@ -8,7 +8,8 @@
 // The choice is that of scores in 64 bits.  It is made in 32 (FP64 runs at a
 // 64th of the rate here): where two neighbours in the order are nearer than 32
 // bits can tell, the warp repeats the token's choice in 64.  With keys that are
-// the logits themselves nothing is rounded and nothing repeated.
+// the logits themselves nothing is rounded and nothing repeated.  (A softmax over
+// +infinity has no scores: that token's choice goes by its logits, its weights are NaN.)
 //
 // Bound: instructions and latency.  A warp takes a token: lane l holds the logits of
 // experts l, l + 32, ..., sorted; a rank is one redux for the best key and one for
@@ -120,7 +121,7 @@ __device__ __noinline__ unsigned best_groups64(const ChoiceArgs& a, const typena
 // their scores in 64 bits.
 template <int DT>
 __device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typename ElemT<DT>::t* row, const float* c, float mx,
-                                                bool by_score, float tau) {
+                                                int best, bool by_score, float tau) {
   const int lane = threadIdx.x & 31, n = a.E / a.groups;
   int per = 32;   // lanes of a group
   while (per * a.groups > 32) per >>= 1;
@@ -134,7 +135,7 @@ __device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typen
     }
   two_best(a1, a2, per);
   float size = fabsf(a1);   // of its terms
-  if (a.best == 2) {
+  if (best == 2) {
     const float second = a2 == -INFINITY ? 0.f : 0.5f * a2;
     a1 = 0.5f * a1 + second;
     size = 0.5f * size + fabsf(second);
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
   if (t >= a.T) return;
   const T* row = static_cast<const T*>(a.logits) + (size_t)(t * a.ld);
   const bool softmax = a.scoring == QMOE_SCORE_SOFTMAX, filter = a.top_groups < a.groups;
-  const bool by_score = a.bias || (filter && a.best == 2);   // keys that are rounded
+  bool by_score = a.bias || (filter && a.best == 2);   // keys that are rounded
 
   float l[NPL];
   bool nan = false;
@@ -317,6 +318,14 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     }
     sum = warp_sum(sum);
   }
+  // A softmax over +infinity has no scores: the weights will say so, and the choice
+  // is by the logits, as without a bias and with each group's best.
+  const bool lost = softmax && by_score && mx == INFINITY;
+  if (lost) {
+    nan = true;
+    by_score = false;
+  }
+  const bool biased = a.bias && !lost;
 
   LaneKeys<NPL> keys;
   unsigned open = kAll;   // groups
@@ -341,7 +350,10 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) c[i] = l[i];
+      for (int i = 0; i < NPL; ++i) {
+        c[i] = l[i];
+        if (lost && a.bias && lane + 32 * i < E && !(a.bias[lane + 32 * i] > -INFINITY)) c[i] = -INFINITY;
+      }
     }
     if (filter) {
       float* sm = reinterpret_cast<float*>(choice_smem + (size_t)warp * a.room);
@@ -349,12 +361,12 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       for (int i = 0; i < NPL; ++i)
         if (lane + 32 * i < E) sm[lane + 32 * i] = c[i];
       __syncwarp();
-      open = best_groups<DT>(a, row, sm, mx, by_score, tau);
+      open = best_groups<DT>(a, row, sm, mx, lost ? 1 : a.best, by_score, tau);
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int e = lane + 32 * i;
-      const float v = a.bias ? c[i] : l[i];
+      const float v = biased ? c[i] : l[i];
       const bool may = c[i] > -INFINITY && (!filter || (open >> ((uint32_t)e * a.group_magic >> 20) & 1u));
       keys.key[i] = may ? topk_order_key(v) : INT_MIN;
     }
@@ -366,8 +378,8 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     int best, at;
     keys.best(best, at);
     const int m = topk_redux_max(best);
-    if (m == INT_MIN || (slot == k && !a.bias)) break;
-    if (a.bias && slot > 0) {
+    if (m == INT_MIN || (slot == k && !biased)) break;
+    if (biased && slot > 0) {
       const float x = ordered_float(before), y = ordered_float(m);
       if (!(x - y > tau + 0x1p-22f * (fabsf(x) + fabsf(y)))) unsure = true;
     }
