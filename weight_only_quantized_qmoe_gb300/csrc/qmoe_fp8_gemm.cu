@@ -57,12 +57,22 @@ struct F8Ring {
   // TMEM columns: two accumulators, then per stage the scales of W and A
   static constexpr int sf_col0 = 2 * BN;
   static constexpr int sf_cols = 4 + 4 * groups;
-  static constexpr int tmem_cols = sf_col0 + stages * sf_cols <= 256 ? 256 : 512;
-  static_assert(sf_col0 + stages * sf_cols <= tmem_cols, "TMEM columns");
+  static constexpr int sum_col0 = sf_col0 + stages * sf_cols;     // the sum of the pieces of 32-bit results
+  static constexpr int tmem_cols = sum_col0 + BN <= 256 ? 256 : 512;
+  static_assert(sum_col0 + BN <= tmem_cols, "TMEM columns");
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
   static_assert(BN * kTileM * 4 <= stages * w_bytes, "a partial tile fits the ring");
 };
+
+// Stages summed in the tensor core at a time, for 32-bit results (see add_tile;
+// relative error of 16384 values in one piece 1.2e-6, in three 4e-7): for pairs whole
+// groups of four stages, which share a word of scales.
+constexpr int kF8Piece = 48;
+template <int OUT>
+__device__ __forceinline__ int f8_piece_end(int from, int end) {
+  return OUT == QMOE_F32 && end - from > kF8Piece ? from + kF8Piece : end;
+}
 
 // One stage, issued by one elected lane: the scales of W and of A's row groups
 // to TMEM, up to four K = 32 MMAs, the commit that frees the stage.
@@ -274,42 +284,45 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     int st = 0, tc = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int tile = first; tile < real && ok; tile += stride, ++tc) {
+    for (int tile = first; tile < real && ok; tile += stride) {
       int n0;
       const RowTile t = tile_of(tile, n0);
       const uint32_t idesc0 = idesc_mxf8(kTileM, (t.rows + 15) & ~15, a.back);
-      const int ab = tc & 1;
-      ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint32_t dacc = tmem + ab * BN;
-      int ks = ks0;
-      while (ks < ks1 && ok) {
+      for (int from = ks0, to; from < ks1 && ok; from = to, ++tc) {
+        to = f8_piece_end<OUT>(from, ks1);
+        const int ab = tc & 1;
+        ok = spin_or_abort(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dacc = tmem + ab * BN;
+        int ks = from;
+        while (ks < to && ok) {
 #pragma unroll
-        for (int u = 0; u < S; ++u) {
-          if (u == st && ks < ks1 && ok) {
-            if (!warp_test_wait(&full[u], ph)) {
-              ok = spin_or_abort(&full[u], ph, a.wait, abort_flag);
-              ok = __all_sync(0xffffffffu, ok);
-            }
-            if (ok) {
-              tc_fence_after();
-              fence_proxy_async_smem();   // the scales were written through the generic proxy
-              f8_stage_elect<RG::groups>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
-                                         adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
-                                         idesc0 | (uint32_t)(ks & 3) << 29 | (uint32_t)(ks & 3) << 4, tmem + RG::sf_col0 + u * RG::sf_cols,
-                                         swdesc0 + (uint64_t)((u * RG::sfw_bytes) >> 4), sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
-                                         ks != ks0 ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[u]);
-              ++ks;
-              if (++st == S) {
-                st = 0;
-                ph ^= 1u;
+          for (int u = 0; u < S; ++u) {
+            if (u == st && ks < to && ok) {
+              if (!warp_test_wait(&full[u], ph)) {
+                ok = spin_or_abort(&full[u], ph, a.wait, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+              }
+              if (ok) {
+                tc_fence_after();
+                fence_proxy_async_smem();   // the scales were written through the generic proxy
+                f8_stage_elect<RG::groups>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
+                                           adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
+                                           idesc0 | (uint32_t)(ks & 3) << 29 | (uint32_t)(ks & 3) << 4, tmem + RG::sf_col0 + u * RG::sf_cols,
+                                           swdesc0 + (uint64_t)((u * RG::sfw_bytes) >> 4), sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
+                                           ks != from ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[u]);
+                ++ks;
+                if (++st == S) {
+                  st = 0;
+                  ph ^= 1u;
+                }
               }
             }
           }
         }
+        if (ok) tc_commit_elect(&acc_full[ab]);
       }
-      if (ok) tc_commit_elect(&acc_full[ab]);
     }
     tc_commit_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -329,18 +342,27 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (rank == 0) store_zeros<OUT>(out, a.ld_out, t.rows, in, half);
         continue;
       }
-      const int ab = tc & 1;
-      ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * BN;
-      if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem + RG::w_off), q, t.rows, half);   // the ring is empty
-      else store_tile<OUT>(acc, out, a.ld_out, t.rows, in, half);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[ab]);
-      ++tc;
+      for (int from = ks0, to; from < ks1; from = to, ++tc) {
+        to = f8_piece_end<OUT>(from, ks1);
+        const int ab = tc & 1;
+        ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        uint32_t acc = lanes + ab * BN;
+        if (OUT == QMOE_F32 && (from != ks0 || to < ks1)) {   // in pieces
+          add_pieces(lanes + RG::sum_col0, acc, t.rows, half, from == ks0);
+          acc = lanes + RG::sum_col0;
+        }
+        if (to == ks1) {
+          if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem + RG::w_off), q, t.rows, half);   // the ring is empty
+          else store_tile<OUT>(acc, out, a.ld_out, t.rows, in, half);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      }
     }
   }
   if constexpr (SPLIT) {
@@ -406,7 +428,6 @@ struct F8RowMaps {
   CUtensorMap of[F8PairRing::bn / 32];
 };
 constexpr int kF8PairThreads = 256 + 32 * kEpiWarps;
-constexpr int kF8Piece = 48;   // stages, for 32-bit results (relative error of 16384 values in one piece 1.2e-6, in three 4e-7)
 
 // One stage: up to four K = 32 MMAs of the pair and the commit that frees it.
 __device__ __forceinline__ void f8_pair_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sfw,

@@ -279,6 +279,25 @@ __device__ __forceinline__ void add_tile(uint32_t taddr, float* out, int64_t ld,
     }
   }
 }
+// sum = piece, or sum + piece, to nearest, of a warp's share of a tile's columns, in
+// TMEM: for tiles whose pieces can wait there.
+__device__ __forceinline__ void add_pieces(uint32_t sum, uint32_t piece, int n, int half, bool first) {
+  for (int c0 = half * 32; c0 < n; c0 += 64) {
+    uint32_t v[32];
+    TC_LD32(piece + c0, v);
+    if (!first) {
+      uint32_t w[32];
+      TC_LD32(sum + c0, w);
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(w[c]) + __uint_as_float(v[c]));
+    } else {
+      tc_wait_ld();
+    }
+    TC_ST32(sum + c0, v);
+  }
+  tc_wait_st();
+}
 template <int OUT>
 __device__ __forceinline__ void store_zeros(typename ElemT<OUT>::t* out, int64_t ld, int n, bool in, int half) {
   if (in)

@@ -121,25 +121,6 @@ struct WgTile {
   int e, n0, k0, lo, hi;   // this CTA's rows of it
 };
 
-// sum = piece, or sum + piece, of a warp's share of a tile's columns, in TMEM.
-__device__ __forceinline__ void add_pieces(uint32_t sum, uint32_t piece, int n, int half, bool first) {
-  for (int c0 = half * 32; c0 < n; c0 += 64) {
-    uint32_t v[32];
-    TC_LD32(piece + c0, v);
-    if (!first) {
-      uint32_t w[32];
-      TC_LD32(sum + c0, w);
-      tc_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(w[c]) + __uint_as_float(v[c]));
-    } else {
-      tc_wait_ld();
-    }
-    TC_ST32(sum + c0, v);
-  }
-  tc_wait_st();
-}
-
 // SPLIT: a cluster shares each tile's rows, and there is one tile a cluster at
 // most.
 template <int OUT, bool SPLIT>
