@@ -11,14 +11,14 @@
 // codes from shared memory and the scales from TMEM.  Its scale blocks are 32
 // values, ours four of them: all four MMAs of 128 values name the same byte of
 // the scale words.  The MMA's M side is 128 weight rows (back: weight columns, the
-// same codes read along M), its N side up to BN rows of A; a ring stage holds 128
+// same codes read along M), its N side up to 32 rows of A; a ring stage holds 128
 // reduction values of both, 128-byte rows copied by TMA.
 //   warp 0    TMA producer (one elected lane)
 //   warp 1    MMA issuer: scales to TMEM, then four K = 32 MMAs a stage
 //   warp 2    scales of A's rows: four bytes a row by cp.async (512 values' worth)
 //   warp 3    scale of the weight block: one byte, spread over 512
 //   warps 4-11 epilogue: TMEM columns to rows of the output
-// Two accumulators of BN columns alternate, so the epilogue of one tile runs
+// Two accumulators of 32 columns alternate, so the epilogue of one tile runs
 // under the MMAs of the next.  CTAs are persistent over the (expert, row tile,
 // weight tile) list, which every CTA derives from the device offsets.  Where
 // there are few tiles, the CTAs of a cluster share a tile's reduction and add up
@@ -35,18 +35,16 @@
 namespace qmoe {
 
 constexpr int kF8StageK = 128;                 // values along the reduction a stage: one swizzle atom
-constexpr int kF8BoxRows = 32;                 // rows of A a copy where a tile is not full
 constexpr int kF8Threads = 128 + 32 * kEpiWarps;
 constexpr long long kF8DrainPolls = 4096;      // parked polls (about 4 ms) a copy in flight is given to land
 
-template <int BN>
 struct F8Ring {
+  static constexpr int bn = 32;                                   // rows of A a tile
   static constexpr int stages = 10;
-  static constexpr int groups = (BN + 127) / 128;                 // 128-row scale groups of A
   static constexpr int w_bytes = kTileM * kF8StageK;
-  static constexpr int a_bytes = BN * kF8StageK;
+  static constexpr int a_bytes = bn * kF8StageK;
   static constexpr int sfw_bytes = 512;
-  static constexpr int sfa_bytes = 512 * groups;
+  static constexpr int sfa_bytes = 512;                           // a group of 128 rows
   static constexpr int w_off = 0;
   static constexpr int a_off = w_off + stages * w_bytes;
   static constexpr int sfw_off = a_off + stages * a_bytes;
@@ -55,14 +53,14 @@ struct F8Ring {
   static constexpr int tp_off = bar_off + 512;                    // first row tile and first row of each expert
   static constexpr int total = tp_off + 2 * (kSortMaxExperts + 2) * 4;
   // TMEM columns: two accumulators, then per stage the scales of W and A
-  static constexpr int sf_col0 = 2 * BN;
-  static constexpr int sf_cols = 4 + 4 * groups;
+  static constexpr int sf_col0 = 2 * bn;
+  static constexpr int sf_cols = 8;
   static constexpr int sum_col0 = sf_col0 + stages * sf_cols;     // the sum of the pieces of 32-bit results
-  static constexpr int tmem_cols = sum_col0 + BN <= 256 ? 256 : 512;
-  static_assert(sum_col0 + BN <= tmem_cols, "TMEM columns");
+  static constexpr int tmem_cols = 256;
+  static_assert(sum_col0 + bn <= tmem_cols, "TMEM columns");
   static_assert(total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
-  static_assert(BN * kTileM * 4 <= stages * w_bytes, "a partial tile fits the ring");
+  static_assert(bn * kTileM * 4 <= stages * w_bytes, "a partial tile fits the ring");
 };
 
 // Stages summed in the tensor core at a time, for 32-bit results (see add_tile;
@@ -74,30 +72,26 @@ __device__ __forceinline__ int f8_piece_end(int from, int end) {
   return OUT == QMOE_F32 && end - from > kF8Piece ? from + kF8Piece : end;
 }
 
-// One stage, issued by one elected lane: the scales of W and of A's row groups
-// to TMEM, up to four K = 32 MMAs, the commit that frees the stage.
-template <int GROUPS>
+// One stage, issued by one elected lane: the scales of W and of A's rows to TMEM, up
+// to four K = 32 MMAs, the commit that frees the stage.
 __device__ __forceinline__ void f8_stage_elect(uint32_t d, uint64_t w, uint64_t wstep, uint64_t a, uint32_t idesc, uint32_t sf,
                                                uint64_t sw, uint64_t sa, uint32_t acc, int nk, uint64_t* empty) {
-  static_assert(GROUPS == 1 || GROUPS == 2, "row groups of A");
   asm volatile(
-      "{\n\t.reg .pred e, p0, p1, q1, q2, q3, g2;\n\t"
-      ".reg .b32 t1, t2;\n\t.reg .b64 x1, y1, y2, y3, z1, z2, z3;\n\t"
+      "{\n\t.reg .pred e, p0, p1, q1, q2, q3;\n\t"
+      ".reg .b32 t1;\n\t.reg .b64 y1, y2, y3, z1, z2, z3;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p0, %8, 0;\n\tsetp.eq.b32 p1, %8, %8;\n\t"
       "setp.gt.and.s32 q1, %9, 1, e;\n\tsetp.gt.and.s32 q2, %9, 2, e;\n\tsetp.gt.and.s32 q3, %9, 3, e;\n\t"
-      "setp.gt.and.s32 g2, %10, 1, e;\n\t"
-      "add.u32 t1, %5, 4;\n\tadd.u32 t2, %5, 8;\n\tadd.u64 x1, %7, 32;\n\t"
+      "add.u32 t1, %5, 4;\n\t"
       "add.u64 y1, %1, %2;\n\tadd.u64 y2, y1, %2;\n\tadd.u64 y3, y2, %2;\n\t"
       "add.u64 z1, %3, 2;\n\tadd.u64 z2, %3, 4;\n\tadd.u64 z3, %3, 6;\n\t"
       "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%5], %6;\n\t"
       "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [t1], %7;\n\t"
-      "@g2 tcgen05.cp.cta_group::1.32x128b.warpx4 [t2], x1;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %3, %4, [%5], [t1], p0;\n\t"
       "@q1 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y1, z1, %4, [%5], [t1], p1;\n\t"
       "@q2 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y2, z2, %4, [%5], [t1], p1;\n\t"
       "@q3 tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], y3, z3, %4, [%5], [t1], p1;\n\t}" ::"r"(d),
-      "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sf), "l"(sw), "l"(sa), "r"(acc), "r"(nk), "n"(GROUPS)
+      "l"(w), "l"(wstep), "l"(a), "r"(idesc), "r"(sf), "l"(sw), "l"(sa), "r"(acc), "r"(nk)
       : "memory");
   tc_commit_elect(empty);
 }
@@ -117,13 +111,12 @@ struct F8KernelArgs {
 
 // SPLIT: a cluster shares each tile's reduction, and there is one tile a cluster
 // at most.
-template <int BN, int OUT, bool SPLIT>
+template <int OUT, bool SPLIT>
 __global__ void __launch_bounds__(kF8Threads, 1)
-    fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_a32,
-                      const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
-  using RG = F8Ring<BN>;
+    fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w, const F8KernelArgs args) {
+  using RG = F8Ring;
   using T = typename ElemT<OUT>::t;
-  constexpr int S = RG::stages;
+  constexpr int S = RG::stages, BN = RG::bn;
   extern __shared__ __align__(1024) uint8_t f8_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f8_smem_raw) + 1023) & ~uintptr_t(1023));
   const Fp8MatmulArgs& a = args.a;
@@ -188,23 +181,15 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       int n0;
       const RowTile t = tile_of(tile, n0);
       if (t.e == a.E) continue;
-      // the rows in one copy if they are many, else in copies of 32
-      const int boxes = (t.rows + kF8BoxRows - 1) / kF8BoxRows;
       for (int ks = ks0; ks < ks1; ++ks, ++it) {
         const int s = it % S;
         ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        mbar_arrive_expect_tx_elect(&full[s], (uint32_t)(boxes * kF8BoxRows * kF8StageK + RG::w_bytes));
+        mbar_arrive_expect_tx_elect(&full[s], (uint32_t)(RG::a_bytes + RG::w_bytes));
         // Test hook: the first stage's barrier is armed, its copies are never issued.
         if (args.inject_stall && it == 0) continue;
-        uint8_t* da = smem + RG::a_off + s * RG::a_bytes;
-        if (boxes == BN / kF8BoxRows) {
-          tma_3d_elect(da, &map_a, ks * kF8StageK, t.start, 0, &full[s]);
-        } else {
-          for (int b = 0; b < boxes; ++b)
-            tma_3d_elect(da + b * kF8BoxRows * kF8StageK, &map_a32, ks * kF8StageK, t.start + b * kF8BoxRows, 0, &full[s]);
-        }
+        tma_3d_elect(smem + RG::a_off + s * RG::a_bytes, &map_a, ks * kF8StageK, t.start, 0, &full[s]);
         uint8_t* dw = smem + RG::w_off + s * RG::w_bytes;
         if (a.back) tma_3d_elect(dw, &map_w, n0, ks * kF8StageK, t.e, &full[s]);
         else tma_3d_elect(dw, &map_w, ks * kF8StageK, n0, t.e, &full[s]);
@@ -219,8 +204,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
   } else if (warp == 2) {
     // ---------------- scales of A's rows ----------------
-    // Row 32 j + lane of a 128-row group goes to bytes lane * 16 + j * 4 of its
-    // chunk: the four bytes of 512 values, of which a stage's MMAs name one.
+    // Row `lane` goes to bytes lane * 16 of the chunk: the four bytes of 512 values, of
+    // which a stage's MMAs name one.
     const uint32_t dst0 = smem_u32(smem + RG::sfa_off) + lane * 16;
     int it = 0;
     bool ok = true;
@@ -228,19 +213,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       int n0;
       const RowTile t = tile_of(tile, n0);
       if (t.e == a.E) continue;
-      const int left = (int)a.R - t.start - lane;   // row 32 j exists: 32 j < left
+      const bool real = t.start + lane < a.R;
       for (int ks = ks0; ks < ks1; ++ks, ++it) {
         const int s = it % S;
         ok = wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint8_t* src = a.a_scales + ((size_t)(ks >> 2) * a.R + t.start + lane) * 4;
-        const uint32_t dst = dst0 + s * RG::sfa_bytes;
-#pragma unroll
-        for (int j = 0; j < BN / 32; ++j) {
-          const bool real = 32 * j < left;
-          cp_async4_or_zero(dst + (j / 4) * 512 + (j & 3) * 4, real ? src + j * 128 : a.a_scales, real ? 4 : 0);
-        }
+        cp_async4_or_zero(dst0 + s * RG::sfa_bytes, real ? src : a.a_scales, real ? 4 : 0);
         cp_async_arrive(&full[s]);
       }
     }
@@ -307,11 +287,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               if (ok) {
                 tc_fence_after();
                 fence_proxy_async_smem();   // the scales were written through the generic proxy
-                f8_stage_elect<RG::groups>(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep,
-                                           adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
-                                           idesc0 | (uint32_t)(ks & 3) << 29 | (uint32_t)(ks & 3) << 4, tmem + RG::sf_col0 + u * RG::sf_cols,
-                                           swdesc0 + (uint64_t)((u * RG::sfw_bytes) >> 4), sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
-                                           ks != from ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[u]);
+                f8_stage_elect(dacc, wdesc0 + (uint64_t)((u * RG::w_bytes) >> 4), wstep, adesc0 + (uint64_t)((u * RG::a_bytes) >> 4),
+                               idesc0 | (uint32_t)(ks & 3) << 29 | (uint32_t)(ks & 3) << 4, tmem + RG::sf_col0 + u * RG::sf_cols,
+                               swdesc0 + (uint64_t)((u * RG::sfw_bytes) >> 4), sadesc0 + (uint64_t)((u * RG::sfa_bytes) >> 4),
+                               ks != from ? 1u : 0u, ks + 1 < ksteps ? 4 : tail, &empty[u]);
                 ++ks;
                 if (++st == S) {
                   st = 0;
@@ -715,15 +694,11 @@ cudaError_t launch_f8(const F8KernelArgs& args, bool pairs, int64_t tiles, int s
     return launch_tiles(fp8_matmul_pair_kernel<OUT>, std::min<int64_t>(2 * tiles, kSms), 2, kF8PairThreads, F8PairRing::total + slack, s, map_a,
                         map_w, args);
   }
-  CUtensorMap map_a, map_part;
-  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, 32) ||
-      !encode_tiles(&map_part, u8, 1, a.a_codes, inner, a.R, 1, pitch, kF8BoxRows))
-    return cudaErrorInvalidValue;
+  CUtensorMap map_a;
+  if (!encode_tiles(&map_a, u8, 1, a.a_codes, inner, a.R, 1, pitch, F8Ring::bn)) return cudaErrorInvalidValue;
   if (split > 1)
-    return launch_tiles(fp8_matmul_kernel<32, OUT, true>, tiles * split, split, kF8Threads, F8Ring<32>::total + slack, s, map_a, map_part,
-                        map_w, args);
-  return launch_tiles(fp8_matmul_kernel<32, OUT, false>, std::min<int64_t>(tiles, kSms), 1, kF8Threads, F8Ring<32>::total + slack, s, map_a,
-                      map_part, map_w, args);
+    return launch_tiles(fp8_matmul_kernel<OUT, true>, tiles * split, split, kF8Threads, F8Ring::total + slack, s, map_a, map_w, args);
+  return launch_tiles(fp8_matmul_kernel<OUT, false>, std::min<int64_t>(tiles, kSms), 1, kF8Threads, F8Ring::total + slack, s, map_a, map_w, args);
 }
 
 // Output tiles there can be at most (the device offsets decide how many there
@@ -757,8 +732,8 @@ int pair_rows(const Fp8MatmulArgs& a) {
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStream_t s) {
-  F8KernelArgs args{a, inject_stall, 32};
-  const int64_t ksteps = ((a.back ? a.N : a.K) + kF8StageK - 1) / kF8StageK, narrow = most_tiles(a, 32, kTileM);
+  F8KernelArgs args{a, inject_stall, F8Ring::bn};
+  const int64_t ksteps = ((a.back ? a.N : a.K) + kF8StageK - 1) / kF8StageK, narrow = most_tiles(a, F8Ring::bn, kTileM);
   auto run = [&](bool pairs, int64_t tiles, int split) {
     if (a.out_dtype == QMOE_F32) return launch_f8<QMOE_F32>(args, pairs, tiles, split, s);
     if (a.out_dtype == QMOE_F16) return launch_f8<QMOE_F16>(args, pairs, tiles, split, s);
