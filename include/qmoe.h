@@ -597,6 +597,7 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a_codes_dev, const uint8_t* a_scales_
  *   dy_dev  dtype [rows, n], x_dev  dtype [rows, k]; QMOE_F16 or QMOE_BF16
  *           (QMOE_F32: UNSUPPORTED)
  *   dw_dev  out_dtype [experts, n, k]
+ * experts <= 1024; rows and experts * n have to be below 2^31 - 512.
  * qmoe_weight_grad_workspace: bytes of workspace (128-byte aligned) for operands
  * with these addresses and strides: 256 bytes an expert where there are many
  * tiles, and a copy of an operand whose rows do not start on 16-byte boundaries.

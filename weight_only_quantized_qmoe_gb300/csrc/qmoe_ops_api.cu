@@ -88,15 +88,18 @@ cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 // less than this.
 constexpr int kReach = 256;
 
-// Shapes of a product grouped by expert: rows, and experts of n rows of k.
+// Shapes of a product grouped by expert: rows, and experts of n rows of k.  Beside the
+// reach of a tile, the eight parts of a weight gradient's rows, in whole stages of 64,
+// may end up to 511 rows past the last.
+constexpr int kGroupedReach = 512;
 qmoe_status check_grouped(int64_t rows, const void* offsets, int experts, int64_t n, int64_t k) {
   OP_CHECK(rows >= 0, "rows %lld is negative", (long long)rows);
-  OP_CHECK(rows < INT_MAX - kReach, "rows %lld do not fit 31 bits", (long long)rows);
+  OP_CHECK(rows <= INT_MAX - kGroupedReach, "rows %lld do not fit 31 bits", (long long)rows);
   OP_CHECK(experts >= 1, "experts %d is not positive", experts);
   OP_SUPPORTED(experts <= kSortMaxExperts, "experts %d: at most %d", experts, kSortMaxExperts);
   OP_CHECK(offsets || experts == 1, "%d experts need offsets", experts);
   OP_CHECK(n >= 1 && k >= 1 && k < (1LL << 30), "a weight of %lld x %lld is out of range", (long long)n, (long long)k);
-  OP_CHECK(n < (INT_MAX - kReach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
+  OP_CHECK(n <= (INT_MAX - kGroupedReach) / experts, "%d experts of %lld rows do not fit 31 bits", experts, (long long)n);
   return QMOE_OK;
 }
 // The bounded waits' status word and limit.

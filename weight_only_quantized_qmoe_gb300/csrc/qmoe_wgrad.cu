@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     t.k0 = kt * kTileM;
     const int lo = row0[t.e], hi = max(row0[t.e + 1], lo);
     const int steps = (hi - lo + kWgRows - 1) / kWgRows, each = (steps + ranks - 1) / ranks;
+    // (their ends may lie past hi, by less than 512 rows: rows are below 2^31 - 512)
     t.lo = min(lo + rank * each * kWgRows, hi);
     t.hi = min(t.lo + each * kWgRows, hi);
     return t;
