@@ -17,7 +17,9 @@
 //   warp 1    MMA issuer, zeros past the last row
 //   warp 3    first rows of the experts
 //   warps 4-11 epilogue: TMEM columns to rows of dw
-// Two accumulators alternate.  CTAs are persistent over the (expert, tile) list.
+// Two accumulators alternate; long sums are taken in pieces, the first of which stays
+// in one and gets the others' added through the other.  CTAs are persistent over the
+// (expert, tile) list.
 // Where there are few tiles, the CTAs of a cluster share a tile's rows and add up
 // their parts in a fixed order.  Operands that TMA cannot read (rows that do not
 // start on 16 bytes) are copied to rows that do first.
@@ -37,13 +39,24 @@ constexpr int kWgPanelBytes = kWgRows * 128;
 constexpr int kWgThreads = 128 + 32 * kEpiWarps;
 constexpr int kWgBN = 256;
 constexpr long long kWgDrainPolls = 4096;
-// Rows summed in the tensor core at a time for 32-bit results (see add_tile; of
-// normal values, relative error of 1024 rows in one piece 1.2e-6, of 32768 3.8e-5).
-constexpr int kWgPiece = 5 * 128;
+// Rows summed in the tensor core at a time, whole stages (see add_tile; of normal
+// values, relative error of 1024 rows in one piece 1.2e-6, of 32768 3.8e-5): for
+// 16-bit results as many as leave out a sixth of their own rounding (2^-11 for f16).
 template <int OUT>
 __device__ __forceinline__ int piece_end(int from, int hi) {
-  return OUT == QMOE_F32 && hi - from > kWgPiece ? from + kWgPiece : hi;
+  constexpr int piece = OUT == QMOE_F32 ? 5 * 128 : 1 << 16;
+  return hi - from > piece ? from + piece : hi;
 }
+// The accumulator of a piece where the pieces of a tile are added up in TMEM: the
+// first one, which the others are added to, keeps a tile's `home`, the others go
+// through the other one.  A tile of one piece leaves the other free for the next.
+struct WgAccs {
+  int home = 0;
+  uint32_t used = 0;   // a bit each: parity of the uses so far
+  __device__ __forceinline__ int of(bool first) const { return first ? home : home ^ 1; }
+  __device__ __forceinline__ uint32_t parity(int ab) const { return used >> ab & 1u; }
+  __device__ __forceinline__ void step(int ab) { used ^= 1u << ab; }
+};
 
 struct WgRing {
   static constexpr int stages = 4;
@@ -129,7 +142,6 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   using RG = WgRing;
   using T = typename ElemT<OUT>::t;
   constexpr int S = RG::stages;
-  constexpr bool kInPieces = OUT == QMOE_F32;   // one accumulator for a piece, the other for their sum
   extern __shared__ __align__(1024) uint8_t wg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(wg_smem_raw) + 1023) & ~uintptr_t(1023));
   const WgradArgs& a = args.a;
@@ -222,16 +234,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     // ---------------- MMA issuer ----------------
     const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), kWgPanelBytes);
     const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), kWgPanelBytes);
-    int it = 0, tc = 0;
+    int it = 0;
+    WgAccs accs;
     bool ok = true;
     for (int tile = first; tile < total && ok; tile += stride) {
       const WgTile t = tile_of(tile);
       if (t.lo >= t.hi) continue;
       const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, kTileM, (min(kWgBN, a.N - t.n0) + 15) & ~15);
-      for (int lo = t.lo, end; lo < t.hi && ok; lo = end, ++tc) {
+      for (int lo = t.lo, end; lo < t.hi && ok; lo = end) {
         end = piece_end<OUT>(lo, t.hi);
-        const int ab = kInPieces ? 0 : tc & 1, use = kInPieces ? tc : tc >> 1;
-        ok = spin_or_abort(&acc_empty[ab], (use & 1) ^ 1, a.wait, abort_flag);
+        const int ab = accs.of(lo == t.lo);
+        ok = spin_or_abort(&acc_empty[ab], accs.parity(ab) ^ 1u, a.wait, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         for (int r = lo; r < end && ok; r += kWgRows, ++it) {
           const int s = it % S;
@@ -252,7 +265,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                             idesc, r != lo ? 1u : 0u, (rows + 15) / 16, &empty[s]);
         }
         if (ok) tc_commit_elect(&acc_full[ab]);
+        accs.step(ab);
       }
+      accs.home ^= 1;
     }
     tc_commit_elect(drain_bar);
     const WaitCfg drain{a.wait.status, kDrainWaitLimit};
@@ -260,7 +275,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp >> 2) - 1;
-    int tc = 0;
+    WgAccs accs;
     bool ok = true;
     for (int tile = first; tile < total && ok; tile += stride) {
       const WgTile t = tile_of(tile);
@@ -276,27 +291,30 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         }
         continue;
       }
-      for (int lo = t.lo, end; lo < t.hi; lo = end, ++tc) {
-        end = piece_end<OUT>(lo, t.hi);
-        const int ab = kInPieces ? 0 : tc & 1, use = kInPieces ? tc : tc >> 1;
-        ok = wait_or_abort(&acc_full[ab], use & 1, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
-        if constexpr (kInPieces) {
-          // the sum of the pieces, in the second accumulator
-          if (lo != t.lo || end < t.hi) add_pieces(acc + kWgBN, acc, n, half, lo == t.lo);
-          if (lo != t.lo) acc += kWgBN;
-        }
-        if (end == t.hi) {
-          if constexpr (SPLIT) put_partial(acc, reinterpret_cast<float*>(smem), q, n, half);   // the ring is empty
-          else store_tile<OUT>(acc, out, a.K, n, in, half);
-        }
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16), sum = lanes + accs.home * kWgBN;
+      auto release = [&](int ab) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      };
+      for (int lo = t.lo, end; lo < t.hi; lo = end) {
+        end = piece_end<OUT>(lo, t.hi);
+        const int ab = accs.of(lo == t.lo);
+        ok = wait_or_abort(&acc_full[ab], accs.parity(ab), a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        accs.step(ab);
+        if (lo != t.lo) {
+          add_pieces(sum, lanes + ab * kWgBN, n, half, false);
+          release(ab);
+        }
       }
+      if (!ok) break;
+      if constexpr (SPLIT) put_partial(sum, reinterpret_cast<float*>(smem), q, n, half);   // the ring is empty
+      else store_tile<OUT>(sum, out, a.K, n, in, half);
+      release(accs.home);
+      accs.home ^= 1;
     }
   }
   if constexpr (SPLIT) {
@@ -380,6 +398,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   using RG = WgPairRing;
   using T = typename ElemT<OUT>::t;
   constexpr int S = RG::stages;
+  // 32-bit results' pieces are many: both accumulators take them in turn, and they are
+  // added up where the results are
+  constexpr bool kAddInMemory = OUT == QMOE_F32;
   extern __shared__ __align__(1024) uint8_t wg_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(wg_smem_raw) + 1023) & ~uintptr_t(1023));
   const WgradArgs& a = args.a;
@@ -469,7 +490,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), RG::panel_bytes);
     const uint64_t dydesc0 = smem_desc_mn128(smem_u32(smem + RG::dy_off), RG::panel_bytes);
     RingAt<S> at;
-    int tc = 0;
+    WgAccs accs;
     bool ok = true;
     bool there = mbar_test_wait(&full[0], 0);   // the next stage, asked ahead as in the products' kernel
     for (int tile = first; tile < total && ok; tile += stride) {
@@ -477,10 +498,10 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       if (t.lo >= t.hi) continue;
       const int half = half_of(t);
       const uint32_t idesc = idesc_wgrad(a.dtype == QMOE_BF16, 2 * kTileM, 2 * half);
-      for (int lo = t.lo, end; lo < t.hi && ok; lo = end, ++tc) {
+      for (int lo = t.lo, end; lo < t.hi && ok; lo = end) {
         end = piece_end<OUT>(lo, t.hi);
-        const int ab = tc & 1;
-        ok = warp_spin_cluster(&acc_empty[ab], ((tc >> 1) & 1) ^ 1, a.wait, abort_flag);
+        const int ab = accs.of(kAddInMemory || lo == t.lo);
+        ok = warp_spin_cluster(&acc_empty[ab], accs.parity(ab) ^ 1u, a.wait, abort_flag);
         for (int r = lo; r < end && ok; r += kWgPairRows) {
           const int s = at.s, rows = min(kWgPairRows, end - r);
           if (!__shfl_sync(0xffffffffu, there, 0)) {
@@ -498,6 +519,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           if (rows > kWgRows) wg_stage_elect<2>(tmem + ab * kWgBN, xd + on, dyd + on, idesc, 1u, (rows - kWgRows + 15) / 16, &empty[s]);
         }
         if (ok) tc_commit_pair_elect(&acc_full[ab]);
+        accs.step(ab);
+        if (kAddInMemory || end == t.hi) accs.home ^= 1;
       }
     }
     tc_commit_pair_elect(drain_bar);
@@ -506,7 +529,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp >> 2) - 1;
-    int tc = 0;
+    WgAccs accs;
     bool ok = true;
     for (int tile = first; tile < total && ok; tile += stride) {
       const WgTile t = tile_of(tile);
@@ -517,18 +540,34 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         store_zeros<OUT>(out, a.K, n, in, half);
         continue;
       }
-      for (int lo = t.lo; lo < t.hi; lo = piece_end<OUT>(lo, t.hi), ++tc) {
-        const int ab = tc & 1;
-        ok = wait_or_abort(&acc_full[ab], (tc >> 1) & 1, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + ab * kWgBN;
-        if (OUT == QMOE_F32 && lo != t.lo) add_tile(acc, reinterpret_cast<float*>(out), a.K, n, in, half);
-        else store_tile<OUT>(acc, out, a.K, n, in, half);
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+      auto release = [&](int ab) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) cluster_bar_arrive(first_cta_bar(&acc_empty[ab]));
+      };
+      for (int lo = t.lo, end; lo < t.hi; lo = end) {
+        end = piece_end<OUT>(lo, t.hi);
+        const int ab = accs.of(kAddInMemory || lo == t.lo);
+        ok = wait_or_abort(&acc_full[ab], accs.parity(ab), a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        accs.step(ab);
+        const uint32_t acc = lanes + ab * kWgBN, sum = lanes + accs.home * kWgBN;
+        if constexpr (kAddInMemory) {
+          if (lo != t.lo) add_tile(acc, reinterpret_cast<float*>(out), a.K, n, in, half);
+          else store_tile<OUT>(acc, out, a.K, n, in, half);
+        } else {
+          if (lo != t.lo) {
+            add_pieces(sum, acc, n, half, false);
+            release(ab);
+          }
+          if (end < t.hi) continue;
+          store_tile<OUT>(sum, out, a.K, n, in, half);
+        }
+        release(accs.home);
+        accs.home ^= 1;
       }
     }
   }
