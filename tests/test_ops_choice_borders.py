@@ -78,7 +78,8 @@ def test_an_infinite_logit_keeps_its_experts(ops, dtype, biased, groups, top, be
         l[:, 50] = -np.inf
     else:
         assert r.ids[9, 0] == 50
-    want, _ = ref8.route(l[hit], k, "softmax", None, groups, top, 1, True, 1.0)
+    with np.errstate(invalid="ignore"):
+        want, _ = ref8.route(l[hit], k, "softmax", None, groups, top, 1, True, 1.0)
     np.testing.assert_array_equal(r.ids[hit].cpu().numpy(), want)
     assert r.ids[2, 0] == 37 and r.ids[5, :2].tolist() == [11, 60] and r.ids[7].tolist() == [0] + [-1] * (k - 1)
     assert torch.isnan(r.weights[2]).all() and torch.isnan(r.weights[5]).all() and torch.isnan(r.weights[9]).all() and torch.isnan(r.weights[7, 0])
@@ -86,5 +87,5 @@ def test_an_infinite_logit_keeps_its_experts(ops, dtype, biased, groups, top, be
     assert torch.equal(r.ids[others], clean.ids[others]) and torch.equal(r.weights[others], clean.weights[others])
     # and so its rows go where the logits say, and show that they have no weights
     plan = ops.expert_sort(r.ids, E)
-    y = ops.combine(torch.ones((T * k, 8), device="cuda"), plan, r.weights)
+    y = ops.combine(torch.ones((T * k, 8), device="cuda"), r.weights, plan)
     assert torch.isnan(y[hit]).all() and torch.isfinite(y[others]).all()
