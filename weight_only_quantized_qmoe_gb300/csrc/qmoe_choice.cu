@@ -121,7 +121,7 @@ __device__ __noinline__ unsigned best_groups64(const ChoiceArgs& a, const typena
 // their scores in 64 bits.
 template <int DT>
 __device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typename ElemT<DT>::t* row, const float* c, float mx,
-                                                int best, bool by_score, float tau) {
+                                                bool by_score, float tau) {
   const int lane = threadIdx.x & 31, n = a.E / a.groups;
   int per = 32;   // lanes of a group
   while (per * a.groups > 32) per >>= 1;
@@ -135,7 +135,7 @@ __device__ __forceinline__ unsigned best_groups(const ChoiceArgs& a, const typen
     }
   two_best(a1, a2, per);
   float size = fabsf(a1);   // of its terms
-  if (best == 2) {
+  if (a.best == 2) {
     const float second = a2 == -INFINITY ? 0.f : 0.5f * a2;
     a1 = 0.5f * a1 + second;
     size = 0.5f * size + fabsf(second);
@@ -222,6 +222,40 @@ __device__ __noinline__ int choose64_of(const ChoiceArgs& a, const typename Elem
   return list[lane];
 }
 
+// The choice of a token whose softmax is over +infinity, so that it has no scores: by
+// the logits, and of the groups with the largest.  c: room for E values.
+template <int DT>
+__device__ __noinline__ int choose_by_logits(const ChoiceArgs& a, const typename ElemT<DT>::t* row, float* c) {
+  const int lane = threadIdx.x & 31, E = a.E, n = E / a.groups;
+  __syncwarp();
+  for (int e = lane; e < E; e += 32) {
+    const float l = load_d<DT>(row, e);
+    c[e] = l > -INFINITY && (!a.bias || a.bias[e] > -INFINITY) ? l : -INFINITY;   // NaN closes too
+  }
+  __syncwarp();
+  float group = -INFINITY;   // of lane g
+  if (lane < a.groups)
+    for (int j = 0; j < n; ++j) group = fmaxf(group, c[lane * n + j]);
+  const int rank = group_rank(group, a.groups == 32 ? kAll : (1u << a.groups) - 1u);
+  const unsigned open = __ballot_sync(kAll, lane < a.groups && rank < a.top_groups);
+  int mine = -1;
+  for (int slot = 0; slot < a.k; ++slot) {
+    int v = INT_MIN, at = INT_MAX;
+    for (int e = lane; e < E; e += 32)
+      if (c[e] > -INFINITY && (open >> (e / n) & 1u) && topk_order_key(c[e]) > v) {
+        v = topk_order_key(c[e]);
+        at = e;
+      }
+    const int best = topk_redux_max(v);
+    if (best == INT_MIN) break;
+    at = topk_redux_min(v == best ? at : INT_MAX);
+    if (lane == slot) mine = at;
+    if (lane == (at & 31)) c[at] = -INFINITY;
+    __syncwarp();
+  }
+  return mine;
+}
+
 // A lane's keys (INT_MIN: none) of experts lane, lane + 32, ...  Up to eight are
 // sorted once, best first, and the head drops out as it is chosen; more are looked
 // through for every rank.
@@ -291,7 +325,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
   if (t >= a.T) return;
   const T* row = static_cast<const T*>(a.logits) + (size_t)(t * a.ld);
   const bool softmax = a.scoring == QMOE_SCORE_SOFTMAX, filter = a.top_groups < a.groups;
-  bool by_score = a.bias || (filter && a.best == 2);   // keys that are rounded
+  const bool by_score = a.bias || (filter && a.best == 2);   // keys that are rounded
 
   float l[NPL];
   bool nan = false;
@@ -318,14 +352,6 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     }
     sum = warp_sum(sum);
   }
-  // A softmax over +infinity has no scores: the weights will say so, and the choice
-  // is by the logits, as without a bias and with each group's best.
-  const bool lost = softmax && by_score && mx == INFINITY;
-  if (lost) {
-    nan = true;
-    by_score = false;
-  }
-  const bool biased = a.bias && !lost;
 
   LaneKeys<NPL> keys;
   unsigned open = kAll;   // groups
@@ -350,10 +376,7 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        c[i] = l[i];
-        if (lost && a.bias && lane + 32 * i < E && !(a.bias[lane + 32 * i] > -INFINITY)) c[i] = -INFINITY;
-      }
+      for (int i = 0; i < NPL; ++i) c[i] = l[i];
     }
     if (filter) {
       float* sm = reinterpret_cast<float*>(choice_smem + (size_t)warp * a.room);
@@ -361,12 +384,12 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
       for (int i = 0; i < NPL; ++i)
         if (lane + 32 * i < E) sm[lane + 32 * i] = c[i];
       __syncwarp();
-      open = best_groups<DT>(a, row, sm, mx, lost ? 1 : a.best, by_score, tau);
+      open = best_groups<DT>(a, row, sm, mx, by_score, tau);
     }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       const int e = lane + 32 * i;
-      const float v = biased ? c[i] : l[i];
+      const float v = a.bias ? c[i] : l[i];
       const bool may = c[i] > -INFINITY && (!filter || (open >> ((uint32_t)e * a.group_magic >> 20) & 1u));
       keys.key[i] = may ? topk_order_key(v) : INT_MIN;
     }
@@ -378,8 +401,8 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     int best, at;
     keys.best(best, at);
     const int m = topk_redux_max(best);
-    if (m == INT_MIN || (slot == k && !biased)) break;
-    if (biased && slot > 0) {
+    if (m == INT_MIN || (slot == k && !a.bias)) break;
+    if (a.bias && slot > 0) {
       const float x = ordered_float(before), y = ordered_float(m);
       if (!(x - y > tau + 0x1p-22f * (fabsf(x) + fabsf(y)))) unsure = true;
     }
@@ -411,6 +434,9 @@ __global__ void __launch_bounds__(32 * kChoiceWarps) choice_kernel(const ChoiceA
     if (n <= 32) mine = choose64_of<DT>(a, row, lane < n ? list[lane] : -1, mx, list);
     else mine = choose64<DT>(a, row, mx, open, room);
   }
+
+  // every score was NaN, so that nothing could be chosen
+  if (softmax && by_score && mx == INFINITY) mine = choose_by_logits<DT>(a, row, reinterpret_cast<float*>(choice_smem + (size_t)warp * a.room));
 
   const float chosen = mine >= 0 ? load_d<DT>(row, mine) : -INFINITY;
   float w = 0.f;
