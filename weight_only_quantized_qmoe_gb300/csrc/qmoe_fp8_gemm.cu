@@ -28,8 +28,11 @@
 // experts of 1536 x 2048: 51 to 56 us, 6 TB/s of the weights of those that have
 // rows, which bound it).  Many rows take pairs of CTAs, further down.
 //
-// Every wait is bounded; a timeout aborts all roles, drains what is in
-// flight, frees TMEM and is reported by qmoe_op_poll_status.
+// Every wait on an mbarrier is bounded; a timeout aborts all roles, drains what is in
+// flight, frees TMEM and is reported by qmoe_op_poll_status.  Three waits have no limit
+// of their own: for the kernel before (op_begin); at the barriers of the CTA and of the
+// cluster, which every warp comes to, whatever its waits gave; and for tensor memory,
+// which is free (kAloneBytes).
 #include "qmoe_tile.cuh"
 
 namespace qmoe {
@@ -58,7 +61,7 @@ struct F8Ring {
   static constexpr int sum_col0 = sf_col0 + stages * sf_cols;     // the sum of the pieces of 32-bit results
   static constexpr int tmem_cols = 256;
   static_assert(sum_col0 + bn <= tmem_cols, "TMEM columns");
-  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(total > kAloneBytes && total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
   static_assert(bn * kTileM * 4 <= stages * w_bytes, "a partial tile fits the ring");
 };
@@ -397,7 +400,7 @@ struct F8PairRing {
   static constexpr int sf_col0 = 2 * bn;
   static constexpr int sf_cols = 12;                              // W's four columns, then A's eight
   static_assert(sf_col0 + sf_groups * sf_cols <= 512, "TMEM columns");
-  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(total > kAloneBytes && total + 1024 <= 227 * 1024, "shared memory");
   static_assert(a_bytes % 1024 == 0, "swizzle atoms");
 };
 // Copies of A's rows of every size that a tile has, 16 to 112 rows a CTA, so that a

@@ -32,8 +32,9 @@
 // stores take 107).  BN = 192 is what two accumulators and the scales leave of
 // TMEM; BN = 64 puts more multiprocessors to work where there are few tiles.
 //
-// Every wait is bounded; a timeout aborts all roles, drains what is in
-// flight, frees TMEM and is reported by qmoe_op_poll_status.
+// Every wait on an mbarrier is bounded; a timeout aborts all roles, drains what is in
+// flight, frees TMEM and is reported by qmoe_op_poll_status.  (Not so the waits for the
+// kernel before and for tensor memory, and the barriers that every warp comes to.)
 #include <algorithm>
 
 #include "qmoe_ops.cuh"
@@ -71,7 +72,7 @@ struct MxRing {
   static constexpr int sf_col0 = 2 * BN;
   static constexpr int sf_cols = 8 + 8 * groups;
   static_assert(sf_col0 + stages * sf_cols <= kMxTmemCols, "TMEM columns");
-  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(total > kAloneBytes && total + 1024 <= 227 * 1024, "shared memory");
   static_assert(b_bytes % 1024 == 0 && a_bytes % 1024 == 0, "swizzle atoms");
 };
 

@@ -27,8 +27,9 @@
 //     then 4 epilogue warps (tcgen05.ld);
 //   * persistent CTAs stride over the (item, weight-tile) list; fc1 rows are
 //     interleaved gate/up so the GLU pairs sit in adjacent TMEM lanes;
-//   * every wait is bounded; a timeout aborts all roles, drains in-flight
-//     copies and MMAs, frees TMEM and records QMOE_ERR_TIMEOUT.
+//   * every wait on an mbarrier or a counter is bounded; a timeout aborts all
+//     roles, drains in-flight copies and MMAs, frees TMEM and records
+//     QMOE_ERR_TIMEOUT.
 #include "qmoe_prefill.cuh"
 #include "qmoe_tc.cuh"
 
@@ -365,6 +366,8 @@ struct Ring {
   __host__ __device__ static int epi_off(int sb) { return w_off + stages * wslot(sb); }
   __host__ __device__ static int bar_off(int sb) { return epi_off(sb) + kEpiBytes; }
   __host__ __device__ static int total(int sb) { return bar_off(sb) + 1024; }
+  // (a k-step of weights is 128 rows of 64 codes at least)
+  static_assert(w_off + stages * ksub * 1024 * BITS + kEpiBytes > kAloneBytes, "shared memory");
 };
 
 __device__ __forceinline__ void red_add_v4_f32(float* p, float a, float b, float c, float d) {

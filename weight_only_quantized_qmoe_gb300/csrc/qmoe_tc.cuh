@@ -7,6 +7,11 @@
 
 namespace qmoe {
 
+// A kernel with tensor memory takes more than half of a multiprocessor's shared memory,
+// so that no two of them meet there: its allocation, which has no limit, then waits
+// for nothing that a kernel launched ahead (and itself waiting for this one) holds.
+constexpr int kAloneBytes = 114 * 1024;
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
                "r"(ncols)

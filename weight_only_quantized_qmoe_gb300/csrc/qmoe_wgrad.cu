@@ -28,7 +28,7 @@
 // 4.6 for the aligned copies; the launch, one round of the ring and the stores bound
 // it); more take pairs of CTAs, further down.
 //
-// Every wait is bounded, as in the products' kernels.
+// Waits are bounded as in the 8-bit products' kernels.
 #include "qmoe_tile.cuh"
 
 namespace qmoe {
@@ -69,7 +69,7 @@ struct WgRing {
   static constexpr int row_off = bar_off + 512;                 // first row of each expert
   static constexpr int total = row_off + (kSortMaxExperts + 1) * 4;
   static constexpr int tmem_cols = 2 * kWgBN;
-  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(total > kAloneBytes && total + 1024 <= 227 * 1024, "shared memory");
   static_assert(kWgBN * kTileM * 4 <= bar_off, "a partial tile fits the ring");
 };
 
@@ -363,7 +363,7 @@ struct WgPairRing {
   static constexpr int bar_off = dy_off + stages * dy_bytes;
   static constexpr int row_off = bar_off + 512;
   static constexpr int total = row_off + (kSortMaxExperts + 1) * 4;
-  static_assert(total + 1024 <= 227 * 1024, "shared memory");
+  static_assert(total > kAloneBytes && total + 1024 <= 227 * 1024, "shared memory");
 };
 
 // The maps of every expert with rows: those of all rows, ended at its last.  A warp
