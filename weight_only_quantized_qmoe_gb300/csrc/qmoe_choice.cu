@@ -14,12 +14,15 @@
 // Bound: instructions and latency.  A warp takes a token: lane l holds the logits of
 // experts l, l + 32, ..., sorted; a rank is one redux for the best key and one for
 // the lowest index at it.  The logits are read once, two 4-byte words a token and
-// rank written.  (8192 tokens, eight of 256 experts in f32, 8.4 MB: softmax 10.5 us,
-// sigmoid with a bias 14.5, with the four best of eight groups 17 to 20, softmax
-// with a bias 23; the gradient 4.3.  Half of the issue slots are used.  Few tokens
-// are repeated in 64 bits, some ten of these, but one that is takes as long as a
-// third of the others together; more CTAs, fewer registers or a warp that loads its
-// next token's logits early changed nothing.)
+// rank written.  (8192 tokens, eight of 256 experts in f32, 8.4 MB: softmax 10.4 us,
+// sigmoid with a random bias 15.6, with the four best of eight groups 17.3, softmax
+// with a bias 22.5; the gradient 4.3.  Half of the issue slots are used.  Some ten of
+// these tokens are repeated in 64 bits, and one that is takes as long as a third of
+// the others together; more CTAs, fewer registers or a warp that loads its next
+// token's logits early changed nothing.)  Equal neighbours are repeated too, and a bias
+// of zeros makes many where logits are coarse or their scores near one: bf16 logits
+// of spread 1.5 and 8 by sigmoid 23 and 39 us, by softmax 56 and 102; f32 logits of
+// spread 5 and 8 by sigmoid 26 and 36.
 #include <algorithm>
 #include <climits>
 

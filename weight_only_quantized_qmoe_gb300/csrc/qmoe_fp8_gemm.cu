@@ -26,7 +26,8 @@
 //
 // That is the form for few rows (1 x 2048 x 2048: 5.9 us; 32 tokens to 8 of 128
 // experts of 1536 x 2048: 51 to 56 us, 6 TB/s of the weights of those that have
-// rows, which bound it).  Many rows take pairs of CTAs, further down.
+// rows, which bound it; 16 x 8192 x 16384 25.3, with a 32-bit result in pieces 25.5).
+// Many rows take pairs of CTAs, further down.
 //
 // Every wait on an mbarrier is bounded; a timeout aborts all roles, drains what is in
 // flight, frees TMEM and is reported by qmoe_op_poll_status.  Three waits have no limit
@@ -746,7 +747,9 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int inject_stall, cudaStre
   // tiles of 32 rows while they are all under way at once, or an expert has few rows
   // (us, narrow / pairs: 64 x 2048 x 2048 over all 7.7 / 7.4, 300 rows 13.5 / 8.0;
   // experts of 1536 x 2048, 2 rows each of 128 50.8 / 52.0, 16 of 64 38.9 / 39.1, 32
-  // of 64 48.9 / 40.3)
+  // of 64 48.9 / 40.3; uneven spreads are not told apart: 4096 rows over 256 experts in
+  // narrow tiles, even 133, half of them one expert's 157, all 65, where the dense
+  // product of as many rows takes 15)
   if (narrow > kSms && rows >= 24) {
     args.bn = pair_rows(a);
     return run(true, most_tiles(a, args.bn, 2 * kTileM), 1);

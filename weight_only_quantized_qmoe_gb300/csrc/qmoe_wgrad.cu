@@ -687,7 +687,9 @@ cudaError_t launch_wg(const WgKernelArgs& args, cudaStream_t s) {
   // A tile's rows over the CTAs of a cluster while there are CTAs without a tile, if
   // the rows, spread evenly, fill 24 stages (us with / without: 2048 rows of 256 x
   // 256, in 8 parts, 10.2 / 17.2; 4000 of 1024 x 1024, in 4, 17.0 / 30.9; 32768 of
-  // 64 x 64, in 8, 23.5 / 153; but 1000 of 1024 x 1024, 16 stages in 4, 11.9 / 11.1).
+  // 64 x 64, in 8, 23.5 / 153; but 1000 of 1024 x 1024, 16 stages in 4, 11.9 / 11.1.
+  // Uneven spreads are not told apart: 32768 rows over 16 experts of 256 x 256, even 15,
+  // all of one expert, in 4, 66; dense, in 8, 37).
   const int64_t steps = (a.R / a.E + kWgRows - 1) / kWgRows;
   int split = 1;
   while (steps >= 24 && split < 8 && tiles * split * 2 <= kSms && split * 8 <= steps) split *= 2;
