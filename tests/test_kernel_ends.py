@@ -49,3 +49,15 @@ def test_no_other_kernel_has_tensor_memory():
     from test_ops_sources import CSRC
     users = [n for n in sorted(os.listdir(CSRC)) if n.endswith((".cu", ".cuh")) and re.search(r"\btmem_dealloc\w*\(tmem", code(n))]
     assert users == sorted(WITH_TMEM)
+
+
+@pytest.mark.parametrize("name,kernel", [("qmoe_prefill.cu", "gemm_kernel"), ("qmoe_mx4_gemm.cu", "mx4_matmul_kernel"),
+                                         ("qmoe_fp8_gemm.cu", "fp8_matmul_kernel"), ("qmoe_wgrad.cu", "weight_grad_kernel")])
+def test_a_cta_waits_for_its_own_commits(name, kernel):
+    # the producer for the stages', the epilogue for the accumulators', the issuer for
+    # its last one
+    text = kernels(name)[kernel]
+    assert set(re.findall(r"tc_commit_elect\(&?(\w+)", text)) <= {"empty", "acc_full", "drain_bar"}
+    producer = text[text.index("if (warp == 0) {"):text.index("else if (warp == ")]
+    assert re.search(r"\n    drain_ring<\w+>\(empty, ", producer)
+    assert "wait_or_abort(&acc_full[ab]" in text and "mbar_wait_bounded(drain_bar, 0" in text

@@ -40,7 +40,6 @@ namespace qmoe {
 
 constexpr int kF8StageK = 128;                 // values along the reduction a stage: one swizzle atom
 constexpr int kF8Threads = 128 + 32 * kEpiWarps;
-constexpr long long kF8DrainPolls = 4096;      // parked polls (about 4 ms) a copy in flight is given to land
 
 struct F8Ring {
   static constexpr int bn = 32;                                   // rows of A a tile
@@ -199,13 +198,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         else tma_3d_elect(dw, &map_w, ks * kF8StageK, n0, t.e, &full[s]);
       }
     }
-    if (!ok) {
-      // After a wait that ran out the copies in flight must land before the CTA
-      // leaves: wait for the last stages' barriers, with a limit, as the scale
-      // warps may have left them short.
-      const WaitCfg drain{a.wait.status, kF8DrainPolls};
-      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
-    }
+    // (after a wait that ran out the scale warps may have left the stages short)
+    if (!ok) drain_ring<S>(full, it, a.wait.status, kDrainPolls);
+    drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
   } else if (warp == 2) {
     // ---------------- scales of A's rows ----------------
     // Row `lane` goes to bytes lane * 16 of the chunk: the four bytes of 512 values, of
@@ -534,8 +529,8 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
       }
       // (both CTAs' copies count on the first one's barriers; the second one's own
       // never complete, so it waits for as long as the limit says)
-      if (!ok) drain_ring<S>(full, it, a.wait.status, kF8DrainPolls);
-      if (warp == 0) drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kF8DrainPolls);   // see pair_end
+      if (!ok) drain_ring<S>(full, it, a.wait.status, kDrainPolls);
+      if (warp == 0) drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
@@ -638,7 +633,7 @@ __global__ void __launch_bounds__(kF8PairThreads, 1)
         if (lane == 0) cluster_bar_arrive(first_cta_bar(&sf_full[sf.s]));
       }
     }
-    if (warp == 4) drain_ring<G>(sf_empty, groups, a.wait.status, ok ? kDrainWaitLimit : kF8DrainPolls);   // see pair_end
+    if (warp == 4) drain_ring<G>(sf_empty, groups, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
   } else if (warp >= 8) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp >> 2) - 2;

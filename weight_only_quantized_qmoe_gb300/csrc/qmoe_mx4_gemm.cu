@@ -50,7 +50,6 @@ constexpr int kMxTmemCols = 512;
 constexpr int kMxThreads = 256;
 constexpr int kMxEpiPitch = 144;               // bytes of a staged output row (128 + 16: banks)
 constexpr int kMxMaxExperts = 1024;
-constexpr long long kMxDrainPolls = 4096;      // parked polls (about 4 ms) a copy in flight is given to land
 
 template <int BN>
 struct MxRing {
@@ -287,13 +286,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         tma_2d_elect(smem + RG::b_off + s * RG::b_bytes, &map_w, ks * kMxRowBytes, t.e * a.N + t.n0, &full[s]);
       }
     }
-    if (!ok) {
-      // After a wait that ran out the copies in flight must land before the CTA
-      // leaves: wait for the last stages' barriers, with a limit, as the scale
-      // loaders may have left them short.
-      const WaitCfg drain{a.wait.status, kMxDrainPolls};
-      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
-    }
+    // (after a wait that ran out the scale loaders may have left the stages short)
+    if (!ok) drain_ring<S>(full, it, a.wait.status, kDrainPolls);
+    drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
   } else if (warp == 2 || warp == 3) {
     // ---------------- scale loaders: warp 2 + h takes the 128-value chunk h of each stage ----------------
     // Row 32 j + lane of a 128-row group goes to bytes lane * 16 + j * 4 of its

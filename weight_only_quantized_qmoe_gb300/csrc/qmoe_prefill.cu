@@ -627,6 +627,7 @@ __global__ void __launch_bounds__((Ring<DEC, BITS>::threads), 1)
         mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, drain);
       }
     }
+    drain_ring<kStages>(empty, issued, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
   } else if (warp == 1) {
     // ---------------- MMA issuer: the whole warp, one elected lane issues ----------------
     const uint32_t a0 = tmem + RG::acol0;

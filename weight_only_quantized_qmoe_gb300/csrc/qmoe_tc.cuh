@@ -116,6 +116,21 @@ __device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, co
   return false;
 }
 
+// Waits for the barriers of the last S of `it` stages, with a limit: for copies in
+// flight (after a wait that ran out they must land before the CTA leaves), or for the
+// commits that free the stages.  A commit arrives on its own, some time after its MMAs,
+// and nothing says that the arrivals of two come in order: none may come to a CTA that
+// has left, where it would change another CTA's shared memory, so the producer waits
+// for each stage's last.
+template <int S>
+__device__ __forceinline__ void drain_ring(uint64_t* bars, int it, int* status, long long polls) {
+  const WaitCfg drain{status, polls};
+  for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&bars[i % S], (i / S) & 1, drain);
+}
+// Parked polls (about 4 ms) that a copy in flight, or a commit, is given after a wait
+// that ran out.
+constexpr long long kDrainPolls = 4096;
+
 __device__ __forceinline__ void mbar_arrive_expect_tx_elect(uint64_t* bar, uint32_t bytes) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"

@@ -69,14 +69,12 @@ __device__ __forceinline__ void cluster_sync_all() {
   __syncwarp();   // the barrier is the whole warp's, and lanes leave a wait one by one
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Last of a pair, behind a barrier of the CTA.  A commit arrives on its own, some
-// time after its MMAs, and nothing orders the arrivals of two commits: none may come
-// to a CTA that has left, where it would change another CTA's shared memory.  So both
-// CTAs wait for every one of them: a producer for the last phase of each stage's
-// barrier and a scale warp for that of each group's (drain_ring), the epilogue for
-// every accumulator, and here the second CTA for the issuer's last commit, as the
-// issuer did.  (After a wait that ran out the phases to come are not known: what the
-// issuer did commit arrives within the limits of these waits, thousands of MMAs long.)
+// Last of a pair, behind a barrier of the CTA.  Both CTAs wait for every commit that
+// arrives in them (see drain_ring): a producer for the last phase of each stage's
+// barrier and a scale warp for that of each group's, the epilogue for every
+// accumulator, and here the second CTA for the issuer's last commit, as the issuer did.
+// (After a wait that ran out the phases to come are not known: what the issuer did
+// commit arrives within the limits of these waits, thousands of MMAs long.)
 // Arrivals by threads come before their own arrival at the cluster's barrier, behind
 // which neither CTA leaves before the other.
 __device__ __forceinline__ void pair_end(uint64_t* drain_bar, int rank, int* status) {
@@ -138,14 +136,6 @@ struct RingAt {
     }
   }
 };
-// Waits for the barriers of the last S of `it` stages, with a limit: for copies in
-// flight (after a wait that ran out they must land before the CTA leaves), or for the
-// commits that free the stages.
-template <int S>
-__device__ __forceinline__ void drain_ring(uint64_t* bars, int it, int* status, long long polls) {
-  const WaitCfg drain{status, polls};
-  for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&bars[i % S], (i / S) & 1, drain);
-}
 // spin_or_abort for such a phase: one answer for the whole warp.
 __device__ __forceinline__ bool warp_spin_cluster(uint64_t* bar, uint32_t parity, const WaitCfg& w, volatile int* abort_flag) {
   const long long limit = w.limit * 64;

@@ -38,7 +38,6 @@ constexpr int kWgPanel = 64;                    // columns of a panel (128 bytes
 constexpr int kWgPanelBytes = kWgRows * 128;
 constexpr int kWgThreads = 128 + 32 * kEpiWarps;
 constexpr int kWgBN = 256;
-constexpr long long kWgDrainPolls = 4096;
 // Rows summed in the tensor core at a time, whole stages (see add_tile; of normal
 // values, relative error of 1024 rows in one piece 1.2e-6, of 32768 3.8e-5): for
 // 16-bit results as many as leave out a sixth of their own rounding (2^-11 for f16).
@@ -225,11 +224,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
           tma_3d_elect(smem + RG::dy_off + s * RG::dy_bytes + p * kWgPanelBytes, &map_dy, t.n0 + p * kWgPanel, r, 0, &full[s]);
       }
     }
-    if (!ok) {
-      // the copies in flight must land before the CTA leaves
-      const WaitCfg drain{a.wait.status, kWgDrainPolls};
-      for (int i = it > S ? it - S : 0; i < it; ++i) mbar_wait_bounded(&full[i % S], (i / S) & 1, drain);
-    }
+    if (!ok) drain_ring<S>(full, it, a.wait.status, kDrainPolls);
+    drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     const uint64_t xdesc0 = smem_desc_mn128(smem_u32(smem + RG::x_off), kWgPanelBytes);
@@ -482,8 +478,8 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       }
       // (both CTAs' copies count on the first one's barriers; the second one's own
       // never complete, so it waits for as long as the limit says)
-      if (!ok) drain_ring<S>(full, it, a.wait.status, kWgDrainPolls);
-      if (warp == 0) drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kWgDrainPolls);   // see pair_end
+      if (!ok) drain_ring<S>(full, it, a.wait.status, kDrainPolls);
+      if (warp == 0) drain_ring<S>(empty, it, a.wait.status, ok ? kDrainWaitLimit : kDrainPolls);
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer ----------------
